@@ -263,7 +263,22 @@ def _own(st):
         b = sdm.sdm_recurrence_backward(sh, st["za"], st["zb"], st["v"], r["states"], st["dy"], A=st["A"], bias=st["bias"],
                                         offsets=st["offsets"], dhT=st["dhT"])
         out.update({k: b[k] for k in ("dza", "dzb", "dv", "dA", "dbias", "dh0")})
+        _leave_dy_as_the_plain_form_does(st)
     return out
+
+
+def _leave_dy_as_the_plain_form_does(st):
+    """The plain form adds the final states' gradient to the last rows of dy,
+    and where dy is in 32 bits that is the state's own dy: a further pass on
+    the same state starts from the sum.  So it does here."""
+    dy, dhT, off = st["dy"], st["dhT"], st["offsets"]
+    if dy.dtype != torch.float32:
+        return
+    if off is None:
+        dy.view(dhT.shape[0], -1, dy.shape[1])[:, -1] += dhT
+        return
+    some = off[1:] > off[:-1]                      # an empty sequence adds nothing
+    dy.index_add_(0, (off[1:] - 1).clamp_(min=0), dhT * some[:, None])
 
 
 def run(state):

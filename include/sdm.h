@@ -60,7 +60,9 @@ typedef enum {
   SDM_ERR_DUPLICATE_SLOT = 6   /* device: a slot repeated within one write set  */
 } sdm_status;
 
-typedef enum { SDM_F32 = 0, SDM_BF16 = 1 } sdm_dtype;
+/* SDM_E4M3 (8-bit float, 4 exponent bits, largest value 448) is an output
+ * type of sdm_add_rmsnorm only; every other argument takes the first two. */
+typedef enum { SDM_F32 = 0, SDM_BF16 = 1, SDM_E4M3 = 2 } sdm_dtype;
 typedef enum { SDM_SCORE_DOT = 0, SDM_SCORE_IDW = 1 } sdm_score_kind;
 typedef enum { SDM_UPDATE_EQ4 = 0, SDM_UPDATE_SHARED_RESIDUAL = 1 } sdm_update_form;
 
@@ -262,6 +264,134 @@ sdm_status sdm_forward(const sdm_shape* shape, const void* q_w, const void* q_r,
                        const void* v, float* M, float* y, int32_t* idx_w,
                        float* wt_w, int32_t* idx_r, float* wt_r, void* workspace,
                        size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gated delta recurrence: the dense counterpart of sdm_scan, one slot of
+ * weight 1 per channel with the gates formed from their logits
+ * [SDM notes 2.4: alpha = exp(-A softplus(z + b)), beta = sigmoid(z)].
+ * For every sequence, row t and channel c:
+ *   alpha = exp(-A[c] * softplus(za[t,c] + bias[c])),  beta = sigmoid(zb[t,c]);
+ *   h~ = alpha h[t-1];  h[t] = h~ + beta (v[t,c] - h~);  y[t,c] = h[t].
+ * The state h is float32 throughout; y is h rounded to the shape's dtype.
+ *
+ * Rows are packed: sequence s owns rows offsets[s] .. offsets[s+1]-1 of the
+ * [rows, D] tensors.  `offsets` is a DEVICE array of n_seq + 1 int32, not
+ * decreasing, within [0, rows]; NULL cuts the rows into n_seq equal parts.
+ * A sequence may have no rows (its final state is its initial one).  Rows of
+ * no sequence (before offsets[0], from offsets[n_seq] on) are neither read nor
+ * written.  Offsets that break these rules are found on the device: nothing is
+ * written and SDM_ERR_DEVICE_BOUNDS is recorded. */
+typedef struct {
+  int n_seq;              /* sequences, 0..65535                                 */
+  int rows;               /* rows of the packed tensors                          */
+  int D;                  /* channels, a multiple of 8, at most 65536            */
+  int ld;                 /* elements between rows of za, zb, v (so that they can */
+                          /* be column ranges of one wider projection); a        */
+                          /* multiple of 8, at least D; 0 = D                    */
+  int ld_grad;            /* the same of dza, dzb, dv; 0 = D                     */
+  sdm_dtype dtype;        /* of za, zb, v, y, dy, dza, dzb, dv: SDM_F32/SDM_BF16 */
+} sdm_recurrence;
+
+/* Bytes of device workspace the forward / backward pass needs, and of the
+ * `states` array that carries what the backward pass needs from the forward
+ * one (0 for an invalid shape). */
+size_t sdm_recurrence_workspace_size(const sdm_recurrence* shape);
+size_t sdm_recurrence_states_size(const sdm_recurrence* shape);
+
+/* Forward pass.
+ *   za, zb, v: [rows, D] (rows ld apart); A, bias: [D] float32, NULL = ones /
+ *   zeros; offsets: see above, or NULL;
+ *   h0: [n_seq, D] float32 initial states, or NULL for zeros;
+ *   y:  [rows, D] out;  hT: [n_seq, D] float32 final states out, or NULL (may
+ *   be h0 itself: states updated in place);
+ *   states: NULL, or caller-owned scratch of sdm_recurrence_states_size bytes
+ *   that sdm_recurrence_backward reads (contents private to the library);
+ *   workspace: at least sdm_recurrence_workspace_size bytes, contents
+ *   irrelevant on entry and on return; calls that may overlap on the GPU
+ *   (other streams, captured graphs that run at the same time) need one each.
+ * Apart from hT = h0, outputs must not overlap inputs or one another.  Results
+ * are the same from run to run, bit for bit. */
+sdm_status sdm_recurrence_forward(const sdm_recurrence* shape, const void* za, const void* zb,
+                                  const void* v, const float* A, const float* bias,
+                                  const int32_t* offsets, const float* h0, void* y, float* hT,
+                                  float* states, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/* Backward pass of sdm_recurrence_forward, for the same shape, inputs and
+ * offsets and the `states` it wrote.
+ *   dy: [rows, D] gradient of y;  dhT: [n_seq, D] float32 gradient of hT, or
+ *   NULL for zeros;
+ *   dza, dzb, dv: [rows, D] out (rows ld_grad apart);
+ *   dA, dbias: [D] float32 out, sums over every row of every sequence, or
+ *   NULL;  dh0: [n_seq, D] float32 out, or NULL (may be dhT itself).
+ * Gradients are written, not added to what the arrays held.  Workspace,
+ * overlap and repeatability as in the forward pass.  With n_seq = 0 only dA
+ * and dbias are written (zeros). */
+sdm_status sdm_recurrence_backward(const sdm_recurrence* shape, const void* za, const void* zb,
+                                   const void* v, const float* A, const float* bias,
+                                   const int32_t* offsets, const float* states, const void* dy,
+                                   const float* dhT, void* dza, void* dzb, void* dv, float* dA,
+                                   float* dbias, float* dh0, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/* One token per sequence on a pool of states (decode): row i of the inputs
+ * steps state row slots[i] in place and writes y row i.  Of the shape, rows
+ * is the number of tokens; n_seq and ld_grad only need to be valid.
+ *   state: [n_slots, D] float32, in place;  slots: [rows] int32, or NULL for
+ *   row i = state row i (rows <= n_slots).  A negative slot is padding: that
+ *   row of y and every state row stay as they are.  A slot >= n_slots
+ *   (SDM_ERR_DEVICE_BOUNDS) or one that an earlier row already has
+ *   (SDM_ERR_DUPLICATE_SLOT) is skipped in the same way and recorded.
+ * Needs no workspace.  y must not overlap an input. */
+sdm_status sdm_recurrence_step(const sdm_recurrence* shape, const void* za, const void* zb,
+                               const void* v, const float* A, const float* bias, float* state,
+                               int n_slots, const int32_t* slots, void* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Residual addition and RMS-Norm in front of a layer's projections (the norm
+ * behind the read is sdm_rmsnorm_gate), optionally with the output in 8 bits:
+ *   s = x + residual, rounded to the shape's dtype (s = x without a residual);
+ *   n = s / sqrt(mean_c s_c^2 + eps) * gamma, from the rounded s, in float32;
+ *   out = n in SDM_F32 or SDM_BF16; or, for SDM_E4M3, per row (group = 0) or
+ *   per `group` channels: scale = max(max|n| / 448, 2^-126), float32, and
+ *   out = n / scale rounded to nearest even, so that out * scale stands for n.
+ * A NaN in a row makes the row's outputs and scales NaN. */
+typedef struct {
+  int rows;               /* rows                                                */
+  int D;                  /* channels, a multiple of 8, at most 16384            */
+  sdm_dtype dtype;        /* of x, residual, s, dout, ds, dx: SDM_F32 / SDM_BF16 */
+} sdm_norm;
+
+/* Forward.
+ *   x, residual: [rows, D]; residual may be NULL;  gamma: [D] float32 or NULL
+ *   for ones;  eps: > 0;
+ *   s: [rows, D] out, or NULL (may be x or residual itself: the residual
+ *   stream updated in place);
+ *   out: [rows, D] in out_dtype: SDM_F32, SDM_BF16 or SDM_E4M3;
+ *   group: 0, 32, 64 or 128 (dividing D; 0 unless out_dtype is SDM_E4M3);
+ *   scale: [rows] or [rows, D / group] float32 out, for SDM_E4M3 only. */
+sdm_status sdm_add_rmsnorm(const sdm_norm* shape, const void* x, const void* residual,
+                           const float* gamma, float eps, void* s, void* out,
+                           sdm_dtype out_dtype, int group, float* scale, void* stream);
+
+/* Bytes of device workspace sdm_add_rmsnorm_backward needs (0 for an invalid
+ * shape). */
+size_t sdm_add_rmsnorm_workspace_size(const sdm_norm* shape);
+
+/* Backward of the 16/32-bit forward from the s it wrote (x and residual have
+ * the same gradient dx):
+ *   w = dout gamma;  inv = 1 / sqrt(mean s^2 + eps);
+ *   dx = ds + inv (w - s inv mean_c(w s inv));  dgamma = sum_rows dout s inv.
+ *   dout: [rows, D] gradient of out, in the shape's dtype;  ds: [rows, D]
+ *   gradient that reaches s from elsewhere, or NULL;  dx: [rows, D] out (may
+ *   be dout or ds itself);  dgamma: [D] float32 out, written, or NULL;
+ *   workspace: at least sdm_add_rmsnorm_workspace_size bytes if dgamma is
+ *   given (else it may be NULL), one per overlapping call.
+ * Results are the same from run to run, bit for bit. */
+sdm_status sdm_add_rmsnorm_backward(const sdm_norm* shape, const void* s, const void* dout,
+                                    const float* gamma, const void* ds, float eps, void* dx,
+                                    float* dgamma, void* workspace, size_t ws_bytes,
+                                    void* stream);
 
 /* Synchronizes `stream`, then returns and clears the device status word of
  * the current device (SDM_OK if no device-side failure was recorded). */

@@ -18,7 +18,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libsdm_gb300.so")
 
-SDM_F32, SDM_BF16 = 0, 1
+SDM_F32, SDM_BF16, SDM_E4M3 = 0, 1, 2
 SDM_SCORE_DOT, SDM_SCORE_IDW = 0, 1
 SDM_UPDATE_EQ4, SDM_UPDATE_SHARED_RESIDUAL = 0, 1
 
@@ -30,7 +30,10 @@ EXPORTS = ["sdm_status_string", "sdm_subscores", "sdm_select", "sdm_address",
            "sdm_undo_workspace_size", "sdm_scan_undo", "sdm_rmsnorm_gate", "sdm_decode",
            "sdm_forward", "sdm_forward_windows",
            "sdm_get_device_status",
-           "sdm_set_scan_tuning", "sdm_selftest_wait_timeout", "sdm_measure_row_traffic"]
+           "sdm_set_scan_tuning", "sdm_selftest_wait_timeout", "sdm_measure_row_traffic",
+           "sdm_recurrence_workspace_size", "sdm_recurrence_states_size",
+           "sdm_recurrence_forward", "sdm_recurrence_backward", "sdm_recurrence_step",
+           "sdm_add_rmsnorm", "sdm_add_rmsnorm_workspace_size", "sdm_add_rmsnorm_backward"]
 
 
 class SdmUnavailable(RuntimeError):
@@ -65,6 +68,31 @@ class Epilogue(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int)]
 
 
+class Recurrence(ctypes.Structure):
+    """Mirror of ``sdm_recurrence`` in include/sdm.h."""
+    _fields_ = [("n_seq", ctypes.c_int), ("rows", ctypes.c_int), ("D", ctypes.c_int),
+                ("ld", ctypes.c_int), ("ld_grad", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+    def __repr__(self):
+        return "Recurrence(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class Norm(ctypes.Structure):
+    """Mirror of ``sdm_norm`` in include/sdm.h."""
+    _fields_ = [("rows", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+    def __repr__(self):
+        return "Norm(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+def make_recurrence(n_seq, rows, D, dtype=SDM_BF16, ld=0, ld_grad=0) -> Recurrence:
+    return Recurrence(n_seq, rows, D, ld, ld_grad, dtype)
+
+
+def make_norm(rows, D, dtype=SDM_BF16) -> Norm:
+    return Norm(rows, D, dtype)
+
+
 def make_shape(B, H, T, n_sub, d_h, d_v, W, R, k_w=0, k_r=0, in_dtype=SDM_BF16,
                score=SDM_SCORE_DOT, idw_eps=1e-3, update=SDM_UPDATE_EQ4) -> Shape:
     return Shape(B, H, T, n_sub, d_h, d_v, W, R, k_w, k_r, in_dtype, score, idw_eps, update)
@@ -86,6 +114,7 @@ def lib():
     except OSError as e:
         raise SdmUnavailable(f"cannot load {LIB_PATH}: {e}") from e
     P, SP, I = ctypes.c_void_p, ctypes.POINTER(Shape), ctypes.c_int
+    RP, NP, Z = ctypes.POINTER(Recurrence), ctypes.POINTER(Norm), ctypes.c_size_t
     sig = {
         "sdm_status_string": ([I], ctypes.c_char_p),
         "sdm_subscores": ([SP, P, P, P, P], I),
@@ -106,6 +135,14 @@ def lib():
         "sdm_selftest_wait_timeout": ([ctypes.c_longlong, P], I),
         "sdm_measure_row_traffic": ([P, P, ctypes.c_longlong, ctypes.c_longlong, I, I, I, I, I,
                                      ctypes.c_uint, P], I),
+        "sdm_recurrence_workspace_size": ([RP], Z),
+        "sdm_recurrence_states_size": ([RP], Z),
+        "sdm_recurrence_forward": ([RP] + [P] * 11 + [Z, P], I),
+        "sdm_recurrence_backward": ([RP] + [P] * 16 + [Z, P], I),
+        "sdm_recurrence_step": ([RP] + [P] * 6 + [I, P, P, P], I),
+        "sdm_add_rmsnorm": ([NP, P, P, P, ctypes.c_float, P, P, I, I, P, P], I),
+        "sdm_add_rmsnorm_workspace_size": ([NP], Z),
+        "sdm_add_rmsnorm_backward": ([NP, P, P, P, P, ctypes.c_float, P, P, P, Z, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -410,3 +447,243 @@ def sdm_measure_row_traffic(src, dst, col_slice: int, T: int, loads: int, stores
                                       _stream(stream)),
         "sdm_measure_row_traffic")
     return chains * dv * T * (loads + stores) * 4
+
+
+# ------------------------------------------------- recurrence and residual norm
+
+_TORCH = {SDM_F32: torch.float32, SDM_BF16: torch.bfloat16, SDM_E4M3: torch.float8_e4m3fn}
+
+
+def _torch_dtype(dtype: int, what: str) -> torch.dtype:
+    if dtype not in _TORCH:
+        raise SdmError(1, what)
+    return _TORCH[dtype]
+
+
+class _Call:
+    """The device, the stream and the allocations of one call.  Tensors the
+    binding makes belong to the stream the kernels run on, so that the caching
+    allocator hands their memory on in that stream's order."""
+    __slots__ = ("device", "index", "torch_stream", "stream")
+
+    def __init__(self, like: torch.Tensor, stream):
+        if not like.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        self.device, self.index = like.device, torch.cuda.current_device()
+        if self.device.index != self.index:
+            raise ValueError(f"tensors are on {like.device}, but the current device is "
+                             f"cuda:{self.index}; call under torch.cuda.device({like.device})")
+        self.torch_stream = None
+        if stream is None:
+            self.stream = torch._C._cuda_getCurrentRawStream(self.index)
+        elif hasattr(stream, "cuda_stream"):
+            self.torch_stream, self.stream = stream, stream.cuda_stream
+        else:
+            self.stream = int(stream)
+            self.torch_stream = (torch.cuda.ExternalStream(self.stream, device=self.device)
+                                 if self.stream else torch.cuda.default_stream(self.device))
+
+    def empty(self, shape, dtype):
+        if self.torch_stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.torch_stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def ptr(self, t, name, dtype, numel):
+        """Address of a contiguous tensor of this dtype and at least `numel` elements."""
+        if t is None:
+            return None
+        if t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.numel() < numel:
+            raise ValueError(f"{name} has {t.numel()} elements, the shape needs {numel}")
+        return t.data_ptr()
+
+    def rows(self, t, name, dtype, rows, D, ld):
+        """Address of a [rows, D] tensor whose rows are `ld` elements apart
+        (leading dimensions that flatten to `rows` are fine when ld = D)."""
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if ld == D:
+            return self.ptr(t, name, dtype, rows * D)
+        if t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != D:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {D})")
+        if rows > 0 and (t.stride(1) != 1 or t.stride(0) != ld):
+            raise ValueError(f"{name} has strides {t.stride()}, expected ({ld}, 1)")
+        return t.data_ptr()
+
+
+def _required(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
+
+
+def sdm_recurrence_workspace_size(sh: Recurrence) -> int:
+    """Bytes of device workspace the recurrence's forward / backward pass needs."""
+    return int(lib().sdm_recurrence_workspace_size(ctypes.byref(sh)))
+
+
+def sdm_recurrence_states_size(sh: Recurrence) -> int:
+    """Bytes of the states the forward pass saves for the backward pass."""
+    return int(lib().sdm_recurrence_states_size(ctypes.byref(sh)))
+
+
+def _recurrence_inputs(c: _Call, sh: Recurrence, dt, za, zb, v, A, bias, offsets):
+    D, ld = sh.D, sh.ld or sh.D
+    return (c.rows(za, "za", dt, sh.rows, D, ld), c.rows(zb, "zb", dt, sh.rows, D, ld),
+            c.rows(v, "v", dt, sh.rows, D, ld), c.ptr(A, "A", torch.float32, D),
+            c.ptr(bias, "bias", torch.float32, D),
+            c.ptr(offsets, "offsets", torch.int32, sh.n_seq + 1))
+
+
+def _scratch(c: _Call, workspace, need: int):
+    if workspace is None:
+        workspace = c.empty((max(need, 16),), torch.uint8)
+        return workspace, workspace.data_ptr(), need
+    n = workspace.numel() * workspace.element_size()
+    return workspace, c.ptr(workspace, "workspace", workspace.dtype, 0), n
+
+
+def sdm_recurrence_forward(sh: Recurrence, za, zb, v, A=None, bias=None, offsets=None, h0=None,
+                           y=None, hT=None, states=None, save_states=False, workspace=None,
+                           stream=None):
+    """Gated delta recurrence over packed sequences.  za, zb, v [rows, D] (row
+    stride ``sh.ld``); A, bias [D] float32; offsets [n_seq + 1] int32 on the
+    device or None for equal parts; h0 [n_seq, D] float32.  Returns
+    dict(y, hT, states); states (for the backward pass) only if given or
+    ``save_states``."""
+    L, c = lib(), _Call(za, stream)
+    dt, D, f32 = _torch_dtype(sh.dtype, "sdm_recurrence_forward"), sh.D, torch.float32
+    if y is None:
+        y = c.empty((sh.rows, D), dt)
+    if hT is None:
+        hT = c.empty((sh.n_seq, D), f32)
+    n_states = 0
+    if save_states or states is not None:
+        n_states = sdm_recurrence_states_size(sh) // 4
+        if states is None:
+            states = c.empty((n_states,), f32)
+    ins = _recurrence_inputs(c, sh, dt, za, zb, v, A, bias, offsets)
+    ws, wsp, nws = _scratch(c, workspace, sdm_recurrence_workspace_size(sh))
+    _ok(L.sdm_recurrence_forward(ctypes.byref(sh), *ins, c.ptr(h0, "h0", f32, sh.n_seq * D),
+                                 c.ptr(y, "y", dt, sh.rows * D),
+                                 c.ptr(hT, "hT", f32, sh.n_seq * D),
+                                 c.ptr(states, "states", f32, n_states), wsp, nws, c.stream),
+        "sdm_recurrence_forward")
+    return dict(y=y, hT=hT, states=states)
+
+
+def sdm_recurrence_backward(sh: Recurrence, za, zb, v, states, dy, A=None, bias=None,
+                            offsets=None, dhT=None, dza=None, dzb=None, dv=None, dA=None,
+                            dbias=None, dh0=None, workspace=None, stream=None):
+    """Gradients of sdm_recurrence_forward from dy [rows, D] and dhT [n_seq, D]
+    float32 (None = zeros) with the states it saved.  dza, dzb, dv have row
+    stride ``sh.ld_grad`` and must be given where that is not D.  Returns
+    dict(dza, dzb, dv, dA, dbias, dh0); dA (dbias) is made only where A (bias)
+    is given."""
+    L, c = lib(), _Call(za, stream)
+    dt, D, f32 = _torch_dtype(sh.dtype, "sdm_recurrence_backward"), sh.D, torch.float32
+    ldg = sh.ld_grad or D
+    if ldg == D:
+        dza = c.empty((sh.rows, D), dt) if dza is None else dza
+        dzb = c.empty((sh.rows, D), dt) if dzb is None else dzb
+        dv = c.empty((sh.rows, D), dt) if dv is None else dv
+    if dA is None and A is not None:
+        dA = c.empty((D,), f32)
+    if dbias is None and bias is not None:
+        dbias = c.empty((D,), f32)
+    if dh0 is None:
+        dh0 = c.empty((sh.n_seq, D), f32)
+    za, zb, v, A_, bias_, off = _recurrence_inputs(c, sh, dt, za, zb, v, A, bias, offsets)
+    ws, wsp, nws = _scratch(c, workspace, sdm_recurrence_workspace_size(sh))
+    _ok(L.sdm_recurrence_backward(
+        ctypes.byref(sh), za, zb, v, A_, bias_, off,
+        c.ptr(_required(states, "states"), "states", f32, sdm_recurrence_states_size(sh) // 4),
+        c.ptr(_required(dy, "dy"), "dy", dt, sh.rows * D), c.ptr(dhT, "dhT", f32, sh.n_seq * D),
+        c.rows(dza, "dza", dt, sh.rows, D, ldg), c.rows(dzb, "dzb", dt, sh.rows, D, ldg),
+        c.rows(dv, "dv", dt, sh.rows, D, ldg), c.ptr(dA, "dA", f32, D),
+        c.ptr(dbias, "dbias", f32, D), c.ptr(dh0, "dh0", f32, sh.n_seq * D), wsp, nws, c.stream),
+        "sdm_recurrence_backward")
+    return dict(dza=dza, dzb=dzb, dv=dv, dA=dA, dbias=dbias, dh0=dh0)
+
+
+def sdm_recurrence_step(sh: Recurrence, za, zb, v, state, A=None, bias=None, slots=None, y=None,
+                        stream=None):
+    """One token per sequence: row i of za, zb, v [rows, D] steps state row
+    slots[i] (int32; negative = padding; None = row i) of state [n_slots, D]
+    float32 in place.  Returns y [rows, D]."""
+    L, c = lib(), _Call(za, stream)
+    dt, D = _torch_dtype(sh.dtype, "sdm_recurrence_step"), sh.D
+    if y is None:
+        y = c.empty((sh.rows, D), dt)
+    if state.dim() != 2 or state.shape[1] != D:
+        raise ValueError(f"state has shape {tuple(state.shape)}, expected (n_slots, {D})")
+    za, zb, v, A, bias, _ = _recurrence_inputs(c, sh, dt, za, zb, v, A, bias, None)
+    _ok(L.sdm_recurrence_step(ctypes.byref(sh), za, zb, v, A, bias,
+                              c.ptr(state, "state", torch.float32, 0), state.shape[0],
+                              c.ptr(slots, "slots", torch.int32, sh.rows),
+                              c.ptr(y, "y", dt, sh.rows * D), c.stream), "sdm_recurrence_step")
+    return y
+
+
+def sdm_add_rmsnorm(sh: Norm, x, residual=None, gamma=None, eps: float = 1e-6, s=None, out=None,
+                    out_dtype=SDM_BF16, group: int = 0, scale=None, stream=None):
+    """Residual addition and RMS-Norm of x [rows, D]; returns dict(s, out,
+    scale).  s = x + residual is made (or written where given) with a residual;
+    scale [rows] (group = 0) or [rows, D / group] float32 for SDM_E4M3."""
+    L, c = lib(), _Call(x, stream)
+    dt, odt = _torch_dtype(sh.dtype, "sdm_add_rmsnorm"), _torch_dtype(out_dtype, "sdm_add_rmsnorm")
+    n, f32 = sh.rows * sh.D, torch.float32
+    if s is None and residual is not None:
+        s = c.empty((sh.rows, sh.D), dt)
+    if out is None:
+        out = c.empty((sh.rows, sh.D), odt)
+    n_scale = 0
+    if out_dtype == SDM_E4M3:
+        if group < 0 or (group and sh.D % group):
+            raise SdmError(1, "sdm_add_rmsnorm")
+        n_scale = sh.rows * (sh.D // group if group else 1)
+        if scale is None:
+            scale = c.empty((sh.rows, sh.D // group) if group else (sh.rows,), f32)
+    _ok(L.sdm_add_rmsnorm(ctypes.byref(sh), c.ptr(x, "x", dt, n),
+                          c.ptr(residual, "residual", dt, n), c.ptr(gamma, "gamma", f32, sh.D),
+                          eps, c.ptr(s, "s", dt, n), c.ptr(out, "out", odt, n), out_dtype, group,
+                          c.ptr(scale, "scale", f32, n_scale), c.stream), "sdm_add_rmsnorm")
+    return dict(s=s, out=out, scale=scale)
+
+
+def sdm_add_rmsnorm_workspace_size(sh: Norm) -> int:
+    """Bytes of device workspace sdm_add_rmsnorm_backward needs."""
+    return int(lib().sdm_add_rmsnorm_workspace_size(ctypes.byref(sh)))
+
+
+def sdm_add_rmsnorm_backward(sh: Norm, s, dout, gamma=None, ds=None, eps: float = 1e-6, dx=None,
+                             dgamma=None, workspace=None, stream=None):
+    """Gradients of sdm_add_rmsnorm from dout [rows, D] and ds [rows, D] (the
+    gradient that reaches s from elsewhere, or None).  Returns dict(dx,
+    dgamma); dx is the gradient of x and of residual, dgamma is made only
+    where gamma is given."""
+    L, c = lib(), _Call(s, stream)
+    dt, n, f32 = _torch_dtype(sh.dtype, "sdm_add_rmsnorm_backward"), sh.rows * sh.D, torch.float32
+    if dx is None:
+        dx = c.empty((sh.rows, sh.D), dt)
+    if dgamma is None and gamma is not None:
+        dgamma = c.empty((sh.D,), f32)
+    ws, wsp, nws = None, None, 0
+    if dgamma is not None:
+        ws, wsp, nws = _scratch(c, workspace, sdm_add_rmsnorm_workspace_size(sh))
+    _ok(L.sdm_add_rmsnorm_backward(ctypes.byref(sh), c.ptr(s, "s", dt, n),
+                                   c.ptr(_required(dout, "dout"), "dout", dt, n),
+                                   c.ptr(gamma, "gamma", f32, sh.D), c.ptr(ds, "ds", dt, n), eps,
+                                   c.ptr(dx, "dx", dt, n), c.ptr(dgamma, "dgamma", f32, sh.D),
+                                   wsp, nws, c.stream), "sdm_add_rmsnorm_backward")
+    return dict(dx=dx, dgamma=dgamma)

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libsdm_gb300.so")
 SOURCES = ["sdm_api.cu", "address.cu", "plan.cu", "scan.cu", "undo.cu", "epilogue.cu",
-           "decode.cu", "sdm_noalloc.cu", "rowtraffic.cu"]
+           "decode.cu", "sdm_noalloc.cu", "rowtraffic.cu", "recurrence.cu",
+           "residual_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -123,6 +123,46 @@ cudaError_t launch_decode(const Dims& d, const void* q_w, const void* q_r, const
                           const void* g, const float* gamma, float eps, void* out,
                           int out_dtype, cudaStream_t stream);
 
+// Gated delta recurrence (recurrence.cu).  Parameters of one call, validated.
+struct RecurrenceDims {
+  int n_seq, rows, D;
+  long long ld, ld_grad;
+  int dtype;
+};
+struct RecurrenceInputs {
+  const void* za;
+  const void* zb;
+  const void* v;
+  const float* A;
+  const float* bias;
+  const int32_t* offsets;
+};
+size_t recurrence_workspace_bytes(const RecurrenceDims& d);
+size_t recurrence_states_bytes(const RecurrenceDims& d);
+cudaError_t launch_recurrence_forward(const RecurrenceDims& d, const RecurrenceInputs& in,
+                                      const float* h0, void* y, float* hT, float* states,
+                                      void* workspace, unsigned* status, cudaStream_t stream);
+cudaError_t launch_recurrence_backward(const RecurrenceDims& d, const RecurrenceInputs& in,
+                                       const float* states, const void* dy, const float* dhT,
+                                       void* dza, void* dzb, void* dv, float* dA, float* dbias,
+                                       float* dh0, void* workspace, unsigned* status,
+                                       cudaStream_t stream);
+cudaError_t launch_recurrence_step(const RecurrenceDims& d, const RecurrenceInputs& in,
+                                   float* state, int n_slots, const int32_t* slots, void* y,
+                                   unsigned* status, cudaStream_t stream);
+
+// Residual addition and RMS-Norm (residual_norm.cu).
+struct NormDims {
+  int rows, D, dtype;
+};
+size_t add_rmsnorm_workspace_bytes(const NormDims& d);
+cudaError_t launch_add_rmsnorm(const NormDims& d, const void* x, const void* residual,
+                               const float* gamma, float eps, void* s, void* out, int out_dtype,
+                               int group, float* scale, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm_backward(const NormDims& d, const void* s, const void* dout,
+                                        const float* gamma, const void* ds, float eps, void* dx,
+                                        float* dgamma, void* workspace, cudaStream_t stream);
+
 // Limits of the current device, queried once per device (sdm_api.cu): SM
 // count, shared memory per SM, and the opt-in maximum per CTA.
 struct DeviceLimits {

@@ -80,9 +80,40 @@ sdm_status check_shape(const sdm_shape* sh, Dims* d) {
   return SDM_OK;
 }
 
+sdm_status check_recurrence(const sdm_recurrence* sh, bool equal_parts, RecurrenceDims* d) {
+  if (!sh) return SDM_ERR_INVALID_ARG;
+  if (sh->n_seq < 0 || sh->rows < 0 || sh->D < 1 || sh->ld < 0 || sh->ld_grad < 0)
+    return SDM_ERR_INVALID_ARG;
+  if (sh->dtype != SDM_F32 && sh->dtype != SDM_BF16) return SDM_ERR_INVALID_ARG;
+  if ((sh->ld && sh->ld < sh->D) || (sh->ld_grad && sh->ld_grad < sh->D))
+    return SDM_ERR_INVALID_ARG;
+  if (equal_parts && sh->n_seq > 0 && sh->rows % sh->n_seq != 0) return SDM_ERR_INVALID_ARG;
+  // Supported envelope (16-byte rows, whatever the dtype).
+  if (sh->n_seq > 65535 || sh->D > 65536) return SDM_ERR_UNSUPPORTED;
+  if (sh->D % 8 != 0 || sh->ld % 8 != 0 || sh->ld_grad % 8 != 0) return SDM_ERR_UNSUPPORTED;
+  *d = RecurrenceDims{sh->n_seq, sh->rows, sh->D, sh->ld ? sh->ld : sh->D,
+                      sh->ld_grad ? sh->ld_grad : sh->D, (int)sh->dtype};
+  return SDM_OK;
+}
+
+sdm_status check_norm(const sdm_norm* sh, NormDims* d) {
+  if (!sh) return SDM_ERR_INVALID_ARG;
+  if (sh->rows < 0 || sh->D < 1) return SDM_ERR_INVALID_ARG;
+  if (sh->dtype != SDM_F32 && sh->dtype != SDM_BF16) return SDM_ERR_INVALID_ARG;
+  if (sh->D % 8 != 0 || sh->D > 16384) return SDM_ERR_UNSUPPORTED;
+  *d = NormDims{sh->rows, sh->D, (int)sh->dtype};
+  return SDM_OK;
+}
+
 bool empty_work(const Dims& d) { return (long long)d.B * d.H * d.T == 0; }
 
 sdm_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA; }
+
+// Pointers that may be NULL but must be aligned if they are not.
+#define SDM_CHECK_OPTIONAL(p) \
+  do {                        \
+    if ((p) && !aligned16(p)) return SDM_ERR_INVALID_ARG; \
+  } while (0)
 
 #define SDM_CHECK_PTR(p) \
   do {                   \
@@ -491,6 +522,164 @@ sdm_status sdm_decode(const sdm_shape* shape, const void* q_w, const void* q_r, 
                                  epi ? epi->eps : 0.f, epi ? epi->out : nullptr,
                                  epi ? (int)epi->out_dtype : 0,
                                  static_cast<cudaStream_t>(stream)));
+}
+
+size_t sdm_recurrence_workspace_size(const sdm_recurrence* shape) {
+  RecurrenceDims d;
+  if (check_recurrence(shape, false, &d) != SDM_OK) return 0;
+  return recurrence_workspace_bytes(d);
+}
+
+size_t sdm_recurrence_states_size(const sdm_recurrence* shape) {
+  RecurrenceDims d;
+  if (check_recurrence(shape, false, &d) != SDM_OK) return 0;
+  return recurrence_states_bytes(d);
+}
+
+sdm_status sdm_recurrence_forward(const sdm_recurrence* shape, const void* za, const void* zb,
+                                  const void* v, const float* A, const float* bias,
+                                  const int32_t* offsets, const float* h0, void* y, float* hT,
+                                  float* states, void* workspace, size_t ws_bytes,
+                                  void* stream) {
+  RecurrenceDims d;
+  sdm_status st = check_recurrence(shape, !offsets, &d);
+  if (st != SDM_OK) return st;
+  if (d.n_seq == 0) return SDM_OK;   // no work: pointers are not looked at
+  if (d.rows > 0) {
+    SDM_CHECK_PTR(za);
+    SDM_CHECK_PTR(zb);
+    SDM_CHECK_PTR(v);
+    SDM_CHECK_PTR(y);
+  }
+  SDM_CHECK_OPTIONAL(A);
+  SDM_CHECK_OPTIONAL(bias);
+  SDM_CHECK_OPTIONAL(offsets);
+  SDM_CHECK_OPTIONAL(h0);
+  SDM_CHECK_OPTIONAL(hT);
+  SDM_CHECK_OPTIONAL(states);
+  SDM_CHECK_PTR(workspace);
+  if (ws_bytes < recurrence_workspace_bytes(d)) return SDM_ERR_INVALID_ARG;
+  unsigned* sp = nullptr;
+  if ((st = status_ptr(&sp)) != SDM_OK) return st;
+  return from_cuda(launch_recurrence_forward(d, RecurrenceInputs{za, zb, v, A, bias, offsets}, h0,
+                                             y, hT, states, workspace, sp,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+sdm_status sdm_recurrence_backward(const sdm_recurrence* shape, const void* za, const void* zb,
+                                   const void* v, const float* A, const float* bias,
+                                   const int32_t* offsets, const float* states, const void* dy,
+                                   const float* dhT, void* dza, void* dzb, void* dv, float* dA,
+                                   float* dbias, float* dh0, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  RecurrenceDims d;
+  sdm_status st = check_recurrence(shape, !offsets, &d);
+  if (st != SDM_OK) return st;
+  if (d.n_seq == 0 && !dA && !dbias) return SDM_OK;
+  if (d.n_seq > 0) {
+    if (d.rows > 0) {
+      SDM_CHECK_PTR(za);
+      SDM_CHECK_PTR(zb);
+      SDM_CHECK_PTR(v);
+      SDM_CHECK_PTR(dy);
+      SDM_CHECK_PTR(dza);
+      SDM_CHECK_PTR(dzb);
+      SDM_CHECK_PTR(dv);
+    }
+    SDM_CHECK_PTR(states);
+    SDM_CHECK_OPTIONAL(A);
+    SDM_CHECK_OPTIONAL(bias);
+    SDM_CHECK_OPTIONAL(offsets);
+    SDM_CHECK_OPTIONAL(dhT);
+    SDM_CHECK_OPTIONAL(dh0);
+    SDM_CHECK_PTR(workspace);
+    if (ws_bytes < recurrence_workspace_bytes(d)) return SDM_ERR_INVALID_ARG;
+  }
+  SDM_CHECK_OPTIONAL(dA);
+  SDM_CHECK_OPTIONAL(dbias);
+  unsigned* sp = nullptr;
+  if ((st = status_ptr(&sp)) != SDM_OK) return st;
+  return from_cuda(launch_recurrence_backward(d, RecurrenceInputs{za, zb, v, A, bias, offsets},
+                                              states, dy, dhT, dza, dzb, dv, dA, dbias, dh0,
+                                              workspace, sp, static_cast<cudaStream_t>(stream)));
+}
+
+sdm_status sdm_recurrence_step(const sdm_recurrence* shape, const void* za, const void* zb,
+                               const void* v, const float* A, const float* bias, float* state,
+                               int n_slots, const int32_t* slots, void* y, void* stream) {
+  RecurrenceDims d;
+  sdm_status st = check_recurrence(shape, false, &d);
+  if (st != SDM_OK) return st;
+  if (n_slots < 0 || (!slots && d.rows > n_slots)) return SDM_ERR_INVALID_ARG;
+  if (d.rows == 0) return SDM_OK;   // no work: pointers are not looked at
+  SDM_CHECK_PTR(za);
+  SDM_CHECK_PTR(zb);
+  SDM_CHECK_PTR(v);
+  SDM_CHECK_PTR(y);
+  if (n_slots > 0) SDM_CHECK_PTR(state);
+  SDM_CHECK_OPTIONAL(A);
+  SDM_CHECK_OPTIONAL(bias);
+  SDM_CHECK_OPTIONAL(slots);
+  unsigned* sp = nullptr;
+  if ((st = status_ptr(&sp)) != SDM_OK) return st;
+  return from_cuda(launch_recurrence_step(d, RecurrenceInputs{za, zb, v, A, bias, nullptr}, state,
+                                          n_slots, slots, y, sp,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+sdm_status sdm_add_rmsnorm(const sdm_norm* shape, const void* x, const void* residual,
+                           const float* gamma, float eps, void* s, void* out,
+                           sdm_dtype out_dtype, int group, float* scale, void* stream) {
+  NormDims d;
+  sdm_status st = check_norm(shape, &d);
+  if (st != SDM_OK) return st;
+  if (!(eps > 0.f) || !(eps < INFINITY)) return SDM_ERR_INVALID_ARG;
+  if (out_dtype != SDM_F32 && out_dtype != SDM_BF16 && out_dtype != SDM_E4M3)
+    return SDM_ERR_INVALID_ARG;
+  if (group != 0) {
+    if (out_dtype != SDM_E4M3 || group < 0 || d.D % group != 0) return SDM_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return SDM_ERR_UNSUPPORTED;
+  }
+  if (d.rows == 0) return SDM_OK;   // no work: pointers are not looked at
+  SDM_CHECK_PTR(x);
+  SDM_CHECK_PTR(out);
+  SDM_CHECK_OPTIONAL(residual);
+  SDM_CHECK_OPTIONAL(gamma);
+  SDM_CHECK_OPTIONAL(s);
+  if (out_dtype == SDM_E4M3) SDM_CHECK_PTR(scale);
+  return from_cuda(launch_add_rmsnorm(d, x, residual, gamma, eps, s, out, out_dtype, group, scale,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t sdm_add_rmsnorm_workspace_size(const sdm_norm* shape) {
+  NormDims d;
+  if (check_norm(shape, &d) != SDM_OK) return 0;
+  return add_rmsnorm_workspace_bytes(d);
+}
+
+sdm_status sdm_add_rmsnorm_backward(const sdm_norm* shape, const void* s, const void* dout,
+                                    const float* gamma, const void* ds, float eps, void* dx,
+                                    float* dgamma, void* workspace, size_t ws_bytes,
+                                    void* stream) {
+  NormDims d;
+  sdm_status st = check_norm(shape, &d);
+  if (st != SDM_OK) return st;
+  if (!(eps > 0.f) || !(eps < INFINITY)) return SDM_ERR_INVALID_ARG;
+  if (d.rows == 0 && !dgamma) return SDM_OK;
+  if (d.rows > 0) {
+    SDM_CHECK_PTR(s);
+    SDM_CHECK_PTR(dout);
+    SDM_CHECK_PTR(dx);
+    SDM_CHECK_OPTIONAL(gamma);
+    SDM_CHECK_OPTIONAL(ds);
+    if (dgamma) {
+      SDM_CHECK_PTR(workspace);
+      if (ws_bytes < add_rmsnorm_workspace_bytes(d)) return SDM_ERR_INVALID_ARG;
+    }
+  }
+  SDM_CHECK_OPTIONAL(dgamma);
+  return from_cuda(launch_add_rmsnorm_backward(d, s, dout, gamma, ds, eps, dx, dgamma, workspace,
+                                               static_cast<cudaStream_t>(stream)));
 }
 
 sdm_status sdm_get_device_status(void* stream) {

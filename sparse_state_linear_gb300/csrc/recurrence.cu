@@ -10,13 +10,13 @@
 //   dv = beta g,  dzb = g (v - alpha h[t-1]) beta (1 - beta),
 //   dl = g a h[t-1] (gradient of ln alpha),
 //   dza = -A sigmoid(za + b) dl,  dA = sum -softplus(za + b) dl,  db = sum dza.
+#include <cuda.h>   // CUtensorMap and its enums; the encoder comes through the runtime
+
 #include "common.cuh"
 #include "internal.h"
 
 namespace sdm {
 namespace {
-
-constexpr int kChunk = 128;   // rows between saved states
 
 // ------------------------------------------------------------------- gates
 __device__ __forceinline__ float ex2(float x) {
@@ -103,11 +103,76 @@ __device__ __forceinline__ void store4(void* base, size_t i, int dt, float4 v) {
                                                  *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// ------------------------------------------------------------- pairs of floats
+// Two float32 operations in one instruction (the packed forms of sm_100 on).
+__device__ __forceinline__ uint64_t bits2(float2 a) { return *reinterpret_cast<uint64_t*>(&a); }
+__device__ __forceinline__ float2 float2_of(uint64_t a) { return *reinterpret_cast<float2*>(&a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// The larger of two numbers, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// log2(1 + e) for e in [0, 1], two at a time: the polynomial of log1p_unit
+// with its coefficients times log2(e).
+__device__ __forceinline__ float2 log2p1_unit(float2 e) {
+  float2 p = both(-0.00317605701f * kLog2e);
+  p = fma2(p, e, both(0.0195425265f * kLog2e));
+  p = fma2(p, e, both(-0.0563736111f * kLog2e));
+  p = fma2(p, e, both(0.105436236f * kLog2e));
+  p = fma2(p, e, both(-0.152696669f * kLog2e));
+  p = fma2(p, e, both(0.196632743f * kLog2e));
+  p = fma2(p, e, both(-0.249516159f * kLog2e));
+  p = fma2(p, e, both(0.333297104f * kLog2e));
+  p = fma2(p, e, both(-0.499998927f * kLog2e));
+  p = fma2(p, e, both(kLog2e));
+  return mul2(p, e);
+}
+
+// a = (1 - beta) alpha and b = beta v of two channels; nA = -A.
+__device__ __forceinline__ void gate_pair(float2 za, float2 zb, float2 v, float2 nA, float2 bias,
+                                          float2& a, float2& b) {
+  const float2 x = mul2(add2(za, bias), both(kLog2e));
+  const float2 e = make_float2(ex2(-fabsf(x.x)), ex2(-fabsf(x.y)));
+  const float2 sp = add2(make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)), log2p1_unit(e));
+  const float2 l = mul2(nA, sp);
+  // sigmoid(z) = 1 / (1 + 2^-z'), 1 - sigmoid = 2^-z' / (1 + 2^-z'); z' held
+  // above -126 so that 2^-z' stays finite.
+  float2 z = mul2(zb, both(kLog2e));
+  z = make_float2(max_nan(z.x, -126.f), max_nan(z.y, -126.f));
+  const float2 eb = make_float2(ex2(-z.x), ex2(-z.y));
+  const float2 d = add2(eb, both(1.f));
+  const float2 beta = make_float2(rcp(d.x), rcp(d.y));
+  a = mul2(mul2(eb, beta), make_float2(ex2(l.x), ex2(l.y)));
+  b = mul2(beta, v);
+}
+
 // ------------------------------------------------------------------ packing
-// Chunk c of sequence s (first row o) has number o / kChunk + s + c: distinct
-// for all chunks of all sequences, below rows / kChunk + n_seq, and growing
-// with s and c.
-__host__ __device__ inline int chunk_numbers(int rows, int n_seq) { return rows / kChunk + n_seq; }
+// A tile is L rows of one sequence by 64 channels.  Chunk c (of L rows) of
+// sequence s whose first row is o has number o / L + s + c: distinct for all
+// chunks of all sequences, below rows / L + n_seq, and growing with s and c.
+constexpr int kCols = 64;
+
+__host__ __device__ inline long long chunk_numbers(int rows, int n_seq, int L) {
+  return (long long)rows / L + n_seq;
+}
 
 struct Packed {
   const int32_t* offsets;
@@ -129,6 +194,8 @@ __device__ bool offsets_ok(const Packed& P) {
   return !__syncthreads_or(bad);
 }
 
+constexpr int kStateRows = 64;   // rows between saved states
+
 struct Args {
   RecurrenceDims d;
   RecurrenceInputs in;
@@ -147,32 +214,437 @@ struct Args {
   unsigned* status;
 };
 
-// One thread per channel and sequence, one row after the other.
-__global__ void __launch_bounds__(128) forward_kernel(const Args P) {
+// --------------------------------------------------------------------- scan
+// What a block has to know of a tile, found out by the warp that fetches it.
+struct Tile {
+  int rows;      // valid rows, 1..L; 0: no tile is left
+  int row0;      // first row
+  int seq, chunk;
+  int number;    // of the chunk, indexes flags and data
+  int back;      // number - back is the chunk before (after, in the backward pass)
+  int col0;      // first channel
+  int last;      // the sequence's last chunk
+};
+
+// Workspace of one call: a header (ticket counter, abort word), one flag per
+// tile, and a float pair per chunk and channel.
+struct Chain {
+  unsigned* ticket;
+  unsigned* abort;
+  unsigned* flags;    // [numbers][col tiles]
+  float* P;           // [numbers][D]
+  float* S;           // [numbers][D]
+};
+
+constexpr int kGroup = 16;                                    // chunks per group, see below
+constexpr unsigned long long kWaitNs = 4000000000ull;         // limit of every wait
+
+__device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_release(unsigned* p, unsigned v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+// x: first channel (a multiple of 64, so 16-byte aligned), y: first row; what
+// lies outside the tensor arrives as zeros.
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
+                                         uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];\n" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The sequence a chunk number belongs to (a whole warp calls it): the last s
+// with base(s) = begin(s) / L + s <= number, or -1.
+template <int L>
+__device__ int sequence_of(const Packed& P, int number) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = P.n_seq;
+  if (P.begin(0) / L > number) return -1;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, s = lo + lane * step;
+    const bool below = s < hi && P.begin(s) / L + s <= number;
+    const int n = __popc(__ballot_sync(0xffffffffu, below));
+    const int next = lo + n * step;
+    lo += (n - 1) * step;
+    hi = next < hi ? next : hi;
+  }
+  return lo;
+}
+
+// Four channels of a row in shared memory or registers.
+__device__ __forceinline__ void load_row(const float* p, float2& lo, float2& hi) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  lo = make_float2(v.x, v.y);
+  hi = make_float2(v.z, v.w);
+}
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float2& lo, float2& hi) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  lo = make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
+  hi = make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store_row(float* p, float2 lo, float2 hi) {
+  *reinterpret_cast<float4*>(p) = make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, float2 lo, float2 hi) {
+  const __nv_bfloat162 a = __float22bfloat162_rn(lo), b = __float22bfloat162_rn(hi);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ float2 shfl_xor2(float2 a, int m) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, a.x, m), __shfl_xor_sync(0xffffffffu, a.y, m));
+}
+
+template <typename T, int R, int NT, int STAGES>
+struct ForwardShape {
+  static constexpr int kWarps = NT / 32, L = NT / 16 * R, kTileBytes = L * kCols * (int)sizeof(T);
+  static constexpr int kStageBytes = 3 * kTileBytes;
+  static constexpr int kSmem = STAGES * kStageBytes + 128;    // + alignment
+};
+
+struct ForwardArgs {
+  CUtensorMap za, zb, v;
+  Packed packed;
+  const float* A;
+  const float* bias;
+  const float* h0;
+  void* y;
+  float* hT;
+  float* states;
+  Chain chain;
+  int D, col_tiles;
+  unsigned tiles;
+  unsigned* status;
+};
+
+// Fetch the next tile that has rows (a whole warp calls it): takes tickets
+// until one does, starts the copy of its inputs into `buf` and describes it in
+// *out.  `ticket` (lane 0) was taken earlier and is replaced by a new one, so
+// that its latency lies behind other work.
+template <int L, class Start, class Empty>
+__device__ __forceinline__ void fetch(const Packed& packed, const Chain& chain, unsigned tiles,
+                                      int col_tiles, bool reverse, unsigned& ticket, Tile* out,
+                                      Start start, Empty empty) {
+  const int lane = threadIdx.x & 31;
+  while (true) {
+    const unsigned k = __shfl_sync(0xffffffffu, ticket, 0);
+    if (k >= tiles) {
+      if (lane == 0) out->rows = 0;
+      break;
+    }
+    if (lane == 0) ticket = atomicAdd(chain.ticket, 1u);
+    Tile t;
+    const unsigned q = reverse ? tiles - 1 - k : k;
+    const int number = (int)(q / (unsigned)col_tiles);
+    t.col0 = (int)(q % (unsigned)col_tiles) * kCols;
+    int o, len;
+    if (packed.offsets) {
+      t.seq = sequence_of<L>(packed, number);
+      if (t.seq < 0) continue;
+      o = packed.begin(t.seq);
+      len = packed.begin(t.seq + 1) - o;
+      t.chunk = number - (o / L + t.seq);
+      t.back = 1;
+    } else {
+      // Equal lengths: chunk c of every sequence before chunk c + 1 of any, so
+      // that a chunk's predecessor is as far back as can be.
+      t.chunk = number / packed.n_seq;
+      t.seq = number % packed.n_seq;
+      o = packed.begin(t.seq);
+      len = packed.rows / packed.n_seq;
+      t.back = packed.n_seq;
+    }
+    t.number = number;
+    t.row0 = o + t.chunk * L;
+    t.rows = len - t.chunk * L;
+    t.last = t.rows <= L;
+    if (t.rows > L) t.rows = L;
+    if (t.rows <= 0) {
+      if (t.chunk == 0) empty(t);
+      continue;
+    }
+    if (lane == 0) {
+      *out = t;
+      start(t);
+    }
+    break;
+  }
+  __syncwarp();
+}
+
+// The state in front of a tile from what the chunks before it published (a
+// whole warp; each lane two channels).  Chunks are in groups of kGroup: the
+// last of a group publishes the state behind it, the others the pair (P, S)
+// with which a state h in front of them becomes P h + S behind them (the first
+// chunk of a sequence has its initial state in S and P = 0).  So a tile needs
+// the state behind the group before and the pairs of its own group, always
+// folded in the same order: results do not depend on timing, and the serial
+// chain through the grid has one link per kGroup chunks, not one per chunk.
+// Returns false if the wait ran out or another block gave up.
+__device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int chunk, int D,
+                                            int col_tiles, float2& h) {
+  const int lane = threadIdx.x & 31, i = chunk % kGroup, n = i + (chunk >= kGroup ? 1 : 0);
+  bool ready = lane >= n, ok = true;
+  const unsigned* flag = ch.flags +
+      ((size_t)t.number - (size_t)(lane < n ? lane + 1 : 0) * t.back) * col_tiles + t.col0 / kCols;
+  uint64_t t0 = 0;
+  for (int spin = 0;; ++spin) {
+    if (!ready) ready = load_acquire(flag) != 0;
+    if (__all_sync(0xffffffffu, ready)) break;
+    if ((spin & 63) == 63) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      ok = now - t0 < kWaitNs && load_acquire(ch.abort) == 0;
+      if (!__all_sync(0xffffffffu, ok)) return false;
+    }
+  }
+  const int c = t.col0 + lane * 2;
+  h = make_float2(0.f, 0.f);
+  if (c < D) {
+    const float* P = ch.P + (size_t)t.number * D + c;
+    const float* S = ch.S + (size_t)t.number * D + c;
+    const size_t step = (size_t)t.back * D;
+    if (chunk >= kGroup) h = __ldcg(reinterpret_cast<const float2*>(S - (i + 1) * step));
+    constexpr int kBatch = kGroup / 2;
+    for (int k0 = 0; k0 < i; k0 += kBatch) {
+      float2 p[kBatch], s[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k < i) {
+          p[k] = __ldcg(reinterpret_cast<const float2*>(P - (i - k0 - k) * step));
+          s[k] = __ldcg(reinterpret_cast<const float2*>(S - (i - k0 - k) * step));
+        }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k < i) h = fma2(p[k], h, s[k]);
+    }
+  }
+  return true;
+}
+
+// A block of NT threads for the arithmetic (a half-warp takes R rows by 64
+// channels, four channels a thread) and one warp that fetches tiles and folds
+// what the chunks before published, so that neither holds the others up.  Per
+// tile there are two barriers: (1) among the arithmetic warps, every warp's
+// pair is in shared memory; (2) of all, the state in front of the tile is.
+template <typename T, int R, int NT, int STAGES, int MINB>
+__global__ void __launch_bounds__(NT + 32, MINB)
+    forward_kernel(const __grid_constant__ ForwardArgs P) {
+  using Sh = ForwardShape<T, R, NT, STAGES>;
+  constexpr int L = Sh::L, W = Sh::kWarps;
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + ((128 - (smem_u32(raw) & 127)) & 127);
+  __shared__ uint64_t full[STAGES];
+  __shared__ Tile tiles[STAGES];
+  __shared__ float4 total[W][2][16];       // (P, S) of each warp's rows
+  __shared__ float2 carry[2][kCols / 2];   // the state in front of the tile
+  __shared__ int gave_up;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!offsets_ok(P.packed)) {
-    if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+    if (tid == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int c = blockIdx.x * blockDim.x + threadIdx.x, s = blockIdx.y, D = P.d.D, dt = P.d.dtype;
-  if (c >= D) return;
-  const float A = P.in.A ? P.in.A[c] : 1.f, bias = P.in.bias ? P.in.bias[c] : 0.f;
-  const int t0 = P.packed.begin(s), t1 = P.packed.begin(s + 1);
-  float h = P.h0 ? P.h0[(size_t)s * D + c] : 0.f;
-  for (int t = t0; t < t1; ++t) {
-    if (P.states && (t - t0) % kChunk == 0)
-      P.states[(size_t)(t0 / kChunk + s + (t - t0) / kChunk) * D + c] = h;
-    const size_t i = (size_t)t * P.d.ld + c;
-    const Gate g = make_gate(load_scalar(P.in.za, i, dt), load_scalar(P.in.zb, i, dt), A, bias);
-    h = fmaf(g.keep * g.alpha, h, g.beta * load_scalar(P.in.v, i, dt));
-    store_scalar(P.y, (size_t)t * D + c, dt, h);
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
+    gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (P.hT) P.hT[(size_t)s * D + c] = h;
+  __syncthreads();
+  int it = 0;
+
+  if (warp == W) {
+    unsigned ticket = 0;
+    auto get = [&](int st) {
+      fetch<L>(
+          P.packed, P.chain, P.tiles, P.col_tiles, false, ticket, &tiles[st],
+          [&](const Tile& t) {
+            unsigned char* buf = smem + st * Sh::kStageBytes;
+            mbar_expect(&full[st], Sh::kStageBytes);
+            tma_load(buf, &P.za, t.col0, t.row0, &full[st]);
+            tma_load(buf + Sh::kTileBytes, &P.zb, t.col0, t.row0, &full[st]);
+            tma_load(buf + 2 * Sh::kTileBytes, &P.v, t.col0, t.row0, &full[st]);
+          },
+          [&](const Tile& t) {             // a sequence without rows
+            const int c = t.col0 + lane * 2;
+            if (P.hT && c < P.D) {
+              const size_t i = (size_t)t.seq * P.D + c;
+              *reinterpret_cast<float2*>(P.hT + i) =
+                  P.h0 ? *reinterpret_cast<const float2*>(P.h0 + i) : make_float2(0.f, 0.f);
+            }
+          });
+    };
+    if (lane == 0) ticket = atomicAdd(P.chain.ticket, 1u);
+    for (int s = 0; s < STAGES; ++s) get(s);
+    __syncthreads();
+    for (;; ++it) {
+      const Tile t = tiles[it % STAGES];
+      if (t.rows == 0) break;
+      float2 h = make_float2(0.f, 0.f);
+      if (t.chunk == 0) {
+        const int c = t.col0 + lane * 2;
+        if (P.h0 && c < P.D) h = *reinterpret_cast<const float2*>(P.h0 + (size_t)t.seq * P.D + c);
+      } else if (!fold_before(P.chain, t, t.chunk, P.D, P.col_tiles, h)) {
+        gave_up = 1;
+      }
+      carry[it & 1][lane] = h;
+      __syncthreads();                     // (2)
+      if (gave_up) break;
+      get(it % STAGES);                    // its inputs are in registers
+    }
+  } else {
+    const int c4 = (lane & 15) * 4, first = (tid >> 4) * R;   // first row in the tile
+    __syncthreads();
+    for (;; ++it) {
+      const int st = it % STAGES;
+      const Tile t = tiles[st];
+      if (t.rows == 0) break;
+      const int c = t.col0 + c4;
+      const bool in = c < P.D;
+      float2 nA[2] = {both(-1.f), both(-1.f)}, bias[2] = {both(0.f), both(0.f)};
+      if (in && P.A) {
+        load_row(P.A + c, nA[0], nA[1]);
+        nA[0] = mul2(nA[0], both(-1.f));
+        nA[1] = mul2(nA[1], both(-1.f));
+      }
+      if (in && P.bias) load_row(P.bias + c, bias[0], bias[1]);
+      if (!mbar_wait_bounded(&full[st], (it / STAGES) & 1, kWaitNs)) gave_up = 1;
+
+      // Gates of this thread's R rows, and the pair (p, s) of all of them.
+      const T* buf = reinterpret_cast<const T*>(smem + st * Sh::kStageBytes) + first * kCols + c4;
+      float2 a[R][2], b[R][2];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float2 za[2], zb[2], v[2];
+        load_row(buf + r * kCols, za[0], za[1]);
+        load_row(buf + (L + r) * kCols, zb[0], zb[1]);
+        load_row(buf + (2 * L + r) * kCols, v[0], v[1]);
+        gate_pair(za[0], zb[0], v[0], nA[0], bias[0], a[r][0], b[r][0]);
+        gate_pair(za[1], zb[1], v[1], nA[1], bias[1], a[r][1], b[r][1]);
+      }
+      if (t.rows < L) {                    // rows behind the sequence change nothing
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (first + r >= t.rows) {
+            a[r][0] = a[r][1] = both(1.f);
+            b[r][0] = b[r][1] = both(0.f);
+          }
+      }
+      float2 p[2] = {a[0][0], a[0][1]}, s[2] = {b[0][0], b[0][1]};
+#pragma unroll
+      for (int r = 1; r < R; ++r) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          s[k] = fma2(a[r][k], s[k], b[r][k]);
+          p[k] = mul2(a[r][k], p[k]);
+        }
+      }
+      // The lower half-warp's rows come before the upper's.
+      float2 pl[2], sl[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        pl[k] = shfl_xor2(p[k], 16);
+        sl[k] = shfl_xor2(s[k], 16);
+      }
+      if (lane >= 16) {
+        store_row(reinterpret_cast<float*>(&total[warp][0][lane & 15]), mul2(p[0], pl[0]),
+                  mul2(p[1], pl[1]));
+        store_row(reinterpret_cast<float*>(&total[warp][1][lane & 15]), fma2(p[0], sl[0], s[0]),
+                  fma2(p[1], sl[1], s[1]));
+      }
+      named_bar_sync(1, NT);               // (1)
+      // (P, S) of the rows before this thread's.
+      float2 bp[2] = {both(1.f), both(1.f)}, bs[2] = {both(0.f), both(0.f)};
+      for (int w = 0; w < warp; ++w) {
+        float2 wp[2], ws[2];
+        load_row(reinterpret_cast<const float*>(&total[w][0][lane & 15]), wp[0], wp[1]);
+        load_row(reinterpret_cast<const float*>(&total[w][1][lane & 15]), ws[0], ws[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          bs[k] = fma2(wp[k], bs[k], ws[k]);
+          bp[k] = mul2(wp[k], bp[k]);
+        }
+      }
+      if (lane >= 16) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          bs[k] = fma2(pl[k], bs[k], sl[k]);
+          bp[k] = mul2(pl[k], bp[k]);
+        }
+      }
+      // The last rows' threads know the tile's pair.  They publish it now; or,
+      // where the tile ends a group or begins its sequence, the state behind
+      // it once that is known (with P = 0: whatever is in front of it).  The
+      // first tile waits although it could publish at once because its block
+      // may still be reading h0, which the last tile may overwrite (hT = h0).
+      const bool publisher = warp == W - 1 && !t.last;
+      const bool late = t.chunk % kGroup == kGroup - 1 || t.chunk == 0;
+      const size_t at = (size_t)t.number * P.D + c;
+      unsigned* flag = P.chain.flags + (size_t)t.number * P.col_tiles + t.col0 / kCols;
+      if (publisher && !late) {
+        if (lane >= 16 && in) {
+          store_row(P.chain.P + at, mul2(p[0], bp[0]), mul2(p[1], bp[1]));
+          store_row(P.chain.S + at, fma2(p[0], bs[0], s[0]), fma2(p[1], bs[1], s[1]));
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) store_release(flag, 1u);
+      }
+      __syncthreads();                     // (2)
+      if (gave_up) break;
+      float2 h[2];
+      load_row(reinterpret_cast<const float*>(&carry[it & 1][(lane & 15) * 2]), h[0], h[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) h[k] = fma2(bp[k], h[k], bs[k]);
+      if (publisher && late) {
+        if (lane >= 16 && in) {
+          store_row(P.chain.P + at, both(0.f), both(0.f));
+          store_row(P.chain.S + at, fma2(p[0], h[0], s[0]), fma2(p[1], h[1], s[1]));
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) store_release(flag, 1u);
+      }
+      if (in) {
+        if (P.states && first % kStateRows == 0 && first < t.rows) {
+          const int begin = t.row0 - t.chunk * L;
+          const size_t n = (size_t)(begin / kStateRows + t.seq + (t.chunk * L + first) / kStateRows);
+          store_row(P.states + n * P.D + c, h[0], h[1]);
+        }
+        T* y = reinterpret_cast<T*>(P.y) + (size_t)(t.row0 + first) * P.D + c;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          h[0] = fma2(a[r][0], h[0], b[r][0]);
+          h[1] = fma2(a[r][1], h[1], b[r][1]);
+          if (first + r < t.rows) store_row(y + (size_t)r * P.D, h[0], h[1]);
+        }
+        if (P.hT && t.last && first < t.rows && t.rows <= first + R)
+          store_row(P.hT + (size_t)t.seq * P.D + c, h[0], h[1]);
+      }
+    }
+  }
+  if (gave_up && tid == 0) {
+    // Tell the other blocks, and leave no copy in flight behind.
+    record_status(P.status, SDM_ERR_TIMEOUT);
+    atomicExch(P.chain.abort, 1u);
+    for (int x = it; x < it + STAGES; ++x)
+      if (tiles[x % STAGES].rows > 0) mbar_wait_bounded(&full[x % STAGES], (x / STAGES) & 1, kWaitNs);
+  }
 }
 
 // As above from the last chunk to the first: the states before the chunk's
 // rows again from the saved one, then the gradients.
 __global__ void __launch_bounds__(32) backward_kernel(const Args P) {
-  __shared__ float hs[kChunk][32];
+  __shared__ float hs[kStateRows][32];
   if (!offsets_ok(P.packed)) {
     if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     return;
@@ -182,9 +654,9 @@ __global__ void __launch_bounds__(32) backward_kernel(const Args P) {
   const float A = P.in.A ? P.in.A[c] : 1.f, bias = P.in.bias ? P.in.bias[c] : 0.f;
   const int t0 = P.packed.begin(s), t1 = P.packed.begin(s + 1);
   float r = P.dhT ? P.dhT[(size_t)s * D + c] : 0.f, dA = 0.f, db = 0.f;
-  for (int k = (t1 - t0 + kChunk - 1) / kChunk - 1; k >= 0; --k) {
-    const int b = t0 + k * kChunk, e = b + kChunk < t1 ? b + kChunk : t1;
-    float h = P.states[(size_t)(t0 / kChunk + s + k) * D + c];
+  for (int k = (t1 - t0 + kStateRows - 1) / kStateRows - 1; k >= 0; --k) {
+    const int b = t0 + k * kStateRows, e = b + kStateRows < t1 ? b + kStateRows : t1;
+    float h = P.states[(size_t)(t0 / kStateRows + s + k) * D + c];
     for (int t = b; t < e; ++t) {
       hs[t - b][threadIdx.x] = h;
       const size_t i = (size_t)t * P.d.ld + c;
@@ -281,29 +753,134 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const Args P, float*
 
 }  // namespace
 
+namespace {
+
+constexpr size_t kHeaderBytes = 256;
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+int col_tiles_of(int D) { return (D + kCols - 1) / kCols; }
+
+// Bytes of a call whose chunks have L rows: header and flags (cleared by every
+// call), then two floats per chunk and channel.
+size_t chain_cleared_bytes(const RecurrenceDims& d, int L) {
+  return round256(kHeaderBytes + (size_t)chunk_numbers(d.rows, d.n_seq, L) * col_tiles_of(d.D) * 4);
+}
+size_t chain_bytes(const RecurrenceDims& d, int L) {
+  return chain_cleared_bytes(d, L) + 2 * round256((size_t)chunk_numbers(d.rows, d.n_seq, L) * d.D * 4);
+}
+
+Chain chain_in(void* workspace, const RecurrenceDims& d, int L) {
+  char* w = static_cast<char*>(workspace);
+  char* data = w + chain_cleared_bytes(d, L);
+  Chain c;
+  c.ticket = reinterpret_cast<unsigned*>(w);
+  c.abort = reinterpret_cast<unsigned*>(w + 128);
+  c.flags = reinterpret_cast<unsigned*>(w + kHeaderBytes);
+  c.P = reinterpret_cast<float*>(data);
+  c.S = reinterpret_cast<float*>(data + round256((size_t)chunk_numbers(d.rows, d.n_seq, L) * d.D * 4));
+  return c;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// Map of a [rows, D] tensor with rows `ld` elements apart, in boxes of
+// box_rows x 64 channels.
+bool make_map(CUtensorMap* map, const void* base, int dtype, int rows, int D, long long ld,
+              int box_rows) {
+  const EncodeTiled f = encoder();
+  if (!f) return false;
+  const cuuint64_t e = dtype == SDM_BF16 ? 2 : 4;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * e};
+  const cuuint32_t box[2] = {(cuuint32_t)kCols, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  return f(map, dtype == SDM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+           2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tiles of a call: all chunk numbers where the lengths are on the device,
+// else the chunks there are.
+unsigned tiles_of(const RecurrenceDims& d, bool offsets, int L) {
+  long long n = chunk_numbers(d.rows, d.n_seq, L);
+  if (!offsets) {
+    const long long per = (d.rows / d.n_seq + L - 1) / L;
+    n = (per > 0 ? per : 1) * d.n_seq;
+  }
+  return (unsigned)(n * col_tiles_of(d.D));
+}
+
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename T, int R, int NT, int STAGES, int MINB>
+cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, const float* h0,
+                       void* y, float* hT, float* states, void* workspace, unsigned* status,
+                       cudaStream_t stream) {
+  using Sh = ForwardShape<T, R, NT, STAGES>;
+  constexpr int L = Sh::L;
+  static_assert(L % kStateRows == 0 && kStateRows % R == 0, "states fall on a thread's first row");
+  ForwardArgs P;
+  if (d.rows > 0 && (!make_map(&P.za, in.za, d.dtype, d.rows, d.D, d.ld, L) ||
+                     !make_map(&P.zb, in.zb, d.dtype, d.rows, d.D, d.ld, L) ||
+                     !make_map(&P.v, in.v, d.dtype, d.rows, d.D, d.ld, L)))
+    return cudaErrorInvalidValue;
+  P.packed = Packed{in.offsets, d.n_seq, d.rows};
+  P.A = in.A;
+  P.bias = in.bias;
+  P.h0 = h0;
+  P.y = y;
+  P.hT = hT;
+  P.states = states;
+  P.chain = chain_in(workspace, d, L);
+  P.D = d.D;
+  P.col_tiles = col_tiles_of(d.D);
+  P.tiles = tiles_of(d, in.offsets != nullptr, L);
+  P.status = status;
+  const auto kernel = forward_kernel<T, R, NT, STAGES, MINB>;
+  cudaError_t e = allow_smem(kernel, Sh::kSmem);
+  if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, chain_cleared_bytes(d, L), stream);
+  if (e != cudaSuccess) return e;
+  const unsigned most = (unsigned)(MINB * device_limits().sms);
+  kernel<<<P.tiles < most ? P.tiles : most, NT + 32, Sh::kSmem, stream>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 size_t recurrence_workspace_bytes(const RecurrenceDims& d) {
-  return (size_t)(d.n_seq + 1) * 2 * d.D * sizeof(float);
+  const size_t back = (size_t)(d.n_seq + 1) * 2 * d.D * sizeof(float);
+  const size_t fwd = chain_bytes(d, 64);
+  return back > fwd ? back : fwd;
 }
 
 size_t recurrence_states_bytes(const RecurrenceDims& d) {
-  return (size_t)chunk_numbers(d.rows, d.n_seq) * d.D * sizeof(float);
+  return (size_t)chunk_numbers(d.rows, d.n_seq, kStateRows) * d.D * sizeof(float);
 }
 
 cudaError_t launch_recurrence_forward(const RecurrenceDims& d, const RecurrenceInputs& in,
                                       const float* h0, void* y, float* hT, float* states,
                                       void* workspace, unsigned* status, cudaStream_t stream) {
-  (void)workspace;
-  Args P{};
-  P.d = d;
-  P.in = in;
-  P.packed = Packed{in.offsets, d.n_seq, d.rows};
-  P.h0 = h0;
-  P.y = y;
-  P.hT = hT;
-  P.states = states;
-  P.status = status;
-  forward_kernel<<<dim3((d.D + 127) / 128, d.n_seq), 128, 0, stream>>>(P);
-  return cudaGetLastError();
+  if (d.dtype == SDM_BF16)
+    return forward_as<__nv_bfloat16, 4, 256, 2, 3>(d, in, h0, y, hT, states, workspace, status, stream);
+  return forward_as<float, 4, 256, 2, 2>(d, in, h0, y, hT, states, workspace, status, stream);
 }
 
 cudaError_t launch_recurrence_backward(const RecurrenceDims& d, const RecurrenceInputs& in,

@@ -226,14 +226,12 @@ struct Tile {
   int last;      // the sequence's last chunk
 };
 
-// Workspace of one call: a header (ticket counter, abort word), one flag per
-// tile, and a float pair per chunk and channel.
+// Workspace of one call: a header (ticket counter, abort word), cleared to
+// zeros, and a pair (P, S) of floats per chunk and channel, cleared to all ones.
 struct Chain {
   unsigned* ticket;
   unsigned* abort;
-  unsigned* flags;    // [numbers][col tiles]
-  float* P;           // [numbers][D]
-  float* S;           // [numbers][D]
+  float* pairs;       // [numbers][D][2]
 };
 
 constexpr int kGroup = 16;                                    // chunks per group, see below
@@ -244,8 +242,27 @@ __device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ void store_release(unsigned* p, unsigned v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(p), "r"(v) : "memory");
+// Pairs are published word by word: a word of all ones (a NaN that no result
+// keeps, see publish) is one that is not there yet, any other is its value.
+// So there is no flag, no fence, and no order that the words have to keep.
+constexpr unsigned kUnset = 0xffffffffu;
+__device__ __forceinline__ uint4 load_pairs(const float* p) {
+  uint4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ bool unset(uint4 v) {
+  return v.x == kUnset || v.y == kUnset || v.z == kUnset || v.w == kUnset;
+}
+__device__ __forceinline__ unsigned word(float x) { return x != x ? 0x7fffffffu : __float_as_uint(x); }
+// The pairs of two channels.
+__device__ __forceinline__ void publish(float* p, float2 P, float2 S) {
+  asm volatile("st.relaxed.gpu.global.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"l"(p), "r"(word(P.x)),
+               "r"(word(S.x)), "r"(word(P.y)), "r"(word(S.y))
+               : "memory");
 }
 __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)),
@@ -391,42 +408,37 @@ __device__ __forceinline__ void fetch(const Packed& packed, const Chain& chain, 
 // chain through the grid has one link per kGroup chunks, not one per chunk.
 // Returns false if the wait ran out or another block gave up.
 __device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int chunk, int D,
-                                            int col_tiles, float2& h) {
-  const int lane = threadIdx.x & 31, i = chunk % kGroup, n = i + (chunk >= kGroup ? 1 : 0);
-  bool ready = lane >= n, ok = true;
-  const unsigned* flag = ch.flags +
-      ((size_t)t.number - (size_t)(lane < n ? lane + 1 : 0) * t.back) * col_tiles + t.col0 / kCols;
-  uint64_t t0 = 0;
-  for (int spin = 0;; ++spin) {
-    if (!ready) ready = load_acquire(flag) != 0;
-    if (__all_sync(0xffffffffu, ready)) break;
-    if ((spin & 63) == 63) {
-      const uint64_t now = global_ns();
-      if (t0 == 0) t0 = now;
-      ok = now - t0 < kWaitNs && load_acquire(ch.abort) == 0;
-      if (!__all_sync(0xffffffffu, ok)) return false;
-    }
-  }
-  const int c = t.col0 + lane * 2;
+                                            float2& h) {
+  const int lane = threadIdx.x & 31, c = t.col0 + lane * 2;
+  const int n = chunk % kGroup + (chunk >= kGroup ? 1 : 0);
+  const size_t step = (size_t)t.back * D * 2;
+  const float* from = ch.pairs + ((size_t)t.number * D + c) * 2;
   h = make_float2(0.f, 0.f);
-  if (c < D) {
-    const float* P = ch.P + (size_t)t.number * D + c;
-    const float* S = ch.S + (size_t)t.number * D + c;
-    const size_t step = (size_t)t.back * D;
-    if (chunk >= kGroup) h = __ldcg(reinterpret_cast<const float2*>(S - (i + 1) * step));
-    constexpr int kBatch = kGroup / 2;
-    for (int k0 = 0; k0 < i; k0 += kBatch) {
-      float2 p[kBatch], s[kBatch];
+  constexpr int kBatch = kGroup / 2;
+  uint64_t t0 = 0;
+  for (int k0 = 0; k0 < n; k0 += kBatch) {
+    uint4 q[kBatch];
+    for (int spin = 0;; ++spin) {
+      bool missing = false;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (k0 + k < i) {
-          p[k] = __ldcg(reinterpret_cast<const float2*>(P - (i - k0 - k) * step));
-          s[k] = __ldcg(reinterpret_cast<const float2*>(S - (i - k0 - k) * step));
+        if (k0 + k < n && c < D) {
+          q[k] = load_pairs(from - (n - k0 - k) * step);
+          missing |= unset(q[k]);
         }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (k0 + k < i) h = fma2(p[k], h, s[k]);
+      if (!__any_sync(0xffffffffu, missing)) break;
+      if ((spin & 63) == 63) {
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        const bool ok = now - t0 < kWaitNs && load_acquire(ch.abort) == 0;
+        if (!__all_sync(0xffffffffu, ok)) return false;
+      }
     }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (k0 + k < n && c < D)
+        h = fma2(make_float2(__uint_as_float(q[k].x), __uint_as_float(q[k].z)), h,
+                 make_float2(__uint_as_float(q[k].y), __uint_as_float(q[k].w)));
   }
   return true;
 }
@@ -493,7 +505,7 @@ __global__ void __launch_bounds__(NT + 32, MINB)
       if (t.chunk == 0) {
         const int c = t.col0 + lane * 2;
         if (P.h0 && c < P.D) h = *reinterpret_cast<const float2*>(P.h0 + (size_t)t.seq * P.D + c);
-      } else if (!fold_before(P.chain, t, t.chunk, P.D, P.col_tiles, h)) {
+      } else if (!fold_before(P.chain, t, t.chunk, P.D, h)) {
         gave_up = 1;
       }
       carry[it & 1][lane] = h;
@@ -588,16 +600,10 @@ __global__ void __launch_bounds__(NT + 32, MINB)
       // may still be reading h0, which the last tile may overwrite (hT = h0).
       const bool publisher = warp == W - 1 && !t.last;
       const bool late = t.chunk % kGroup == kGroup - 1 || t.chunk == 0;
-      const size_t at = (size_t)t.number * P.D + c;
-      unsigned* flag = P.chain.flags + (size_t)t.number * P.col_tiles + t.col0 / kCols;
-      if (publisher && !late) {
-        if (lane >= 16 && in) {
-          store_row(P.chain.P + at, mul2(p[0], bp[0]), mul2(p[1], bp[1]));
-          store_row(P.chain.S + at, fma2(p[0], bs[0], s[0]), fma2(p[1], bs[1], s[1]));
-        }
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) store_release(flag, 1u);
+      float* at = P.chain.pairs + ((size_t)t.number * P.D + c) * 2;
+      if (publisher && !late && lane >= 16 && in) {
+        publish(at, mul2(p[0], bp[0]), fma2(p[0], bs[0], s[0]));
+        publish(at + 4, mul2(p[1], bp[1]), fma2(p[1], bs[1], s[1]));
       }
       __syncthreads();                     // (2)
       if (gave_up) break;
@@ -605,14 +611,9 @@ __global__ void __launch_bounds__(NT + 32, MINB)
       load_row(reinterpret_cast<const float*>(&carry[it & 1][(lane & 15) * 2]), h[0], h[1]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) h[k] = fma2(bp[k], h[k], bs[k]);
-      if (publisher && late) {
-        if (lane >= 16 && in) {
-          store_row(P.chain.P + at, both(0.f), both(0.f));
-          store_row(P.chain.S + at, fma2(p[0], h[0], s[0]), fma2(p[1], h[1], s[1]));
-        }
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) store_release(flag, 1u);
+      if (publisher && late && lane >= 16 && in) {
+        publish(at, both(0.f), fma2(p[0], h[0], s[0]));
+        publish(at + 4, both(0.f), fma2(p[1], h[1], s[1]));
       }
       if (in) {
         if (P.states && first % kStateRows == 0 && first < t.rows) {
@@ -760,25 +761,22 @@ constexpr size_t kHeaderBytes = 256;
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 int col_tiles_of(int D) { return (D + kCols - 1) / kCols; }
 
-// Bytes of a call whose chunks have L rows: header and flags (cleared by every
-// call), then two floats per chunk and channel.
-size_t chain_cleared_bytes(const RecurrenceDims& d, int L) {
-  return round256(kHeaderBytes + (size_t)chunk_numbers(d.rows, d.n_seq, L) * col_tiles_of(d.D) * 4);
-}
+// Bytes of a call whose chunks have L rows: the header, then the pairs.
 size_t chain_bytes(const RecurrenceDims& d, int L) {
-  return chain_cleared_bytes(d, L) + 2 * round256((size_t)chunk_numbers(d.rows, d.n_seq, L) * d.D * 4);
+  return kHeaderBytes + round256((size_t)chunk_numbers(d.rows, d.n_seq, L) * d.D * 8);
 }
 
-Chain chain_in(void* workspace, const RecurrenceDims& d, int L) {
+Chain chain_in(void* workspace) {
   char* w = static_cast<char*>(workspace);
-  char* data = w + chain_cleared_bytes(d, L);
-  Chain c;
-  c.ticket = reinterpret_cast<unsigned*>(w);
-  c.abort = reinterpret_cast<unsigned*>(w + 128);
-  c.flags = reinterpret_cast<unsigned*>(w + kHeaderBytes);
-  c.P = reinterpret_cast<float*>(data);
-  c.S = reinterpret_cast<float*>(data + round256((size_t)chunk_numbers(d.rows, d.n_seq, L) * d.D * 4));
-  return c;
+  return Chain{reinterpret_cast<unsigned*>(w), reinterpret_cast<unsigned*>(w + 128),
+               reinterpret_cast<float*>(w + kHeaderBytes)};
+}
+
+cudaError_t clear_chain(void* workspace, const RecurrenceDims& d, int L, cudaStream_t stream) {
+  const cudaError_t e = cudaMemsetAsync(workspace, 0, kHeaderBytes, stream);
+  if (e != cudaSuccess) return e;
+  return cudaMemsetAsync(static_cast<char*>(workspace) + kHeaderBytes, 0xff,
+                         chain_bytes(d, L) - kHeaderBytes, stream);
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -849,14 +847,14 @@ cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, cons
   P.y = y;
   P.hT = hT;
   P.states = states;
-  P.chain = chain_in(workspace, d, L);
+  P.chain = chain_in(workspace);
   P.D = d.D;
   P.col_tiles = col_tiles_of(d.D);
   P.tiles = tiles_of(d, in.offsets != nullptr, L);
   P.status = status;
   const auto kernel = forward_kernel<T, R, NT, STAGES, MINB>;
   cudaError_t e = allow_smem(kernel, Sh::kSmem);
-  if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, chain_cleared_bytes(d, L), stream);
+  if (e == cudaSuccess) e = clear_chain(workspace, d, L, stream);
   if (e != cudaSuccess) return e;
   const unsigned most = (unsigned)(MINB * device_limits().sms);
   kernel<<<P.tiles < most ? P.tiles : most, NT + 32, Sh::kSmem, stream>>>(P);

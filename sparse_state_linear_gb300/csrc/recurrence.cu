@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace sdm {
 namespace {
@@ -216,7 +217,7 @@ struct Args {
 
 // --------------------------------------------------------------------- scan
 // What a block has to know of a tile, found out by the warp that fetches it.
-struct Tile {
+struct __align__(16) Tile {
   int rows;      // valid rows, 1..L; 0: no tile is left
   int row0;      // first row
   int seq, chunk;
@@ -268,6 +269,23 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)),
                "r"(bytes)
                : "memory");
+}
+// Wait for an mbarrier phase (a whole warp calls it); false once the limit has
+// passed or another warp of the block has given up (which the first to do so
+// marks).
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, volatile int* gave_up) {
+  bool there = mbar_test_wait(bar, parity);
+  for (uint64_t t0 = 0; !there;) {
+    for (int i = 0; i < 32 && !there; ++i) there = mbar_try_wait(bar, parity);
+    if (there) break;
+    const uint64_t now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (*gave_up || now - t0 > kWaitNs) {
+      *gave_up = 1;
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, there);
 }
 // x: first channel (a multiple of 64, so 16-byte aligned), y: first row; what
 // lies outside the tensor arrives as zeros.
@@ -321,13 +339,6 @@ __device__ __forceinline__ float2 shfl_xor2(float2 a, int m) {
   return make_float2(__shfl_xor_sync(0xffffffffu, a.x, m), __shfl_xor_sync(0xffffffffu, a.y, m));
 }
 
-template <typename T, int R, int NT, int STAGES>
-struct ForwardShape {
-  static constexpr int kWarps = NT / 32, L = NT / 16 * R, kTileBytes = L * kCols * (int)sizeof(T);
-  static constexpr int kStageBytes = 3 * kTileBytes;
-  static constexpr int kSmem = STAGES * kStageBytes + 128;    // + alignment
-};
-
 struct ForwardArgs {
   CUtensorMap za, zb, v;
   Packed packed;
@@ -343,23 +354,21 @@ struct ForwardArgs {
   unsigned* status;
 };
 
-// Fetch the next tile that has rows (a whole warp calls it): takes tickets
-// until one does, starts the copy of its inputs into `buf` and describes it in
-// *out.  `ticket` (lane 0) was taken earlier and is replaced by a new one, so
-// that its latency lies behind other work.
-template <int L, class Start, class Empty>
-__device__ __forceinline__ void fetch(const Packed& packed, const Chain& chain, unsigned tiles,
-                                      int col_tiles, bool reverse, unsigned& ticket, Tile* out,
-                                      Start start, Empty empty) {
+// The next tile that has rows (a whole warp calls it): takes tickets until one
+// does; false when there is none left.  `ticket` (lane 0) was taken earlier and
+// is replaced by a new one, so that its latency lies behind other work.
+template <int L, class Empty>
+__device__ __forceinline__ bool fetch(const Packed& packed, const Chain& chain, unsigned tiles,
+                                      int col_tiles, bool reverse, unsigned& ticket, Tile& t,
+                                      Empty empty) {
   const int lane = threadIdx.x & 31;
   while (true) {
     const unsigned k = __shfl_sync(0xffffffffu, ticket, 0);
     if (k >= tiles) {
-      if (lane == 0) out->rows = 0;
-      break;
+      t.rows = 0;
+      return false;
     }
     if (lane == 0) ticket = atomicAdd(chain.ticket, 1u);
-    Tile t;
     const unsigned q = reverse ? tiles - 1 - k : k;
     const int number = (int)(q / (unsigned)col_tiles);
     t.col0 = (int)(q % (unsigned)col_tiles) * kCols;
@@ -389,13 +398,16 @@ __device__ __forceinline__ void fetch(const Packed& packed, const Chain& chain, 
       if (t.chunk == 0) empty(t);
       continue;
     }
-    if (lane == 0) {
-      *out = t;
-      start(t);
-    }
-    break;
+    return true;
   }
-  __syncwarp();
+}
+
+// Whether a chunk publishes the state behind it (with P = 0), known only after
+// the fold, not its pair: the last of a group, and a sequence's first.  The
+// first's would be known at once, but this way its block's read of h0 has
+// happened when the chunks behind go on, and the last may overwrite h0 (hT = h0).
+__device__ __forceinline__ bool publishes_state(int chunk) {
+  return chunk % kGroup == kGroup - 1 || chunk == 0;
 }
 
 // The state in front of a tile from what the chunks before it published (a
@@ -443,202 +455,342 @@ __device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int 
   return true;
 }
 
-// A block of NT threads for the arithmetic (a half-warp takes R rows by 64
-// channels, four channels a thread) and one warp that fetches tiles and folds
-// what the chunks before published, so that neither holds the others up.  Per
-// tile there are two barriers: (1) among the arithmetic warps, every warp's
-// pair is in shared memory; (2) of all, the state in front of the tile is.
-template <typename T, int R, int NT, int STAGES, int MINB>
-__global__ void __launch_bounds__(NT + 32, MINB)
-    forward_kernel(const __grid_constant__ ForwardArgs P) {
-  using Sh = ForwardShape<T, R, NT, STAGES>;
-  constexpr int L = Sh::L, W = Sh::kWarps;
+// Registers parked in tensor memory: the calling warp's 32 lanes of it, one
+// 32-bit column per register, read back by the same threads.
+__device__ __forceinline__ void park16(uint32_t taddr, const float2 (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x),
+      "f"(v[3].y), "f"(v[4].x), "f"(v[4].y), "f"(v[5].x), "f"(v[5].y), "f"(v[6].x), "f"(v[6].y),
+      "f"(v[7].x), "f"(v[7].y)
+      : "memory");
+}
+__device__ __forceinline__ void parked() {
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void unpark16(uint32_t taddr, float2 (&v)[8]) {
+  float r[16];
+  tc::ld16(taddr, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = make_float2(r[2 * i], r[2 * i + 1]);
+}
+
+// A block is eight warps for the arithmetic (a half-warp takes R rows by 64
+// channels, four channels a thread) and four more: one fetches tiles, one
+// publishes their pairs, two (even and odd tiles) fold what the chunks before
+// published into the state in front of them.
+//
+// That state comes from other blocks, a microsecond or two after a tile's pair
+// is out.  So the arithmetic warps do not wait for it: they form a tile's
+// gates, put a and b aside in tensor memory (which nothing else here uses),
+// go on to the next tile, and only then come back to finish the one before.
+//
+// Inputs come in units of one tensor's tile (16 KB), in a ring of kUnits.
+// Barriers, all in shared memory: a tile's description is there (known), a
+// unit is (full) and has been read (empty); a tile's warps' pairs are there
+// (paired), the state in front of it is (folded), both have been read (taken).
+constexpr int kWarps = 8;
+constexpr int kUnits = 5;
+constexpr int kSlots = 2;    // tiles between gates and outputs
+constexpr int kInfo = 8;     // ring of descriptions: longer than any tile's life
+constexpr int kThreads = (kWarps + 4) * 32;
+
+template <typename T>
+struct ForwardShape {
+  static constexpr int R = 16 / sizeof(T);                              // rows per thread
+  static constexpr int L = 2 * kWarps * R;                              // rows per tile
+  static constexpr int kUnitBytes = L * kCols * (int)sizeof(T);
+  static constexpr int kSmem = kUnits * kUnitBytes + 128;               // + alignment
+  static constexpr int kParkCols = 8 * R;                               // per thread and tile
+  static constexpr int kSlotCols = kWarps / 4 * kParkCols;
+  static constexpr int kTmemCols = kSlots * kSlotCols;                  // a power of two
+  static_assert(kStateRows % R == 0, "states fall on a thread's first row");
+};
+
+// The pair of a whole tile from its warps' (two channels per lane).
+__device__ __forceinline__ void tile_pair(const float (*total)[2][kCols], int lane, float2& P,
+                                          float2& S) {
+  P = both(1.f);
+  S = both(0.f);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float2 wp = *reinterpret_cast<const float2*>(&total[w][0][lane * 2]);
+    const float2 ws = *reinterpret_cast<const float2*>(&total[w][1][lane * 2]);
+    S = fma2(wp, S, ws);
+    P = mul2(wp, P);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_constant__ ForwardArgs P) {
+  using Sh = ForwardShape<T>;
+  constexpr int L = Sh::L, R = Sh::R, W = kWarps;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((128 - (smem_u32(raw) & 127)) & 127);
-  __shared__ uint64_t full[STAGES];
-  __shared__ Tile tiles[STAGES];
-  __shared__ float4 total[W][2][16];       // (P, S) of each warp's rows
-  __shared__ float2 carry[2][kCols / 2];   // the state in front of the tile
-  __shared__ int gave_up;
+  __shared__ uint64_t full[kUnits], empty[kUnits], known[kInfo], paired[kSlots], folded[kSlots],
+      taken[kSlots];
+  __shared__ Tile tiles[kInfo];
+  __shared__ __align__(16) float total[kSlots][W][2][kCols];   // (P, S) of each warp's rows
+  __shared__ __align__(16) float lower[kSlots][W][2][kCols];   // and of its lower half-warp's
+  __shared__ __align__(16) float carry[kSlots][kCols];         // the state in front of the tile
+  __shared__ uint32_t tmem_base;
+  __shared__ int quit;
+  volatile int* gave_up = &quit;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!offsets_ok(P.packed)) {
     if (tid == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     return;
   }
+  if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
   if (tid == 0) {
-    for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
-    gave_up = 0;
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], W);
+    }
+    for (int s = 0; s < kInfo; ++s) mbar_init(&known[s], 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&paired[s], W);
+      mbar_init(&folded[s], 1);
+      mbar_init(&taken[s], W + 1);
+    }
+    quit = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
+  tc::fence_before_sync();
   __syncthreads();
-  int it = 0;
+  tc::fence_after_sync();
 
-  if (warp == W) {
+  if (warp == W) {                         // fetches
     unsigned ticket = 0;
-    auto get = [&](int st) {
-      fetch<L>(
-          P.packed, P.chain, P.tiles, P.col_tiles, false, ticket, &tiles[st],
-          [&](const Tile& t) {
-            unsigned char* buf = smem + st * Sh::kStageBytes;
-            mbar_expect(&full[st], Sh::kStageBytes);
-            tma_load(buf, &P.za, t.col0, t.row0, &full[st]);
-            tma_load(buf + Sh::kTileBytes, &P.zb, t.col0, t.row0, &full[st]);
-            tma_load(buf + 2 * Sh::kTileBytes, &P.v, t.col0, t.row0, &full[st]);
-          },
-          [&](const Tile& t) {             // a sequence without rows
-            const int c = t.col0 + lane * 2;
-            if (P.hT && c < P.D) {
-              const size_t i = (size_t)t.seq * P.D + c;
-              *reinterpret_cast<float2*>(P.hT + i) =
-                  P.h0 ? *reinterpret_cast<const float2*>(P.h0 + i) : make_float2(0.f, 0.f);
-            }
-          });
-    };
     if (lane == 0) ticket = atomicAdd(P.chain.ticket, 1u);
-    for (int s = 0; s < STAGES; ++s) get(s);
-    __syncthreads();
-    for (;; ++it) {
-      const Tile t = tiles[it % STAGES];
+    int u = 0;                             // units asked for
+    bool more = true;
+    for (int n = 0; more; ++n) {
+      Tile t;
+      more = fetch<L>(P.packed, P.chain, P.tiles, P.col_tiles, false, ticket, t,
+                      [&](const Tile& e) {               // a sequence without rows
+                        const int c = e.col0 + lane * 2;
+                        if (P.hT && c < P.D) {
+                          const size_t i = (size_t)e.seq * P.D + c;
+                          *reinterpret_cast<float2*>(P.hT + i) =
+                              P.h0 ? *reinterpret_cast<const float2*>(P.h0 + i)
+                                   : make_float2(0.f, 0.f);
+                        }
+                      });
+      bool there = true;
+      for (int j = 0; j < 3 && there; ++j, ++u) {
+        const int k = u % kUnits;
+        there = u < kUnits || wait_phase(&empty[k], (u / kUnits - 1) & 1, gave_up);
+        if (!there) break;
+        if (lane == 0) {
+          if (j == 0) {
+            tiles[n % kInfo] = t;
+            mbar_arrive(&known[n % kInfo]);
+          }
+          if (more) {
+            mbar_expect(&full[k], Sh::kUnitBytes);
+            tma_load(smem + k * Sh::kUnitBytes, j == 0 ? &P.za : j == 1 ? &P.zb : &P.v, t.col0,
+                     t.row0, &full[k]);
+          } else {
+            mbar_arrive(&full[k]);
+          }
+        }
+        __syncwarp();
+      }
+      if (!there) break;
+    }
+    // Stay until every copy has arrived, also when the block gives up.
+    for (int x = u > kUnits ? u - kUnits : 0; x < u; ++x)
+      mbar_wait_bounded(&full[x % kUnits], (x / kUnits) & 1, kWaitNs);
+  } else if (warp == W + 1) {              // publishes
+    for (int it = 0;; ++it) {
+      const int slot = it % kSlots;
+      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, gave_up)) break;
+      const Tile t = tiles[it % kInfo];
       if (t.rows == 0) break;
+      if (!wait_phase(&paired[slot], (it / kSlots) & 1, gave_up)) break;
+      const int c = t.col0 + lane * 2;
+      if (!t.last && !publishes_state(t.chunk)) {
+        float2 p, s;
+        tile_pair(total[slot], lane, p, s);
+        if (c < P.D) publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, p, s);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&taken[slot]);
+    }
+  } else if (warp > W + 1) {               // folds
+    for (int it = warp - (W + 2);; it += 2) {
+      const int slot = it % kSlots;
+      // The end may come before this warp's next tile.
+      if (it > 0) {
+        if (!wait_phase(&known[(it - 1) % kInfo], ((it - 1) / kInfo) & 1, gave_up)) break;
+        if (tiles[(it - 1) % kInfo].rows == 0) break;
+      }
+      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, gave_up)) break;
+      const Tile t = tiles[it % kInfo];
+      if (t.rows == 0) break;
+      const int c = t.col0 + lane * 2;
       float2 h = make_float2(0.f, 0.f);
       if (t.chunk == 0) {
-        const int c = t.col0 + lane * 2;
         if (P.h0 && c < P.D) h = *reinterpret_cast<const float2*>(P.h0 + (size_t)t.seq * P.D + c);
       } else if (!fold_before(P.chain, t, t.chunk, P.D, h)) {
-        gave_up = 1;
+        *gave_up = 1;
+        break;
       }
-      carry[it & 1][lane] = h;
-      __syncthreads();                     // (2)
-      if (gave_up) break;
-      get(it % STAGES);                    // its inputs are in registers
+      if (it >= kSlots && !wait_phase(&taken[slot], (it / kSlots - 1) & 1, gave_up)) break;
+      *reinterpret_cast<float2*>(&carry[slot][lane * 2]) = h;
+      if (!t.last && publishes_state(t.chunk)) {
+        if (!wait_phase(&paired[slot], (it / kSlots) & 1, gave_up)) break;
+        float2 p, s;
+        tile_pair(total[slot], lane, p, s);
+        if (c < P.D)
+          publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, both(0.f), fma2(p, h, s));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&folded[slot]);
     }
-  } else {
+  } else {                                 // gates and outputs
     const int c4 = (lane & 15) * 4, first = (tid >> 4) * R;   // first row in the tile
-    __syncthreads();
-    for (;; ++it) {
-      const int st = it % STAGES;
-      const Tile t = tiles[st];
-      if (t.rows == 0) break;
-      const int c = t.col0 + c4;
-      const bool in = c < P.D;
-      float2 nA[2] = {both(-1.f), both(-1.f)}, bias[2] = {both(0.f), both(0.f)};
-      if (in && P.A) {
-        load_row(P.A + c, nA[0], nA[1]);
-        nA[0] = mul2(nA[0], both(-1.f));
-        nA[1] = mul2(nA[1], both(-1.f));
-      }
-      if (in && P.bias) load_row(P.bias + c, bias[0], bias[1]);
-      if (!mbar_wait_bounded(&full[st], (it / STAGES) & 1, kWaitNs)) gave_up = 1;
-
-      // Gates of this thread's R rows, and the pair (p, s) of all of them.
-      const T* buf = reinterpret_cast<const T*>(smem + st * Sh::kStageBytes) + first * kCols + c4;
-      float2 a[R][2], b[R][2];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float2 za[2], zb[2], v[2];
-        load_row(buf + r * kCols, za[0], za[1]);
-        load_row(buf + (L + r) * kCols, zb[0], zb[1]);
-        load_row(buf + (2 * L + r) * kCols, v[0], v[1]);
-        gate_pair(za[0], zb[0], v[0], nA[0], bias[0], a[r][0], b[r][0]);
-        gate_pair(za[1], zb[1], v[1], nA[1], bias[1], a[r][1], b[r][1]);
-      }
-      if (t.rows < L) {                    // rows behind the sequence change nothing
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (first + r >= t.rows) {
-            a[r][0] = a[r][1] = both(1.f);
-            b[r][0] = b[r][1] = both(0.f);
+    const uint32_t park = tmem_base + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * Sh::kParkCols;
+    int end = 0x7fffffff;                  // number of this block's tiles, once known
+    for (int it = 0; it - 1 < end; ++it) {
+      if (it < end) {
+        const int slot = it % kSlots, u = it * 3;
+        if (!wait_phase(&full[u % kUnits], (u / kUnits) & 1, gave_up)) break;
+        const Tile t = tiles[it % kInfo];
+        if (t.rows == 0) {
+          end = it;
+        } else {
+          const int c = t.col0 + c4;
+          float2 nA[2] = {both(-1.f), both(-1.f)}, bias[2] = {both(0.f), both(0.f)};
+          if (c < P.D && P.A) {
+            load_row(P.A + c, nA[0], nA[1]);
+            nA[0] = mul2(nA[0], both(-1.f));
+            nA[1] = mul2(nA[1], both(-1.f));
           }
-      }
-      float2 p[2] = {a[0][0], a[0][1]}, s[2] = {b[0][0], b[0][1]};
+          if (c < P.D && P.bias) load_row(P.bias + c, bias[0], bias[1]);
+          if (!wait_phase(&full[(u + 1) % kUnits], ((u + 1) / kUnits) & 1, gave_up)) break;
+          if (!wait_phase(&full[(u + 2) % kUnits], ((u + 2) / kUnits) & 1, gave_up)) break;
+          const size_t from = (size_t)first * kCols + c4;
+          const T* bza = reinterpret_cast<const T*>(smem + (u % kUnits) * Sh::kUnitBytes) + from;
+          const T* bzb = reinterpret_cast<const T*>(smem + ((u + 1) % kUnits) * Sh::kUnitBytes) + from;
+          const T* bv = reinterpret_cast<const T*>(smem + ((u + 2) % kUnits) * Sh::kUnitBytes) + from;
+          // Four rows at a time: gates, the pair of all rows so far, aside.
+          float2 p[2], s[2];
 #pragma unroll
-      for (int r = 1; r < R; ++r) {
+          for (int r4 = 0; r4 < R; r4 += 4) {
+            float2 a[8], b[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          s[k] = fma2(a[r][k], s[k], b[r][k]);
-          p[k] = mul2(a[r][k], p[k]);
+            for (int r = 0; r < 4; ++r) {
+              float2 za[2], zb[2], v[2];
+              load_row(bza + (r4 + r) * kCols, za[0], za[1]);
+              load_row(bzb + (r4 + r) * kCols, zb[0], zb[1]);
+              load_row(bv + (r4 + r) * kCols, v[0], v[1]);
+              gate_pair(za[0], zb[0], v[0], nA[0], bias[0], a[2 * r], b[2 * r]);
+              gate_pair(za[1], zb[1], v[1], nA[1], bias[1], a[2 * r + 1], b[2 * r + 1]);
+            }
+            if (t.rows < L) {              // rows behind the sequence change nothing
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (first + r4 + r >= t.rows) {
+                  a[2 * r] = a[2 * r + 1] = both(1.f);
+                  b[2 * r] = b[2 * r + 1] = both(0.f);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                if (r4 + r == 0) {
+                  p[k] = a[k];
+                  s[k] = b[k];
+                } else {
+                  s[k] = fma2(a[2 * r + k], s[k], b[2 * r + k]);
+                  p[k] = mul2(a[2 * r + k], p[k]);
+                }
+              }
+            }
+            park16(park + slot * Sh::kSlotCols + r4 * 8, a);
+            park16(park + slot * Sh::kSlotCols + r4 * 8 + 16, b);
+          }
+          __syncwarp();
+          if (lane < 3) mbar_arrive(&empty[(u + lane) % kUnits]);
+          // The warp's pair (the lower half-warp's rows come first).
+          float2 pl[2], sl[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            pl[k] = shfl_xor2(p[k], 16);
+            sl[k] = shfl_xor2(s[k], 16);
+          }
+          if (it >= kSlots && !wait_phase(&taken[slot], (it / kSlots - 1) & 1, gave_up)) break;
+          if (lane >= 16) {
+            store_row(&total[slot][warp][0][c4], mul2(p[0], pl[0]), mul2(p[1], pl[1]));
+            store_row(&total[slot][warp][1][c4], fma2(p[0], sl[0], s[0]), fma2(p[1], sl[1], s[1]));
+          } else {
+            store_row(&lower[slot][warp][0][c4], p[0], p[1]);
+            store_row(&lower[slot][warp][1][c4], s[0], s[1]);
+          }
+          parked();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&paired[slot]);
         }
       }
-      // The lower half-warp's rows come before the upper's.
-      float2 pl[2], sl[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        pl[k] = shfl_xor2(p[k], 16);
-        sl[k] = shfl_xor2(s[k], 16);
-      }
-      if (lane >= 16) {
-        store_row(reinterpret_cast<float*>(&total[warp][0][lane & 15]), mul2(p[0], pl[0]),
-                  mul2(p[1], pl[1]));
-        store_row(reinterpret_cast<float*>(&total[warp][1][lane & 15]), fma2(p[0], sl[0], s[0]),
-                  fma2(p[1], sl[1], s[1]));
-      }
-      named_bar_sync(1, NT);               // (1)
-      // (P, S) of the rows before this thread's.
-      float2 bp[2] = {both(1.f), both(1.f)}, bs[2] = {both(0.f), both(0.f)};
+      const int out = it - 1;              // the tile to finish
+      if (out < 0) continue;
+      const int slot = out % kSlots;
+      const Tile t = tiles[out % kInfo];
+      const int c = t.col0 + c4;
+      if (!wait_phase(&paired[slot], (out / kSlots) & 1, gave_up)) break;
+      if (!wait_phase(&folded[slot], (out / kSlots) & 1, gave_up)) break;
+      float2 h[2];
+      load_row(&carry[slot][c4], h[0], h[1]);
       for (int w = 0; w < warp; ++w) {
         float2 wp[2], ws[2];
-        load_row(reinterpret_cast<const float*>(&total[w][0][lane & 15]), wp[0], wp[1]);
-        load_row(reinterpret_cast<const float*>(&total[w][1][lane & 15]), ws[0], ws[1]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          bs[k] = fma2(wp[k], bs[k], ws[k]);
-          bp[k] = mul2(wp[k], bp[k]);
-        }
+        load_row(&total[slot][w][0][c4], wp[0], wp[1]);
+        load_row(&total[slot][w][1][c4], ws[0], ws[1]);
+        h[0] = fma2(wp[0], h[0], ws[0]);
+        h[1] = fma2(wp[1], h[1], ws[1]);
       }
       if (lane >= 16) {
+        float2 wp[2], ws[2];
+        load_row(&lower[slot][warp][0][c4], wp[0], wp[1]);
+        load_row(&lower[slot][warp][1][c4], ws[0], ws[1]);
+        h[0] = fma2(wp[0], h[0], ws[0]);
+        h[1] = fma2(wp[1], h[1], ws[1]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&taken[slot]);
+      const int row = t.chunk * L + first;                     // in the sequence
+      if (P.states && row % kStateRows == 0 && first < t.rows && c < P.D) {
+        const int begin = t.row0 - t.chunk * L;
+        const size_t n = (size_t)(begin / kStateRows + t.seq + row / kStateRows);
+        store_row(P.states + n * P.D + c, h[0], h[1]);
+      }
+      T* y = reinterpret_cast<T*>(P.y) + (size_t)(t.row0 + first) * P.D + c;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          bs[k] = fma2(pl[k], bs[k], sl[k]);
-          bp[k] = mul2(pl[k], bp[k]);
+      for (int r4 = 0; r4 < R; r4 += 4) {
+        float2 a[8], b[8];
+        unpark16(park + slot * Sh::kSlotCols + r4 * 8, a);
+        unpark16(park + slot * Sh::kSlotCols + r4 * 8 + 16, b);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          h[0] = fma2(a[2 * r], h[0], b[2 * r]);
+          h[1] = fma2(a[2 * r + 1], h[1], b[2 * r + 1]);
+          if (c < P.D && first + r4 + r < t.rows) store_row(y, h[0], h[1]);
+          y += P.D;
         }
       }
-      // The last rows' threads know the tile's pair.  They publish it now; or,
-      // where the tile ends a group or begins its sequence, the state behind
-      // it once that is known (with P = 0: whatever is in front of it).  The
-      // first tile waits although it could publish at once because its block
-      // may still be reading h0, which the last tile may overwrite (hT = h0).
-      const bool publisher = warp == W - 1 && !t.last;
-      const bool late = t.chunk % kGroup == kGroup - 1 || t.chunk == 0;
-      float* at = P.chain.pairs + ((size_t)t.number * P.D + c) * 2;
-      if (publisher && !late && lane >= 16 && in) {
-        publish(at, mul2(p[0], bp[0]), fma2(p[0], bs[0], s[0]));
-        publish(at + 4, mul2(p[1], bp[1]), fma2(p[1], bs[1], s[1]));
-      }
-      __syncthreads();                     // (2)
-      if (gave_up) break;
-      float2 h[2];
-      load_row(reinterpret_cast<const float*>(&carry[it & 1][(lane & 15) * 2]), h[0], h[1]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) h[k] = fma2(bp[k], h[k], bs[k]);
-      if (publisher && late && lane >= 16 && in) {
-        publish(at, both(0.f), fma2(p[0], h[0], s[0]));
-        publish(at + 4, both(0.f), fma2(p[1], h[1], s[1]));
-      }
-      if (in) {
-        if (P.states && first % kStateRows == 0 && first < t.rows) {
-          const int begin = t.row0 - t.chunk * L;
-          const size_t n = (size_t)(begin / kStateRows + t.seq + (t.chunk * L + first) / kStateRows);
-          store_row(P.states + n * P.D + c, h[0], h[1]);
-        }
-        T* y = reinterpret_cast<T*>(P.y) + (size_t)(t.row0 + first) * P.D + c;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          h[0] = fma2(a[r][0], h[0], b[r][0]);
-          h[1] = fma2(a[r][1], h[1], b[r][1]);
-          if (first + r < t.rows) store_row(y + (size_t)r * P.D, h[0], h[1]);
-        }
-        if (P.hT && t.last && first < t.rows && t.rows <= first + R)
-          store_row(P.hT + (size_t)t.seq * P.D + c, h[0], h[1]);
-      }
+      if (P.hT && t.last && first < t.rows && t.rows <= first + R && c < P.D)
+        store_row(P.hT + (size_t)t.seq * P.D + c, h[0], h[1]);
     }
   }
-  if (gave_up && tid == 0) {
-    // Tell the other blocks, and leave no copy in flight behind.
+  __syncthreads();
+  if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
+  if (quit && tid == 0) {                  // tell the other blocks
     record_status(P.status, SDM_ERR_TIMEOUT);
     atomicExch(P.chain.abort, 1u);
-    for (int x = it; x < it + STAGES; ++x)
-      if (tiles[x % STAGES].rows > 0) mbar_wait_bounded(&full[x % STAGES], (x / STAGES) & 1, kWaitNs);
   }
 }
 
@@ -828,13 +980,12 @@ cudaError_t allow_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <typename T, int R, int NT, int STAGES, int MINB>
+template <typename T>
 cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, const float* h0,
                        void* y, float* hT, float* states, void* workspace, unsigned* status,
                        cudaStream_t stream) {
-  using Sh = ForwardShape<T, R, NT, STAGES>;
+  using Sh = ForwardShape<T>;
   constexpr int L = Sh::L;
-  static_assert(L % kStateRows == 0 && kStateRows % R == 0, "states fall on a thread's first row");
   ForwardArgs P;
   if (d.rows > 0 && (!make_map(&P.za, in.za, d.dtype, d.rows, d.D, d.ld, L) ||
                      !make_map(&P.zb, in.zb, d.dtype, d.rows, d.D, d.ld, L) ||
@@ -852,12 +1003,12 @@ cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, cons
   P.col_tiles = col_tiles_of(d.D);
   P.tiles = tiles_of(d, in.offsets != nullptr, L);
   P.status = status;
-  const auto kernel = forward_kernel<T, R, NT, STAGES, MINB>;
+  const auto kernel = forward_kernel<T>;
   cudaError_t e = allow_smem(kernel, Sh::kSmem);
   if (e == cudaSuccess) e = clear_chain(workspace, d, L, stream);
   if (e != cudaSuccess) return e;
-  const unsigned most = (unsigned)(MINB * device_limits().sms);
-  kernel<<<P.tiles < most ? P.tiles : most, NT + 32, Sh::kSmem, stream>>>(P);
+  const unsigned most = (unsigned)(2 * device_limits().sms);
+  kernel<<<P.tiles < most ? P.tiles : most, kThreads, Sh::kSmem, stream>>>(P);
   return cudaGetLastError();
 }
 
@@ -865,7 +1016,7 @@ cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, cons
 
 size_t recurrence_workspace_bytes(const RecurrenceDims& d) {
   const size_t back = (size_t)(d.n_seq + 1) * 2 * d.D * sizeof(float);
-  const size_t fwd = chain_bytes(d, 64);
+  const size_t fwd = chain_bytes(d, d.dtype == SDM_BF16 ? ForwardShape<__nv_bfloat16>::L : ForwardShape<float>::L);
   return back > fwd ? back : fwd;
 }
 
@@ -877,8 +1028,8 @@ cudaError_t launch_recurrence_forward(const RecurrenceDims& d, const RecurrenceI
                                       const float* h0, void* y, float* hT, float* states,
                                       void* workspace, unsigned* status, cudaStream_t stream) {
   if (d.dtype == SDM_BF16)
-    return forward_as<__nv_bfloat16, 4, 256, 2, 3>(d, in, h0, y, hT, states, workspace, status, stream);
-  return forward_as<float, 4, 256, 2, 2>(d, in, h0, y, hT, states, workspace, status, stream);
+    return forward_as<__nv_bfloat16>(d, in, h0, y, hT, states, workspace, status, stream);
+  return forward_as<float>(d, in, h0, y, hT, states, workspace, status, stream);
 }
 
 cudaError_t launch_recurrence_backward(const RecurrenceDims& d, const RecurrenceInputs& in,

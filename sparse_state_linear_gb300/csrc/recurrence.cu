@@ -33,23 +33,18 @@ __device__ __forceinline__ float rcp(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// ln(1 + e) for e in [0, 1]: e times the degree-9 polynomial that interpolates
-// ln(1 + e) / e at the Chebyshev points of [0, 1].  Relative error 1.3e-7 for
-// every e, which the logarithm instruction (an absolute bound) does not give
-// where the gate hardly decays.
-__device__ __forceinline__ float log1p_unit(float e) {
-  float p = -0.00317605701f;
-  p = fmaf(p, e, 0.0195425265f);
-  p = fmaf(p, e, -0.0563736111f);
-  p = fmaf(p, e, 0.105436236f);
-  p = fmaf(p, e, -0.152696669f);
-  p = fmaf(p, e, 0.196632743f);
-  p = fmaf(p, e, -0.249516159f);
-  p = fmaf(p, e, 0.333297104f);
-  p = fmaf(p, e, -0.499998927f);
-  p = fmaf(p, e, 1.f);
-  return p * e;
+// log2(1 + e) for e in [0, 1]: 2 log2(e) atanh(t) with t = e / (2 + e), as t
+// times the degree-4 polynomial in t^2 that interpolates the rest at the
+// Chebyshev points of [0, 1/9] (relative error 4e-9).  With the roundings the
+// relative error is below 6.5 half steps for every e; the logarithm instruction
+// has an absolute bound, which is not enough where the gate hardly decays.
+constexpr float kLog0 = 2.88539004f, kLog1 = 0.961791694f, kLog2 = 0.577432871f,
+                kLog3 = 0.403451949f, kLog4 = 0.406230867f;
+__device__ __forceinline__ float log2p1_unit(float e) {
+  const float t = e * rcp(e + 2.f), z = t * t;
+  return t * fmaf(fmaf(fmaf(fmaf(kLog4, z, kLog3), z, kLog2), z, kLog1), z, kLog0);
 }
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct Gate {
   float sp;      // softplus(za + bias)
@@ -63,7 +58,7 @@ __device__ __forceinline__ Gate make_gate(float za, float zb, float A, float bia
   Gate g;
   const float x = za + bias;
   const float e = ex2(-fabsf(x) * kLog2e);
-  g.sp = fmaxf(x, 0.f) + log1p_unit(e);
+  g.sp = fmaxf(x, 0.f) + kLn2 * log2p1_unit(e);
   g.alpha = ex2(-A * kLog2e * g.sp);
   const float r = rcp(1.f + e);
   g.sig = x >= 0.f ? r : e * r;
@@ -131,20 +126,15 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// log2(1 + e) for e in [0, 1], two at a time: the polynomial of log1p_unit
-// with its coefficients times log2(e).
+// log2p1_unit, two at a time.
 __device__ __forceinline__ float2 log2p1_unit(float2 e) {
-  float2 p = both(-0.00317605701f * kLog2e);
-  p = fma2(p, e, both(0.0195425265f * kLog2e));
-  p = fma2(p, e, both(-0.0563736111f * kLog2e));
-  p = fma2(p, e, both(0.105436236f * kLog2e));
-  p = fma2(p, e, both(-0.152696669f * kLog2e));
-  p = fma2(p, e, both(0.196632743f * kLog2e));
-  p = fma2(p, e, both(-0.249516159f * kLog2e));
-  p = fma2(p, e, both(0.333297104f * kLog2e));
-  p = fma2(p, e, both(-0.499998927f * kLog2e));
-  p = fma2(p, e, both(kLog2e));
-  return mul2(p, e);
+  const float2 d = add2(e, both(2.f));
+  const float2 t = mul2(e, make_float2(rcp(d.x), rcp(d.y))), z = mul2(t, t);
+  float2 p = fma2(both(kLog4), z, both(kLog3));
+  p = fma2(p, z, both(kLog2));
+  p = fma2(p, z, both(kLog1));
+  p = fma2(p, z, both(kLog0));
+  return mul2(p, t);
 }
 
 // a = (1 - beta) alpha and b = beta v of two channels; nA = -A.
@@ -255,9 +245,7 @@ __device__ __forceinline__ uint4 load_pairs(const float* p) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ bool unset(uint4 v) {
-  return v.x == kUnset || v.y == kUnset || v.z == kUnset || v.w == kUnset;
-}
+__device__ __forceinline__ unsigned largest(uint4 v) { return max(max(v.x, v.y), max(v.z, v.w)); }
 __device__ __forceinline__ unsigned word(float x) { return x != x ? 0x7fffffffu : __float_as_uint(x); }
 // The pairs of two channels.
 __device__ __forceinline__ void publish(float* p, float2 P, float2 S) {
@@ -270,13 +258,41 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
+// Test of an mbarrier phase that lets the thread sleep until it completes, for
+// about ten microseconds at most (a warp that spins takes issue slots from the
+// arithmetic).
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// A position in a ring of N barriers and its phase.
+template <int N>
+struct Ring {
+  int at = 0;
+  unsigned phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // Wait for an mbarrier phase (a whole warp calls it); false once the limit has
 // passed or another warp of the block has given up (which the first to do so
 // marks).
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, volatile int* gave_up) {
-  bool there = mbar_test_wait(bar, parity);
+  bool there = mbar_sleep_wait(bar, parity);
   for (uint64_t t0 = 0; !there;) {
-    for (int i = 0; i < 32 && !there; ++i) there = mbar_try_wait(bar, parity);
+    there = mbar_sleep_wait(bar, parity);
     if (there) break;
     const uint64_t now = global_ns();
     if (t0 == 0) t0 = now;
@@ -423,22 +439,30 @@ __device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int 
                                             float2& h) {
   const int lane = threadIdx.x & 31, c = t.col0 + lane * 2;
   const int n = chunk % kGroup + (chunk >= kGroup ? 1 : 0);
+  const bool in = c < D;
   const size_t step = (size_t)t.back * D * 2;
-  const float* from = ch.pairs + ((size_t)t.number * D + c) * 2;
+  const float* near = ch.pairs + ((size_t)t.number * D + c) * 2 - step;   // the chunk before
+  const float* from = near - (size_t)(n - 1) * step;                      // the furthest
   h = make_float2(0.f, 0.f);
   constexpr int kBatch = kGroup / 2;
   uint64_t t0 = 0;
-  for (int k0 = 0; k0 < n; k0 += kBatch) {
+  for (int k0 = 0; k0 < n; k0 += kBatch, from += kBatch * step) {
     uint4 q[kBatch];
     for (int spin = 0;; ++spin) {
-      bool missing = false;
+      // Mostly the nearest is the last to arrive: look for it alone first.
+      unsigned most = in ? largest(load_pairs(near)) : 0u;
+      if (__all_sync(0xffffffffu, most != kUnset)) {
+        const float* f = from;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (k0 + k < n && c < D) {
-          q[k] = load_pairs(from - (n - k0 - k) * step);
-          missing |= unset(q[k]);
+        for (int k = 0; k < kBatch; ++k, f += step) {
+          q[k] = make_uint4(0x3f800000u, 0u, 0x3f800000u, 0u);            // changes nothing
+          if (k0 + k < n && in) q[k] = load_pairs(f);
         }
-      if (!__any_sync(0xffffffffu, missing)) break;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) most = max(most, largest(q[k]));
+        if (__all_sync(0xffffffffu, most != kUnset)) break;
+      }
+      __nanosleep(100);
       if ((spin & 63) == 63) {
         const uint64_t now = global_ns();
         if (t0 == 0) t0 = now;
@@ -448,9 +472,8 @@ __device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int 
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
-      if (k0 + k < n && c < D)
-        h = fma2(make_float2(__uint_as_float(q[k].x), __uint_as_float(q[k].z)), h,
-                 make_float2(__uint_as_float(q[k].y), __uint_as_float(q[k].w)));
+      h = fma2(make_float2(__uint_as_float(q[k].x), __uint_as_float(q[k].z)), h,
+               make_float2(__uint_as_float(q[k].y), __uint_as_float(q[k].w)));
   }
   return true;
 }
@@ -654,11 +677,13 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   } else {                                 // gates and outputs
     const int c4 = (lane & 15) * 4, first = (tid >> 4) * R;   // first row in the tile
     const uint32_t park = tmem_base + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * Sh::kParkCols;
+    const uint32_t from = (uint32_t)((first * kCols + c4) * sizeof(T));
+    Ring<kUnits> unit;
     int end = 0x7fffffff;                  // number of this block's tiles, once known
     for (int it = 0; it - 1 < end; ++it) {
       if (it < end) {
-        const int slot = it % kSlots, u = it * 3;
-        if (!wait_phase(&full[u % kUnits], (u / kUnits) & 1, gave_up)) break;
+        const int slot = it & 1;
+        if (!wait_phase(&full[unit.at], unit.phase, gave_up)) break;
         const Tile t = tiles[it % kInfo];
         if (t.rows == 0) {
           end = it;
@@ -671,15 +696,21 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
             nA[1] = mul2(nA[1], both(-1.f));
           }
           if (c < P.D && P.bias) load_row(P.bias + c, bias[0], bias[1]);
-          if (!wait_phase(&full[(u + 1) % kUnits], ((u + 1) / kUnits) & 1, gave_up)) break;
-          if (!wait_phase(&full[(u + 2) % kUnits], ((u + 2) / kUnits) & 1, gave_up)) break;
-          const size_t from = (size_t)first * kCols + c4;
-          const T* bza = reinterpret_cast<const T*>(smem + (u % kUnits) * Sh::kUnitBytes) + from;
-          const T* bzb = reinterpret_cast<const T*>(smem + ((u + 1) % kUnits) * Sh::kUnitBytes) + from;
-          const T* bv = reinterpret_cast<const T*>(smem + ((u + 2) % kUnits) * Sh::kUnitBytes) + from;
+          int at[3];
+          at[0] = unit.at;
+          unit.next();
+          at[1] = unit.at;
+          if (!wait_phase(&full[unit.at], unit.phase, gave_up)) break;
+          unit.next();
+          at[2] = unit.at;
+          if (!wait_phase(&full[unit.at], unit.phase, gave_up)) break;
+          unit.next();
+          const T* bza = reinterpret_cast<const T*>(smem + at[0] * Sh::kUnitBytes + from);
+          const T* bzb = reinterpret_cast<const T*>(smem + at[1] * Sh::kUnitBytes + from);
+          const T* bv = reinterpret_cast<const T*>(smem + at[2] * Sh::kUnitBytes + from);
           // Four rows at a time: gates, the pair of all rows so far, aside.
-          float2 p[2], s[2];
-#pragma unroll
+          float2 p[2] = {both(1.f), both(1.f)}, s[2] = {both(0.f), both(0.f)};
+#pragma unroll 1
           for (int r4 = 0; r4 < R; r4 += 4) {
             float2 a[8], b[8];
 #pragma unroll
@@ -703,20 +734,15 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
             for (int r = 0; r < 4; ++r) {
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                if (r4 + r == 0) {
-                  p[k] = a[k];
-                  s[k] = b[k];
-                } else {
-                  s[k] = fma2(a[2 * r + k], s[k], b[2 * r + k]);
-                  p[k] = mul2(a[2 * r + k], p[k]);
-                }
+                s[k] = fma2(a[2 * r + k], s[k], b[2 * r + k]);
+                p[k] = mul2(a[2 * r + k], p[k]);
               }
             }
             park16(park + slot * Sh::kSlotCols + r4 * 8, a);
             park16(park + slot * Sh::kSlotCols + r4 * 8 + 16, b);
           }
           __syncwarp();
-          if (lane < 3) mbar_arrive(&empty[(u + lane) % kUnits]);
+          if (lane < 3) mbar_arrive(&empty[lane == 0 ? at[0] : lane == 1 ? at[1] : at[2]]);
           // The warp's pair (the lower half-warp's rows come first).
           float2 pl[2], sl[2];
 #pragma unroll
@@ -724,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
             pl[k] = shfl_xor2(p[k], 16);
             sl[k] = shfl_xor2(s[k], 16);
           }
-          if (it >= kSlots && !wait_phase(&taken[slot], (it / kSlots - 1) & 1, gave_up)) break;
+          if (it >= kSlots && !wait_phase(&taken[slot], ((it >> 1) - 1) & 1, gave_up)) break;
           if (lane >= 16) {
             store_row(&total[slot][warp][0][c4], mul2(p[0], pl[0]), mul2(p[1], pl[1]));
             store_row(&total[slot][warp][1][c4], fma2(p[0], sl[0], s[0]), fma2(p[1], sl[1], s[1]));
@@ -739,11 +765,11 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       }
       const int out = it - 1;              // the tile to finish
       if (out < 0) continue;
-      const int slot = out % kSlots;
+      const int slot = out & 1;
       const Tile t = tiles[out % kInfo];
       const int c = t.col0 + c4;
-      if (!wait_phase(&paired[slot], (out / kSlots) & 1, gave_up)) break;
-      if (!wait_phase(&folded[slot], (out / kSlots) & 1, gave_up)) break;
+      if (!wait_phase(&paired[slot], (out >> 1) & 1, gave_up)) break;
+      if (!wait_phase(&folded[slot], (out >> 1) & 1, gave_up)) break;
       float2 h[2];
       load_row(&carry[slot][c4], h[0], h[1]);
       for (int w = 0; w < warp; ++w) {
@@ -769,7 +795,8 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
         store_row(P.states + n * P.D + c, h[0], h[1]);
       }
       T* y = reinterpret_cast<T*>(P.y) + (size_t)(t.row0 + first) * P.D + c;
-#pragma unroll
+      int left = c < P.D ? t.rows - first : 0;                 // rows to store
+#pragma unroll 1
       for (int r4 = 0; r4 < R; r4 += 4) {
         float2 a[8], b[8];
         unpark16(park + slot * Sh::kSlotCols + r4 * 8, a);
@@ -778,9 +805,10 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
         for (int r = 0; r < 4; ++r) {
           h[0] = fma2(a[2 * r], h[0], b[2 * r]);
           h[1] = fma2(a[2 * r + 1], h[1], b[2 * r + 1]);
-          if (c < P.D && first + r4 + r < t.rows) store_row(y, h[0], h[1]);
-          y += P.D;
+          if (r < left) store_row(y + (size_t)r * P.D, h[0], h[1]);
         }
+        left -= 4;
+        y += (size_t)4 * P.D;
       }
       if (P.hT && t.last && first < t.rows && t.rows <= first + R && c < P.D)
         store_row(P.hT + (size_t)t.seq * P.D + c, h[0], h[1]);

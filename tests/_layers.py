@@ -3,11 +3,11 @@ the largest error a float32 implementation of the same formulas can make.
 
 U is float32's half step.  The relative errors of one gate, from the error
 bounds of the operations it is made of (2^x instruction 4 U, reciprocal 2 U,
-each float32 operation U, the logarithm polynomial 2.2 U), are
+each float32 operation U, the logarithm 6.5 U), are
   e = exp(-|x|):              3 U |x| + 4 U
   sigmoid(x), sigmoid(-x):    (6 |x| + 12) U
-  softplus(x):                (3 |x| + 10) U
-  alpha = exp(-l), l = A sp:  (l (3 |x| + 14) + 4) U
+  softplus(x):                (3 |x| + 13) U
+  alpha = exp(-l), l = A sp:  (l (3 |x| + 17) + 4) U
 and they enter a sum of products through its majorant, the same recurrence on
 absolute values (H for the states, G for their gradients): every term of h[t]
 is a product with one more factor a per step, whatever the order in which the
@@ -45,8 +45,8 @@ def recurrence(za, zb, v, A, bias, off, h0=None, dy=None, dhT=None):
     alpha, beta, keep, sig = torch.exp(-lam), torch.sigmoid(zb), torch.sigmoid(-zb), torch.sigmoid(x)
     far = lambda t: torch.nan_to_num(t.abs(), posinf=200.0).clamp(max=200.0)   # exp(-200) is 0 in float32
     e_s = (6 * far(zb) + 12) * U
-    e_sp = (3 * far(x) + 10) * U
-    e_alpha = (lam.clamp(max=200.0) * (3 * far(x) + 14) + 4) * U
+    e_sp = (3 * far(x) + 13) * U
+    e_alpha = (lam.clamp(max=200.0) * (3 * far(x) + 17) + 4) * U
     e_a, e_b, e_sig = e_s + e_alpha + U, e_s + U, (6 * far(x) + 12) * U
     a, b = keep * alpha, beta * v
     nan = lambda *s: torch.full(s, float("nan"), dtype=torch.float64)

@@ -126,30 +126,46 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// The packed forms take no immediates.  Their constants are made once, out of
+// the compiler's sight: it would otherwise move them into registers again
+// before every use (about seven of 42 instructions per element).
+struct Constants {
+  float2 log2e, one, two, k0, k1, k2, k3, k4;
+};
+__device__ __forceinline__ float2 hidden(float x) {
+  uint64_t r;
+  asm volatile("mov.b64 %0, {%1, %1};\n" : "=l"(r) : "f"(x));
+  return float2_of(r);
+}
+__device__ __forceinline__ Constants constants() {
+  return Constants{hidden(kLog2e), hidden(1.f),   hidden(2.f),   hidden(kLog0),
+                   hidden(kLog1),  hidden(kLog2), hidden(kLog3), hidden(kLog4)};
+}
+
 // log2p1_unit, two at a time.
-__device__ __forceinline__ float2 log2p1_unit(float2 e) {
-  const float2 d = add2(e, both(2.f));
+__device__ __forceinline__ float2 log2p1_unit(const Constants& K, float2 e) {
+  const float2 d = add2(e, K.two);
   const float2 t = mul2(e, make_float2(rcp(d.x), rcp(d.y))), z = mul2(t, t);
-  float2 p = fma2(both(kLog4), z, both(kLog3));
-  p = fma2(p, z, both(kLog2));
-  p = fma2(p, z, both(kLog1));
-  p = fma2(p, z, both(kLog0));
+  float2 p = fma2(K.k4, z, K.k3);
+  p = fma2(p, z, K.k2);
+  p = fma2(p, z, K.k1);
+  p = fma2(p, z, K.k0);
   return mul2(p, t);
 }
 
 // a = (1 - beta) alpha and b = beta v of two channels; nA = -A.
-__device__ __forceinline__ void gate_pair(float2 za, float2 zb, float2 v, float2 nA, float2 bias,
-                                          float2& a, float2& b) {
-  const float2 x = mul2(add2(za, bias), both(kLog2e));
+__device__ __forceinline__ void gate_pair(const Constants& K, float2 za, float2 zb, float2 v,
+                                          float2 nA, float2 bias, float2& a, float2& b) {
+  const float2 x = mul2(add2(za, bias), K.log2e);
   const float2 e = make_float2(ex2(-fabsf(x.x)), ex2(-fabsf(x.y)));
-  const float2 sp = add2(make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)), log2p1_unit(e));
+  const float2 sp = add2(make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)), log2p1_unit(K, e));
   const float2 l = mul2(nA, sp);
   // sigmoid(z) = 1 / (1 + 2^-z'), 1 - sigmoid = 2^-z' / (1 + 2^-z'); z' held
   // above -126 so that 2^-z' stays finite.
-  float2 z = mul2(zb, both(kLog2e));
+  float2 z = mul2(zb, K.log2e);
   z = make_float2(max_nan(z.x, -126.f), max_nan(z.y, -126.f));
   const float2 eb = make_float2(ex2(-z.x), ex2(-z.y));
-  const float2 d = add2(eb, both(1.f));
+  const float2 d = add2(eb, K.one);
   const float2 beta = make_float2(rcp(d.x), rcp(d.y));
   a = mul2(mul2(eb, beta), make_float2(ex2(l.x), ex2(l.y)));
   b = mul2(beta, v);
@@ -290,18 +306,23 @@ struct Ring {
 // passed or another warp of the block has given up (which the first to do so
 // marks).
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, volatile int* gave_up) {
-  bool there = mbar_sleep_wait(bar, parity);
-  for (uint64_t t0 = 0; !there;) {
-    there = mbar_sleep_wait(bar, parity);
-    if (there) break;
+  for (uint64_t t0 = 0; !__all_sync(0xffffffffu, mbar_sleep_wait(bar, parity));) {
     const uint64_t now = global_ns();
     if (t0 == 0) t0 = now;
-    if (*gave_up || now - t0 > kWaitNs) {
+    if (__any_sync(0xffffffffu, *gave_up || now - t0 > kWaitNs)) {
       *gave_up = 1;
-      break;
+      return false;
     }
   }
-  return __all_sync(0xffffffffu, there);
+  return true;
+}
+// Arrive from one lane, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(bool p, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %0, 0;\n"
+      " @p mbarrier.arrive.shared::cta.b64 _, [%1];\n}\n" ::"r"((uint32_t)p),
+      "r"(smem_u32(bar))
+      : "memory");
 }
 // x: first channel (a multiple of 64, so 16-byte aligned), y: first row; what
 // lies outside the tensor arrives as zeros.
@@ -350,6 +371,23 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, float2 lo, float2 hi
   const __nv_bfloat162 a = __float22bfloat162_rn(lo), b = __float22bfloat162_rn(hi);
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
                                             *reinterpret_cast<const uint32_t*>(&b));
+}
+// The same to global memory where `p` holds, without a branch.
+__device__ __forceinline__ void store_row_if(bool p, float* at, float2 lo, float2 hi) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %0, 0;\n"
+      " @p st.global.v4.f32 [%1], {%2, %3, %4, %5};\n}\n" ::"r"((uint32_t)p),
+      "l"(at), "f"(lo.x), "f"(lo.y), "f"(hi.x), "f"(hi.y)
+      : "memory");
+}
+__device__ __forceinline__ void store_row_if(bool p, __nv_bfloat16* at, float2 lo, float2 hi) {
+  const __nv_bfloat162 a = __float22bfloat162_rn(lo), b = __float22bfloat162_rn(hi);
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %0, 0;\n"
+      " @p st.global.v2.b32 [%1], {%2, %3};\n}\n" ::"r"((uint32_t)p),
+      "l"(at), "r"(*reinterpret_cast<const uint32_t*>(&a)),
+      "r"(*reinterpret_cast<const uint32_t*>(&b))
+      : "memory");
 }
 __device__ __forceinline__ float2 shfl_xor2(float2 a, int m) {
   return make_float2(__shfl_xor_sync(0xffffffffu, a.x, m), __shfl_xor_sync(0xffffffffu, a.y, m));
@@ -512,7 +550,8 @@ __device__ __forceinline__ void unpark16(uint32_t taddr, float2 (&v)[8]) {
 // Inputs come in units of one tensor's tile (16 KB), in a ring of kUnits.
 // Barriers, all in shared memory: a tile's description is there (known), a
 // unit is (full) and has been read (empty); a tile's warps' pairs are there
-// (paired), the state in front of it is (folded), both have been read (taken).
+// (paired) and have been summed up (summed), the state in front of it is
+// (folded), both have been read (taken).
 constexpr int kWarps = 8;
 constexpr int kUnits = 5;
 constexpr int kSlots = 2;    // tiles between gates and outputs
@@ -531,17 +570,21 @@ struct ForwardShape {
   static_assert(kStateRows % R == 0, "states fall on a thread's first row");
 };
 
-// The pair of a whole tile from its warps' (two channels per lane).
-__device__ __forceinline__ void tile_pair(const float (*total)[2][kCols], int lane, float2& P,
-                                          float2& S) {
+// The pairs of a tile's warps become those of all rows in front of each warp;
+// returns the whole tile's (two channels per lane).
+__device__ __forceinline__ void running_pairs(float (*total)[2][kCols], int lane, float2& P,
+                                              float2& S) {
   P = both(1.f);
   S = both(0.f);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const float2 wp = *reinterpret_cast<const float2*>(&total[w][0][lane * 2]);
-    const float2 ws = *reinterpret_cast<const float2*>(&total[w][1][lane * 2]);
-    S = fma2(wp, S, ws);
-    P = mul2(wp, P);
+    float2* const wp = reinterpret_cast<float2*>(&total[w][0][lane * 2]);
+    float2* const ws = reinterpret_cast<float2*>(&total[w][1][lane * 2]);
+    const float2 p = *wp, s = *ws;
+    *wp = P;
+    *ws = S;
+    S = fma2(p, S, s);
+    P = mul2(p, P);
   }
 }
 
@@ -551,11 +594,13 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   constexpr int L = Sh::L, R = Sh::R, W = kWarps;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((128 - (smem_u32(raw) & 127)) & 127);
-  __shared__ uint64_t full[kUnits], empty[kUnits], known[kInfo], paired[kSlots], folded[kSlots],
-      taken[kSlots];
+  __shared__ uint64_t full[kUnits], empty[kUnits], known[kInfo], paired[kSlots], summed[kSlots],
+      folded[kSlots], taken[kSlots];
   __shared__ Tile tiles[kInfo];
-  __shared__ __align__(16) float total[kSlots][W][2][kCols];   // (P, S) of each warp's rows
+  __shared__ __align__(16) float total[kSlots][W][2][kCols];   // (P, S) of each warp's rows,
+                                                               // then of all rows in front of it
   __shared__ __align__(16) float lower[kSlots][W][2][kCols];   // and of its lower half-warp's
+  __shared__ __align__(16) float whole[kSlots][2][kCols];      // the tile's
   __shared__ __align__(16) float carry[kSlots][kCols];         // the state in front of the tile
   __shared__ uint32_t tmem_base;
   __shared__ int quit;
@@ -575,8 +620,9 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
     for (int s = 0; s < kInfo; ++s) mbar_init(&known[s], 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&paired[s], W);
+      mbar_init(&summed[s], 1);
       mbar_init(&folded[s], 1);
-      mbar_init(&taken[s], W + 1);
+      mbar_init(&taken[s], W);
     }
     quit = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -635,13 +681,18 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       if (t.rows == 0) break;
       if (!wait_phase(&paired[slot], (it / kSlots) & 1, gave_up)) break;
       const int c = t.col0 + lane * 2;
-      if (!t.last && !publishes_state(t.chunk)) {
-        float2 p, s;
-        tile_pair(total[slot], lane, p, s);
-        if (c < P.D) publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, p, s);
+      float2 p, s;
+      running_pairs(total[slot], lane, p, s);
+      if (!t.last) {
+        if (publishes_state(t.chunk)) {    // left to the fold
+          *reinterpret_cast<float2*>(&whole[slot][0][lane * 2]) = p;
+          *reinterpret_cast<float2*>(&whole[slot][1][lane * 2]) = s;
+        } else if (c < P.D) {
+          publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, p, s);
+        }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&taken[slot]);
+      mbar_arrive_if(lane == 0, &summed[slot]);
     }
   } else if (warp > W + 1) {               // folds
     for (int it = warp - (W + 2);; it += 2) {
@@ -665,19 +716,20 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       if (it >= kSlots && !wait_phase(&taken[slot], (it / kSlots - 1) & 1, gave_up)) break;
       *reinterpret_cast<float2*>(&carry[slot][lane * 2]) = h;
       if (!t.last && publishes_state(t.chunk)) {
-        if (!wait_phase(&paired[slot], (it / kSlots) & 1, gave_up)) break;
-        float2 p, s;
-        tile_pair(total[slot], lane, p, s);
+        if (!wait_phase(&summed[slot], (it / kSlots) & 1, gave_up)) break;
+        const float2 p = *reinterpret_cast<const float2*>(&whole[slot][0][lane * 2]);
+        const float2 s = *reinterpret_cast<const float2*>(&whole[slot][1][lane * 2]);
         if (c < P.D)
           publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, both(0.f), fma2(p, h, s));
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&folded[slot]);
+      mbar_arrive_if(lane == 0, &folded[slot]);
     }
   } else {                                 // gates and outputs
     const int c4 = (lane & 15) * 4, first = (tid >> 4) * R;   // first row in the tile
     const uint32_t park = tmem_base + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * Sh::kParkCols;
     const uint32_t from = (uint32_t)((first * kCols + c4) * sizeof(T));
+    const Constants K = constants();
     Ring<kUnits> unit;
     int end = 0x7fffffff;                  // number of this block's tiles, once known
     for (int it = 0; it - 1 < end; ++it) {
@@ -719,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
               load_row(bza + (r4 + r) * kCols, za[0], za[1]);
               load_row(bzb + (r4 + r) * kCols, zb[0], zb[1]);
               load_row(bv + (r4 + r) * kCols, v[0], v[1]);
-              gate_pair(za[0], zb[0], v[0], nA[0], bias[0], a[2 * r], b[2 * r]);
-              gate_pair(za[1], zb[1], v[1], nA[1], bias[1], a[2 * r + 1], b[2 * r + 1]);
+              gate_pair(K, za[0], zb[0], v[0], nA[0], bias[0], a[2 * r], b[2 * r]);
+              gate_pair(K, za[1], zb[1], v[1], nA[1], bias[1], a[2 * r + 1], b[2 * r + 1]);
             }
             if (t.rows < L) {              // rows behind the sequence change nothing
 #pragma unroll
@@ -742,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
             park16(park + slot * Sh::kSlotCols + r4 * 8 + 16, b);
           }
           __syncwarp();
-          if (lane < 3) mbar_arrive(&empty[lane == 0 ? at[0] : lane == 1 ? at[1] : at[2]]);
+          mbar_arrive_if(lane < 3, &empty[lane == 0 ? at[0] : lane == 1 ? at[1] : at[2]]);
           // The warp's pair (the lower half-warp's rows come first).
           float2 pl[2], sl[2];
 #pragma unroll
@@ -760,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
           }
           parked();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&paired[slot]);
+          mbar_arrive_if(lane == 0, &paired[slot]);
         }
       }
       const int out = it - 1;              // the tile to finish
@@ -768,26 +820,23 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       const int slot = out & 1;
       const Tile t = tiles[out % kInfo];
       const int c = t.col0 + c4;
-      if (!wait_phase(&paired[slot], (out >> 1) & 1, gave_up)) break;
+      if (!wait_phase(&summed[slot], (out >> 1) & 1, gave_up)) break;
       if (!wait_phase(&folded[slot], (out >> 1) & 1, gave_up)) break;
       float2 h[2];
       load_row(&carry[slot][c4], h[0], h[1]);
-      for (int w = 0; w < warp; ++w) {
-        float2 wp[2], ws[2];
-        load_row(&total[slot][w][0][c4], wp[0], wp[1]);
-        load_row(&total[slot][w][1][c4], ws[0], ws[1]);
-        h[0] = fma2(wp[0], h[0], ws[0]);
-        h[1] = fma2(wp[1], h[1], ws[1]);
-      }
+      float2 wp[2], ws[2];
+      load_row(&total[slot][warp][0][c4], wp[0], wp[1]);
+      load_row(&total[slot][warp][1][c4], ws[0], ws[1]);
+      h[0] = fma2(wp[0], h[0], ws[0]);
+      h[1] = fma2(wp[1], h[1], ws[1]);
       if (lane >= 16) {
-        float2 wp[2], ws[2];
         load_row(&lower[slot][warp][0][c4], wp[0], wp[1]);
         load_row(&lower[slot][warp][1][c4], ws[0], ws[1]);
         h[0] = fma2(wp[0], h[0], ws[0]);
         h[1] = fma2(wp[1], h[1], ws[1]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&taken[slot]);
+      mbar_arrive_if(lane == 0, &taken[slot]);
       const int row = t.chunk * L + first;                     // in the sequence
       if (P.states && row % kStateRows == 0 && first < t.rows && c < P.D) {
         const int begin = t.row0 - t.chunk * L;
@@ -805,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
         for (int r = 0; r < 4; ++r) {
           h[0] = fma2(a[2 * r], h[0], b[2 * r]);
           h[1] = fma2(a[2 * r + 1], h[1], b[2 * r + 1]);
-          if (r < left) store_row(y + (size_t)r * P.D, h[0], h[1]);
+          store_row_if(r < left, y + (size_t)r * P.D, h[0], h[1]);
         }
         left -= 4;
         y += (size_t)4 * P.D;

@@ -201,25 +201,10 @@ __device__ bool offsets_ok(const Packed& P) {
   return !__syncthreads_or(bad);
 }
 
-constexpr int kStateRows = 64;   // rows between saved states
+// Rows between saved states = rows of a backward tile.
+template <typename T>
+constexpr int kStateRows = 128 / (int)sizeof(T);
 
-struct Args {
-  RecurrenceDims d;
-  RecurrenceInputs in;
-  Packed packed;
-  const float* h0;
-  void* y;
-  float* hT;
-  float* states;
-  const void* dy;
-  const float* dhT;
-  void* dza;
-  void* dzb;
-  void* dv;
-  float* dh0;
-  float* partial;
-  unsigned* status;
-};
 
 // --------------------------------------------------------------------- scan
 // What a block has to know of a tile, found out by the warp that fetches it.
@@ -228,9 +213,10 @@ struct __align__(16) Tile {
   int row0;      // first row
   int seq, chunk;
   int number;    // of the chunk, indexes flags and data
-  int back;      // number - back is the chunk before (after, in the backward pass)
+  int back;      // number - back is the chunk before along the chain
   int col0;      // first channel
-  int last;      // the sequence's last chunk
+  int pos;       // along the chain: chunks before it (after it, in the backward pass)
+  int last;      // the chain's last chunk
 };
 
 // Workspace of one call: a header (ticket counter, abort word), cleared to
@@ -411,10 +397,11 @@ struct ForwardArgs {
 // The next tile that has rows (a whole warp calls it): takes tickets until one
 // does; false when there is none left.  `ticket` (lane 0) was taken earlier and
 // is replaced by a new one, so that its latency lies behind other work.
-template <int L, class Empty>
+// `skip` is called for a number without rows: of a sequence without any (its
+// chunk 0), or of no chunk at all (seq < 0).
+template <int L, bool kReverse, class Skip>
 __device__ __forceinline__ bool fetch(const Packed& packed, const Chain& chain, unsigned tiles,
-                                      int col_tiles, bool reverse, unsigned& ticket, Tile& t,
-                                      Empty empty) {
+                                      int col_tiles, unsigned& ticket, Tile& t, Skip skip) {
   const int lane = threadIdx.x & 31;
   while (true) {
     const unsigned k = __shfl_sync(0xffffffffu, ticket, 0);
@@ -423,35 +410,44 @@ __device__ __forceinline__ bool fetch(const Packed& packed, const Chain& chain, 
       return false;
     }
     if (lane == 0) ticket = atomicAdd(chain.ticket, 1u);
-    const unsigned q = reverse ? tiles - 1 - k : k;
-    const int number = (int)(q / (unsigned)col_tiles);
-    t.col0 = (int)(q % (unsigned)col_tiles) * kCols;
-    int o, len;
+    const unsigned q = kReverse ? tiles - 1 - k : k;
+    t.number = (int)(q / (unsigned)col_tiles);
+    t.col0 = (int)(q - (unsigned)t.number * (unsigned)col_tiles) * kCols;
+    int o = 0, len = 0;
+    t.chunk = 0;
     if (packed.offsets) {
-      t.seq = sequence_of<L>(packed, number);
-      if (t.seq < 0) continue;
-      o = packed.begin(t.seq);
-      len = packed.begin(t.seq + 1) - o;
-      t.chunk = number - (o / L + t.seq);
+      t.seq = sequence_of<L>(packed, t.number);
+      if (t.seq >= 0) {
+        o = packed.begin(t.seq);
+        len = packed.begin(t.seq + 1) - o;
+        t.chunk = t.number - (o / L + t.seq);
+      }
       t.back = 1;
     } else {
       // Equal lengths: chunk c of every sequence before chunk c + 1 of any, so
       // that a chunk's predecessor is as far back as can be.
-      t.chunk = number / packed.n_seq;
-      t.seq = number % packed.n_seq;
-      o = packed.begin(t.seq);
+      t.chunk = t.number / packed.n_seq;
+      t.seq = t.number - t.chunk * packed.n_seq;
       len = packed.rows / packed.n_seq;
+      o = len * t.seq;
       t.back = packed.n_seq;
     }
-    t.number = number;
     t.row0 = o + t.chunk * L;
     t.rows = len - t.chunk * L;
-    t.last = t.rows <= L;
-    if (t.rows > L) t.rows = L;
     if (t.rows <= 0) {
-      if (t.chunk == 0) empty(t);
+      if (t.chunk > 0) t.seq = -1;
+      skip(t);
       continue;
     }
+    if (kReverse) {
+      t.pos = (t.rows - 1) / L;
+      t.last = t.chunk == 0;
+      t.back = -t.back;
+    } else {
+      t.pos = t.chunk;
+      t.last = t.rows <= L;
+    }
+    if (t.rows > L) t.rows = L;
     return true;
   }
 }
@@ -460,8 +456,8 @@ __device__ __forceinline__ bool fetch(const Packed& packed, const Chain& chain, 
 // the fold, not its pair: the last of a group, and a sequence's first.  The
 // first's would be known at once, but this way its block's read of h0 has
 // happened when the chunks behind go on, and the last may overwrite h0 (hT = h0).
-__device__ __forceinline__ bool publishes_state(int chunk) {
-  return chunk % kGroup == kGroup - 1 || chunk == 0;
+__device__ __forceinline__ bool publishes_state(int pos) {
+  return pos % kGroup == kGroup - 1 || pos == 0;
 }
 
 // The state in front of a tile from what the chunks before it published (a
@@ -473,14 +469,13 @@ __device__ __forceinline__ bool publishes_state(int chunk) {
 // folded in the same order: results do not depend on timing, and the serial
 // chain through the grid has one link per kGroup chunks, not one per chunk.
 // Returns false if the wait ran out or another block gave up.
-__device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int chunk, int D,
-                                            float2& h) {
+__device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int D, float2& h) {
   const int lane = threadIdx.x & 31, c = t.col0 + lane * 2;
-  const int n = chunk % kGroup + (chunk >= kGroup ? 1 : 0);
+  const int n = t.pos % kGroup + (t.pos >= kGroup ? 1 : 0);
   const bool in = c < D;
-  const size_t step = (size_t)t.back * D * 2;
+  const ptrdiff_t step = (ptrdiff_t)t.back * D * 2;
   const float* near = ch.pairs + ((size_t)t.number * D + c) * 2 - step;   // the chunk before
-  const float* from = near - (size_t)(n - 1) * step;                      // the furthest
+  const float* from = near - (n - 1) * step;                      // the furthest
   h = make_float2(0.f, 0.f);
   constexpr int kBatch = kGroup / 2;
   uint64_t t0 = 0;
@@ -567,7 +562,7 @@ struct ForwardShape {
   static constexpr int kParkCols = 8 * R;                               // per thread and tile
   static constexpr int kSlotCols = kWarps / 4 * kParkCols;
   static constexpr int kTmemCols = kSlots * kSlotCols;                  // a power of two
-  static_assert(kStateRows % R == 0, "states fall on a thread's first row");
+  static_assert(kStateRows<T> % R == 0, "states fall on a thread's first row");
 };
 
 // The pairs of a tile's warps become those of all rows in front of each warp;
@@ -638,10 +633,10 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
     bool more = true;
     for (int n = 0; more; ++n) {
       Tile t;
-      more = fetch<L>(P.packed, P.chain, P.tiles, P.col_tiles, false, ticket, t,
+      more = fetch<L, false>(P.packed, P.chain, P.tiles, P.col_tiles, ticket, t,
                       [&](const Tile& e) {               // a sequence without rows
                         const int c = e.col0 + lane * 2;
-                        if (P.hT && c < P.D) {
+                        if (P.hT && e.seq >= 0 && c < P.D) {
                           const size_t i = (size_t)e.seq * P.D + c;
                           *reinterpret_cast<float2*>(P.hT + i) =
                               P.h0 ? *reinterpret_cast<const float2*>(P.h0 + i)
@@ -684,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       float2 p, s;
       running_pairs(total[slot], lane, p, s);
       if (!t.last) {
-        if (publishes_state(t.chunk)) {    // left to the fold
+        if (publishes_state(t.pos)) {      // left to the fold
           *reinterpret_cast<float2*>(&whole[slot][0][lane * 2]) = p;
           *reinterpret_cast<float2*>(&whole[slot][1][lane * 2]) = s;
         } else if (c < P.D) {
@@ -709,13 +704,13 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       float2 h = make_float2(0.f, 0.f);
       if (t.chunk == 0) {
         if (P.h0 && c < P.D) h = *reinterpret_cast<const float2*>(P.h0 + (size_t)t.seq * P.D + c);
-      } else if (!fold_before(P.chain, t, t.chunk, P.D, h)) {
+      } else if (!fold_before(P.chain, t, P.D, h)) {
         *gave_up = 1;
         break;
       }
       if (it >= kSlots && !wait_phase(&taken[slot], (it / kSlots - 1) & 1, gave_up)) break;
       *reinterpret_cast<float2*>(&carry[slot][lane * 2]) = h;
-      if (!t.last && publishes_state(t.chunk)) {
+      if (!t.last && publishes_state(t.pos)) {
         if (!wait_phase(&summed[slot], (it / kSlots) & 1, gave_up)) break;
         const float2 p = *reinterpret_cast<const float2*>(&whole[slot][0][lane * 2]);
         const float2 s = *reinterpret_cast<const float2*>(&whole[slot][1][lane * 2]);
@@ -838,9 +833,9 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       __syncwarp();
       mbar_arrive_if(lane == 0, &taken[slot]);
       const int row = t.chunk * L + first;                     // in the sequence
-      if (P.states && row % kStateRows == 0 && first < t.rows && c < P.D) {
+      if (P.states && row % kStateRows<T> == 0 && first < t.rows && c < P.D) {
         const int begin = t.row0 - t.chunk * L;
-        const size_t n = (size_t)(begin / kStateRows + t.seq + row / kStateRows);
+        const size_t n = (size_t)(begin / kStateRows<T> + t.seq + row / kStateRows<T>);
         store_row(P.states + n * P.D + c, h[0], h[1]);
       }
       T* y = reinterpret_cast<T*>(P.y) + (size_t)(t.row0 + first) * P.D + c;
@@ -871,61 +866,449 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   }
 }
 
-// As above from the last chunk to the first: the states before the chunk's
-// rows again from the saved one, then the gradients.
-__global__ void __launch_bounds__(32) backward_kernel(const Args P) {
-  __shared__ float hs[kStateRows][32];
-  if (!offsets_ok(P.packed)) {
-    if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
-    return;
-  }
-  const int c = blockIdx.x * 32 + threadIdx.x, s = blockIdx.y, D = P.d.D, dt = P.d.dtype;
-  if (c >= D) return;
-  const float A = P.in.A ? P.in.A[c] : 1.f, bias = P.in.bias ? P.in.bias[c] : 0.f;
-  const int t0 = P.packed.begin(s), t1 = P.packed.begin(s + 1);
-  float r = P.dhT ? P.dhT[(size_t)s * D + c] : 0.f, dA = 0.f, db = 0.f;
-  for (int k = (t1 - t0 + kStateRows - 1) / kStateRows - 1; k >= 0; --k) {
-    const int b = t0 + k * kStateRows, e = b + kStateRows < t1 ? b + kStateRows : t1;
-    float h = P.states[(size_t)(t0 / kStateRows + s + k) * D + c];
-    for (int t = b; t < e; ++t) {
-      hs[t - b][threadIdx.x] = h;
-      const size_t i = (size_t)t * P.d.ld + c;
-      const Gate g = make_gate(load_scalar(P.in.za, i, dt), load_scalar(P.in.zb, i, dt), A, bias);
-      h = fmaf(g.keep * g.alpha, h, g.beta * load_scalar(P.in.v, i, dt));
-    }
-    for (int t = e - 1; t >= b; --t) {
-      const size_t i = (size_t)t * P.d.ld + c, o = (size_t)t * P.d.ld_grad + c;
-      const Gate g = make_gate(load_scalar(P.in.za, i, dt), load_scalar(P.in.zb, i, dt), A, bias);
-      const float before = hs[t - b][threadIdx.x];
-      const float gr = load_scalar(P.dy, (size_t)t * D + c, dt) + r;
-      const float dlog = gr * g.keep * g.alpha * before;
-      const float dza = -A * g.sig * dlog;
-      r = g.keep * g.alpha * gr;
-      dA -= g.sp * dlog;
-      db += dza;
-      store_scalar(P.dza, o, dt, dza);
-      store_scalar(P.dzb, o, dt,
-                   gr * (load_scalar(P.in.v, i, dt) - g.alpha * before) * g.beta * g.keep);
-      store_scalar(P.dv, o, dt, g.beta * gr);
-    }
-  }
-  if (P.dh0) P.dh0[(size_t)s * D + c] = r;
-  P.partial[(size_t)s * 2 * D + c] = dA;
-  P.partial[(size_t)s * 2 * D + D + c] = db;
+// ----------------------------------------------------------------- backward
+// The gates of two channels again, all that the gradients need of them: a,
+// beta, 1 - beta, softplus (times log2 e) and sigmoid of za + bias.
+struct Gates2 {
+  float2 a, beta, keep, sp, sig;
+};
+__device__ __forceinline__ Gates2 gates_pair(const Constants& K, float2 za, float2 zb, float2 A,
+                                             float2 bias) {
+  Gates2 g;
+  const float2 x = mul2(add2(za, bias), K.log2e);
+  const float2 e = make_float2(ex2(-fabsf(x.x)), ex2(-fabsf(x.y)));
+  g.sp = add2(make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)), log2p1_unit(K, e));
+  const float2 f = add2(e, K.one);
+  g.sig = mul2(make_float2(x.x >= 0.f ? 1.f : e.x, x.y >= 0.f ? 1.f : e.y),
+               make_float2(rcp(f.x), rcp(f.y)));
+  const float2 l = mul2(A, g.sp);
+  float2 z = mul2(zb, K.log2e);
+  z = make_float2(max_nan(z.x, -126.f), max_nan(z.y, -126.f));
+  const float2 eb = make_float2(ex2(-z.x), ex2(-z.y));
+  const float2 d = add2(eb, K.one);
+  g.beta = make_float2(rcp(d.x), rcp(d.y));
+  g.keep = mul2(eb, g.beta);
+  g.a = mul2(g.keep, make_float2(ex2(-l.x), ex2(-l.y)));
+  return g;
 }
 
-__global__ void reduce_kernel(const Args P, float* dA, float* dbias) {
-  if (!offsets_ok(P.packed)) return;
-  const int c = blockIdx.x * blockDim.x + threadIdx.x, D = P.d.D;
-  if (c >= D) return;
-  float a = 0.f, b = 0.f;
-  for (int s = 0; s < P.d.n_seq; ++s) {
-    a += P.partial[(size_t)s * 2 * D + c];
-    b += P.partial[(size_t)s * 2 * D + D + c];
-  }
-  if (dA) dA[c] = a;
-  if (dbias) dbias[c] = b;
+// A row's a (four channels) in the place of its za and zb in shared memory,
+// which are as many bytes (twice as many for float32).
+__device__ __forceinline__ void keep_a(float* za, float*, float2 lo, float2 hi) { store_row(za, lo, hi); }
+__device__ __forceinline__ void take_a(const float* za, const float*, float2& lo, float2& hi) {
+  load_row(za, lo, hi);
 }
+__device__ __forceinline__ void keep_a(__nv_bfloat16* za, __nv_bfloat16* zb, float2 lo, float2 hi) {
+  *reinterpret_cast<float2*>(za) = lo;
+  *reinterpret_cast<float2*>(zb) = hi;
+}
+__device__ __forceinline__ void take_a(const __nv_bfloat16* za, const __nv_bfloat16* zb, float2& lo,
+                                       float2& hi) {
+  lo = *reinterpret_cast<const float2*>(za);
+  hi = *reinterpret_cast<const float2*>(zb);
+}
+// Four columns of tensor memory.
+__device__ __forceinline__ void unpark4(uint32_t taddr, float2& lo, float2& hi) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(lo.x), "=f"(lo.y), "=f"(hi.x), "=f"(hi.y)
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(lo.x), "+f"(lo.y), "+f"(hi.x), "+f"(hi.y)
+               :
+               : "memory");
+}
+
+struct BackwardArgs {
+  CUtensorMap za, zb, v, dy;
+  Packed packed;
+  const float* A;
+  const float* bias;
+  const float* states;
+  const float* dhT;
+  void* dza;
+  void* dzb;
+  void* dv;
+  float* dh0;
+  float* partial;     // [numbers][2][D]
+  Chain chain;
+  int D, col_tiles;
+  long long ld_grad;
+  unsigned tiles;
+  unsigned* status;
+};
+
+// The chain runs from the last chunk to the first; what it carries is r, the
+// gradient of the state in front of a chunk (r[t] = a[t] (dy[t] + r[t+1])), and
+// what a chunk publishes is the pair (P, Q) with r_front = P r_behind + Q.  The
+// states inside a tile come from the saved one in front of it without a wait.
+//
+// A block is four warps for the arithmetic (a half-warp takes R rows) and
+// three more: one fetches tiles, one sums up the half-warps' pairs and
+// publishes, one folds.  Of a tile's gates, a goes into shared memory and the
+// rest into tensor memory, so that three blocks fit an SM.
+constexpr int kBackWarps = 4;
+constexpr int kHalves = 2 * kBackWarps;
+constexpr int kBackStages = 2;
+constexpr int kBackInfo = 4;
+constexpr int kBackThreads = (kBackWarps + 3) * 32;
+constexpr int kBackBlocks = 3;
+
+template <typename T>
+struct BackwardShape {
+  static constexpr int R = 16 / sizeof(T);
+  static constexpr int L = kHalves * R;
+  static constexpr int kUnitBytes = L * kCols * (int)sizeof(T);
+  static constexpr int kStageBytes = 4 * kUnitBytes;
+  static constexpr int kSmem = kBackStages * kStageBytes + 128;
+  static constexpr int kTmemCols = 16 * R;
+  static_assert(L == kStateRows<T>, "a saved state in front of every tile");
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kBackThreads, kBackBlocks)
+    backward_kernel(const __grid_constant__ BackwardArgs P) {
+  using Sh = BackwardShape<T>;
+  constexpr int L = Sh::L, R = Sh::R, W = kBackWarps;
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + ((128 - (smem_u32(raw) & 127)) & 127);
+  __shared__ uint64_t full[kBackStages], empty[kBackStages], known[kBackInfo], paired, summed[2],
+      folded[2];
+  __shared__ Tile tiles[kBackInfo];
+  // Of each half-warp's rows P, S (of the states) and Q (of the gradients); then
+  // P of the rows behind them, the state in front of them, Q of the rows behind.
+  __shared__ __align__(16) float half[kHalves][3][kCols];
+  __shared__ __align__(16) float whole[2][kCols];
+  __shared__ __align__(16) float carry[2][kCols];
+  __shared__ __align__(16) float sums[W][2][kCols];            // of the gradients of A and bias
+  __shared__ uint32_t tmem_base;
+  __shared__ int quit;
+  volatile int* gave_up = &quit;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!offsets_ok(P.packed)) {
+    if (tid == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
+  if (tid == 0) {
+    for (int s = 0; s < kBackStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], W);
+    }
+    for (int s = 0; s < kBackInfo; ++s) mbar_init(&known[s], 1);
+    mbar_init(&paired, W);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&summed[s], 1);
+      mbar_init(&folded[s], 1);
+    }
+    quit = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+
+  if (warp == W) {                         // fetches
+    unsigned ticket = 0;
+    if (lane == 0) ticket = atomicAdd(P.chain.ticket, 1u);
+    bool more = true;
+    int n = 0;
+    for (; more; ++n) {
+      Tile t;
+      more = fetch<L, true>(
+          P.packed, P.chain, P.tiles, P.col_tiles, ticket, t, [&](const Tile& e) {
+            const int c = e.col0 + lane * 2;
+            if (c >= P.D) return;
+            float* part = P.partial + (size_t)e.number * 2 * P.D + c;
+            *reinterpret_cast<float2*>(part) = make_float2(0.f, 0.f);
+            *reinterpret_cast<float2*>(part + P.D) = make_float2(0.f, 0.f);
+            if (P.dh0 && e.seq >= 0) {
+              const size_t i = (size_t)e.seq * P.D + c;
+              *reinterpret_cast<float2*>(P.dh0 + i) =
+                  P.dhT ? *reinterpret_cast<const float2*>(P.dhT + i) : make_float2(0.f, 0.f);
+            }
+          });
+      const int st = n % kBackStages;
+      if (n >= kBackStages && !wait_phase(&empty[st], (n / kBackStages - 1) & 1, gave_up)) break;
+      if (lane == 0) {
+        tiles[n % kBackInfo] = t;
+        mbar_arrive(&known[n % kBackInfo]);
+        if (more) {
+          unsigned char* buf = smem + st * Sh::kStageBytes;
+          mbar_expect(&full[st], Sh::kStageBytes);
+          tma_load(buf, &P.za, t.col0, t.row0, &full[st]);
+          tma_load(buf + Sh::kUnitBytes, &P.zb, t.col0, t.row0, &full[st]);
+          tma_load(buf + 2 * Sh::kUnitBytes, &P.v, t.col0, t.row0, &full[st]);
+          tma_load(buf + 3 * Sh::kUnitBytes, &P.dy, t.col0, t.row0, &full[st]);
+        } else {
+          mbar_arrive(&full[st]);
+        }
+      }
+      __syncwarp();
+    }
+    // Stay until every copy has arrived, also when the block gives up.
+    for (int x = n > kBackStages ? n - kBackStages : 0; x < n; ++x)
+      mbar_wait_bounded(&full[x % kBackStages], (x / kBackStages) & 1, kWaitNs);
+  } else if (warp == W + 1) {              // sums up and publishes
+    Tile before;
+    for (int it = 0;; ++it) {
+      if (!wait_phase(&known[it % kBackInfo], (it / kBackInfo) & 1, gave_up)) break;
+      const Tile t = tiles[it % kBackInfo];
+      const int c = t.col0 + lane * 2;
+      float2 h = make_float2(0.f, 0.f);
+      if (t.rows > 0 && c < P.D) {
+        const int begin = t.row0 - t.chunk * L;
+        h = __ldg(reinterpret_cast<const float2*>(
+            P.states + (size_t)(begin / L + t.seq + t.chunk) * P.D + c));
+      }
+      if (!wait_phase(&paired, it & 1, gave_up)) break;
+      // The arithmetic warps are past the tile before: its sums are complete.
+      float2 sa = both(0.f), sb = both(0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        sa = add2(sa, *reinterpret_cast<const float2*>(&sums[w][0][lane * 2]));
+        sb = add2(sb, *reinterpret_cast<const float2*>(&sums[w][1][lane * 2]));
+      }
+      if (t.rows > 0) {
+#pragma unroll
+        for (int w = 0; w < kHalves; ++w) {
+          float2* const ws = reinterpret_cast<float2*>(&half[w][1][lane * 2]);
+          const float2 s = *ws;
+          *ws = h;
+          h = fma2(*reinterpret_cast<const float2*>(&half[w][0][lane * 2]), h, s);
+        }
+        float2 p = both(1.f), q = both(0.f);
+#pragma unroll
+        for (int w = kHalves - 1; w >= 0; --w) {
+          float2* const wp = reinterpret_cast<float2*>(&half[w][0][lane * 2]);
+          float2* const wq = reinterpret_cast<float2*>(&half[w][2][lane * 2]);
+          const float2 p0 = *wp, q0 = *wq;
+          *wp = p;
+          *wq = q;
+          q = fma2(p0, q, q0);
+          p = mul2(p0, p);
+        }
+        if (!t.last) {
+          if (publishes_state(t.pos)) {    // left to the fold
+            *reinterpret_cast<float2*>(&whole[0][lane * 2]) = p;
+            *reinterpret_cast<float2*>(&whole[1][lane * 2]) = q;
+          } else if (c < P.D) {
+            publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, p, q);
+          }
+        }
+        __syncwarp();
+        mbar_arrive_if(lane == 0, &summed[it & 1]);
+      }
+      if (it > 0) {
+        const int cb = before.col0 + lane * 2;
+        if (cb < P.D) {
+          float* part = P.partial + (size_t)before.number * 2 * P.D + cb;
+          *reinterpret_cast<float2*>(part) = sa;
+          *reinterpret_cast<float2*>(part + P.D) = sb;
+        }
+      }
+      if (t.rows == 0) break;
+      before = t;
+    }
+  } else if (warp == W + 2) {              // folds
+    for (int it = 0;; ++it) {
+      if (!wait_phase(&known[it % kBackInfo], (it / kBackInfo) & 1, gave_up)) break;
+      const Tile t = tiles[it % kBackInfo];
+      if (t.rows == 0) break;
+      const int c = t.col0 + lane * 2;
+      float2 r = make_float2(0.f, 0.f);
+      if (t.pos == 0) {
+        if (P.dhT && c < P.D)
+          r = *reinterpret_cast<const float2*>(P.dhT + (size_t)t.seq * P.D + c);
+      } else if (!fold_before(P.chain, t, P.D, r)) {
+        *gave_up = 1;
+        break;
+      }
+      // All warps are past the tile that last used this carry.
+      if (it > 0 && !wait_phase(&summed[(it - 1) & 1], ((it - 1) >> 1) & 1, gave_up)) break;
+      *reinterpret_cast<float2*>(&carry[it & 1][lane * 2]) = r;
+      if (!t.last && publishes_state(t.pos)) {
+        if (!wait_phase(&summed[it & 1], (it >> 1) & 1, gave_up)) break;
+        const float2 p = *reinterpret_cast<const float2*>(&whole[0][lane * 2]);
+        const float2 q = *reinterpret_cast<const float2*>(&whole[1][lane * 2]);
+        if (c < P.D)
+          publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, both(0.f), fma2(p, r, q));
+      }
+      __syncwarp();
+      mbar_arrive_if(lane == 0, &folded[it & 1]);
+    }
+  } else {                                 // gates and gradients
+    const Constants K = constants();
+    const int c4 = (lane & 15) * 4, hw = tid >> 4, first = hw * R;
+    const uint32_t park = tmem_base + ((uint32_t)warp << 21);
+    for (int it = 0;; ++it) {
+      const int st = it % kBackStages;
+      if (!wait_phase(&full[st], (it / kBackStages) & 1, gave_up)) break;
+      const Tile t = tiles[it % kBackInfo];
+      if (t.rows == 0) {                   // lets the last sums be written
+        mbar_arrive_if(lane == 0, &paired);
+        break;
+      }
+      const int c = t.col0 + c4;
+      const bool in = c < P.D;
+      float2 A[2] = {both(1.f), both(1.f)}, bias[2] = {both(0.f), both(0.f)};
+      if (in && P.A) load_row(P.A + c, A[0], A[1]);
+      if (in && P.bias) load_row(P.bias + c, bias[0], bias[1]);
+      T* bza = reinterpret_cast<T*>(smem + st * Sh::kStageBytes) + first * kCols + c4;
+      T* bzb = bza + L * kCols;
+      T* bv = bzb + L * kCols;
+      T* bdy = bv + L * kCols;
+      // Gates, set aside, and the pairs of this half-warp's rows: (p, s) of
+      // the states, (p, q) of the gradients.
+      float2 p[2] = {both(1.f), both(1.f)}, s[2] = {both(0.f), both(0.f)}, q[2] = {both(0.f), both(0.f)};
+#pragma unroll 2
+      for (int r = 0; r < R; ++r) {
+        float2 za[2], zb[2], v[2], dy[2];
+        load_row(bza + r * kCols, za[0], za[1]);
+        load_row(bzb + r * kCols, zb[0], zb[1]);
+        load_row(bv + r * kCols, v[0], v[1]);
+        load_row(bdy + r * kCols, dy[0], dy[1]);
+        Gates2 g[2];
+        g[0] = gates_pair(K, za[0], zb[0], A[0], bias[0]);
+        g[1] = gates_pair(K, za[1], zb[1], A[1], bias[1]);
+        if (first + r >= t.rows) {         // a row behind the sequence changes nothing
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            g[k].a = both(1.f);
+            g[k].beta = g[k].keep = g[k].sp = g[k].sig = v[k] = dy[k] = both(0.f);
+          }
+          store_row(bv + r * kCols, v[0], v[1]);
+          store_row(bdy + r * kCols, dy[0], dy[1]);
+        }
+        float2 aside[8] = {g[0].beta, g[1].beta, g[0].keep, g[1].keep,
+                           g[0].sp,   g[1].sp,   g[0].sig,  g[1].sig};
+        park16(park + r * 16, aside);
+        keep_a(bza + r * kCols, bzb + r * kCols, g[0].a, g[1].a);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          s[k] = fma2(g[k].a, s[k], mul2(g[k].beta, v[k]));
+          p[k] = mul2(g[k].a, p[k]);
+          q[k] = fma2(p[k], dy[k], q[k]);
+        }
+      }
+      store_row(&half[hw][0][c4], p[0], p[1]);
+      store_row(&half[hw][1][c4], s[0], s[1]);
+      store_row(&half[hw][2][c4], q[0], q[1]);
+      parked();
+      __syncwarp();
+      mbar_arrive_if(lane == 0, &paired);
+      // w[r] = a h[r-1], the decayed state in front of each row.
+      if (!wait_phase(&summed[it & 1], (it >> 1) & 1, gave_up)) break;
+      float2 h[2], w[R][2];
+      load_row(&half[hw][1][c4], h[0], h[1]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float2 a[2], beta[2], v[2];
+        take_a(bza + r * kCols, bzb + r * kCols, a[0], a[1]);
+        unpark4(park + r * 16, beta[0], beta[1]);
+        load_row(bv + r * kCols, v[0], v[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          w[r][k] = mul2(a[k], h[k]);
+          h[k] = fma2(beta[k], v[k], w[r][k]);
+        }
+      }
+      float2 rr[2], bp[2], bq[2];
+      load_row(&half[hw][0][c4], bp[0], bp[1]);
+      load_row(&half[hw][2][c4], bq[0], bq[1]);
+      if (!wait_phase(&folded[it & 1], (it >> 1) & 1, gave_up)) break;
+      load_row(&carry[it & 1][c4], rr[0], rr[1]);
+      rr[0] = fma2(bp[0], rr[0], bq[0]);
+      rr[1] = fma2(bp[1], rr[1], bq[1]);
+      float2 sa[2] = {both(0.f), both(0.f)}, sb[2] = {both(0.f), both(0.f)};
+      const size_t o = (size_t)(t.row0 + first) * P.ld_grad + c;
+      const int left = in ? t.rows - first : 0;
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r) {
+        float2 a[2], v[2], dy[2], m[8];
+        unpark16(park + r * 16, m);
+        take_a(bza + r * kCols, bzb + r * kCols, a[0], a[1]);
+        load_row(bv + r * kCols, v[0], v[1]);
+        load_row(bdy + r * kCols, dy[0], dy[1]);
+        float2 dza[2], dzb[2], dv[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 beta = m[k], keep = m[2 + k], sp = m[4 + k], sig = m[6 + k];
+          const float2 g = add2(dy[k], rr[k]);
+          dv[k] = mul2(beta, g);
+          // v - alpha h times 1 - beta is keep v - a h.
+          dzb[k] = mul2(dv[k], fma2(keep, v[k], make_float2(-w[r][k].x, -w[r][k].y)));
+          const float2 dlog = mul2(g, w[r][k]);
+          sa[k] = fma2(sp, dlog, sa[k]);
+          const float2 d = mul2(A[k], mul2(sig, dlog));
+          sb[k] = add2(sb[k], d);
+          dza[k] = make_float2(-d.x, -d.y);
+          rr[k] = mul2(a[k], g);
+        }
+        const size_t at = o + (size_t)r * P.ld_grad;
+        store_row_if(r < left, reinterpret_cast<T*>(P.dza) + at, dza[0], dza[1]);
+        store_row_if(r < left, reinterpret_cast<T*>(P.dzb) + at, dzb[0], dzb[1]);
+        store_row_if(r < left, reinterpret_cast<T*>(P.dv) + at, dv[0], dv[1]);
+      }
+      if (P.dh0 && t.last && hw == 0 && in)
+        store_row(P.dh0 + (size_t)t.seq * P.D + c, rr[0], rr[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        sa[k] = mul2(add2(sa[k], shfl_xor2(sa[k], 16)), both(-kLn2));
+        sb[k] = mul2(add2(sb[k], shfl_xor2(sb[k], 16)), both(-1.f));
+      }
+      if (lane < 16) {
+        store_row(&sums[warp][0][c4], sa[0], sa[1]);
+        store_row(&sums[warp][1][c4], sb[0], sb[1]);
+      }
+      // This stage was written to: order that before the copy that comes next.
+      tc::fence_smem_to_async();
+      __syncwarp();
+      mbar_arrive_if(lane == 0, &empty[st]);
+    }
+  }
+  __syncthreads();
+  if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
+  if (quit && tid == 0) {                  // tell the other blocks
+    record_status(P.status, SDM_ERR_TIMEOUT);
+    atomicExch(P.chain.abort, 1u);
+  }
+}
+
+// Sums of the tiles' gradients of A and bias, always in the same order: 32
+// channels a block, each of 32 warps every 32nd chunk, then the warps.
+__global__ void __launch_bounds__(1024)
+    column_sums_kernel(const Packed packed, const float* partial, int numbers, int D, float* dA,
+                       float* dbias) {
+  __shared__ float warps[2][32][33];
+  if (!offsets_ok(packed)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float a = 0.f, b = 0.f;
+  if (c < D) {
+#pragma unroll 4
+    for (int n = warp; n < numbers; n += 32) {
+      a += __ldg(partial + (size_t)n * 2 * D + c);
+      b += __ldg(partial + (size_t)n * 2 * D + D + c);
+    }
+  }
+  warps[0][warp][lane] = a;
+  warps[1][warp][lane] = b;
+  __syncthreads();
+  if (warp < 2 && c < D) {
+    float* out = warp == 0 ? dA : dbias;
+    float sum = 0.f;
+    for (int w = 0; w < 32; ++w) sum += warps[warp][w][lane];
+    if (out) out[c] = sum;
+  }
+}
+
+struct Args {
+  RecurrenceDims d;
+  RecurrenceInputs in;
+  void* y;
+  unsigned* status;
+};
 
 // ---------------------------------------------------------------- one token
 // Four channels per thread (8 or 16 bytes of each input, 16 of the state), a
@@ -1092,13 +1475,16 @@ cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, cons
 }  // namespace
 
 size_t recurrence_workspace_bytes(const RecurrenceDims& d) {
-  const size_t back = (size_t)(d.n_seq + 1) * 2 * d.D * sizeof(float);
-  const size_t fwd = chain_bytes(d, d.dtype == SDM_BF16 ? ForwardShape<__nv_bfloat16>::L : ForwardShape<float>::L);
+  const bool b16 = d.dtype == SDM_BF16;
+  const size_t fwd = chain_bytes(d, b16 ? ForwardShape<__nv_bfloat16>::L : ForwardShape<float>::L);
+  const int L = b16 ? BackwardShape<__nv_bfloat16>::L : BackwardShape<float>::L;
+  const size_t back = chain_bytes(d, L) + (size_t)chunk_numbers(d.rows, d.n_seq, L) * 2 * d.D * 4;
   return back > fwd ? back : fwd;
 }
 
 size_t recurrence_states_bytes(const RecurrenceDims& d) {
-  return (size_t)chunk_numbers(d.rows, d.n_seq, kStateRows) * d.D * sizeof(float);
+  const int L = d.dtype == SDM_BF16 ? kStateRows<__nv_bfloat16> : kStateRows<float>;
+  return (size_t)chunk_numbers(d.rows, d.n_seq, L) * d.D * sizeof(float);
 }
 
 cudaError_t launch_recurrence_forward(const RecurrenceDims& d, const RecurrenceInputs& in,
@@ -1109,28 +1495,68 @@ cudaError_t launch_recurrence_forward(const RecurrenceDims& d, const RecurrenceI
   return forward_as<float>(d, in, h0, y, hT, states, workspace, status, stream);
 }
 
-cudaError_t launch_recurrence_backward(const RecurrenceDims& d, const RecurrenceInputs& in,
-                                       const float* states, const void* dy, const float* dhT,
-                                       void* dza, void* dzb, void* dv, float* dA, float* dbias,
-                                       float* dh0, void* workspace, unsigned* status,
-                                       cudaStream_t stream) {
-  Args P{};
-  P.d = d;
-  P.in = in;
+namespace {
+
+template <typename T>
+cudaError_t backward_as(const RecurrenceDims& d, const RecurrenceInputs& in, const float* states,
+                        const void* dy, const float* dhT, void* dza, void* dzb, void* dv,
+                        float* dA, float* dbias, float* dh0, void* workspace, unsigned* status,
+                        cudaStream_t stream) {
+  using Sh = BackwardShape<T>;
+  constexpr int L = Sh::L;
+  BackwardArgs P;
+  if (d.rows > 0 && (!make_map(&P.za, in.za, d.dtype, d.rows, d.D, d.ld, L) ||
+                     !make_map(&P.zb, in.zb, d.dtype, d.rows, d.D, d.ld, L) ||
+                     !make_map(&P.v, in.v, d.dtype, d.rows, d.D, d.ld, L) ||
+                     !make_map(&P.dy, dy, d.dtype, d.rows, d.D, d.D, L)))
+    return cudaErrorInvalidValue;
   P.packed = Packed{in.offsets, d.n_seq, d.rows};
-  P.states = const_cast<float*>(states);
-  P.dy = dy;
+  P.A = in.A;
+  P.bias = in.bias;
+  P.states = states;
   P.dhT = dhT;
   P.dza = dza;
   P.dzb = dzb;
   P.dv = dv;
   P.dh0 = dh0;
-  P.partial = static_cast<float*>(workspace);
+  P.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + chain_bytes(d, L));
+  P.chain = chain_in(workspace);
+  P.D = d.D;
+  P.col_tiles = col_tiles_of(d.D);
+  P.ld_grad = d.ld_grad;
+  P.tiles = tiles_of(d, in.offsets != nullptr, L);
   P.status = status;
-  if (d.n_seq > 0) backward_kernel<<<dim3((d.D + 31) / 32, d.n_seq), 32, 0, stream>>>(P);
-  if (d.n_seq == 0) P.packed.offsets = nullptr;
-  if (dA || dbias) reduce_kernel<<<(d.D + 127) / 128, 128, 0, stream>>>(P, dA, dbias);
+  const auto kernel = backward_kernel<T>;
+  cudaError_t e = allow_smem(kernel, Sh::kSmem);
+  if (e == cudaSuccess) e = clear_chain(workspace, d, L, stream);
+  if (e != cudaSuccess) return e;
+  const unsigned most = (unsigned)(kBackBlocks * device_limits().sms);
+  kernel<<<P.tiles < most ? P.tiles : most, kBackThreads, Sh::kSmem, stream>>>(P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || (!dA && !dbias)) return e;
+  column_sums_kernel<<<(d.D + 31) / 32, 1024, 0, stream>>>(
+      P.packed, P.partial, (int)(P.tiles / P.col_tiles), d.D, dA, dbias);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_recurrence_backward(const RecurrenceDims& d, const RecurrenceInputs& in,
+                                       const float* states, const void* dy, const float* dhT,
+                                       void* dza, void* dzb, void* dv, float* dA, float* dbias,
+                                       float* dh0, void* workspace, unsigned* status,
+                                       cudaStream_t stream) {
+  if (d.n_seq == 0) {                      // sums over nothing
+    cudaError_t e = cudaSuccess;
+    if (dA) e = cudaMemsetAsync(dA, 0, (size_t)d.D * 4, stream);
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)d.D * 4, stream);
+    return e;
+  }
+  if (d.dtype == SDM_BF16)
+    return backward_as<__nv_bfloat16>(d, in, states, dy, dhT, dza, dzb, dv, dA, dbias, dh0,
+                                      workspace, status, stream);
+  return backward_as<float>(d, in, states, dy, dhT, dza, dzb, dv, dA, dbias, dh0, workspace,
+                            status, stream);
 }
 
 cudaError_t launch_recurrence_step(const RecurrenceDims& d, const RecurrenceInputs& in,

@@ -14,23 +14,13 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "packed.cuh"
 #include "tcgen05.cuh"
 
 namespace sdm {
 namespace {
 
 // ------------------------------------------------------------------- gates
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-  return r;
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
 
 // log2(1 + e) for e in [0, 1]: 2 log2(e) atanh(t) with t = e / (2 + e), as t
@@ -100,32 +90,6 @@ __device__ __forceinline__ void store4(void* base, size_t i, int dt, float4 v) {
 }
 
 // ------------------------------------------------------------- pairs of floats
-// Two float32 operations in one instruction (the packed forms of sm_100 on).
-__device__ __forceinline__ uint64_t bits2(float2 a) { return *reinterpret_cast<uint64_t*>(&a); }
-__device__ __forceinline__ float2 float2_of(uint64_t a) { return *reinterpret_cast<float2*>(&a); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-  return float2_of(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return float2_of(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return float2_of(r);
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-// The larger of two numbers, NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // The packed forms take no immediates.  Their constants are made once, out of
 // the compiler's sight: it would otherwise move them into registers again
 // before every use (about seven of 42 instructions per element).

@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "packed.cuh"
 
 namespace sdm {
 namespace {
@@ -28,19 +29,17 @@ template <>
 struct Eight<__nv_bfloat16> {
   uint4 w;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
   }
-  __device__ __forceinline__ void set(const float (&f)[8]) {
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      const __nv_bfloat162 b = __float22bfloat162_rn(f[i]);
       u[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
     w = make_uint4(u[0], u[1], u[2], u[3]);
@@ -54,13 +53,15 @@ struct Eight<float> {
     lo = reinterpret_cast<const float4*>(p)[0];
     hi = reinterpret_cast<const float4*>(p)[1];
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = lo.x; f[1] = lo.y; f[2] = lo.z; f[3] = lo.w;
-    f[4] = hi.x; f[5] = hi.y; f[6] = hi.z; f[7] = hi.w;
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
+    f[0] = make_float2(lo.x, lo.y);
+    f[1] = make_float2(lo.z, lo.w);
+    f[2] = make_float2(hi.x, hi.y);
+    f[3] = make_float2(hi.z, hi.w);
   }
-  __device__ __forceinline__ void set(const float (&f)[8]) {
-    lo = make_float4(f[0], f[1], f[2], f[3]);
-    hi = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {
+    lo = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    hi = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
   }
   __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = lo;
@@ -68,9 +69,9 @@ struct Eight<float> {
   }
 };
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t e4m3x2(float2 v) {
   uint16_t q;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(q) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(q) : "f"(v.y), "f"(v.x));
   return q;
 }
 
@@ -104,17 +105,24 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[N], int tea
   }
 }
 
-// The largest over a team, of the bit patterns of |values|: a NaN is above
-// every number.
+// The largest over a team of values that are not negative; NaN if one is.  As
+// bit patterns: a NaN (its sign taken off) is above every number.
 template <int TW>
-__device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* red, int team) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  if (TW == 1) return v;
-  if ((threadIdx.x & 31) == 0) red[(threadIdx.x >> 5) % TW] = v;
-  named_bar_sync(1 + team, TW * 32);
+__device__ __forceinline__ float team_max(float m, uint32_t* red, int team) {
+  uint32_t v = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7fffffffu);
+  if (TW > 1) {
+    if ((threadIdx.x & 31) == 0) red[(threadIdx.x >> 5) % TW] = v;
+    named_bar_sync(1 + team, TW * 32);
 #pragma unroll
-  for (int k = 0; k < TW; ++k) v = max(v, red[k]);
-  return v;
+    for (int k = 0; k < TW; ++k) v = max(v, red[k]);
+  }
+  return __uint_as_float(v);
+}
+__device__ __forceinline__ float largest(const float2 (&n)[4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_nan(m, max_nan(fabsf(n[i].x), fabsf(n[i].y)));
+  return m;
 }
 
 struct ForwardArgs {
@@ -124,16 +132,18 @@ struct ForwardArgs {
   float eps;
   void* s;
   void* out;
-  int out_dtype, group;
+  int group;
   float* scale;
   int rows, D;
+  float one_over_D;
 };
 
-template <typename T, int TW, int NV>
+template <typename T, int TW, int NV, int kOut>
 __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P) {
   __shared__ float red[2][kTeams<TW>][TW][1];
   __shared__ uint32_t redmax[2][kTeams<TW>][TW];
   const int team = threadIdx.x / (TW * 32), lane = threadIdx.x % (TW * 32), D = P.D;
+  const int group_log = 31 - __clz(P.group | 1);
   int flip = 0;
   for (long long row = (long long)blockIdx.x * kTeams<TW> + team; row < P.rows;
        row += (long long)gridDim.x * kTeams<TW>, flip ^= 1) {
@@ -147,85 +157,82 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
         if (P.residual) res[j].load(static_cast<const T*>(P.residual) + base + c);
       }
     }
-    float ss[1] = {0.f};
+    float2 ss2 = both(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
       if (c < D) {
-        float f[8];
+        float2 f[4];
         s[j].get(f);
         if (P.residual) {
-          float r[8];
+          float2 r[4];
           res[j].get(r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] += r[i];
+          for (int i = 0; i < 4; ++i) f[i] = add2(f[i], r[i]);
           s[j].set(f);                     // rounds
           s[j].get(f);
         }
         if (P.s) s[j].store(static_cast<T*>(P.s) + base + c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss[0] = fmaf(f[i], f[i], ss[0]);
+        for (int i = 0; i < 4; ++i) ss2 = fma2(f[i], f[i], ss2);
       }
     }
+    float ss[1] = {ss2.x + ss2.y};
     team_sum<TW, 1>(ss, red[flip][team], team);
-    const float inv = 1.f / sqrtf(ss[0] / (float)D + P.eps);
-    // n, of the 8-bit output kept until the scale is known.
-    float n[NV][8];
-    uint32_t most = 0;
+    const float2 inv = both(rsqrtf(fmaf(ss[0], P.one_over_D, P.eps)));
+    // n, kept where the scale of the 8-bit output has yet to be found.
+    float2 n[NV][4];
+    float most = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
       if (c < D) {
         s[j].get(n[j]);
-        Eight<float> g;
-        if (P.gamma) g.load(P.gamma + c);
-        float gm[8];
-        g.get(gm);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          n[j][i] *= inv;
-          if (P.gamma) n[j][i] *= gm[i];
+        for (int i = 0; i < 4; ++i) n[j][i] = mul2(n[j][i], inv);
+        if (P.gamma) {
+          Eight<float> g;
+          float2 gm[4];
+          g.load(P.gamma + c);
+          g.get(gm);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) n[j][i] = mul2(n[j][i], gm[i]);
         }
-        if (P.out_dtype == SDM_BF16) {
+        if (kOut == SDM_BF16) {
           Eight<__nv_bfloat16> o;
           o.set(n[j]);
           o.store(static_cast<__nv_bfloat16*>(P.out) + base + c);
-        } else if (P.out_dtype == SDM_F32) {
+        } else if (kOut == SDM_F32) {
           Eight<float> o;
           o.set(n[j]);
           o.store(static_cast<float*>(P.out) + base + c);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(n[j][i]) & 0x7fffffffu);
+        } else if (P.group == 0) {
+          most = max_nan(most, largest(n[j]));
         }
       }
     }
-    if (P.out_dtype != SDM_E4M3) continue;
+    if (kOut != SDM_E4M3) continue;
     if (P.group == 0) most = team_max<TW>(most, redmax[flip][team], team);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
       if (P.group) {                       // 4, 8 or 16 neighbouring threads
-        most = 0;
-        if (c < D) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(n[j][i]) & 0x7fffffffu);
-        }
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        if (P.group >= 64) most = max(most, __shfl_xor_sync(0xffffffffu, most, 4));
-        if (P.group >= 128) most = max(most, __shfl_xor_sync(0xffffffffu, most, 8));
+        most = c < D ? largest(n[j]) : 0.f;
+        most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        if (P.group >= 64) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 4));
+        if (P.group >= 128) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 8));
       }
-      const float amax = __uint_as_float(most);
-      const float scale = amax != amax ? amax : fmaxf(amax / kE4m3Max, 1.17549435e-38f);
-      const float by = 1.f / scale;
+      const float scale = max_nan(most * (1.f / kE4m3Max), 1.17549435e-38f);
+      const float2 by = both(rcp(scale));
       if (c < D) {
         uint2 q;
-        q.x = e4m3x2(n[j][0] * by, n[j][1] * by) | e4m3x2(n[j][2] * by, n[j][3] * by) << 16;
-        q.y = e4m3x2(n[j][4] * by, n[j][5] * by) | e4m3x2(n[j][6] * by, n[j][7] * by) << 16;
+        q.x = e4m3x2(mul2(n[j][0], by)) | e4m3x2(mul2(n[j][1], by)) << 16;
+        q.y = e4m3x2(mul2(n[j][2], by)) | e4m3x2(mul2(n[j][3], by)) << 16;
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.out) + base + c) = q;
         if (P.group) {
-          if (c % P.group == 0) P.scale[(size_t)row * (D / P.group) + c / P.group] = scale;
+          if ((c & (P.group - 1)) == 0)
+            P.scale[(size_t)row * (D >> group_log) + (c >> group_log)] = scale;
         } else if (c == 0) {
           P.scale[row] = scale;
         }
@@ -244,6 +251,7 @@ struct BackwardArgs {
   void* dx;
   float* partial;      // [blocks][D], or null
   int rows, D;
+  float one_over_D;
 };
 
 // Threads keep their channels from row to row, so that the gradient of gamma
@@ -252,13 +260,13 @@ struct BackwardArgs {
 template <typename T, int TW, int NV>
 __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs P) {
   __shared__ float red[2][kTeams<TW>][TW][2];
-  extern __shared__ float teams[];         // [kTeams - 1][TW * NV * 256]
+  extern __shared__ __align__(16) float teams[];   // [kTeams - 1][TW * NV * 256]
   const int team = threadIdx.x / (TW * 32), lane = threadIdx.x % (TW * 32), D = P.D;
-  float acc[NV][8];
+  float2 acc[NV][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[j][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[j][i] = both(0.f);
   int flip = 0;
   for (long long row = (long long)blockIdx.x * kTeams<TW> + team; row < P.rows;
        row += (long long)gridDim.x * kTeams<TW>, flip ^= 1) {
@@ -273,46 +281,65 @@ __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs
         if (P.ds) more[j].load(static_cast<const T*>(P.ds) + base + c);
       }
     }
-    float v[2] = {0.f, 0.f};               // sum s^2, sum w s
+    float2 ss = both(0.f), ws = both(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
       if (c < D) {
-        float fs[8], fd[8], gm[8];
+        float2 fs[4], w[4];
         s[j].get(fs);
-        d[j].get(fd);
-        Eight<float> g;
-        if (P.gamma) g.load(P.gamma + c);
-        g.get(gm);
+        d[j].get(w);
+        if (P.gamma) {
+          Eight<float> g;
+          float2 gm[4];
+          g.load(P.gamma + c);
+          g.get(gm);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[0] = fmaf(fs[i], fs[i], v[0]);
-          v[1] = fmaf(P.gamma ? fd[i] * gm[i] : fd[i], fs[i], v[1]);
+          for (int i = 0; i < 4; ++i) w[i] = mul2(w[i], gm[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ss = fma2(fs[i], fs[i], ss);
+          ws = fma2(w[i], fs[i], ws);
         }
       }
     }
+    float v[2] = {ss.x + ss.y, ws.x + ws.y};
     team_sum<TW, 2>(v, red[flip][team], team);
-    const float inv = 1.f / sqrtf(v[0] / (float)D + P.eps), mean = v[1] * inv / (float)D;
+    const float inv1 = rsqrtf(fmaf(v[0], P.one_over_D, P.eps));
+    const float2 inv = both(inv1), mean = both(-v[1] * inv1 * P.one_over_D);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
       if (c < D) {
-        float fs[8], fd[8], gm[8], fm[8];
+        float2 fs[4], fd[4], w[4], dx[4];
         s[j].get(fs);
         d[j].get(fd);
-        Eight<float> g;
-        if (P.gamma) g.load(P.gamma + c);
-        g.get(gm);
-        if (P.ds) more[j].get(fm);
+        if (P.gamma) {
+          Eight<float> g;
+          float2 gm[4];
+          g.load(P.gamma + c);
+          g.get(gm);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float hat = fs[i] * inv, w = P.gamma ? fd[i] * gm[i] : fd[i];
-          acc[j][i] = fmaf(fd[i], hat, acc[j][i]);
-          const float dx = inv * fmaf(-hat, mean, w);
-          fs[i] = P.ds ? fm[i] + dx : dx;
+          for (int i = 0; i < 4; ++i) w[i] = mul2(fd[i], gm[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = fd[i];
+        }
+        if (P.ds) {
+          more[j].get(dx);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dx[i] = both(0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 hat = mul2(fs[i], inv);
+          acc[j][i] = fma2(fd[i], hat, acc[j][i]);
+          dx[i] = fma2(inv, fma2(hat, mean, w[i]), dx[i]);
         }
         Eight<T> o;
-        o.set(fs);
+        o.set(dx);
         o.store(static_cast<T*>(P.dx) + base + c);
       }
     }
@@ -320,20 +347,21 @@ __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs
   if (!P.partial) return;
   constexpr int kRow = TW * NV * 256;
   if (kTeams<TW> > 1) {
-    if (team > 0)
+    float2* const mine = reinterpret_cast<float2*>(teams) + lane * 4;
+    if (team > 0) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          teams[(team - 1) * kRow + (j * TW * 32 + lane) * kVec + i] = acc[j][i];
+        for (int i = 0; i < 4; ++i) mine[((team - 1) * kRow + j * TW * 256) / 2 + i] = acc[j][i];
+    }
     __syncthreads();
     if (team > 0) return;
+    for (int k = 0; k < kTeams<TW> - 1; ++k)
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        for (int k = 0; k < kTeams<TW> - 1; ++k)
-          acc[j][i] += teams[k * kRow + (j * TW * 32 + lane) * kVec + i];
+        for (int i = 0; i < 4; ++i)
+          acc[j][i] = add2(acc[j][i], mine[(k * kRow + j * TW * 256) / 2 + i]);
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -370,10 +398,16 @@ constexpr int kPartsPerSm = 2;
 int most_parts() { return kPartsPerSm * device_limits().sms; }
 
 template <typename T, int TW, int NV>
-cudaError_t forward_as(const ForwardArgs& P, cudaStream_t stream) {
+cudaError_t forward_as(const ForwardArgs& P, int out_dtype, cudaStream_t stream) {
   const long long want = ((long long)P.rows + kTeams<TW> - 1) / kTeams<TW>;
   const long long most = 1 << 20;
-  forward_kernel<T, TW, NV><<<(unsigned)(want < most ? want : most), kBlock<TW>, 0, stream>>>(P);
+  const unsigned blocks = (unsigned)(want < most ? want : most);
+  if (out_dtype == SDM_E4M3)
+    forward_kernel<T, TW, NV, SDM_E4M3><<<blocks, kBlock<TW>, 0, stream>>>(P);
+  else if (out_dtype == SDM_BF16)
+    forward_kernel<T, TW, NV, SDM_BF16><<<blocks, kBlock<TW>, 0, stream>>>(P);
+  else
+    forward_kernel<T, TW, NV, SDM_F32><<<blocks, kBlock<TW>, 0, stream>>>(P);
   return cudaGetLastError();
 }
 
@@ -424,11 +458,11 @@ size_t add_rmsnorm_workspace_bytes(const NormDims& d) {
 cudaError_t launch_add_rmsnorm(const NormDims& d, const void* x, const void* residual,
                                const float* gamma, float eps, void* s, void* out, int out_dtype,
                                int group, float* scale, cudaStream_t stream) {
-  const ForwardArgs P{x, residual, gamma, eps, s, out, out_dtype, group, scale, d.rows, d.D};
+  const ForwardArgs P{x, residual, gamma, eps, s, out, group, scale, d.rows, d.D, 1.f / (float)d.D};
   return with_team(d.D, few_rows(d.rows), [&](auto tw, auto nv) {
     return d.dtype == SDM_BF16
-               ? forward_as<__nv_bfloat16, decltype(tw)::value, decltype(nv)::value>(P, stream)
-               : forward_as<float, decltype(tw)::value, decltype(nv)::value>(P, stream);
+               ? forward_as<__nv_bfloat16, decltype(tw)::value, decltype(nv)::value>(P, out_dtype, stream)
+               : forward_as<float, decltype(tw)::value, decltype(nv)::value>(P, out_dtype, stream);
   });
 }
 
@@ -437,7 +471,7 @@ cudaError_t launch_add_rmsnorm_backward(const NormDims& d, const void* s, const 
                                         float* dgamma, void* workspace, cudaStream_t stream) {
   if (d.rows == 0) return cudaMemsetAsync(dgamma, 0, (size_t)d.D * sizeof(float), stream);
   const BackwardArgs P{s,  dout,   gamma, ds, eps, dx, dgamma ? static_cast<float*>(workspace) : nullptr,
-                       d.rows, d.D};
+                       d.rows, d.D, 1.f / (float)d.D};
   return with_team(d.D, few_rows(d.rows), [&](auto tw, auto nv) {
     return d.dtype == SDM_BF16
                ? backward_as<__nv_bfloat16, decltype(tw)::value, decltype(nv)::value>(P, dgamma, stream)

@@ -37,6 +37,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
   return float2_of(r);
 }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // The larger of two numbers, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {

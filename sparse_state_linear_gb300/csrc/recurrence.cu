@@ -106,32 +106,42 @@ __device__ __forceinline__ Constants constants() {
                    hidden(kLog1),  hidden(kLog2), hidden(kLog3), hidden(kLog4)};
 }
 
-// log2p1_unit, two at a time.
-__device__ __forceinline__ float2 log2p1_unit(const Constants& K, float2 e) {
+// What the exponent of alpha is made of, for two channels: x = (za + bias)
+// log2(e) from bias already times log2(e), e = 2^-|x| and
+// softplus = max(x, 0) + log2(1 + e), as log2p1_unit.
+__device__ __forceinline__ void softplus_pair(const Constants& K, float2 za, float2 bias2,
+                                              float2& x, float2& e, float2& sp) {
+  x = fma2(za, K.log2e, bias2);
+  e = make_float2(ex2(-fabsf(x.x)), ex2(-fabsf(x.y)));
   const float2 d = add2(e, K.two);
   const float2 t = mul2(e, make_float2(rcp(d.x), rcp(d.y))), z = mul2(t, t);
   float2 p = fma2(K.k4, z, K.k3);
   p = fma2(p, z, K.k2);
   p = fma2(p, z, K.k1);
   p = fma2(p, z, K.k0);
-  return mul2(p, t);
+  sp = fma2(p, t, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
 
-// a = (1 - beta) alpha and b = beta v of two channels; nA = -A.
-__device__ __forceinline__ void gate_pair(const Constants& K, float2 za, float2 zb, float2 v,
-                                          float2 nA, float2 bias, float2& a, float2& b) {
-  const float2 x = mul2(add2(za, bias), K.log2e);
-  const float2 e = make_float2(ex2(-fabsf(x.x)), ex2(-fabsf(x.y)));
-  const float2 sp = add2(make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)), log2p1_unit(K, e));
-  const float2 l = mul2(nA, sp);
-  // sigmoid(z) = 1 / (1 + 2^-z'), 1 - sigmoid = 2^-z' / (1 + 2^-z'); z' held
-  // above -126 so that 2^-z' stays finite.
-  float2 z = mul2(zb, K.log2e);
+// sigmoid(z) = 1 / (1 + 2^-z') with z' = z log2(e), held above -126 so that
+// 2^-z' stays finite.
+__device__ __forceinline__ void sigmoid_pair(const Constants& K, float2 zb, float2& z, float2& eb,
+                                             float2& beta) {
+  z = mul2(zb, K.log2e);
   z = make_float2(max_nan(z.x, -126.f), max_nan(z.y, -126.f));
-  const float2 eb = make_float2(ex2(-z.x), ex2(-z.y));
+  eb = make_float2(ex2(-z.x), ex2(-z.y));
   const float2 d = add2(eb, K.one);
-  const float2 beta = make_float2(rcp(d.x), rcp(d.y));
-  a = mul2(mul2(eb, beta), make_float2(ex2(l.x), ex2(l.y)));
+  beta = make_float2(rcp(d.x), rcp(d.y));
+}
+
+// a = (1 - beta) alpha and b = beta v of two channels.  1 - beta is 2^-z' beta,
+// so that a is beta 2^-(z' + A softplus).
+__device__ __forceinline__ void gate_pair(const Constants& K, float2 za, float2 zb, float2 v,
+                                          float2 A, float2 bias2, float2& a, float2& b) {
+  float2 x, e, sp, z, eb, beta;
+  softplus_pair(K, za, bias2, x, e, sp);
+  sigmoid_pair(K, zb, z, eb, beta);
+  const float2 l = fma2(A, sp, z);
+  a = mul2(beta, make_float2(ex2(-l.x), ex2(-l.y)));
   b = mul2(beta, v);
 }
 
@@ -700,13 +710,11 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
           end = it;
         } else {
           const int c = t.col0 + c4;
-          float2 nA[2] = {both(-1.f), both(-1.f)}, bias[2] = {both(0.f), both(0.f)};
-          if (c < P.D && P.A) {
-            load_row(P.A + c, nA[0], nA[1]);
-            nA[0] = mul2(nA[0], both(-1.f));
-            nA[1] = mul2(nA[1], both(-1.f));
-          }
+          float2 A[2] = {both(1.f), both(1.f)}, bias[2] = {both(0.f), both(0.f)};
+          if (c < P.D && P.A) load_row(P.A + c, A[0], A[1]);
           if (c < P.D && P.bias) load_row(P.bias + c, bias[0], bias[1]);
+          bias[0] = mul2(bias[0], K.log2e);
+          bias[1] = mul2(bias[1], K.log2e);
           int at[3];
           at[0] = unit.at;
           unit.next();
@@ -730,8 +738,8 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
               load_row(bza + (r4 + r) * kCols, za[0], za[1]);
               load_row(bzb + (r4 + r) * kCols, zb[0], zb[1]);
               load_row(bv + (r4 + r) * kCols, v[0], v[1]);
-              gate_pair(K, za[0], zb[0], v[0], nA[0], bias[0], a[2 * r], b[2 * r]);
-              gate_pair(K, za[1], zb[1], v[1], nA[1], bias[1], a[2 * r + 1], b[2 * r + 1]);
+              gate_pair(K, za[0], zb[0], v[0], A[0], bias[0], a[2 * r], b[2 * r]);
+              gate_pair(K, za[1], zb[1], v[1], A[1], bias[1], a[2 * r + 1], b[2 * r + 1]);
             }
             if (t.rows < L) {              // rows behind the sequence change nothing
 #pragma unroll
@@ -837,22 +845,17 @@ struct Gates2 {
   float2 a, beta, keep, sp, sig;
 };
 __device__ __forceinline__ Gates2 gates_pair(const Constants& K, float2 za, float2 zb, float2 A,
-                                             float2 bias) {
+                                             float2 bias2) {
   Gates2 g;
-  const float2 x = mul2(add2(za, bias), K.log2e);
-  const float2 e = make_float2(ex2(-fabsf(x.x)), ex2(-fabsf(x.y)));
-  g.sp = add2(make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)), log2p1_unit(K, e));
+  float2 x, e, z, eb;
+  softplus_pair(K, za, bias2, x, e, g.sp);
   const float2 f = add2(e, K.one);
   g.sig = mul2(make_float2(x.x >= 0.f ? 1.f : e.x, x.y >= 0.f ? 1.f : e.y),
                make_float2(rcp(f.x), rcp(f.y)));
-  const float2 l = mul2(A, g.sp);
-  float2 z = mul2(zb, K.log2e);
-  z = make_float2(max_nan(z.x, -126.f), max_nan(z.y, -126.f));
-  const float2 eb = make_float2(ex2(-z.x), ex2(-z.y));
-  const float2 d = add2(eb, K.one);
-  g.beta = make_float2(rcp(d.x), rcp(d.y));
+  sigmoid_pair(K, zb, z, eb, g.beta);
   g.keep = mul2(eb, g.beta);
-  g.a = mul2(g.keep, make_float2(ex2(-l.x), ex2(-l.y)));
+  const float2 l = fma2(A, g.sp, z);
+  g.a = mul2(g.beta, make_float2(ex2(-l.x), ex2(-l.y)));
   return g;
 }
 
@@ -1119,6 +1122,8 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
       float2 A[2] = {both(1.f), both(1.f)}, bias[2] = {both(0.f), both(0.f)};
       if (in && P.A) load_row(P.A + c, A[0], A[1]);
       if (in && P.bias) load_row(P.bias + c, bias[0], bias[1]);
+      bias[0] = mul2(bias[0], K.log2e);
+      bias[1] = mul2(bias[1], K.log2e);
       T* bza = reinterpret_cast<T*>(smem + st * Sh::kStageBytes) + first * kCols + c4;
       T* bzb = bza + L * kCols;
       T* bv = bzb + L * kCols;
@@ -1186,6 +1191,8 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
       rr[0] = fma2(bp[0], rr[0], bq[0]);
       rr[1] = fma2(bp[1], rr[1], bq[1]);
       float2 sa[2] = {both(0.f), both(0.f)}, sb[2] = {both(0.f), both(0.f)};
+      A[0] = sub2(both(0.f), A[0]);
+      A[1] = sub2(both(0.f), A[1]);
       const size_t o = (size_t)(t.row0 + first) * P.ld_grad + c;
       const int left = in ? t.rows - first : 0;
 #pragma unroll
@@ -1202,12 +1209,11 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
           const float2 g = add2(dy[k], rr[k]);
           dv[k] = mul2(beta, g);
           // v - alpha h times 1 - beta is keep v - a h.
-          dzb[k] = mul2(dv[k], fma2(keep, v[k], make_float2(-w[r][k].x, -w[r][k].y)));
+          dzb[k] = mul2(dv[k], sub2(mul2(keep, v[k]), w[r][k]));
           const float2 dlog = mul2(g, w[r][k]);
           sa[k] = fma2(sp, dlog, sa[k]);
-          const float2 d = mul2(A[k], mul2(sig, dlog));
-          sb[k] = add2(sb[k], d);
-          dza[k] = make_float2(-d.x, -d.y);
+          dza[k] = mul2(A[k], mul2(sig, dlog));
+          sb[k] = add2(sb[k], dza[k]);
           rr[k] = mul2(a[k], g);
         }
         const size_t at = o + (size_t)r * P.ld_grad;
@@ -1220,7 +1226,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         sa[k] = mul2(add2(sa[k], shfl_xor2(sa[k], 16)), both(-kLn2));
-        sb[k] = mul2(add2(sb[k], shfl_xor2(sb[k], 16)), both(-1.f));
+        sb[k] = add2(sb[k], shfl_xor2(sb[k], 16));
       }
       if (lane < 16) {
         store_row(&sums[warp][0][c4], sa[0], sa[1]);

@@ -8,6 +8,10 @@ each float32 operation U, the logarithm 6.5 U), are
   sigmoid(x), sigmoid(-x):    (6 |x| + 12) U
   softplus(x):                (3 |x| + 13) U
   alpha = exp(-l), l = A sp:  (l (3 |x| + 17) + 4) U
+with |x| of x = za + bias standing for |za| + |bias| (each is multiplied by
+log2(e) and rounded before the sum), and for a = (1 - beta) alpha the same
+whether the factors or their exponents are put together (an exponent's error
+is three roundings of it at most),
 and they enter a sum of products through its majorant, the same recurrence on
 absolute values (H for the states, G for their gradients): every term of h[t]
 is a product with one more factor a per step, whatever the order in which the
@@ -44,10 +48,11 @@ def recurrence(za, zb, v, A, bias, off, h0=None, dy=None, dhT=None):
     lam = A * sp
     alpha, beta, keep, sig = torch.exp(-lam), torch.sigmoid(zb), torch.sigmoid(-zb), torch.sigmoid(x)
     far = lambda t: torch.nan_to_num(t.abs(), posinf=200.0).clamp(max=200.0)   # exp(-200) is 0 in float32
+    size = far(za.abs() + bias.abs())
     e_s = (6 * far(zb) + 12) * U
-    e_sp = (3 * far(x) + 13) * U
-    e_alpha = (lam.clamp(max=200.0) * (3 * far(x) + 17) + 4) * U
-    e_a, e_b, e_sig = e_s + e_alpha + U, e_s + U, (6 * far(x) + 12) * U
+    e_sp = (3 * size + 13) * U
+    e_alpha = (lam.clamp(max=200.0) * (3 * size + 17) + 4) * U
+    e_a, e_b, e_sig = e_s + e_alpha + U, e_s + U, (6 * size + 12) * U
     a, b = keep * alpha, beta * v
     nan = lambda *s: torch.full(s, float("nan"), dtype=torch.float64)
     y, Ey, before, H, Eb = nan(rows, D), nan(rows, D), nan(rows, D), nan(rows, D), nan(rows, D)

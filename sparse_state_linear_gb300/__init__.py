@@ -450,8 +450,14 @@ def sdm_measure_row_traffic(src, dst, col_slice: int, T: int, loads: int, stores
 
 
 # ------------------------------------------------- recurrence and residual norm
+#
+# These are called once per layer and token, so their checks are few steps: a
+# tensor in order costs one test, and only one that is not is looked at closely.
 
 _TORCH = {SDM_F32: torch.float32, SDM_BF16: torch.bfloat16, SDM_E4M3: torch.float8_e4m3fn}
+_F32, _I32 = torch.float32, torch.int32
+_device_now = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _torch_dtype(dtype: int, what: str) -> torch.dtype:
@@ -460,71 +466,74 @@ def _torch_dtype(dtype: int, what: str) -> torch.dtype:
     return _TORCH[dtype]
 
 
-class _Call:
-    """The device, the stream and the allocations of one call.  Tensors the
-    binding makes belong to the stream the kernels run on, so that the caching
-    allocator hands their memory on in that stream's order."""
-    __slots__ = ("device", "index", "torch_stream", "stream")
-
-    def __init__(self, like: torch.Tensor, stream):
-        if not like.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        self.device, self.index = like.device, torch.cuda.current_device()
-        if self.device.index != self.index:
-            raise ValueError(f"tensors are on {like.device}, but the current device is "
-                             f"cuda:{self.index}; call under torch.cuda.device({like.device})")
-        self.torch_stream = None
-        if stream is None:
-            self.stream = torch._C._cuda_getCurrentRawStream(self.index)
-        elif hasattr(stream, "cuda_stream"):
-            self.torch_stream, self.stream = stream, stream.cuda_stream
-        else:
-            self.stream = int(stream)
-            self.torch_stream = (torch.cuda.ExternalStream(self.stream, device=self.device)
-                                 if self.stream else torch.cuda.default_stream(self.device))
-
-    def empty(self, shape, dtype):
-        if self.torch_stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.torch_stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def ptr(self, t, name, dtype, numel):
-        """Address of a contiguous tensor of this dtype and at least `numel` elements."""
-        if t is None:
-            return None
-        if t.dtype != dtype:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        if t.get_device() != self.index:
-            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.numel() < numel:
-            raise ValueError(f"{name} has {t.numel()} elements, the shape needs {numel}")
-        return t.data_ptr()
-
-    def rows(self, t, name, dtype, rows, D, ld):
-        """Address of a [rows, D] tensor whose rows are `ld` elements apart
-        (leading dimensions that flatten to `rows` are fine when ld = D)."""
-        if t is None:
-            raise ValueError(f"{name} is required")
-        if ld == D:
-            return self.ptr(t, name, dtype, rows * D)
-        if t.dtype != dtype:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        if t.get_device() != self.index:
-            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != D:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {D})")
-        if rows > 0 and (t.stride(1) != 1 or t.stride(0) != ld):
-            raise ValueError(f"{name} has strides {t.stride()}, expected ({ld}, 1)")
-        return t.data_ptr()
+def _where(like: torch.Tensor, stream):
+    """(device index, raw stream, torch stream or None) of a call.  The torch
+    stream is there where the caller names one: what the binding allocates then
+    belongs to it, so that the caching allocator hands the memory on in the
+    order of the stream the kernels run on."""
+    dev = like.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if dev != _device_now():
+        raise ValueError(f"tensors are on cuda:{dev}, but the current device is "
+                         f"cuda:{_device_now()}; call under torch.cuda.device({dev})")
+    if stream is None:
+        return dev, _raw_stream(dev), None
+    if hasattr(stream, "cuda_stream"):
+        return dev, stream.cuda_stream, stream
+    raw = int(stream)
+    return dev, raw, (torch.cuda.ExternalStream(raw, device=like.device) if raw
+                      else torch.cuda.default_stream(like.device))
 
 
-def _required(t, name):
+def _make(shape, dtype, like, torch_stream):
+    if torch_stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(torch_stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _refuse(t, name, dtype, numel, dev):
     if t is None:
         raise ValueError(f"{name} is required")
-    return t
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} has {t.numel()} elements, the shape needs {numel}")
+
+
+def _at(t, name, dtype, numel, dev):
+    """Address of a contiguous tensor of this dtype and at least `numel` elements."""
+    if (t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()
+            or t.numel() < numel):
+        _refuse(t, name, dtype, numel, dev)
+    return t.data_ptr()
+
+
+def _rows_at(t, name, dtype, rows, D, ld, dev):
+    """Address of a [rows, D] tensor whose rows are `ld` elements apart
+    (leading dimensions that flatten to `rows` are fine when ld = D)."""
+    if ld == D:
+        return _at(t, name, dtype, rows * D, dev)
+    if t is None or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype, rows * D, dev)
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != D:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {D})")
+    if rows > 0 and (t.stride(1) != 1 or (rows > 1 and t.stride(0) != ld)):
+        raise ValueError(f"{name} has strides {t.stride()}, expected ({ld}, 1)")
+    return t.data_ptr()
+
+
+def _scratch(workspace, need, like, torch_stream, dev):
+    """(workspace, its address, its bytes), made where the caller gives none."""
+    if workspace is None:
+        workspace = _make((max(need, 16),), torch.uint8, like, torch_stream)
+        return workspace, workspace.data_ptr(), need
+    return (workspace, _at(workspace, "workspace", workspace.dtype, 0, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def sdm_recurrence_workspace_size(sh: Recurrence) -> int:
@@ -537,22 +546,6 @@ def sdm_recurrence_states_size(sh: Recurrence) -> int:
     return int(lib().sdm_recurrence_states_size(ctypes.byref(sh)))
 
 
-def _recurrence_inputs(c: _Call, sh: Recurrence, dt, za, zb, v, A, bias, offsets):
-    D, ld = sh.D, sh.ld or sh.D
-    return (c.rows(za, "za", dt, sh.rows, D, ld), c.rows(zb, "zb", dt, sh.rows, D, ld),
-            c.rows(v, "v", dt, sh.rows, D, ld), c.ptr(A, "A", torch.float32, D),
-            c.ptr(bias, "bias", torch.float32, D),
-            c.ptr(offsets, "offsets", torch.int32, sh.n_seq + 1))
-
-
-def _scratch(c: _Call, workspace, need: int):
-    if workspace is None:
-        workspace = c.empty((max(need, 16),), torch.uint8)
-        return workspace, workspace.data_ptr(), need
-    n = workspace.numel() * workspace.element_size()
-    return workspace, c.ptr(workspace, "workspace", workspace.dtype, 0), n
-
-
 def sdm_recurrence_forward(sh: Recurrence, za, zb, v, A=None, bias=None, offsets=None, h0=None,
                            y=None, hT=None, states=None, save_states=False, workspace=None,
                            stream=None):
@@ -561,24 +554,31 @@ def sdm_recurrence_forward(sh: Recurrence, za, zb, v, A=None, bias=None, offsets
     device or None for equal parts; h0 [n_seq, D] float32.  Returns
     dict(y, hT, states); states (for the backward pass) only if given or
     ``save_states``."""
-    L, c = lib(), _Call(za, stream)
-    dt, D, f32 = _torch_dtype(sh.dtype, "sdm_recurrence_forward"), sh.D, torch.float32
+    L = lib()
+    dev, raw, ts = _where(za, stream)
+    dt, rows, D, n, ref = _torch_dtype(sh.dtype, "sdm_recurrence_forward"), sh.rows, sh.D, sh.n_seq, ctypes.byref(sh)
+    ld = sh.ld or D
     if y is None:
-        y = c.empty((sh.rows, D), dt)
+        y = _make((rows, D), dt, za, ts)
     if hT is None:
-        hT = c.empty((sh.n_seq, D), f32)
+        hT = _make((n, D), _F32, za, ts)
     n_states = 0
     if save_states or states is not None:
-        n_states = sdm_recurrence_states_size(sh) // 4
+        n_states = L.sdm_recurrence_states_size(ref) // 4
         if states is None:
-            states = c.empty((n_states,), f32)
-    ins = _recurrence_inputs(c, sh, dt, za, zb, v, A, bias, offsets)
-    ws, wsp, nws = _scratch(c, workspace, sdm_recurrence_workspace_size(sh))
-    _ok(L.sdm_recurrence_forward(ctypes.byref(sh), *ins, c.ptr(h0, "h0", f32, sh.n_seq * D),
-                                 c.ptr(y, "y", dt, sh.rows * D),
-                                 c.ptr(hT, "hT", f32, sh.n_seq * D),
-                                 c.ptr(states, "states", f32, n_states), wsp, nws, c.stream),
-        "sdm_recurrence_forward")
+            states = _make((n_states,), _F32, za, ts)
+    ws, wsp, nws = _scratch(workspace, L.sdm_recurrence_workspace_size(ref), za, ts, dev)
+    rc = L.sdm_recurrence_forward(
+        ref, _rows_at(za, "za", dt, rows, D, ld, dev), _rows_at(zb, "zb", dt, rows, D, ld, dev),
+        _rows_at(v, "v", dt, rows, D, ld, dev),
+        None if A is None else _at(A, "A", _F32, D, dev),
+        None if bias is None else _at(bias, "bias", _F32, D, dev),
+        None if offsets is None else _at(offsets, "offsets", _I32, n + 1, dev),
+        None if h0 is None else _at(h0, "h0", _F32, n * D, dev),
+        _at(y, "y", dt, rows * D, dev), _at(hT, "hT", _F32, n * D, dev),
+        None if states is None else _at(states, "states", _F32, n_states, dev), wsp, nws, raw)
+    if rc:
+        raise SdmError(rc, "sdm_recurrence_forward")
     return dict(y=y, hT=hT, states=states)
 
 
@@ -590,29 +590,37 @@ def sdm_recurrence_backward(sh: Recurrence, za, zb, v, states, dy, A=None, bias=
     stride ``sh.ld_grad`` and must be given where that is not D.  Returns
     dict(dza, dzb, dv, dA, dbias, dh0); dA (dbias) is made only where A (bias)
     is given."""
-    L, c = lib(), _Call(za, stream)
-    dt, D, f32 = _torch_dtype(sh.dtype, "sdm_recurrence_backward"), sh.D, torch.float32
-    ldg = sh.ld_grad or D
+    L = lib()
+    dev, raw, ts = _where(za, stream)
+    dt, rows, D, n, ref = _torch_dtype(sh.dtype, "sdm_recurrence_backward"), sh.rows, sh.D, sh.n_seq, ctypes.byref(sh)
+    ld, ldg = sh.ld or D, sh.ld_grad or D
     if ldg == D:
-        dza = c.empty((sh.rows, D), dt) if dza is None else dza
-        dzb = c.empty((sh.rows, D), dt) if dzb is None else dzb
-        dv = c.empty((sh.rows, D), dt) if dv is None else dv
+        dza = _make((rows, D), dt, za, ts) if dza is None else dza
+        dzb = _make((rows, D), dt, za, ts) if dzb is None else dzb
+        dv = _make((rows, D), dt, za, ts) if dv is None else dv
     if dA is None and A is not None:
-        dA = c.empty((D,), f32)
+        dA = _make((D,), _F32, za, ts)
     if dbias is None and bias is not None:
-        dbias = c.empty((D,), f32)
+        dbias = _make((D,), _F32, za, ts)
     if dh0 is None:
-        dh0 = c.empty((sh.n_seq, D), f32)
-    za, zb, v, A_, bias_, off = _recurrence_inputs(c, sh, dt, za, zb, v, A, bias, offsets)
-    ws, wsp, nws = _scratch(c, workspace, sdm_recurrence_workspace_size(sh))
-    _ok(L.sdm_recurrence_backward(
-        ctypes.byref(sh), za, zb, v, A_, bias_, off,
-        c.ptr(_required(states, "states"), "states", f32, sdm_recurrence_states_size(sh) // 4),
-        c.ptr(_required(dy, "dy"), "dy", dt, sh.rows * D), c.ptr(dhT, "dhT", f32, sh.n_seq * D),
-        c.rows(dza, "dza", dt, sh.rows, D, ldg), c.rows(dzb, "dzb", dt, sh.rows, D, ldg),
-        c.rows(dv, "dv", dt, sh.rows, D, ldg), c.ptr(dA, "dA", f32, D),
-        c.ptr(dbias, "dbias", f32, D), c.ptr(dh0, "dh0", f32, sh.n_seq * D), wsp, nws, c.stream),
-        "sdm_recurrence_backward")
+        dh0 = _make((n, D), _F32, za, ts)
+    ws, wsp, nws = _scratch(workspace, L.sdm_recurrence_workspace_size(ref), za, ts, dev)
+    rc = L.sdm_recurrence_backward(
+        ref, _rows_at(za, "za", dt, rows, D, ld, dev), _rows_at(zb, "zb", dt, rows, D, ld, dev),
+        _rows_at(v, "v", dt, rows, D, ld, dev),
+        None if A is None else _at(A, "A", _F32, D, dev),
+        None if bias is None else _at(bias, "bias", _F32, D, dev),
+        None if offsets is None else _at(offsets, "offsets", _I32, n + 1, dev),
+        _at(states, "states", _F32, L.sdm_recurrence_states_size(ref) // 4, dev),
+        _at(dy, "dy", dt, rows * D, dev),
+        None if dhT is None else _at(dhT, "dhT", _F32, n * D, dev),
+        _rows_at(dza, "dza", dt, rows, D, ldg, dev), _rows_at(dzb, "dzb", dt, rows, D, ldg, dev),
+        _rows_at(dv, "dv", dt, rows, D, ldg, dev),
+        None if dA is None else _at(dA, "dA", _F32, D, dev),
+        None if dbias is None else _at(dbias, "dbias", _F32, D, dev),
+        _at(dh0, "dh0", _F32, n * D, dev), wsp, nws, raw)
+    if rc:
+        raise SdmError(rc, "sdm_recurrence_backward")
     return dict(dza=dza, dzb=dzb, dv=dv, dA=dA, dbias=dbias, dh0=dh0)
 
 
@@ -621,17 +629,25 @@ def sdm_recurrence_step(sh: Recurrence, za, zb, v, state, A=None, bias=None, slo
     """One token per sequence: row i of za, zb, v [rows, D] steps state row
     slots[i] (int32; negative = padding; None = row i) of state [n_slots, D]
     float32 in place.  Returns y [rows, D]."""
-    L, c = lib(), _Call(za, stream)
-    dt, D = _torch_dtype(sh.dtype, "sdm_recurrence_step"), sh.D
+    L = lib()
+    dev, raw, ts = _where(za, stream)
+    dt, rows, D = _torch_dtype(sh.dtype, "sdm_recurrence_step"), sh.rows, sh.D
+    ld = sh.ld or D
     if y is None:
-        y = c.empty((sh.rows, D), dt)
-    if state.dim() != 2 or state.shape[1] != D:
+        y = _make((rows, D), dt, za, ts)
+    n_slots, width = state.shape
+    if width != D:
         raise ValueError(f"state has shape {tuple(state.shape)}, expected (n_slots, {D})")
-    za, zb, v, A, bias, _ = _recurrence_inputs(c, sh, dt, za, zb, v, A, bias, None)
-    _ok(L.sdm_recurrence_step(ctypes.byref(sh), za, zb, v, A, bias,
-                              c.ptr(state, "state", torch.float32, 0), state.shape[0],
-                              c.ptr(slots, "slots", torch.int32, sh.rows),
-                              c.ptr(y, "y", dt, sh.rows * D), c.stream), "sdm_recurrence_step")
+    rc = L.sdm_recurrence_step(
+        ctypes.byref(sh), _rows_at(za, "za", dt, rows, D, ld, dev),
+        _rows_at(zb, "zb", dt, rows, D, ld, dev), _rows_at(v, "v", dt, rows, D, ld, dev),
+        None if A is None else _at(A, "A", _F32, D, dev),
+        None if bias is None else _at(bias, "bias", _F32, D, dev),
+        _at(state, "state", _F32, 0, dev), n_slots,
+        None if slots is None else _at(slots, "slots", _I32, rows, dev),
+        _at(y, "y", dt, rows * D, dev), raw)
+    if rc:
+        raise SdmError(rc, "sdm_recurrence_step")
     return y
 
 
@@ -640,24 +656,29 @@ def sdm_add_rmsnorm(sh: Norm, x, residual=None, gamma=None, eps: float = 1e-6, s
     """Residual addition and RMS-Norm of x [rows, D]; returns dict(s, out,
     scale).  s = x + residual is made (or written where given) with a residual;
     scale [rows] (group = 0) or [rows, D / group] float32 for SDM_E4M3."""
-    L, c = lib(), _Call(x, stream)
+    L = lib()
+    dev, raw, ts = _where(x, stream)
     dt, odt = _torch_dtype(sh.dtype, "sdm_add_rmsnorm"), _torch_dtype(out_dtype, "sdm_add_rmsnorm")
-    n, f32 = sh.rows * sh.D, torch.float32
+    rows, D = sh.rows, sh.D
+    n, n_scale = rows * D, 0
     if s is None and residual is not None:
-        s = c.empty((sh.rows, sh.D), dt)
+        s = _make((rows, D), dt, x, ts)
     if out is None:
-        out = c.empty((sh.rows, sh.D), odt)
-    n_scale = 0
+        out = _make((rows, D), odt, x, ts)
     if out_dtype == SDM_E4M3:
-        if group < 0 or (group and sh.D % group):
+        if group < 0 or (group and D % group):
             raise SdmError(1, "sdm_add_rmsnorm")
-        n_scale = sh.rows * (sh.D // group if group else 1)
+        n_scale = rows * (D // group if group else 1)
         if scale is None:
-            scale = c.empty((sh.rows, sh.D // group) if group else (sh.rows,), f32)
-    _ok(L.sdm_add_rmsnorm(ctypes.byref(sh), c.ptr(x, "x", dt, n),
-                          c.ptr(residual, "residual", dt, n), c.ptr(gamma, "gamma", f32, sh.D),
-                          eps, c.ptr(s, "s", dt, n), c.ptr(out, "out", odt, n), out_dtype, group,
-                          c.ptr(scale, "scale", f32, n_scale), c.stream), "sdm_add_rmsnorm")
+            scale = _make((rows, D // group) if group else (rows,), _F32, x, ts)
+    rc = L.sdm_add_rmsnorm(
+        ctypes.byref(sh), _at(x, "x", dt, n, dev),
+        None if residual is None else _at(residual, "residual", dt, n, dev),
+        None if gamma is None else _at(gamma, "gamma", _F32, D, dev), eps,
+        None if s is None else _at(s, "s", dt, n, dev), _at(out, "out", odt, n, dev), out_dtype,
+        group, None if scale is None else _at(scale, "scale", _F32, n_scale, dev), raw)
+    if rc:
+        raise SdmError(rc, "sdm_add_rmsnorm")
     return dict(s=s, out=out, scale=scale)
 
 
@@ -672,18 +693,23 @@ def sdm_add_rmsnorm_backward(sh: Norm, s, dout, gamma=None, ds=None, eps: float 
     gradient that reaches s from elsewhere, or None).  Returns dict(dx,
     dgamma); dx is the gradient of x and of residual, dgamma is made only
     where gamma is given."""
-    L, c = lib(), _Call(s, stream)
-    dt, n, f32 = _torch_dtype(sh.dtype, "sdm_add_rmsnorm_backward"), sh.rows * sh.D, torch.float32
+    L = lib()
+    dev, raw, ts = _where(s, stream)
+    dt, rows, D = _torch_dtype(sh.dtype, "sdm_add_rmsnorm_backward"), sh.rows, sh.D
+    n = rows * D
     if dx is None:
-        dx = c.empty((sh.rows, sh.D), dt)
+        dx = _make((rows, D), dt, s, ts)
     if dgamma is None and gamma is not None:
-        dgamma = c.empty((sh.D,), f32)
+        dgamma = _make((D,), _F32, s, ts)
     ws, wsp, nws = None, None, 0
     if dgamma is not None:
-        ws, wsp, nws = _scratch(c, workspace, sdm_add_rmsnorm_workspace_size(sh))
-    _ok(L.sdm_add_rmsnorm_backward(ctypes.byref(sh), c.ptr(s, "s", dt, n),
-                                   c.ptr(_required(dout, "dout"), "dout", dt, n),
-                                   c.ptr(gamma, "gamma", f32, sh.D), c.ptr(ds, "ds", dt, n), eps,
-                                   c.ptr(dx, "dx", dt, n), c.ptr(dgamma, "dgamma", f32, sh.D),
-                                   wsp, nws, c.stream), "sdm_add_rmsnorm_backward")
+        ws, wsp, nws = _scratch(workspace, L.sdm_add_rmsnorm_workspace_size(ctypes.byref(sh)), s,
+                                ts, dev)
+    rc = L.sdm_add_rmsnorm_backward(
+        ctypes.byref(sh), _at(s, "s", dt, n, dev), _at(dout, "dout", dt, n, dev),
+        None if gamma is None else _at(gamma, "gamma", _F32, D, dev),
+        None if ds is None else _at(ds, "ds", dt, n, dev), eps, _at(dx, "dx", dt, n, dev),
+        None if dgamma is None else _at(dgamma, "dgamma", _F32, D, dev), wsp, nws, raw)
+    if rc:
+        raise SdmError(rc, "sdm_add_rmsnorm_backward")
     return dict(dx=dx, dgamma=dgamma)

@@ -12,6 +12,8 @@
 //   dza = -A sigmoid(za + b) dl,  dA = sum -softplus(za + b) dl,  db = sum dza.
 #include <cuda.h>   // CUtensorMap and its enums; the encoder comes through the runtime
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "packed.cuh"
@@ -193,13 +195,18 @@ struct __align__(16) Tile {
   int last;      // the chain's last chunk
 };
 
-// Workspace of one call: a header (ticket counter, abort word), cleared to
-// zeros, and a pair (P, S) of floats per chunk and channel, cleared to all ones.
+// Workspace of one call, cleared to all ones by one memset: a header (ticket
+// counter, from 2^32 - 1 on; abort word, 0 once a block has given up) and a pair
+// (P, S) of floats per chunk and channel.
 struct Chain {
   unsigned* ticket;
   unsigned* abort;
   float* pairs;       // [numbers][D][2]
 };
+
+__device__ __forceinline__ unsigned next_ticket(const Chain& c) {
+  return atomicAdd(c.ticket, 1u) + 1u;
+}
 
 constexpr int kGroup = 16;                                    // chunks per group, see below
 constexpr unsigned long long kWaitNs = 4000000000ull;         // limit of every wait
@@ -383,7 +390,7 @@ __device__ __forceinline__ bool fetch(const Packed& packed, const Chain& chain, 
       t.rows = 0;
       return false;
     }
-    if (lane == 0) ticket = atomicAdd(chain.ticket, 1u);
+    if (lane == 0) ticket = next_ticket(chain);
     const unsigned q = kReverse ? tiles - 1 - k : k;
     t.number = (int)(q / (unsigned)col_tiles);
     t.col0 = (int)(q - (unsigned)t.number * (unsigned)col_tiles) * kCols;
@@ -473,7 +480,7 @@ __device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int 
       if ((spin & 63) == 63) {
         const uint64_t now = global_ns();
         if (t0 == 0) t0 = now;
-        const bool ok = now - t0 < kWaitNs && load_acquire(ch.abort) == 0;
+        const bool ok = now - t0 < kWaitNs && load_acquire(ch.abort) != 0;
         if (!__all_sync(0xffffffffu, ok)) return false;
       }
     }
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
 
   if (warp == W) {                         // fetches
     unsigned ticket = 0;
-    if (lane == 0) ticket = atomicAdd(P.chain.ticket, 1u);
+    if (lane == 0) ticket = next_ticket(P.chain);
     int u = 0;                             // units asked for
     bool more = true;
     for (int n = 0; more; ++n) {
@@ -834,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
   if (quit && tid == 0) {                  // tell the other blocks
     record_status(P.status, SDM_ERR_TIMEOUT);
-    atomicExch(P.chain.abort, 1u);
+    atomicExch(P.chain.abort, 0u);
   }
 }
 
@@ -978,7 +985,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
 
   if (warp == W) {                         // fetches
     unsigned ticket = 0;
-    if (lane == 0) ticket = atomicAdd(P.chain.ticket, 1u);
+    if (lane == 0) ticket = next_ticket(P.chain);
     bool more = true;
     int n = 0;
     for (; more; ++n) {
@@ -1242,7 +1249,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
   if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
   if (quit && tid == 0) {                  // tell the other blocks
     record_status(P.status, SDM_ERR_TIMEOUT);
-    atomicExch(P.chain.abort, 1u);
+    atomicExch(P.chain.abort, 0u);
   }
 }
 
@@ -1355,10 +1362,7 @@ Chain chain_in(void* workspace) {
 }
 
 cudaError_t clear_chain(void* workspace, const RecurrenceDims& d, int L, cudaStream_t stream) {
-  const cudaError_t e = cudaMemsetAsync(workspace, 0, kHeaderBytes, stream);
-  if (e != cudaSuccess) return e;
-  return cudaMemsetAsync(static_cast<char*>(workspace) + kHeaderBytes, 0xff,
-                         chain_bytes(d, L) - kHeaderBytes, stream);
+  return cudaMemsetAsync(workspace, 0xff, chain_bytes(d, L), stream);
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1405,9 +1409,16 @@ unsigned tiles_of(const RecurrenceDims& d, bool offsets, int L) {
   return (unsigned)(n * col_tiles_of(d.D));
 }
 
+// Dynamic shared memory of a kernel, allowed once per device.
 template <class K>
-cudaError_t allow_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (f == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  return f;
 }
 
 template <typename T>
@@ -1434,7 +1445,8 @@ cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, cons
   P.tiles = tiles_of(d, in.offsets != nullptr, L);
   P.status = status;
   const auto kernel = forward_kernel<T>;
-  cudaError_t e = allow_smem(kernel, Sh::kSmem);
+  static std::atomic<bool> allowed[64];   // false
+  cudaError_t e = allow_smem(kernel, Sh::kSmem, allowed);
   if (e == cudaSuccess) e = clear_chain(workspace, d, L, stream);
   if (e != cudaSuccess) return e;
   const unsigned most = (unsigned)(2 * device_limits().sms);
@@ -1497,7 +1509,8 @@ cudaError_t backward_as(const RecurrenceDims& d, const RecurrenceInputs& in, con
   P.tiles = tiles_of(d, in.offsets != nullptr, L);
   P.status = status;
   const auto kernel = backward_kernel<T>;
-  cudaError_t e = allow_smem(kernel, Sh::kSmem);
+  static std::atomic<bool> allowed[64];   // false
+  cudaError_t e = allow_smem(kernel, Sh::kSmem, allowed);
   if (e == cudaSuccess) e = clear_chain(workspace, d, L, stream);
   if (e != cudaSuccess) return e;
   const unsigned most = (unsigned)(kBackBlocks * device_limits().sms);

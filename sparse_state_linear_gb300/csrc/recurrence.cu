@@ -378,14 +378,81 @@ struct ForwardArgs {
   unsigned* status;
 };
 
+// The order in which chunks of packed sequences are handed out.  Taken as they
+// are numbered, the chunks in flight would be neighbours of one sequence, each
+// waiting for the one before.  So the numbers are cut into kParts parts, where
+// sequences begin, of about equal length, and handed out in turn, one of each
+// part; parts that run out drop out.  A chunk still comes after its predecessor.
+// Measured, forward and backward at 10007 x 1000 float32 in 11 sequences: 144 us
+// in one part, 123 in four.
+constexpr int kParts = 4;
+struct Order {
+  int begin[kParts];       // of the parts, sorted by length
+  int length[kParts];
+};
+
+template <int L>
+__device__ Order order_of(const Packed& P, int numbers) {
+  int at[kParts + 1];
+  at[0] = 0;
+  at[kParts] = numbers;
+#pragma unroll
+  for (int j = 1; j < kParts; ++j) {
+    const int aim = (int)((long long)numbers * j / kParts), s = sequence_of<L>(P, aim);
+    const int lo = s < 0 ? 0 : P.begin(s) / L + s, hi = s < 0 ? P.begin(0) / L : P.begin(s + 1) / L + s + 1;
+    at[j] = aim - lo < hi - aim ? lo : min(hi, numbers);
+  }
+  Order o;
+#pragma unroll
+  for (int j = 0; j < kParts; ++j) {
+    o.begin[j] = at[j];
+    o.length[j] = at[j + 1] - at[j];
+  }
+#pragma unroll
+  for (int i = 0; i < kParts - 1; ++i)
+#pragma unroll
+    for (int j = 0; j < kParts - 1 - i; ++j)
+      if (o.length[j] > o.length[j + 1]) {
+        const int b = o.begin[j], l = o.length[j];
+        o.begin[j] = o.begin[j + 1];
+        o.length[j] = o.length[j + 1];
+        o.begin[j + 1] = b;
+        o.length[j + 1] = l;
+      }
+  return o;
+}
+
+// The number that is handed out q-th; backwards through each part if kReverse.
+template <bool kReverse>
+__device__ __forceinline__ int number_at(const Order& o, int q) {
+  int done = 0, number = 0;
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    const int parts = kParts - i, count = (o.length[i] - done) * parts;
+    if (!found && q < count) {
+      found = true;
+      const int round = q / parts, j = i + q - round * parts;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k)
+        if (k == j)
+          number = kReverse ? o.begin[k] + o.length[k] - 1 - done - round : o.begin[k] + done + round;
+    }
+    q -= count;
+    done = o.length[i];
+  }
+  return number;
+}
+
 // The next tile that has rows (a whole warp calls it): takes tickets until one
 // does; false when there is none left.  `ticket` (lane 0) was taken earlier and
 // is replaced by a new one, so that its latency lies behind other work.
 // `skip` is called for a number without rows: of a sequence without any (its
 // chunk 0), or of no chunk at all (seq < 0).
 template <int L, bool kReverse, class Skip>
-__device__ __forceinline__ bool fetch(const Packed& packed, const Chain& chain, unsigned tiles,
-                                      int col_tiles, unsigned& ticket, Tile& t, Skip skip) {
+__device__ __forceinline__ bool fetch(const Packed& packed, const Order& order, const Chain& chain,
+                                      unsigned tiles, int col_tiles, unsigned& ticket, Tile& t,
+                                      Skip skip) {
   const int lane = threadIdx.x & 31;
   while (true) {
     const unsigned k = __shfl_sync(0xffffffffu, ticket, 0);
@@ -394,12 +461,12 @@ __device__ __forceinline__ bool fetch(const Packed& packed, const Chain& chain, 
       return false;
     }
     if (lane == 0) ticket = next_ticket(chain);
-    const unsigned q = kReverse ? tiles - 1 - k : k;
-    t.number = (int)(q / (unsigned)col_tiles);
-    t.col0 = (int)(q - (unsigned)t.number * (unsigned)col_tiles) * kCols;
+    const int q = (int)(k / (unsigned)col_tiles);
+    t.col0 = (int)(k - (unsigned)q * (unsigned)col_tiles) * kCols;
     int o = 0, len = 0;
     t.chunk = 0;
     if (packed.offsets) {
+      t.number = number_at<kReverse>(order, q);
       t.seq = sequence_of<L>(packed, t.number);
       if (t.seq >= 0) {
         o = packed.begin(t.seq);
@@ -410,6 +477,7 @@ __device__ __forceinline__ bool fetch(const Packed& packed, const Chain& chain, 
     } else {
       // Equal lengths: chunk c of every sequence before chunk c + 1 of any, so
       // that a chunk's predecessor is as far back as can be.
+      t.number = kReverse ? (int)(tiles / (unsigned)col_tiles) - 1 - q : q;
       t.chunk = t.number / packed.n_seq;
       t.seq = t.number - t.chunk * packed.n_seq;
       len = packed.rows / packed.n_seq;
@@ -627,11 +695,13 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   if (warp == W) {                         // fetches
     unsigned ticket = 0;
     if (lane == 0) ticket = next_ticket(P.chain);
+    Order order;
+    if (P.packed.offsets) order = order_of<L>(P.packed, (int)(P.tiles / (unsigned)P.col_tiles));
     int u = 0;                             // units asked for
     bool more = true;
     for (int n = 0; more; ++n) {
       Tile t;
-      more = fetch<L, false>(P.packed, P.chain, P.tiles, P.col_tiles, ticket, t,
+      more = fetch<L, false>(P.packed, order, P.chain, P.tiles, P.col_tiles, ticket, t,
                       [&](const Tile& e) {               // a sequence without rows
                         const int c = e.col0 + lane * 2;
                         if (P.hT && e.seq >= 0 && c < P.D) {
@@ -1003,12 +1073,14 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
   if (warp == W) {                         // fetches
     unsigned ticket = 0;
     if (lane == 0) ticket = next_ticket(P.chain);
+    Order order;
+    if (P.packed.offsets) order = order_of<L>(P.packed, (int)(P.tiles / (unsigned)P.col_tiles));
     bool more = true;
     int n = 0;
     for (; more; ++n) {
       Tile t;
       more = fetch<L, true>(
-          P.packed, P.chain, P.tiles, P.col_tiles, ticket, t, [&](const Tile& e) {
+          P.packed, order, P.chain, P.tiles, P.col_tiles, ticket, t, [&](const Tile& e) {
             const int c = e.col0 + lane * 2;
             if (c >= P.D) return;
             float* part = P.partial + (size_t)e.number * 2 * P.D + c;

@@ -259,19 +259,6 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, unsigned parity) 
   return ok != 0;
 }
 
-// A position in a ring of N barriers and its phase.
-template <int N>
-struct Ring {
-  int at = 0;
-  unsigned phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++at == N) {
-      at = 0;
-      phase ^= 1;
-    }
-  }
-};
-
 // Wait for an mbarrier phase (a whole warp calls it); false once the limit has
 // passed or another warp of the block has given up (which the first to do so
 // marks).
@@ -392,10 +379,19 @@ struct Order {
 };
 
 template <int L>
-__device__ Order order_of(const Packed& P, int numbers) {
+__device__ Order order_of(const Packed& P, int numbers, bool many) {
   int at[kParts + 1];
   at[0] = 0;
   at[kParts] = numbers;
+  if (!many) {             // all in flight within two rounds: one part
+    Order o;
+#pragma unroll
+    for (int j = 0; j < kParts; ++j) {
+      o.begin[j] = 0;
+      o.length[j] = j == kParts - 1 ? numbers : 0;
+    }
+    return o;
+  }
 #pragma unroll
   for (int j = 1; j < kParts; ++j) {
     const int aim = (int)((long long)numbers * j / kParts), s = sequence_of<L>(P, aim);
@@ -609,8 +605,8 @@ __device__ __forceinline__ void unpark16(uint32_t taddr, float2 (&v)[8]) {
 // go on to the next tile, and only then come back to finish the one before.
 //
 // Inputs come in units of one tensor's tile (16 KB), in a ring of kUnits.
-// Barriers, all in shared memory: a tile's description is there (known), a
-// unit is (full) and has been read (empty); a tile's warps' pairs are there
+// Barriers, all in shared memory: a tile's description is there (known), its
+// units are (full) and have been read (empty); its warps' pairs are there
 // (paired) and have been summed up (summed), the state in front of it is
 // (folded), both have been read (taken).
 constexpr int kWarps = 8;
@@ -655,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   constexpr int L = Sh::L, R = Sh::R, W = kWarps;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((128 - (smem_u32(raw) & 127)) & 127);
-  __shared__ uint64_t full[kUnits], empty[kUnits], known[kInfo], paired[kSlots], summed[kSlots],
+  __shared__ uint64_t full[2], empty[2], known[kInfo], paired[kSlots], summed[kSlots],
       folded[kSlots], taken[kSlots];
   __shared__ Tile tiles[kInfo];
   __shared__ __align__(16) float total[kSlots][W][2][kCols];   // (P, S) of each warp's rows,
@@ -674,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   }
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
   if (tid == 0) {
-    for (int s = 0; s < kUnits; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], W);
     }
@@ -696,10 +692,11 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
     unsigned ticket = 0;
     if (lane == 0) ticket = next_ticket(P.chain);
     Order order;
-    if (P.packed.offsets) order = order_of<L>(P.packed, (int)(P.tiles / (unsigned)P.col_tiles));
-    int u = 0;                             // units asked for
+    if (P.packed.offsets)
+      order = order_of<L>(P.packed, (int)(P.tiles / (unsigned)P.col_tiles), P.tiles > 2 * gridDim.x);
     bool more = true;
-    for (int n = 0; more; ++n) {
+    int n = 0, unit = 0;                   // tiles asked for; place of the next unit
+    for (; more; ++n) {
       Tile t;
       more = fetch<L, false>(P.packed, order, P.chain, P.tiles, P.col_tiles, ticket, t,
                       [&](const Tile& e) {               // a sequence without rows
@@ -711,31 +708,38 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
                                    : make_float2(0.f, 0.f);
                         }
                       });
-      bool there = true;
-      for (int j = 0; j < 3 && there; ++j, ++u) {
-        const int k = u % kUnits;
-        there = u < kUnits || wait_phase(&empty[k], (u / kUnits - 1) & 1, gave_up);
-        if (!there) break;
-        if (lane == 0) {
-          if (j == 0) {
-            tiles[n % kInfo] = t;
-            mbar_arrive(&known[n % kInfo]);
-          }
-          if (more) {
-            mbar_expect(&full[k], Sh::kUnitBytes);
-            tma_load(smem + k * Sh::kUnitBytes, j == 0 ? &P.za : j == 1 ? &P.zb : &P.v, t.col0,
-                     t.row0, &full[k]);
-          } else {
-            mbar_arrive(&full[k]);
-          }
-        }
-        __syncwarp();
+      // The places of the first two units held the last two of the tile two
+      // before, that of the third the first of the tile before.
+      if (n >= 2 && !wait_phase(&empty[n & 1], ((n >> 1) - 1) & 1, gave_up)) break;
+      if (lane == 0) {
+        tiles[n % kInfo] = t;
+        mbar_arrive(&known[n % kInfo]);
+        if (more)
+          mbar_expect(&full[n & 1], 3 * Sh::kUnitBytes);
+        else
+          mbar_arrive(&full[n & 1]);
       }
-      if (!there) break;
+      __syncwarp();
+      bool there = true;
+      for (int j = 0; j < 3 && more; ++j) {
+        if (j == 2 && n >= 1)
+          there = wait_phase(&empty[(n - 1) & 1], ((n - 1) >> 1) & 1, gave_up);
+        // Where the block gives up (its results are void then), the copy is made
+        // all the same, so that the barrier completes.
+        if (lane == 0)
+          tma_load(smem + unit * Sh::kUnitBytes, j == 0 ? &P.za : j == 1 ? &P.zb : &P.v, t.col0,
+                   t.row0, &full[n & 1]);
+        if (++unit == kUnits) unit = 0;
+      }
+      __syncwarp();
+      if (!there) {
+        ++n;
+        break;
+      }
     }
     // Stay until every copy has arrived, also when the block gives up.
-    for (int x = u > kUnits ? u - kUnits : 0; x < u; ++x)
-      mbar_wait_bounded(&full[x % kUnits], (x / kUnits) & 1, kWaitNs);
+    for (int x = n > 2 ? n - 2 : 0; x < n; ++x)
+      mbar_wait_bounded(&full[x & 1], (x >> 1) & 1, kWaitNs);
   } else if (warp == W + 1) {              // publishes
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
@@ -776,10 +780,11 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
         *gave_up = 1;
         break;
       }
-      if (it >= kSlots && !wait_phase(&taken[slot], (it / kSlots - 1) & 1, gave_up)) break;
+      // (Which also means that the tile two before has been finished: its state
+      // may be overwritten.)
+      if (!wait_phase(&summed[slot], (it / kSlots) & 1, gave_up)) break;
       *reinterpret_cast<float2*>(&carry[slot][lane * 2]) = h;
       if (!t.last && publishes_state(t.pos)) {
-        if (!wait_phase(&summed[slot], (it / kSlots) & 1, gave_up)) break;
         const float2 p = *reinterpret_cast<const float2*>(&whole[slot][0][lane * 2]);
         const float2 s = *reinterpret_cast<const float2*>(&whole[slot][1][lane * 2]);
         if (c < P.D)
@@ -793,12 +798,12 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
     const uint32_t park = tmem_base + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * Sh::kParkCols;
     const uint32_t from = (uint32_t)((first * kCols + c4) * sizeof(T));
     const Constants K = constants();
-    Ring<kUnits> unit;
+    int unit = 0;                          // place of the tile's first unit
     int end = 0x7fffffff;                  // number of this block's tiles, once known
     for (int it = 0; it - 1 < end; ++it) {
       if (it < end) {
         const int slot = it & 1;
-        if (!wait_phase(&full[unit.at], unit.phase, gave_up)) break;
+        if (!wait_phase(&full[it & 1], (it >> 1) & 1, gave_up)) break;
         const Tile t = tiles[it % kInfo];
         if (t.rows == 0) {
           end = it;
@@ -809,18 +814,11 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
           if (c < P.D && P.bias) load_row(P.bias + c, bias[0], bias[1]);
           bias[0] = mul2(bias[0], K.log2e);
           bias[1] = mul2(bias[1], K.log2e);
-          int at[3];
-          at[0] = unit.at;
-          unit.next();
-          at[1] = unit.at;
-          if (!wait_phase(&full[unit.at], unit.phase, gave_up)) break;
-          unit.next();
-          at[2] = unit.at;
-          if (!wait_phase(&full[unit.at], unit.phase, gave_up)) break;
-          unit.next();
-          const T* bza = reinterpret_cast<const T*>(smem + at[0] * Sh::kUnitBytes + from);
-          const T* bzb = reinterpret_cast<const T*>(smem + at[1] * Sh::kUnitBytes + from);
-          const T* bv = reinterpret_cast<const T*>(smem + at[2] * Sh::kUnitBytes + from);
+          const int u1 = unit + 1 < kUnits ? unit + 1 : 0, u2 = u1 + 1 < kUnits ? u1 + 1 : 0;
+          const T* bza = reinterpret_cast<const T*>(smem + unit * Sh::kUnitBytes + from);
+          const T* bzb = reinterpret_cast<const T*>(smem + u1 * Sh::kUnitBytes + from);
+          const T* bv = reinterpret_cast<const T*>(smem + u2 * Sh::kUnitBytes + from);
+          unit = u2 + 1 < kUnits ? u2 + 1 : 0;
           // Four rows at a time: gates, the pair of all rows so far, aside.
           float2 p[2] = {both(1.f), both(1.f)}, s[2] = {both(0.f), both(0.f)};
 #pragma unroll 1
@@ -855,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
             park16(park + slot * Sh::kSlotCols + r4 * 8 + 16, b);
           }
           __syncwarp();
-          mbar_arrive_if(lane < 3, &empty[lane == 0 ? at[0] : lane == 1 ? at[1] : at[2]]);
+          mbar_arrive_if(lane == 0, &empty[it & 1]);
           // The warp's pair (the lower half-warp's rows come first).
           float2 pl[2], sl[2];
 #pragma unroll
@@ -881,7 +879,6 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       const int slot = out & 1;
       const Tile t = tiles[out % kInfo];
       const int c = t.col0 + c4;
-      if (!wait_phase(&summed[slot], (out >> 1) & 1, gave_up)) break;
       if (!wait_phase(&folded[slot], (out >> 1) & 1, gave_up)) break;
       float2 h[2];
       load_row(&carry[slot][c4], h[0], h[1]);
@@ -1074,7 +1071,8 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
     unsigned ticket = 0;
     if (lane == 0) ticket = next_ticket(P.chain);
     Order order;
-    if (P.packed.offsets) order = order_of<L>(P.packed, (int)(P.tiles / (unsigned)P.col_tiles));
+    if (P.packed.offsets)
+      order = order_of<L>(P.packed, (int)(P.tiles / (unsigned)P.col_tiles), P.tiles > 2 * gridDim.x);
     bool more = true;
     int n = 0;
     for (; more; ++n) {

@@ -628,20 +628,30 @@ struct ForwardShape {
 };
 
 // The pairs of a tile's warps become those of all rows in front of each warp;
-// returns the whole tile's (two channels per lane).
-__device__ __forceinline__ void running_pairs(float (*total)[2][kCols], int lane, float2& P,
-                                              float2& S) {
-  P = both(1.f);
-  S = both(0.f);
+// `whole` gets the whole tile's before anything is written (two channels per
+// lane).
+template <class Whole>
+__device__ __forceinline__ void running_pairs(float (*total)[2][kCols], int lane, Whole whole) {
+  float2 p[kWarps], s[kWarps];
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    float2* const wp = reinterpret_cast<float2*>(&total[w][0][lane * 2]);
-    float2* const ws = reinterpret_cast<float2*>(&total[w][1][lane * 2]);
-    const float2 p = *wp, s = *ws;
-    *wp = P;
-    *ws = S;
-    S = fma2(p, S, s);
-    P = mul2(p, P);
+    p[w] = *reinterpret_cast<const float2*>(&total[w][0][lane * 2]);
+    s[w] = *reinterpret_cast<const float2*>(&total[w][1][lane * 2]);
+  }
+  float2 P = both(1.f), S = both(0.f);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float2 wp = p[w], ws = s[w];
+    p[w] = P;
+    s[w] = S;
+    S = fma2(wp, S, ws);
+    P = mul2(wp, P);
+  }
+  whole(P, S);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    *reinterpret_cast<float2*>(&total[w][0][lane * 2]) = p[w];
+    *reinterpret_cast<float2*>(&total[w][1][lane * 2]) = s[w];
   }
 }
 
@@ -748,16 +758,15 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       if (t.rows == 0) break;
       if (!wait_phase(&paired[slot], (it / kSlots) & 1, gave_up)) break;
       const int c = t.col0 + lane * 2;
-      float2 p, s;
-      running_pairs(total[slot], lane, p, s);
-      if (!t.last) {
+      running_pairs(total[slot], lane, [&](float2 p, float2 s) {
+        if (t.last) return;
         if (publishes_state(t.pos)) {      // left to the fold
           *reinterpret_cast<float2*>(&whole[slot][0][lane * 2]) = p;
           *reinterpret_cast<float2*>(&whole[slot][1][lane * 2]) = s;
         } else if (c < P.D) {
           publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, p, s);
         }
-      }
+      });
       __syncwarp();
       mbar_arrive_if(lane == 0, &summed[slot]);
     }
@@ -1124,31 +1133,19 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
             P.states + (size_t)(begin / L + t.seq + t.chunk) * P.D + c));
       }
       if (!wait_phase(&paired, it & 1, gave_up)) break;
-      // The arithmetic warps are past the tile before: its sums are complete.
-      float2 sa = both(0.f), sb = both(0.f);
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        sa = add2(sa, *reinterpret_cast<const float2*>(&sums[w][0][lane * 2]));
-        sb = add2(sb, *reinterpret_cast<const float2*>(&sums[w][1][lane * 2]));
-      }
       if (t.rows > 0) {
+        // What others wait for goes out first.
+        float2 wp[kHalves], wq[kHalves];
 #pragma unroll
         for (int w = 0; w < kHalves; ++w) {
-          float2* const ws = reinterpret_cast<float2*>(&half[w][1][lane * 2]);
-          const float2 s = *ws;
-          *ws = h;
-          h = fma2(*reinterpret_cast<const float2*>(&half[w][0][lane * 2]), h, s);
+          wp[w] = *reinterpret_cast<const float2*>(&half[w][0][lane * 2]);
+          wq[w] = *reinterpret_cast<const float2*>(&half[w][2][lane * 2]);
         }
         float2 p = both(1.f), q = both(0.f);
 #pragma unroll
         for (int w = kHalves - 1; w >= 0; --w) {
-          float2* const wp = reinterpret_cast<float2*>(&half[w][0][lane * 2]);
-          float2* const wq = reinterpret_cast<float2*>(&half[w][2][lane * 2]);
-          const float2 p0 = *wp, q0 = *wq;
-          *wp = p;
-          *wq = q;
-          q = fma2(p0, q, q0);
-          p = mul2(p0, p);
+          q = fma2(wp[w], q, wq[w]);
+          p = mul2(wp[w], p);
         }
         if (!t.last) {
           if (publishes_state(t.pos)) {    // left to the fold
@@ -1158,6 +1155,31 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
             publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, p, q);
           }
         }
+#pragma unroll
+        for (int w = 0; w < kHalves; ++w) {
+          float2* const ws = reinterpret_cast<float2*>(&half[w][1][lane * 2]);
+          const float2 s = *ws;
+          *ws = h;
+          h = fma2(wp[w], h, s);
+        }
+        p = both(1.f);
+        q = both(0.f);
+#pragma unroll
+        for (int w = kHalves - 1; w >= 0; --w) {
+          *reinterpret_cast<float2*>(&half[w][0][lane * 2]) = p;
+          *reinterpret_cast<float2*>(&half[w][2][lane * 2]) = q;
+          q = fma2(wp[w], q, wq[w]);
+          p = mul2(wp[w], p);
+        }
+      }
+      // The arithmetic warps are past the tile before: its sums are complete.
+      float2 sa = both(0.f), sb = both(0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        sa = add2(sa, *reinterpret_cast<const float2*>(&sums[w][0][lane * 2]));
+        sb = add2(sb, *reinterpret_cast<const float2*>(&sums[w][1][lane * 2]));
+      }
+      if (t.rows > 0) {
         __syncwarp();
         mbar_arrive_if(lane == 0, &summed[it & 1]);
       }

@@ -91,6 +91,8 @@ sdm_status check_recurrence(const sdm_recurrence* sh, bool equal_parts, Recurren
   // Supported envelope (16-byte rows, whatever the dtype).
   if (sh->n_seq > 65535 || sh->D > 65536) return SDM_ERR_UNSUPPORTED;
   if (sh->D % 8 != 0 || sh->ld % 8 != 0 || sh->ld_grad % 8 != 0) return SDM_ERR_UNSUPPORTED;
+  if (((long long)sh->rows / 32 + sh->n_seq) * ((sh->D + 63) / 64) >= (1ll << 31))
+    return SDM_ERR_UNSUPPORTED;            // tiles of 32 rows by 64 channels, counted in 32 bits
   *d = RecurrenceDims{sh->n_seq, sh->rows, sh->D, sh->ld ? sh->ld : sh->D,
                       sh->ld_grad ? sh->ld_grad : sh->D, (int)sh->dtype};
   return SDM_OK;

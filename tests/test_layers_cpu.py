@@ -52,7 +52,7 @@ def step(L, sh, over=None, n_slots=16):
 @pytest.mark.parametrize("kw,code", [
     (dict(n_seq=-1), 1), (dict(rows=-1), 1), (dict(D=0), 1), (dict(ld=-8), 1), (dict(ld_grad=-8), 1),
     (dict(dtype=2), 1), (dict(dtype=9), 1), (dict(ld=56), 1), (dict(ld_grad=56), 1),
-    (dict(n_seq=65536), 2), (dict(D=65544), 2), (dict(D=60), 2), (dict(ld=66), 2), (dict(ld_grad=68), 2),
+    (dict(n_seq=65536), 2), (dict(D=65544), 2), (dict(rows=(1 << 31) - 1, D=65536, n_seq=1), 2), (dict(D=60), 2), (dict(ld=66), 2), (dict(ld_grad=68), 2),
 ])
 def test_recurrence_rejects_bad_shapes(L, kw, code):
     sh = rec(**kw)

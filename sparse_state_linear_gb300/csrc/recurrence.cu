@@ -183,6 +183,19 @@ constexpr int kStateRows = 128 / (int)sizeof(T);
 
 
 // --------------------------------------------------------------------- scan
+// A (or ones) and bias (or zeros) times log2(e) of a tile's channels, brought
+// to shared memory by the warp that fetches it, two channels a lane.
+struct Rates {
+  float2 A, bias;
+};
+__device__ __forceinline__ Rates rates_of(const float* A, const float* bias, int c, int D) {
+  Rates r{both(1.f), both(0.f)};
+  if (A && c < D) r.A = __ldg(reinterpret_cast<const float2*>(A + c));
+  if (bias && c < D) r.bias = __ldg(reinterpret_cast<const float2*>(bias + c));
+  r.bias = mul2(r.bias, both(kLog2e));
+  return r;
+}
+
 // What a block has to know of a tile, found out by the warp that fetches it.
 struct __align__(16) Tile {
   int rows;      // valid rows, 1..L; 0: no tile is left
@@ -587,11 +600,31 @@ __device__ __forceinline__ void park16(uint32_t taddr, const float2 (&v)[8]) {
 __device__ __forceinline__ void parked() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ void unpark16(uint32_t taddr, float2 (&v)[8]) {
-  float r[16];
-  tc::ld16(taddr, r);
+// Asked for; there after the wait, which the registers pass through so that no
+// use of them precedes it.
+__device__ __forceinline__ void ask16(uint32_t taddr, float2 (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y), "=f"(v[2].x), "=f"(v[2].y),
+        "=f"(v[3].x), "=f"(v[3].y), "=f"(v[4].x), "=f"(v[4].y), "=f"(v[5].x), "=f"(v[5].y),
+        "=f"(v[6].x), "=f"(v[6].y), "=f"(v[7].x), "=f"(v[7].y)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void ask4(uint32_t taddr, float2& lo, float2& hi) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(lo.x), "=f"(lo.y), "=f"(hi.x), "=f"(hi.y)
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void asked() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void here(float2 (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = make_float2(r[2 * i], r[2 * i + 1]);
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i].x), "+f"(v[i].y) : : "memory");
 }
 
 // A block is eight warps for the arithmetic (a half-warp takes R rows by 64
@@ -669,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   __shared__ __align__(16) float lower[kSlots][W][2][kCols];   // and of its lower half-warp's
   __shared__ __align__(16) float whole[kSlots][2][kCols];      // the tile's
   __shared__ __align__(16) float carry[kSlots][kCols];         // the state in front of the tile
+  __shared__ __align__(16) float rates[2][2][kCols];           // A, bias
   __shared__ uint32_t tmem_base;
   __shared__ int quit;
   volatile int* gave_up = &quit;
@@ -681,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);              // copies asked for, rates there
       mbar_init(&empty[s], W);
     }
     for (int s = 0; s < kInfo; ++s) mbar_init(&known[s], 1);
@@ -707,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
     bool more = true;
     int n = 0, unit = 0;                   // tiles asked for; place of the next unit
     for (; more; ++n) {
-      Tile t;
+      Tile t{};
       more = fetch<L, false>(P.packed, order, P.chain, P.tiles, P.col_tiles, ticket, t,
                       [&](const Tile& e) {               // a sequence without rows
                         const int c = e.col0 + lane * 2;
@@ -718,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
                                    : make_float2(0.f, 0.f);
                         }
                       });
+      const Rates rt = rates_of(P.A, P.bias, more ? t.col0 + lane * 2 : P.D, P.D);
       // The places of the first two units held the last two of the tile two
       // before, that of the third the first of the tile before.
       if (n >= 2 && !wait_phase(&empty[n & 1], ((n >> 1) - 1) & 1, gave_up)) break;
@@ -741,7 +776,10 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
                    t.row0, &full[n & 1]);
         if (++unit == kUnits) unit = 0;
       }
+      *reinterpret_cast<float2*>(&rates[n & 1][0][lane * 2]) = rt.A;
+      *reinterpret_cast<float2*>(&rates[n & 1][1][lane * 2]) = rt.bias;
       __syncwarp();
+      mbar_arrive_if(lane == 0, &full[n & 1]);
       if (!there) {
         ++n;
         break;
@@ -817,12 +855,9 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
         if (t.rows == 0) {
           end = it;
         } else {
-          const int c = t.col0 + c4;
-          float2 A[2] = {both(1.f), both(1.f)}, bias[2] = {both(0.f), both(0.f)};
-          if (c < P.D && P.A) load_row(P.A + c, A[0], A[1]);
-          if (c < P.D && P.bias) load_row(P.bias + c, bias[0], bias[1]);
-          bias[0] = mul2(bias[0], K.log2e);
-          bias[1] = mul2(bias[1], K.log2e);
+          float2 A[2], bias[2];
+          load_row(&rates[it & 1][0][c4], A[0], A[1]);
+          load_row(&rates[it & 1][1][c4], bias[0], bias[1]);
           const int u1 = unit + 1 < kUnits ? unit + 1 : 0, u2 = u1 + 1 < kUnits ? u1 + 1 : 0;
           const T* bza = reinterpret_cast<const T*>(smem + unit * Sh::kUnitBytes + from);
           const T* bzb = reinterpret_cast<const T*>(smem + u1 * Sh::kUnitBytes + from);
@@ -915,8 +950,11 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
 #pragma unroll 1
       for (int r4 = 0; r4 < R; r4 += 4) {
         float2 a[8], b[8];
-        unpark16(park + slot * Sh::kSlotCols + r4 * 8, a);
-        unpark16(park + slot * Sh::kSlotCols + r4 * 8 + 16, b);
+        ask16(park + slot * Sh::kSlotCols + r4 * 8, a);
+        ask16(park + slot * Sh::kSlotCols + r4 * 8 + 16, b);
+        asked();
+        here(a);
+        here(b);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           h[0] = fma2(a[2 * r], h[0], b[2 * r]);
@@ -974,18 +1012,6 @@ __device__ __forceinline__ void take_a(const __nv_bfloat16* za, const __nv_bfloa
   lo = *reinterpret_cast<const float2*>(za);
   hi = *reinterpret_cast<const float2*>(zb);
 }
-// Four columns of tensor memory.
-__device__ __forceinline__ void unpark4(uint32_t taddr, float2& lo, float2& hi) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n"
-               : "=f"(lo.x), "=f"(lo.y), "=f"(hi.x), "=f"(hi.y)
-               : "r"(taddr)
-               : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+f"(lo.x), "+f"(lo.y), "+f"(hi.x), "+f"(hi.y)
-               :
-               : "memory");
-}
-
 struct BackwardArgs {
   CUtensorMap za, zb, v, dy;
   Packed packed;
@@ -1048,6 +1074,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
   __shared__ __align__(16) float whole[2][kCols];
   __shared__ __align__(16) float carry[2][kCols];
   __shared__ __align__(16) float sums[W][2][kCols];            // of the gradients of A and bias
+  __shared__ __align__(16) float rates[kBackStages][2][kCols]; // A, bias
   __shared__ uint32_t tmem_base;
   __shared__ int quit;
   volatile int* gave_up = &quit;
@@ -1060,7 +1087,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
   if (tid == 0) {
     for (int s = 0; s < kBackStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);              // copies asked for, rates there
       mbar_init(&empty[s], W);
     }
     for (int s = 0; s < kBackInfo; ++s) mbar_init(&known[s], 1);
@@ -1085,7 +1112,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
     bool more = true;
     int n = 0;
     for (; more; ++n) {
-      Tile t;
+      Tile t{};
       more = fetch<L, true>(
           P.packed, order, P.chain, P.tiles, P.col_tiles, ticket, t, [&](const Tile& e) {
             const int c = e.col0 + lane * 2;
@@ -1100,6 +1127,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
             }
           });
       const int st = n % kBackStages;
+      const Rates rt = rates_of(P.A, P.bias, more ? t.col0 + lane * 2 : P.D, P.D);
       if (n >= kBackStages && !wait_phase(&empty[st], (n / kBackStages - 1) & 1, gave_up)) break;
       if (lane == 0) {
         tiles[n % kBackInfo] = t;
@@ -1115,7 +1143,10 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
           mbar_arrive(&full[st]);
         }
       }
+      *reinterpret_cast<float2*>(&rates[st][0][lane * 2]) = rt.A;
+      *reinterpret_cast<float2*>(&rates[st][1][lane * 2]) = rt.bias;
       __syncwarp();
+      mbar_arrive_if(lane == 0, &full[st]);
     }
     // Stay until every copy has arrived, also when the block gives up.
     for (int x = n > kBackStages ? n - kBackStages : 0; x < n; ++x)
@@ -1235,11 +1266,9 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
       }
       const int c = t.col0 + c4;
       const bool in = c < P.D;
-      float2 A[2] = {both(1.f), both(1.f)}, bias[2] = {both(0.f), both(0.f)};
-      if (in && P.A) load_row(P.A + c, A[0], A[1]);
-      if (in && P.bias) load_row(P.bias + c, bias[0], bias[1]);
-      bias[0] = mul2(bias[0], K.log2e);
-      bias[1] = mul2(bias[1], K.log2e);
+      float2 A[2], bias[2];
+      load_row(&rates[st][0][c4], A[0], A[1]);
+      load_row(&rates[st][1][c4], bias[0], bias[1]);
       T* bza = reinterpret_cast<T*>(smem + st * Sh::kStageBytes) + first * kCols + c4;
       T* bzb = bza + L * kCols;
       T* bv = bzb + L * kCols;
@@ -1247,7 +1276,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
       // Gates, set aside, and the pairs of this half-warp's rows: (p, s) of
       // the states, (p, q) of the gradients.
       float2 p[2] = {both(1.f), both(1.f)}, s[2] = {both(0.f), both(0.f)}, q[2] = {both(0.f), both(0.f)};
-#pragma unroll 2
+#pragma unroll 1
       for (int r = 0; r < R; ++r) {
         float2 za[2], zb[2], v[2], dy[2];
         load_row(bza + r * kCols, za[0], za[1]);
@@ -1288,15 +1317,22 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
       float2 h[2], w[R][2];
       load_row(&half[hw][1][c4], h[0], h[1]);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float2 a[2], beta[2], v[2];
-        take_a(bza + r * kCols, bzb + r * kCols, a[0], a[1]);
-        unpark4(park + r * 16, beta[0], beta[1]);
-        load_row(bv + r * kCols, v[0], v[1]);
+      for (int r4 = 0; r4 < R; r4 += 4) {
+        float2 beta[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          w[r][k] = mul2(a[k], h[k]);
-          h[k] = fma2(beta[k], v[k], w[r][k]);
+        for (int r = 0; r < 4; ++r) ask4(park + (r4 + r) * 16, beta[2 * r], beta[2 * r + 1]);
+        asked();
+        here(beta);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float2 a[2], v[2];
+          take_a(bza + (r4 + r) * kCols, bzb + (r4 + r) * kCols, a[0], a[1]);
+          load_row(bv + (r4 + r) * kCols, v[0], v[1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            w[r4 + r][k] = mul2(a[k], h[k]);
+            h[k] = fma2(beta[2 * r + k], v[k], w[r4 + r][k]);
+          }
         }
       }
       float2 rr[2], bp[2], bq[2];
@@ -1314,7 +1350,9 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) {
         float2 a[2], v[2], dy[2], m[8];
-        unpark16(park + r * 16, m);
+        ask16(park + r * 16, m);
+        asked();
+        here(m);
         take_a(bza + r * kCols, bzb + r * kCols, a[0], a[1]);
         load_row(bv + r * kCols, v[0], v[1]);
         load_row(bdy + r * kCols, dy[0], dy[1]);

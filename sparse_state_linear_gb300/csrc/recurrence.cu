@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
           unit = u2 + 1 < kUnits ? u2 + 1 : 0;
           // Four rows at a time: gates, the pair of all rows so far, aside.
           float2 p[2] = {both(1.f), both(1.f)}, s[2] = {both(0.f), both(0.f)};
-#pragma unroll 1
+#pragma unroll
           for (int r4 = 0; r4 < R; r4 += 4) {
             float2 a[8], b[8];
 #pragma unroll
@@ -947,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       }
       T* y = reinterpret_cast<T*>(P.y) + (size_t)(t.row0 + first) * P.D + c;
       int left = c < P.D ? t.rows - first : 0;                 // rows to store
-#pragma unroll 1
+#pragma unroll
       for (int r4 = 0; r4 < R; r4 += 4) {
         float2 a[8], b[8];
         ask16(park + slot * Sh::kSlotCols + r4 * 8, a);
@@ -1038,14 +1038,19 @@ struct BackwardArgs {
 //
 // A block is four warps for the arithmetic (a half-warp takes R rows) and
 // three more: one fetches tiles, one sums up the half-warps' pairs and
-// publishes, one folds.  Of a tile's gates, a goes into shared memory and the
-// rest into tensor memory, so that three blocks fit an SM.
+// publishes, one folds.  Of a tile's gates, a goes into shared memory, in the
+// place of za and zb, and the rest into tensor memory.
+// Blocks per SM, measured: at 32768 x 1024 bf16 107 us with two (no limit on
+// the registers), 113 with three; at 10007 x 1000 float32, whose tiles are half
+// as long, 75 and 69.  Finishing a tile one tile later, as the forward pass
+// does, leaves room for two blocks only: 120 and 68 us.
 constexpr int kBackWarps = 4;
 constexpr int kHalves = 2 * kBackWarps;
 constexpr int kBackStages = 2;
 constexpr int kBackInfo = 4;
 constexpr int kBackThreads = (kBackWarps + 3) * 32;
-constexpr int kBackBlocks = 3;
+template <typename T>
+constexpr int kBackBlocks = sizeof(T) == 2 ? 2 : 3;
 
 template <typename T>
 struct BackwardShape {
@@ -1059,10 +1064,10 @@ struct BackwardShape {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kBackThreads, kBackBlocks)
+__global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
     backward_kernel(const __grid_constant__ BackwardArgs P) {
   using Sh = BackwardShape<T>;
-  constexpr int L = Sh::L, R = Sh::R, W = kBackWarps;
+  constexpr int L = Sh::L, R = Sh::R, W = kBackWarps, kUnroll = sizeof(T) == 2 ? 2 : 1;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((128 - (smem_u32(raw) & 127)) & 127);
   __shared__ uint64_t full[kBackStages], empty[kBackStages], known[kBackInfo], paired, summed[2],
@@ -1276,7 +1281,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
       // Gates, set aside, and the pairs of this half-warp's rows: (p, s) of
       // the states, (p, q) of the gradients.
       float2 p[2] = {both(1.f), both(1.f)}, s[2] = {both(0.f), both(0.f)}, q[2] = {both(0.f), both(0.f)};
-#pragma unroll 1
+#pragma unroll kUnroll
       for (int r = 0; r < R; ++r) {
         float2 za[2], zb[2], v[2], dy[2];
         load_row(bza + r * kCols, za[0], za[1]);
@@ -1347,12 +1352,16 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks)
       A[1] = sub2(both(0.f), A[1]);
       const size_t o = (size_t)(t.row0 + first) * P.ld_grad + c;
       const int left = in ? t.rows - first : 0;
+      float2 ahead[8];
+      ask16(park + (R - 1) * 16, ahead);
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) {
         float2 a[2], v[2], dy[2], m[8];
-        ask16(park + r * 16, m);
         asked();
-        here(m);
+        here(ahead);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = ahead[i];
+        if (r > 0) ask16(park + (r - 1) * 16, ahead);
         take_a(bza + r * kCols, bzb + r * kCols, a[0], a[1]);
         load_row(bv + r * kCols, v[0], v[1]);
         load_row(bdy + r * kCols, dy[0], dy[1]);
@@ -1660,7 +1669,7 @@ cudaError_t backward_as(const RecurrenceDims& d, const RecurrenceInputs& in, con
   cudaError_t e = allow_smem(kernel, Sh::kSmem, allowed);
   if (e == cudaSuccess) e = clear_chain(workspace, d, L, stream);
   if (e != cudaSuccess) return e;
-  const unsigned most = (unsigned)(kBackBlocks * device_limits().sms);
+  const unsigned most = (unsigned)(kBackBlocks<T> * device_limits().sms);
   kernel<<<P.tiles < most ? P.tiles : most, kBackThreads, Sh::kSmem, stream>>>(P);
   e = cudaGetLastError();
   if (e != cudaSuccess || (!dA && !dbias)) return e;

@@ -84,6 +84,15 @@ def test_many_chunks_carry_the_state():
         check(x, None, sdm.SDM_F32, n_seq)
 
 
+@BOTH
+def test_many_tiles_per_block(dtype):
+    # More tiles than the grid holds several times over, so that the blocks'
+    # rings of stages and descriptions go round; packed and equal sequences.
+    off = offsets(5, 1200, 1200, 1201, 2990)
+    check(draw(3000, 2056, 4, dtype, seed=51), off, dtype, 4)
+    check(draw(2400, 2056, 2, dtype, seed=52), None, dtype, 2)
+
+
 def test_no_rate_and_no_bias():
     x = draw(300, 64, 3, sdm.SDM_F32, seed=5, h0=False)
     check(x, None, sdm.SDM_F32, 3, A="none", bias="none")

@@ -300,7 +300,7 @@ size_t sdm_recurrence_states_size(const sdm_recurrence* shape);
 
 /* Forward pass.
  *   za, zb, v: [rows, D] (rows ld apart); A, bias: [D] float32, NULL = ones /
- *   zeros; offsets: see above, or NULL;
+ *   zeros, A not negative; offsets: see above, or NULL;
  *   h0: [n_seq, D] float32 initial states, or NULL for zeros;
  *   y:  [rows, D] out;  hT: [n_seq, D] float32 final states out, or NULL (may
  *   be h0 itself: states updated in place);
@@ -369,7 +369,8 @@ typedef struct {
  *   stream updated in place);
  *   out: [rows, D] in out_dtype: SDM_F32, SDM_BF16 or SDM_E4M3;
  *   group: 0, 32, 64 or 128 (dividing D; 0 unless out_dtype is SDM_E4M3);
- *   scale: [rows] or [rows, D / group] float32 out, for SDM_E4M3 only. */
+ *   scale: [rows] or [rows, D / group] float32 out, for SDM_E4M3 only.
+ * out and scale must not overlap an input or s. */
 sdm_status sdm_add_rmsnorm(const sdm_norm* shape, const void* x, const void* residual,
                            const float* gamma, float eps, void* s, void* out,
                            sdm_dtype out_dtype, int group, float* scale, void* stream);

@@ -23,7 +23,7 @@ namespace sdm {
 namespace {
 
 // ------------------------------------------------------------------- gates
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // log2(1 + e) for e in [0, 1]: 2 log2(e) atanh(t) with t = e / (2 + e), as t
 // times the degree-4 polynomial in t^2 that interpolates the rest at the
@@ -36,42 +36,13 @@ __device__ __forceinline__ float log2p1_unit(float e) {
   const float t = e * rcp(e + 2.f), z = t * t;
   return t * fmaf(fmaf(fmaf(fmaf(kLog4, z, kLog3), z, kLog2), z, kLog1), z, kLog0);
 }
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct Gate {
-  float sp;      // softplus(za + bias)
-  float sig;     // sigmoid(za + bias)
-  float alpha;   // exp(-A sp)
-  float beta;    // sigmoid(zb)
-  float keep;    // 1 - beta, to full relative precision
-};
-
-__device__ __forceinline__ Gate make_gate(float za, float zb, float A, float bias) {
-  Gate g;
-  const float x = za + bias;
-  const float e = ex2(-fabsf(x) * kLog2e);
-  g.sp = fmaxf(x, 0.f) + kLn2 * log2p1_unit(e);
-  g.alpha = ex2(-A * kLog2e * g.sp);
-  const float r = rcp(1.f + e);
-  g.sig = x >= 0.f ? r : e * r;
-  const float eb = ex2(-fabsf(zb) * kLog2e);
-  const float rb = rcp(1.f + eb);
-  g.beta = zb >= 0.f ? rb : eb * rb;
-  g.keep = zb >= 0.f ? eb * rb : rb;
-  return g;
-}
-
-__device__ __forceinline__ void store_scalar(void* base, size_t i, int dt, float x) {
-  if (dt == SDM_F32)
-    reinterpret_cast<float*>(base)[i] = x;
-  else
-    reinterpret_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(x);
-}
-
+// One row of one channel: the state behind it.
 __device__ __forceinline__ float step_one(float h, float za, float zb, float v, float A,
                                           float bias) {
-  const Gate g = make_gate(za, zb, A, bias);
-  return fmaf(g.keep * g.alpha, h, g.beta * v);
+  const float x = za + bias, e = ex2(-fabsf(x) * kLog2e);
+  const float sp = fmaxf(x, 0.f) * kLog2e + log2p1_unit(e);
+  const float z = max_nan(zb * kLog2e, -126.f), beta = rcp(1.f + ex2(-z));   // see sigmoid_pair
+  return fmaf(beta * ex2(-fmaf(A, sp, z)), h, beta * v);
 }
 
 __device__ __forceinline__ float4 load4(const void* base, size_t i, int dt) {
@@ -181,7 +152,6 @@ __device__ bool offsets_ok(const Packed& P) {
 template <typename T>
 constexpr int kStateRows = 128 / (int)sizeof(T);
 
-
 // --------------------------------------------------------------------- scan
 // A (or ones) and bias (or zeros) times log2(e) of a tile's channels, brought
 // to shared memory by the warp that fetches it, two channels a lane.
@@ -201,7 +171,7 @@ struct __align__(16) Tile {
   int rows;      // valid rows, 1..L; 0: no tile is left
   int row0;      // first row
   int seq, chunk;
-  int number;    // of the chunk, indexes flags and data
+  int number;    // of the chunk, indexes what chunks publish
   int back;      // number - back is the chunk before along the chain
   int col0;      // first channel
   int pos;       // along the chain: chunks before it (after it, in the backward pass)
@@ -221,9 +191,9 @@ __device__ __forceinline__ unsigned next_ticket(const Chain& c) {
   return atomicAdd(c.ticket, 1u) + 1u;
 }
 
-// Chunks per group, see fold_before.  Measured at 131072 x 2048 bf16, forward: 407
-// us with 4, 409 with 8, 420 with 16, 459 with 32; backward at 10007 x 1000
-// float32: 108, 97, 108, 112 us.
+// Chunks per group, see fold_before.  Measured, forward at 131072 x 2048 bf16 and
+// backward at 10007 x 1000 float32: 409 and 98 us with 6, 412 and 93 with 8, 431
+// and 115 with 12, 440 and 109 with 16 (a fold waits for and reads more).
 constexpr int kGroup = 8;
 constexpr unsigned long long kWaitNs = 4000000000ull;         // limit of every wait
 
@@ -257,9 +227,8 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
-// Test of an mbarrier phase that lets the thread sleep until it completes, for
-// about ten microseconds at most (a warp that spins takes issue slots from the
-// arithmetic).
+// Test of an mbarrier phase that may let the thread sleep for a while until it
+// completes (a warp that spins takes issue slots from the arithmetic).
 __device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, unsigned parity) {
   uint32_t ok;
   asm volatile(
@@ -636,6 +605,12 @@ __device__ __forceinline__ void here(float2 (&v)[N]) {
 // is out.  So the arithmetic warps do not wait for it: they form a tile's
 // gates, put a and b aside in tensor memory (which nothing else here uses),
 // go on to the next tile, and only then come back to finish the one before.
+//
+// Measured at 131072 x 2048 bf16: 379 us, 2.15 GB once = 0.85 of the copy rate;
+// at 9001 x 1920 float32 in 13 sequences 50 us, 0.82.  With every gate left out
+// (a = za + zb, b = v) the first takes 336 us: what bounds it is the arithmetic,
+// about 20 instructions of every element's 38, on 65% of the issue slots.  A first
+// form in which the block waited for each tile's state took 791 us.
 //
 // Inputs come in units of one tensor's tile (16 KB), in a ring of kUnits.
 // Barriers, all in shared memory: a tile's description is there (known), its

@@ -93,6 +93,19 @@ def test_many_tiles_per_block(dtype):
     check(draw(2400, 2056, 2, dtype, seed=52), None, dtype, 2)
 
 
+@BOTH
+def test_thousands_of_short_sequences(dtype):
+    g = torch.Generator().manual_seed(7)
+    lens = torch.randint(0, 4, (3001,), generator=g)
+    lens[1500] = 700                                 # and a long one among them
+    off = torch.cat([torch.zeros(1, dtype=torch.long), lens.cumsum(0)]).to(torch.int32).to(DEV)
+    check(draw(int(lens.sum()), 72, 3001, dtype, seed=61), off, dtype, 3001)
+
+
+def test_widest_rows():
+    check(draw(5, 65536, 2, sdm.SDM_BF16, seed=62), offsets(0, 2, 5), sdm.SDM_BF16, 2)
+
+
 def test_no_rate_and_no_bias():
     x = draw(300, 64, 3, sdm.SDM_F32, seed=5, h0=False)
     check(x, None, sdm.SDM_F32, 3, A="none", bias="none")
@@ -371,6 +384,18 @@ def test_step_padding_bad_and_repeated_slots():
             assert torch.equal(state[s], clean[s] if s in touched else state0[s]), (slots, s)
 
 
+@BOTH
+def test_step_on_columns_of_one_projection(dtype):
+    rows, D = 19, 40
+    x = draw(rows, D, rows, dtype, seed=14)
+    wide = torch.cat([x["za"], x["zb"], x["v"]], 1)
+    cols = [wide[:, i * D:(i + 1) * D] for i in range(3)]
+    a, b = x["h0"].clone(), x["h0"].clone()
+    y = sdm.sdm_recurrence_step(sdm.make_recurrence(1, rows, D, dtype=dtype, ld=3 * D), *cols, a, A=x["A"], bias=x["bias"])
+    z = sdm.sdm_recurrence_step(sdm.make_recurrence(1, rows, D, dtype=dtype), x["za"], x["zb"], x["v"], b, A=x["A"], bias=x["bias"])
+    assert torch.equal(y, z) and torch.equal(a, b)
+
+
 def test_step_on_many_rows():
     # More rows than a grid's second dimension has blocks.
     rows, D = 70001, 8
@@ -440,6 +465,23 @@ def test_two_calls_at_once():
         torch.cuda.synchronize()
         for p, q in zip(want, got):
             assert torch.equal(p, q)
+
+
+def test_two_backward_calls_at_once():
+    shapes = [(draw(6000, 520, 2, sdm.SDM_BF16, seed=s), sdm.make_recurrence(2, 6000, 520)) for s in (3, 4)]
+    states = [sdm.sdm_recurrence_forward(sh, x["za"], x["zb"], x["v"], A=x["A"], bias=x["bias"], save_states=True)["states"]
+              for x, sh in shapes]
+    call = lambda i, **kw: sdm.sdm_recurrence_backward(shapes[i][1], *(shapes[i][0][k] for k in ("za", "zb", "v")), states[i],
+                                                       shapes[i][0]["dy"], A=shapes[i][0]["A"], bias=shapes[i][0]["bias"], **kw)
+    want = [call(i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in shapes]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [call(i, stream=streams[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        for p, q in zip(want, got):
+            assert all(torch.equal(p[k], q[k]) for k in p)
+    assert sdm.sdm_get_device_status() == 0
 
 
 def test_elements_beyond_32_bits():

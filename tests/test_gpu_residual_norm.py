@@ -11,6 +11,8 @@ sdm = pytest.importorskip("sparse_state_linear_gb300")
 DEV = "cuda:0"
 DT = {sdm.SDM_F32: torch.float32, sdm.SDM_BF16: torch.bfloat16}
 BOTH = pytest.mark.parametrize("dtype", [sdm.SDM_F32, sdm.SDM_BF16], ids=["f32", "bf16"])
+# Enough rows to fill the GPU (at 8 an SM another form takes over), and fewer.
+MANY = [(1301, 512), (1217, 1000), (1300, 2056), (1216, 4104), (1217, 256), (1220, 8200)]
 SIZES = [(1, 8), (3, 32), (7, 64), (64, 1920), (5, 1000), (33, 128), (2, 16384), (301, 520), (4, 8200), (9, 4096), (11, 2048)]
 
 
@@ -29,7 +31,7 @@ def draw(rows, D, dtype, seed=0):
 
 
 @BOTH
-@pytest.mark.parametrize("rows,D", SIZES)
+@pytest.mark.parametrize("rows,D", SIZES + MANY)
 def test_forward(rows, D, dtype):
     x = draw(rows, D, dtype)
     sh = sdm.make_norm(rows, D, dtype=dtype)
@@ -66,7 +68,8 @@ def check_quantised(r, y, E, group):
 
 @BOTH
 @pytest.mark.parametrize("rows,D,group", [(1, 8, 0), (64, 1920, 0), (64, 1920, 128), (5, 1000, 0), (33, 96, 32), (7, 4160, 64),
-                                          (2, 16384, 128), (301, 512, 32), (9, 8200, 0), (3, 128, 128), (6, 2112, 64)])
+                                          (2, 16384, 128), (301, 512, 32), (9, 8200, 0), (3, 128, 128), (6, 2112, 64),
+                                          (1217, 1000, 0), (1301, 512, 128), (1300, 2112, 32), (1216, 4096, 64), (1217, 8200, 0)])
 def test_eight_bits(rows, D, group, dtype):
     x = draw(rows, D, dtype)
     x["x"][0] *= 1e-3
@@ -115,7 +118,7 @@ def test_residual_stream_in_place(dtype):
 
 
 @BOTH
-@pytest.mark.parametrize("rows,D", SIZES + [(2000, 136)])
+@pytest.mark.parametrize("rows,D", SIZES + MANY + [(2000, 136)])
 def test_backward(rows, D, dtype):
     x = draw(rows, D, dtype, seed=1)
     sh = sdm.make_norm(rows, D, dtype=dtype)

@@ -456,8 +456,8 @@ def sdm_measure_row_traffic(src, dst, col_slice: int, T: int, loads: int, stores
 
 _TORCH = {SDM_F32: torch.float32, SDM_BF16: torch.bfloat16, SDM_E4M3: torch.float8_e4m3fn}
 _F32, _I32 = torch.float32, torch.int32
-_device_now = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_device_now = getattr(torch._C, "_cuda_getDevice", None)               # None: torch without CUDA
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _torch_dtype(dtype: int, what: str) -> torch.dtype:

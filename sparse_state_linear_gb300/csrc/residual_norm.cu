@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "packed.cuh"
 
 namespace sdm {
@@ -143,6 +144,7 @@ struct ForwardArgs {
 
 template <typename T, int TW, int NV, int kOut>
 __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P) {
+  wait_for_stream();
   __shared__ float red[2][kTeams<TW>][TW][1];
   __shared__ uint32_t redmax[2][kTeams<TW>][TW];
   const int team = threadIdx.x / (TW * 32), lane = threadIdx.x % (TW * 32), D = P.D;
@@ -262,6 +264,7 @@ struct BackwardArgs {
 // the end, the blocks by column_sums_kernel.
 template <typename T, int TW, int NV>
 __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs P) {
+  wait_for_stream();
   __shared__ float red[2][kTeams<TW>][TW][2];
   extern __shared__ __align__(16) float teams[];   // [kTeams - 1][TW * NV * 256]
   const int team = threadIdx.x / (TW * 32), lane = threadIdx.x % (TW * 32), D = P.D;
@@ -398,6 +401,7 @@ __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs
 // block, each of 32 warps every 32nd part, then the warps.
 __global__ void __launch_bounds__(1024)
     column_sums_kernel(const float* partial, int parts, int D, float* out) {
+  wait_for_stream();
   __shared__ float warps[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float a = 0.f;
@@ -438,13 +442,10 @@ cudaError_t forward_as(const ForwardArgs& P, int out_dtype, cudaStream_t stream)
   const long long want = ((long long)P.rows + kTeams<TW> - 1) / kTeams<TW>;
   const long long most = 1 << 20;
   const unsigned blocks = (unsigned)(want < most ? want : most);
-  if (out_dtype == SDM_E4M3)
-    forward_kernel<T, TW, NV, SDM_E4M3><<<blocks, kBlock<TW>, 0, stream>>>(P);
-  else if (out_dtype == SDM_BF16)
-    forward_kernel<T, TW, NV, SDM_BF16><<<blocks, kBlock<TW>, 0, stream>>>(P);
-  else
-    forward_kernel<T, TW, NV, SDM_F32><<<blocks, kBlock<TW>, 0, stream>>>(P);
-  return cudaGetLastError();
+  const auto kernel = out_dtype == SDM_E4M3   ? forward_kernel<T, TW, NV, SDM_E4M3>
+                      : out_dtype == SDM_BF16 ? forward_kernel<T, TW, NV, SDM_BF16>
+                                              : forward_kernel<T, TW, NV, SDM_F32>;
+  return launch_behind(kernel, blocks, kBlock<TW>, 0, stream, P);
 }
 
 template <typename T, int TW, int NV>
@@ -455,11 +456,10 @@ cudaError_t backward_as(const BackwardArgs& P, float* dgamma, cudaStream_t strea
   const long long want = ((long long)P.rows + kTeams<TW> - 1) / kTeams<TW>;
   const int most = blocks_per_sm(kernel, kBlock<TW>, smem, cache) * device_limits().sms;
   const int blocks = (int)(want < most ? want : most);
-  kernel<<<blocks, kBlock<TW>, smem, stream>>>(P);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(kernel, blocks, kBlock<TW>, smem, stream, P);
   if (e != cudaSuccess || !dgamma) return e;
-  column_sums_kernel<<<(P.D + 31) / 32, 1024, 0, stream>>>(P.partial, blocks, P.D, dgamma);
-  return cudaGetLastError();
+  return launch_behind(column_sums_kernel, (P.D + 31) / 32, 1024, 0, stream, P.partial, blocks, P.D,
+                       dgamma);
 }
 
 // Calls f with the team for rows of D channels: a thread takes 32 bytes of a

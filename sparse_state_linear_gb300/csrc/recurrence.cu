@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "packed.cuh"
 #include "tcgen05.cuh"
 
@@ -178,7 +179,7 @@ struct __align__(16) Tile {
   int last;      // the chain's last chunk
 };
 
-// Workspace of one call, cleared to all ones by one memset: a header (ticket
+// Workspace of one call, cleared to all ones by clear_kernel: a header (ticket
 // counter, from 2^32 - 1 on; abort word, 0 once a block has given up) and a pair
 // (P, S) of floats per chunk and channel.
 struct Chain {
@@ -683,10 +684,6 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   volatile int* gave_up = &quit;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (!offsets_ok(P.packed)) {
-    if (tid == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
-    return;
-  }
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -706,6 +703,12 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  wait_for_stream();
+  if (!offsets_ok(P.packed)) {
+    if (tid == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+    if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
+    return;
+  }
 
   if (warp == W) {                         // fetches
     unsigned ticket = 0;
@@ -1060,10 +1063,6 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
   volatile int* gave_up = &quit;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (!offsets_ok(P.packed)) {
-    if (tid == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
-    return;
-  }
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
   if (tid == 0) {
     for (int s = 0; s < kBackStages; ++s) {
@@ -1082,6 +1081,12 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  wait_for_stream();
+  if (!offsets_ok(P.packed)) {
+    if (tid == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+    if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
+    return;
+  }
 
   if (warp == W) {                         // fetches
     unsigned ticket = 0;
@@ -1384,12 +1389,23 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
   }
 }
 
+// The workspace of a call, all ones.  (A memset would do, but the kernels behind
+// it could then not be launched before it has ended.)
+constexpr int kClearThreads = 256;
+__global__ void __launch_bounds__(kClearThreads) clear_kernel(uint4* p, size_t n) {
+  wait_for_stream();
+  for (size_t i = (size_t)blockIdx.x * kClearThreads + threadIdx.x; i < n;
+       i += (size_t)gridDim.x * kClearThreads)
+    p[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
+}
+
 // Sums of the tiles' gradients of A and bias, always in the same order: 32
 // channels a block, each of 32 warps every 32nd chunk, then the warps.
 __global__ void __launch_bounds__(1024)
     column_sums_kernel(const Packed packed, const float* partial, int numbers, int D, float* dA,
                        float* dbias) {
   __shared__ float warps[2][32][33];
+  wait_for_stream();
   if (!offsets_ok(packed)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float a = 0.f, b = 0.f;
@@ -1429,6 +1445,7 @@ constexpr int kStepThreads = 128;
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const Args P, float* state,
                                                             int n_slots, const int32_t* slots,
                                                             int parts) {
+  wait_for_stream();
   const int D = P.d.D, dt = P.d.dtype;
   const long long blocks = (long long)P.d.rows * parts;
   for (long long w = blockIdx.x; w < blocks; w += gridDim.x) {
@@ -1495,7 +1512,10 @@ Chain chain_in(void* workspace) {
 }
 
 cudaError_t clear_chain(void* workspace, const RecurrenceDims& d, int L, cudaStream_t stream) {
-  return cudaMemsetAsync(workspace, 0xff, chain_bytes(d, L), stream);
+  const size_t n = chain_bytes(d, L) / 16;
+  const size_t most = (size_t)8 * device_limits().sms, want = (n + kClearThreads - 1) / kClearThreads;
+  return launch_behind(clear_kernel, (unsigned)(want < most ? want : most), kClearThreads, 0, stream,
+                       static_cast<uint4*>(workspace), n);
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1583,8 +1603,7 @@ cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, cons
   if (e == cudaSuccess) e = clear_chain(workspace, d, L, stream);
   if (e != cudaSuccess) return e;
   const unsigned most = (unsigned)(2 * device_limits().sms);
-  kernel<<<P.tiles < most ? P.tiles : most, kThreads, Sh::kSmem, stream>>>(P);
-  return cudaGetLastError();
+  return launch_behind(kernel, P.tiles < most ? P.tiles : most, kThreads, Sh::kSmem, stream, P);
 }
 
 }  // namespace
@@ -1647,12 +1666,10 @@ cudaError_t backward_as(const RecurrenceDims& d, const RecurrenceInputs& in, con
   if (e == cudaSuccess) e = clear_chain(workspace, d, L, stream);
   if (e != cudaSuccess) return e;
   const unsigned most = (unsigned)(kBackBlocks<T> * device_limits().sms);
-  kernel<<<P.tiles < most ? P.tiles : most, kBackThreads, Sh::kSmem, stream>>>(P);
-  e = cudaGetLastError();
+  e = launch_behind(kernel, P.tiles < most ? P.tiles : most, kBackThreads, Sh::kSmem, stream, P);
   if (e != cudaSuccess || (!dA && !dbias)) return e;
-  column_sums_kernel<<<(d.D + 31) / 32, 1024, 0, stream>>>(
-      P.packed, P.partial, (int)(P.tiles / P.col_tiles), d.D, dA, dbias);
-  return cudaGetLastError();
+  return launch_behind(column_sums_kernel, (unsigned)(d.D + 31) / 32, 1024, 0, stream, P.packed,
+                       (const float*)P.partial, (int)(P.tiles / P.col_tiles), d.D, dA, dbias);
 }
 
 }  // namespace
@@ -1686,8 +1703,7 @@ cudaError_t launch_recurrence_step(const RecurrenceDims& d, const RecurrenceInpu
   const int parts = (d.D / 4 + kStepThreads - 1) / kStepThreads;
   const long long want = (long long)d.rows * parts;
   const unsigned blocks = (unsigned)(want < (1 << 20) ? want : (1 << 20));
-  step_kernel<<<blocks, kStepThreads, 0, stream>>>(P, state, n_slots, slots, parts);
-  return cudaGetLastError();
+  return launch_behind(step_kernel, blocks, kStepThreads, 0, stream, P, state, n_slots, slots, parts);
 }
 
 }  // namespace sdm

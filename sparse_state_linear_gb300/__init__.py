@@ -461,9 +461,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _torch_dtype(dtype: int, what: str) -> torch.dtype:
-    if dtype not in _TORCH:
+    dt = _TORCH.get(dtype)
+    if dt is None:
         raise SdmError(1, what)
-    return _TORCH[dtype]
+    return dt
 
 
 def _where(like: torch.Tensor, stream):
@@ -479,7 +480,7 @@ def _where(like: torch.Tensor, stream):
                          f"cuda:{_device_now()}; call under torch.cuda.device({dev})")
     if stream is None:
         return dev, _raw_stream(dev), None
-    if hasattr(stream, "cuda_stream"):
+    if isinstance(stream, torch.cuda.Stream):
         return dev, stream.cuda_stream, stream
     raw = int(stream)
     return dev, raw, (torch.cuda.ExternalStream(raw, device=like.device) if raw
@@ -517,7 +518,10 @@ def _rows_at(t, name, dtype, rows, D, ld, dev):
     """Address of a [rows, D] tensor whose rows are `ld` elements apart
     (leading dimensions that flatten to `rows` are fine when ld = D)."""
     if ld == D:
-        return _at(t, name, dtype, rows * D, dev)
+        if (t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()
+                or t.numel() < rows * D):
+            _refuse(t, name, dtype, rows * D, dev)
+        return t.data_ptr()
     if t is None or t.dtype is not dtype or t.get_device() != dev:
         _refuse(t, name, dtype, rows * D, dev)
     if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != D:

@@ -8,7 +8,8 @@
 
 namespace sdm {
 
-// First statement of every kernel launched by launch_behind.
+// In front of the first access to global memory of every kernel launched by
+// launch_behind, in every thread.
 __device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }

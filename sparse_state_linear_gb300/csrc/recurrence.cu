@@ -1018,46 +1018,50 @@ struct BackwardArgs {
 // three more: one fetches tiles, one sums up the half-warps' pairs and
 // publishes, one folds.  Of a tile's gates, a goes into shared memory, in the
 // place of za and zb, and the rest into tensor memory.
-// Blocks per SM, measured: at 32768 x 1024 bf16 107 us with two (no limit on
-// the registers), 113 with three; at 10007 x 1000 float32, whose tiles are half
-// as long, 75 and 69.  Finishing a tile one tile later, as the forward pass
-// does, leaves room for two blocks only: 120 and 68 us.
+//
+// kLag: a tile is finished after the next one's gates, as in the forward pass,
+// so that a fold has a tile's time to come; otherwise at once, which takes less
+// memory and, in float32, leaves room for three blocks (75 us with two, 69 with
+// three at 10007 x 1000; bf16, 32768 x 1024: 108 with two and 113 with three, which
+// are short of registers).  See lags.
 constexpr int kBackWarps = 4;
 constexpr int kHalves = 2 * kBackWarps;
-constexpr int kBackStages = 2;
-constexpr int kBackInfo = 4;
 constexpr int kBackThreads = (kBackWarps + 3) * 32;
-template <typename T>
-constexpr int kBackBlocks = sizeof(T) == 2 ? 2 : 3;
 
-template <typename T>
+template <typename T, bool kLag>
 struct BackwardShape {
   static constexpr int R = 16 / sizeof(T);
   static constexpr int L = kHalves * R;
+  static constexpr int kBlocks = kLag || sizeof(T) == 2 ? 2 : 3;        // per SM
+  static constexpr int kUnits = kLag ? 11 : 8;   // places for tensors' tiles, four of a tile
+  static constexpr int kRing = kLag ? 4 : 2;     // barriers of tiles' copies
+  static constexpr int kOpen = kLag ? 2 : 1;     // tiles between gates and gradients
   static constexpr int kUnitBytes = L * kCols * (int)sizeof(T);
-  static constexpr int kStageBytes = 4 * kUnitBytes;
-  static constexpr int kSmem = kBackStages * kStageBytes + 128;
-  static constexpr int kTmemCols = 16 * R;
+  static constexpr int kSmem = kUnits * kUnitBytes + 128;
+  static constexpr int kOpenCols = 16 * R;
+  static constexpr int kTmemCols = kOpen * kOpenCols;
   static_assert(L == kStateRows<T>, "a saved state in front of every tile");
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
+template <typename T, bool kLag>
+__global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
     backward_kernel(const __grid_constant__ BackwardArgs P) {
-  using Sh = BackwardShape<T>;
-  constexpr int L = Sh::L, R = Sh::R, W = kBackWarps, kUnroll = sizeof(T) == 2 ? 2 : 1;
+  using Sh = BackwardShape<T, kLag>;
+  constexpr int L = Sh::L, R = Sh::R, W = kBackWarps, kRing = Sh::kRing, kOpen = Sh::kOpen;
+  // (With a lag, 32768 x 1024 bf16: 119 us rolled, 120 by two.)
+  constexpr int kUnroll = sizeof(T) == 2 && !kLag ? 2 : 1;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((128 - (smem_u32(raw) & 127)) & 127);
-  __shared__ uint64_t full[kBackStages], empty[kBackStages], known[kBackInfo], paired, summed[2],
-      folded[2];
-  __shared__ Tile tiles[kBackInfo];
+  __shared__ uint64_t full[kRing], empty[kRing], known[kInfo], paired[kOpen], summed[2],
+      folded[2], taken[2];
+  __shared__ Tile tiles[kInfo];
   // Of each half-warp's rows P, S (of the states) and Q (of the gradients); then
   // P of the rows behind them, the state in front of them, Q of the rows behind.
-  __shared__ __align__(16) float half[kHalves][3][kCols];
-  __shared__ __align__(16) float whole[2][kCols];
+  __shared__ __align__(16) float half[kOpen][kHalves][3][kCols];
+  __shared__ __align__(16) float whole[kOpen][2][kCols];
   __shared__ __align__(16) float carry[2][kCols];
-  __shared__ __align__(16) float sums[W][2][kCols];            // of the gradients of A and bias
-  __shared__ __align__(16) float rates[kBackStages][2][kCols]; // A, bias
+  __shared__ __align__(16) float sums[kOpen][W][2][kCols];     // of the gradients of A and bias
+  __shared__ __align__(16) float rates[kRing][2][kCols];       // A, bias
   __shared__ uint32_t tmem_base;
   __shared__ int quit;
   volatile int* gave_up = &quit;
@@ -1065,15 +1069,16 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
   if (tid == 0) {
-    for (int s = 0; s < kBackStages; ++s) {
+    for (int s = 0; s < kRing; ++s) {
       mbar_init(&full[s], 2);              // copies asked for, rates there
       mbar_init(&empty[s], W);
     }
-    for (int s = 0; s < kBackInfo; ++s) mbar_init(&known[s], 1);
-    mbar_init(&paired, W);
+    for (int s = 0; s < kInfo; ++s) mbar_init(&known[s], 1);
+    for (int s = 0; s < kOpen; ++s) mbar_init(&paired[s], W);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&summed[s], 1);
       mbar_init(&folded[s], 1);
+      mbar_init(&taken[s], W);
     }
     quit = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -1095,7 +1100,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
     if (P.packed.offsets)
       order = order_of<L>(P.packed, (int)(P.tiles / (unsigned)P.col_tiles), P.tiles > 2 * gridDim.x);
     bool more = true;
-    int n = 0;
+    int n = 0, unit = 0;                   // tiles asked for; place of the next unit
     for (; more; ++n) {
       Tile t{};
       more = fetch<L, true>(
@@ -1111,36 +1116,70 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
                   P.dhT ? *reinterpret_cast<const float2*>(P.dhT + i) : make_float2(0.f, 0.f);
             }
           });
-      const int st = n % kBackStages;
       const Rates rt = rates_of(P.A, P.bias, more ? t.col0 + lane * 2 : P.D, P.D);
-      if (n >= kBackStages && !wait_phase(&empty[st], (n / kBackStages - 1) & 1, gave_up)) break;
+      // With a lag, the places of the first three units held the last three of
+      // the tile three before, that of the fourth the first of the tile two
+      // before; up to three tiles' copies are under way, so full is a ring of
+      // four: its barrier of the tile four before has been waited for.
+      constexpr int kBehind = kLag ? 3 : 2;
+      if (n >= kBehind &&
+          !wait_phase(&empty[(n - kBehind) % kRing], ((n - kBehind) / kRing) & 1, gave_up))
+        break;
       if (lane == 0) {
-        tiles[n % kBackInfo] = t;
-        mbar_arrive(&known[n % kBackInfo]);
-        if (more) {
-          unsigned char* buf = smem + st * Sh::kStageBytes;
-          mbar_expect(&full[st], Sh::kStageBytes);
-          tma_load(buf, &P.za, t.col0, t.row0, &full[st]);
-          tma_load(buf + Sh::kUnitBytes, &P.zb, t.col0, t.row0, &full[st]);
-          tma_load(buf + 2 * Sh::kUnitBytes, &P.v, t.col0, t.row0, &full[st]);
-          tma_load(buf + 3 * Sh::kUnitBytes, &P.dy, t.col0, t.row0, &full[st]);
-        } else {
-          mbar_arrive(&full[st]);
-        }
+        tiles[n % kInfo] = t;
+        mbar_arrive(&known[n % kInfo]);
+        if (more)
+          mbar_expect(&full[n % kRing], 4 * Sh::kUnitBytes);
+        else
+          mbar_arrive(&full[n % kRing]);
       }
-      *reinterpret_cast<float2*>(&rates[st][0][lane * 2]) = rt.A;
-      *reinterpret_cast<float2*>(&rates[st][1][lane * 2]) = rt.bias;
       __syncwarp();
-      mbar_arrive_if(lane == 0, &full[st]);
+      bool there = true;
+      for (int j = 0; j < 4 && more; ++j) {
+        if (kLag && j == 3 && n >= 2)
+          there = wait_phase(&empty[(n - 2) % kRing], ((n - 2) / kRing) & 1, gave_up);
+        // Where the block gives up (its results are void then), the copy is made
+        // all the same, so that the barrier completes.
+        if (lane == 0)
+          tma_load(smem + unit * Sh::kUnitBytes,
+                   j == 0 ? &P.za : j == 1 ? &P.zb : j == 2 ? &P.v : &P.dy, t.col0, t.row0,
+                   &full[n % kRing]);
+        if (++unit == Sh::kUnits) unit = 0;
+      }
+      *reinterpret_cast<float2*>(&rates[n % kRing][0][lane * 2]) = rt.A;
+      *reinterpret_cast<float2*>(&rates[n % kRing][1][lane * 2]) = rt.bias;
+      __syncwarp();
+      mbar_arrive_if(lane == 0, &full[n % kRing]);
+      if (!there) {
+        ++n;
+        break;
+      }
     }
     // Stay until every copy has arrived, also when the block gives up.
-    for (int x = n > kBackStages ? n - kBackStages : 0; x < n; ++x)
-      mbar_wait_bounded(&full[x % kBackStages], (x / kBackStages) & 1, kWaitNs);
+    for (int x = n > kRing ? n - kRing : 0; x < n; ++x)
+      mbar_wait_bounded(&full[x % kRing], (x / kRing) & 1, kWaitNs);
   } else if (warp == W + 1) {              // sums up and publishes
-    Tile before;
+    Tile before{}, earlier{};              // the tile before this one, and before that
+    auto add_up = [&](int slot, float2& sa, float2& sb) {
+      sa = sb = both(0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        sa = add2(sa, *reinterpret_cast<const float2*>(&sums[slot][w][0][lane * 2]));
+        sb = add2(sb, *reinterpret_cast<const float2*>(&sums[slot][w][1][lane * 2]));
+      }
+    };
+    auto write_sums = [&](const Tile& t, float2 sa, float2 sb) {
+      const int c = t.col0 + lane * 2;
+      if (c < P.D) {
+        float* part = P.partial + (size_t)t.number * 2 * P.D + c;
+        *reinterpret_cast<float2*>(part) = sa;
+        *reinterpret_cast<float2*>(part + P.D) = sb;
+      }
+    };
     for (int it = 0;; ++it) {
-      if (!wait_phase(&known[it % kBackInfo], (it / kBackInfo) & 1, gave_up)) break;
-      const Tile t = tiles[it % kBackInfo];
+      const int slot = it % kOpen;
+      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, gave_up)) break;
+      const Tile t = tiles[it % kInfo];
       const int c = t.col0 + lane * 2;
       float2 h = make_float2(0.f, 0.f);
       if (t.rows > 0 && c < P.D) {
@@ -1148,14 +1187,14 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
         h = __ldg(reinterpret_cast<const float2*>(
             P.states + (size_t)(begin / L + t.seq + t.chunk) * P.D + c));
       }
-      if (!wait_phase(&paired, it & 1, gave_up)) break;
+      if (!wait_phase(&paired[slot], (it / kOpen) & 1, gave_up)) break;
       if (t.rows > 0) {
         // What others wait for goes out first.
         float2 wp[kHalves], wq[kHalves];
 #pragma unroll
         for (int w = 0; w < kHalves; ++w) {
-          wp[w] = *reinterpret_cast<const float2*>(&half[w][0][lane * 2]);
-          wq[w] = *reinterpret_cast<const float2*>(&half[w][2][lane * 2]);
+          wp[w] = *reinterpret_cast<const float2*>(&half[slot][w][0][lane * 2]);
+          wq[w] = *reinterpret_cast<const float2*>(&half[slot][w][2][lane * 2]);
         }
         float2 p = both(1.f), q = both(0.f);
 #pragma unroll
@@ -1165,15 +1204,15 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
         }
         if (!t.last) {
           if (publishes_state(t.pos)) {    // left to the fold
-            *reinterpret_cast<float2*>(&whole[0][lane * 2]) = p;
-            *reinterpret_cast<float2*>(&whole[1][lane * 2]) = q;
+            *reinterpret_cast<float2*>(&whole[slot][0][lane * 2]) = p;
+            *reinterpret_cast<float2*>(&whole[slot][1][lane * 2]) = q;
           } else if (c < P.D) {
             publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, p, q);
           }
         }
 #pragma unroll
         for (int w = 0; w < kHalves; ++w) {
-          float2* const ws = reinterpret_cast<float2*>(&half[w][1][lane * 2]);
+          float2* const ws = reinterpret_cast<float2*>(&half[slot][w][1][lane * 2]);
           const float2 s = *ws;
           *ws = h;
           h = fma2(wp[w], h, s);
@@ -1182,38 +1221,36 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
         q = both(0.f);
 #pragma unroll
         for (int w = kHalves - 1; w >= 0; --w) {
-          *reinterpret_cast<float2*>(&half[w][0][lane * 2]) = p;
-          *reinterpret_cast<float2*>(&half[w][2][lane * 2]) = q;
+          *reinterpret_cast<float2*>(&half[slot][w][0][lane * 2]) = p;
+          *reinterpret_cast<float2*>(&half[slot][w][2][lane * 2]) = q;
           q = fma2(wp[w], q, wq[w]);
           p = mul2(wp[w], p);
         }
       }
-      // The arithmetic warps are past the tile before: its sums are complete.
-      float2 sa = both(0.f), sb = both(0.f);
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        sa = add2(sa, *reinterpret_cast<const float2*>(&sums[w][0][lane * 2]));
-        sb = add2(sb, *reinterpret_cast<const float2*>(&sums[w][1][lane * 2]));
-      }
+      // The arithmetic warps have finished the tile kOpen before, and write its
+      // slot again only after this one has been summed up.
+      float2 sa, sb;
+      add_up(slot, sa, sb);
       if (t.rows > 0) {
         __syncwarp();
         mbar_arrive_if(lane == 0, &summed[it & 1]);
       }
-      if (it > 0) {
-        const int cb = before.col0 + lane * 2;
-        if (cb < P.D) {
-          float* part = P.partial + (size_t)before.number * 2 * P.D + cb;
-          *reinterpret_cast<float2*>(part) = sa;
-          *reinterpret_cast<float2*>(part + P.D) = sb;
+      if (it >= kOpen) write_sums(kLag ? earlier : before, sa, sb);
+      if (t.rows == 0) {
+        if (kLag && it > 0) {
+          add_up(slot ^ 1, sa, sb);
+          write_sums(before, sa, sb);
         }
+        break;
       }
-      if (t.rows == 0) break;
+      earlier = before;
       before = t;
     }
   } else if (warp == W + 2) {              // folds
     for (int it = 0;; ++it) {
-      if (!wait_phase(&known[it % kBackInfo], (it / kBackInfo) & 1, gave_up)) break;
-      const Tile t = tiles[it % kBackInfo];
+      const int slot = it % kOpen;
+      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, gave_up)) break;
+      const Tile t = tiles[it % kInfo];
       if (t.rows == 0) break;
       const int c = t.col0 + lane * 2;
       float2 r = make_float2(0.f, 0.f);
@@ -1224,13 +1261,14 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
         *gave_up = 1;
         break;
       }
-      // All warps are past the tile that last used this carry.
-      if (it > 0 && !wait_phase(&summed[(it - 1) & 1], ((it - 1) >> 1) & 1, gave_up)) break;
+      // The tile that last used this carry has been finished.
+      const int past = kLag ? it : it - 1;
+      if (past >= 0 && !wait_phase(&summed[past & 1], (past >> 1) & 1, gave_up)) break;
       *reinterpret_cast<float2*>(&carry[it & 1][lane * 2]) = r;
       if (!t.last && publishes_state(t.pos)) {
-        if (!wait_phase(&summed[it & 1], (it >> 1) & 1, gave_up)) break;
-        const float2 p = *reinterpret_cast<const float2*>(&whole[0][lane * 2]);
-        const float2 q = *reinterpret_cast<const float2*>(&whole[1][lane * 2]);
+        if (!kLag && !wait_phase(&summed[it & 1], (it >> 1) & 1, gave_up)) break;
+        const float2 p = *reinterpret_cast<const float2*>(&whole[slot][0][lane * 2]);
+        const float2 q = *reinterpret_cast<const float2*>(&whole[slot][1][lane * 2]);
         if (c < P.D)
           publish(P.chain.pairs + ((size_t)t.number * P.D + c) * 2, both(0.f), fma2(p, r, q));
       }
@@ -1241,71 +1279,93 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
     const Constants K = constants();
     const int c4 = (lane & 15) * 4, hw = tid >> 4, first = hw * R;
     const uint32_t park = tmem_base + ((uint32_t)warp << 21);
-    for (int it = 0;; ++it) {
-      const int st = it % kBackStages;
-      if (!wait_phase(&full[st], (it / kBackStages) & 1, gave_up)) break;
-      const Tile t = tiles[it % kBackInfo];
-      if (t.rows == 0) {                   // lets the last sums be written
-        mbar_arrive_if(lane == 0, &paired);
-        break;
+    // This half-warp's first row in the place of tensor j of the tile whose first
+    // unit is u (without a lag a tile never wraps around).
+    auto place = [&](int u, int j) {
+      if (kLag && u + j >= Sh::kUnits) u -= Sh::kUnits;
+      return reinterpret_cast<T*>(smem + u * Sh::kUnitBytes) + first * kCols + c4 +
+             j * (L * kCols);
+    };
+    int unit = 0, unit_before = 0;         // places of a tile's first unit
+    int end = 0x7fffffff;                  // number of this block's tiles, once known
+    int it = 0;
+    for (; it - (kOpen - 1) < end; ++it) {
+      const int finished = kLag ? unit_before : unit;
+      unit_before = unit;
+      if (it < end) {
+        const int slot = it % kOpen;
+        if (!wait_phase(&full[it % kRing], (it / kRing) & 1, gave_up)) break;
+        const Tile t = tiles[it % kInfo];
+        if (t.rows == 0) {
+          end = it;
+        } else {
+          float2 A[2], bias[2];
+          load_row(&rates[it % kRing][0][c4], A[0], A[1]);
+          load_row(&rates[it % kRing][1][c4], bias[0], bias[1]);
+          T *const bza = place(unit, 0), *const bzb = place(unit, 1), *const bv = place(unit, 2),
+                  *const bdy = place(unit, 3);
+          unit = unit + 4 < Sh::kUnits ? unit + 4 : unit + 4 - Sh::kUnits;
+          // Gates, set aside, and the pairs of this half-warp's rows: (p, s) of
+          // the states, (p, q) of the gradients.
+          float2 p[2] = {both(1.f), both(1.f)}, s[2] = {both(0.f), both(0.f)},
+                 q[2] = {both(0.f), both(0.f)};
+#pragma unroll kUnroll
+          for (int r = 0; r < R; ++r) {
+            float2 za[2], zb[2], v[2], dy[2];
+            load_row(bza + r * kCols, za[0], za[1]);
+            load_row(bzb + r * kCols, zb[0], zb[1]);
+            load_row(bv + r * kCols, v[0], v[1]);
+            load_row(bdy + r * kCols, dy[0], dy[1]);
+            Gates2 g[2];
+            g[0] = gates_pair(K, za[0], zb[0], A[0], bias[0]);
+            g[1] = gates_pair(K, za[1], zb[1], A[1], bias[1]);
+            if (first + r >= t.rows) {     // a row behind the sequence changes nothing
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                g[k].a = both(1.f);
+                g[k].beta = g[k].keep = g[k].sp = g[k].sig = v[k] = dy[k] = both(0.f);
+              }
+              store_row(bv + r * kCols, v[0], v[1]);
+              store_row(bdy + r * kCols, dy[0], dy[1]);
+            }
+            float2 aside[8] = {g[0].beta, g[1].beta, g[0].keep, g[1].keep,
+                               g[0].sp,   g[1].sp,   g[0].sig,  g[1].sig};
+            park16(park + slot * Sh::kOpenCols + r * 16, aside);
+            keep_a(bza + r * kCols, bzb + r * kCols, g[0].a, g[1].a);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              s[k] = fma2(g[k].a, s[k], mul2(g[k].beta, v[k]));
+              p[k] = mul2(g[k].a, p[k]);
+              q[k] = fma2(p[k], dy[k], q[k]);
+            }
+          }
+          if (kLag && it >= 2 && !wait_phase(&taken[it & 1], ((it >> 1) - 1) & 1, gave_up)) break;
+          store_row(&half[slot][hw][0][c4], p[0], p[1]);
+          store_row(&half[slot][hw][1][c4], s[0], s[1]);
+          store_row(&half[slot][hw][2][c4], q[0], q[1]);
+          parked();
+          __syncwarp();
+          mbar_arrive_if(lane == 0, &paired[slot]);
+        }
       }
+      const int out = it - (kOpen - 1);    // the tile to finish
+      if (out < 0 || out >= end) continue;
+      const int slot = out % kOpen;
+      const Tile t = tiles[out % kInfo];
       const int c = t.col0 + c4;
       const bool in = c < P.D;
-      float2 A[2], bias[2];
-      load_row(&rates[st][0][c4], A[0], A[1]);
-      load_row(&rates[st][1][c4], bias[0], bias[1]);
-      T* bza = reinterpret_cast<T*>(smem + st * Sh::kStageBytes) + first * kCols + c4;
-      T* bzb = bza + L * kCols;
-      T* bv = bzb + L * kCols;
-      T* bdy = bv + L * kCols;
-      // Gates, set aside, and the pairs of this half-warp's rows: (p, s) of
-      // the states, (p, q) of the gradients.
-      float2 p[2] = {both(1.f), both(1.f)}, s[2] = {both(0.f), both(0.f)}, q[2] = {both(0.f), both(0.f)};
-#pragma unroll kUnroll
-      for (int r = 0; r < R; ++r) {
-        float2 za[2], zb[2], v[2], dy[2];
-        load_row(bza + r * kCols, za[0], za[1]);
-        load_row(bzb + r * kCols, zb[0], zb[1]);
-        load_row(bv + r * kCols, v[0], v[1]);
-        load_row(bdy + r * kCols, dy[0], dy[1]);
-        Gates2 g[2];
-        g[0] = gates_pair(K, za[0], zb[0], A[0], bias[0]);
-        g[1] = gates_pair(K, za[1], zb[1], A[1], bias[1]);
-        if (first + r >= t.rows) {         // a row behind the sequence changes nothing
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            g[k].a = both(1.f);
-            g[k].beta = g[k].keep = g[k].sp = g[k].sig = v[k] = dy[k] = both(0.f);
-          }
-          store_row(bv + r * kCols, v[0], v[1]);
-          store_row(bdy + r * kCols, dy[0], dy[1]);
-        }
-        float2 aside[8] = {g[0].beta, g[1].beta, g[0].keep, g[1].keep,
-                           g[0].sp,   g[1].sp,   g[0].sig,  g[1].sig};
-        park16(park + r * 16, aside);
-        keep_a(bza + r * kCols, bzb + r * kCols, g[0].a, g[1].a);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          s[k] = fma2(g[k].a, s[k], mul2(g[k].beta, v[k]));
-          p[k] = mul2(g[k].a, p[k]);
-          q[k] = fma2(p[k], dy[k], q[k]);
-        }
-      }
-      store_row(&half[hw][0][c4], p[0], p[1]);
-      store_row(&half[hw][1][c4], s[0], s[1]);
-      store_row(&half[hw][2][c4], q[0], q[1]);
-      parked();
-      __syncwarp();
-      mbar_arrive_if(lane == 0, &paired);
+      const uint32_t at_park = park + slot * Sh::kOpenCols;
+      T *const bza = place(finished, 0), *const bzb = place(finished, 1),
+              *const bv = place(finished, 2), *const bdy = place(finished, 3);
+      if (!wait_phase(&summed[out & 1], (out >> 1) & 1, gave_up)) break;
       // w[r] = a h[r-1], the decayed state in front of each row.
-      if (!wait_phase(&summed[it & 1], (it >> 1) & 1, gave_up)) break;
       float2 h[2], w[R][2];
-      load_row(&half[hw][1][c4], h[0], h[1]);
+      load_row(&half[slot][hw][1][c4], h[0], h[1]);
 #pragma unroll
       for (int r4 = 0; r4 < R; r4 += 4) {
         float2 beta[8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) ask4(park + (r4 + r) * 16, beta[2 * r], beta[2 * r + 1]);
+        for (int r = 0; r < 4; ++r) ask4(at_park + (r4 + r) * 16, beta[2 * r], beta[2 * r + 1]);
         asked();
         here(beta);
 #pragma unroll
@@ -1321,19 +1381,25 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
         }
       }
       float2 rr[2], bp[2], bq[2];
-      load_row(&half[hw][0][c4], bp[0], bp[1]);
-      load_row(&half[hw][2][c4], bq[0], bq[1]);
-      if (!wait_phase(&folded[it & 1], (it >> 1) & 1, gave_up)) break;
-      load_row(&carry[it & 1][c4], rr[0], rr[1]);
+      load_row(&half[slot][hw][0][c4], bp[0], bp[1]);
+      load_row(&half[slot][hw][2][c4], bq[0], bq[1]);
+      if (!wait_phase(&folded[out & 1], (out >> 1) & 1, gave_up)) break;
+      load_row(&carry[out & 1][c4], rr[0], rr[1]);
       rr[0] = fma2(bp[0], rr[0], bq[0]);
       rr[1] = fma2(bp[1], rr[1], bq[1]);
-      float2 sa[2] = {both(0.f), both(0.f)}, sb[2] = {both(0.f), both(0.f)};
+      if (kLag) {
+        __syncwarp();
+        mbar_arrive_if(lane == 0, &taken[out & 1]);
+      }
+      float2 A[2];
+      load_row(&rates[out % kRing][0][c4], A[0], A[1]);
       A[0] = sub2(both(0.f), A[0]);
       A[1] = sub2(both(0.f), A[1]);
+      float2 sa[2] = {both(0.f), both(0.f)}, sb[2] = {both(0.f), both(0.f)};
       const size_t o = (size_t)(t.row0 + first) * P.ld_grad + c;
       const int left = in ? t.rows - first : 0;
-      float2 ahead[8];
-      ask16(park + (R - 1) * 16, ahead);
+      float2 ahead[8];                     // the next row's gates are on their way
+      ask16(at_park + (R - 1) * 16, ahead);
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) {
         float2 a[2], v[2], dy[2], m[8];
@@ -1341,7 +1407,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
         here(ahead);
 #pragma unroll
         for (int i = 0; i < 8; ++i) m[i] = ahead[i];
-        if (r > 0) ask16(park + (r - 1) * 16, ahead);
+        if (r > 0) ask16(at_park + (r - 1) * 16, ahead);
         take_a(bza + r * kCols, bzb + r * kCols, a[0], a[1]);
         load_row(bv + r * kCols, v[0], v[1]);
         load_row(bdy + r * kCols, dy[0], dy[1]);
@@ -1372,14 +1438,17 @@ __global__ void __launch_bounds__(kBackThreads, kBackBlocks<T>)
         sb[k] = add2(sb[k], shfl_xor2(sb[k], 16));
       }
       if (lane < 16) {
-        store_row(&sums[warp][0][c4], sa[0], sa[1]);
-        store_row(&sums[warp][1][c4], sb[0], sb[1]);
+        store_row(&sums[slot][warp][0][c4], sa[0], sa[1]);
+        store_row(&sums[slot][warp][1][c4], sb[0], sb[1]);
       }
-      // This stage was written to: order that before the copy that comes next.
+      // This tile's places were written to: order that before the copies that
+      // come next.
       tc::fence_smem_to_async();
       __syncwarp();
-      mbar_arrive_if(lane == 0, &empty[st]);
+      mbar_arrive_if(lane == 0, &empty[out % kRing]);
     }
+    __syncwarp();                          // lets the last sums be written
+    mbar_arrive_if(lane == 0 && it - (kOpen - 1) >= end, &paired[end % kOpen]);
   }
   __syncthreads();
   if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
@@ -1611,7 +1680,7 @@ cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, cons
 size_t recurrence_workspace_bytes(const RecurrenceDims& d) {
   const bool b16 = d.dtype == SDM_BF16;
   const size_t fwd = chain_bytes(d, b16 ? ForwardShape<__nv_bfloat16>::L : ForwardShape<float>::L);
-  const int L = b16 ? BackwardShape<__nv_bfloat16>::L : BackwardShape<float>::L;
+  const int L = b16 ? kStateRows<__nv_bfloat16> : kStateRows<float>;
   const size_t back = chain_bytes(d, L) + (size_t)chunk_numbers(d.rows, d.n_seq, L) * 2 * d.D * 4;
   return back > fwd ? back : fwd;
 }
@@ -1631,12 +1700,23 @@ cudaError_t launch_recurrence_forward(const RecurrenceDims& d, const RecurrenceI
 
 namespace {
 
-template <typename T>
+// Whether the backward pass finishes a tile one tile later.  A chain is a
+// sequence's 64 channels; with few of them many of the tiles at work are of one
+// chain and wait for folds, with many the lag only takes room.  Measured, at once
+// and later, 65536 x 512 bf16: 8 chains 206 and 124 us, 32 150 and 122, 64 125 and
+// 122, 128 110 and 123; 32768 x 1024 float32: 16 chains 261 and 186, 64 187 and
+// 183, 128 167 and 183.  (Sequences' lengths are not known here: one long one among
+// many short ones is taken for many chains.)
+bool lags(const RecurrenceDims& d) {
+  return 2 * (long long)d.n_seq * col_tiles_of(d.D) <= device_limits().sms;
+}
+
+template <typename T, bool kLag>
 cudaError_t backward_as(const RecurrenceDims& d, const RecurrenceInputs& in, const float* states,
                         const void* dy, const float* dhT, void* dza, void* dzb, void* dv,
                         float* dA, float* dbias, float* dh0, void* workspace, unsigned* status,
                         cudaStream_t stream) {
-  using Sh = BackwardShape<T>;
+  using Sh = BackwardShape<T, kLag>;
   constexpr int L = Sh::L;
   BackwardArgs P;
   if (d.rows > 0 && (!make_map(&P.za, in.za, d.dtype, d.rows, d.D, d.ld, L) ||
@@ -1660,12 +1740,12 @@ cudaError_t backward_as(const RecurrenceDims& d, const RecurrenceInputs& in, con
   P.ld_grad = d.ld_grad;
   P.tiles = tiles_of(d, in.offsets != nullptr, L);
   P.status = status;
-  const auto kernel = backward_kernel<T>;
+  const auto kernel = backward_kernel<T, kLag>;
   static std::atomic<bool> allowed[64];   // false
   cudaError_t e = allow_smem(kernel, Sh::kSmem, allowed);
   if (e == cudaSuccess) e = clear_chain(workspace, d, L, stream);
   if (e != cudaSuccess) return e;
-  const unsigned most = (unsigned)(kBackBlocks<T> * device_limits().sms);
+  const unsigned most = (unsigned)(Sh::kBlocks * device_limits().sms);
   e = launch_behind(kernel, P.tiles < most ? P.tiles : most, kBackThreads, Sh::kSmem, stream, P);
   if (e != cudaSuccess || (!dA && !dbias)) return e;
   return launch_behind(column_sums_kernel, (unsigned)(d.D + 31) / 32, 1024, 0, stream, P.packed,
@@ -1685,11 +1765,10 @@ cudaError_t launch_recurrence_backward(const RecurrenceDims& d, const Recurrence
     if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)d.D * 4, stream);
     return e;
   }
-  if (d.dtype == SDM_BF16)
-    return backward_as<__nv_bfloat16>(d, in, states, dy, dhT, dza, dzb, dv, dA, dbias, dh0,
-                                      workspace, status, stream);
-  return backward_as<float>(d, in, states, dy, dhT, dza, dzb, dv, dA, dbias, dh0, workspace,
-                            status, stream);
+  const bool b16 = d.dtype == SDM_BF16;
+  const auto run = lags(d) ? (b16 ? backward_as<__nv_bfloat16, true> : backward_as<float, true>)
+                           : (b16 ? backward_as<__nv_bfloat16, false> : backward_as<float, false>);
+  return run(d, in, states, dy, dhT, dza, dzb, dv, dA, dbias, dh0, workspace, status, stream);
 }
 
 cudaError_t launch_recurrence_step(const RecurrenceDims& d, const RecurrenceInputs& in,

@@ -94,6 +94,24 @@ def test_many_tiles_per_block(dtype):
 
 
 @BOTH
+def test_many_chains(dtype):
+    # More chains (a sequence's 64 channels) than half the multiprocessors: the
+    # backward pass then finishes each tile at once.  Empty, single and long ones.
+    lens = [0, 1, 31, 32, 33, 63, 64, 65, 2, 300] * 8 + [1500, 0]
+    off = offsets(*[3 + sum(lens[:i]) for i in range(len(lens) + 1)])
+    x = draw(sum(lens) + 7, 200, len(lens), dtype, seed=53)
+    check(x, off, dtype, len(lens))
+    check(draw(40 * 330, 136, 40, dtype, seed=54), None, dtype, 40)
+
+
+@BOTH
+def test_one_long_sequence(dtype):
+    # Few chains and many tiles of each in every block.
+    check(draw(20011, 120, 1, dtype, seed=55), offsets(0, 20011), dtype, 1)
+    check(draw(2 * 8000, 72, 2, dtype, seed=56), None, dtype, 2)
+
+
+@BOTH
 def test_thousands_of_short_sequences(dtype):
     g = torch.Generator().manual_seed(7)
     lens = torch.randint(0, 4, (3001,), generator=g)

@@ -229,6 +229,9 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
         if (P.group >= 128) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 8));
       }
       const float scale = max_nan(most * (1.f / kE4m3Max), 1.17549435e-38f);
+      // Times the reciprocal, not divided: an element within a few 2^-24 of a tie
+      // may round to the other neighbour, as it may after a division (111 and 97
+      // of 157 million elements are not what 64 bits give).
       const float2 by = both(rcp(scale));
       if (c < D) {
         uint2 q;

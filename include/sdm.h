@@ -354,7 +354,8 @@ sdm_status sdm_recurrence_step(const sdm_recurrence* shape, const void* za, cons
  *   n = s / sqrt(mean_c s_c^2 + eps) * gamma, from the rounded s, in float32;
  *   out = n in SDM_F32 or SDM_BF16; or, for SDM_E4M3, per row (group = 0) or
  *   per `group` channels: scale = max(max|n| / 448, 2^-126), float32, and
- *   out = n / scale rounded to nearest even, so that out * scale stands for n.
+ *   out = n / scale rounded to nearest even, so that out * scale stands for n
+ *   (both quotients are those of float32, themselves rounded to nearest).
  * A NaN in a row makes the row's outputs and scales NaN. */
 typedef struct {
   int rows;               /* rows                                                */

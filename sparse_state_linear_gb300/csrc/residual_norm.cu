@@ -79,6 +79,29 @@ __device__ __forceinline__ uint32_t e4m3x2(float2 v) {
   return q;
 }
 
+// max / 448, rounded to nearest: a product with the constant's reciprocal is off
+// by an ulp at most, and its remainder, which is exact, says by how much.  (What is
+// infinite has no remainder.)
+__device__ __forceinline__ float scale_of(float most) {
+  constexpr float r = 1.f / kE4m3Max;
+  const float q = most * r, exact = fmaf(fmaf(-kE4m3Max, q, most), r, q);
+  return max_nan(most < INFINITY ? exact : most, 1.17549435e-38f);
+}
+// n / scale, rounded once: the reciprocal r and what it lacks, r (1 - scale r), are
+// together good to 2^-46 of it, and n times their sum is rounded by one multiply-add.
+// (Measured at 16384 x 3840, groups of 128: 1% more time than n r, which puts
+// elements next to a tie of the 8-bit rounding on the wrong side.)
+struct Reciprocal {
+  float2 r, rest;
+};
+__device__ __forceinline__ Reciprocal reciprocal(float scale) {
+  const float r = rcp(scale), lacks = fmaf(-scale, r, 1.f);
+  return Reciprocal{both(r), both(scale < INFINITY ? r * lacks : 0.f)};
+}
+__device__ __forceinline__ float2 divided(float2 n, const Reciprocal& d) {
+  return fma2(n, d.r, mul2(n, d.rest));
+}
+
 // ------------------------------------------------------------------ teams
 // TW warps work on a row; a block has kTeams<TW> of them.
 template <int TW>
@@ -228,15 +251,12 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
         if (P.group >= 64) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 4));
         if (P.group >= 128) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 8));
       }
-      const float scale = max_nan(most * (1.f / kE4m3Max), 1.17549435e-38f);
-      // Times the reciprocal, not divided: an element within a few 2^-24 of a tie
-      // may round to the other neighbour, as it may after a division (111 and 97
-      // of 157 million elements are not what 64 bits give).
-      const float2 by = both(rcp(scale));
+      const float scale = scale_of(most);
+      const Reciprocal by = reciprocal(scale);
       if (c < D) {
         uint2 q;
-        q.x = e4m3x2(mul2(n[j][0], by)) | e4m3x2(mul2(n[j][1], by)) << 16;
-        q.y = e4m3x2(mul2(n[j][2], by)) | e4m3x2(mul2(n[j][3], by)) << 16;
+        q.x = e4m3x2(divided(n[j][0], by)) | e4m3x2(divided(n[j][1], by)) << 16;
+        q.y = e4m3x2(divided(n[j][2], by)) | e4m3x2(divided(n[j][3], by)) << 16;
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.out) + base + c) = q;
         if (P.group) {
           if ((c & (P.group - 1)) == 0)

@@ -42,8 +42,9 @@ __device__ __forceinline__ float step_one(float h, float za, float zb, float v, 
                                           float bias) {
   const float x = za + bias, e = ex2(-fabsf(x) * kLog2e);
   const float sp = fmaxf(x, 0.f) * kLog2e + log2p1_unit(e);
-  const float z = max_nan(zb * kLog2e, -126.f), beta = rcp(1.f + ex2(-z));   // see sigmoid_pair
-  return fmaf(beta * ex2(-fmaf(A, sp, z)), h, beta * v);
+  const float z = zb * kLog2e, beta = rcp(1.f + ex2(-z));                    // see decay_pair
+  const float a = fmaxf(beta, 1.f - beta) * ex2(-fmaf(A, sp, fmaxf(z, 0.f)));
+  return fmaf(a, h, beta * v);
 }
 
 __device__ __forceinline__ float4 load4(const void* base, size_t i, int dt) {
@@ -96,26 +97,34 @@ __device__ __forceinline__ void softplus_pair(const Constants& K, float2 za, flo
   sp = fma2(p, t, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
 
-// sigmoid(z) = 1 / (1 + 2^-z') with z' = z log2(e), held above -126 so that
-// 2^-z' stays finite.
+// beta = sigmoid(zb) = 1 / (1 + 2^-z) with z = zb log2(e) (2^-z may be infinite:
+// beta is 0), and a = (1 - beta) alpha.  1 - beta is r 2^-max(z, 0) with
+// r = 1 / (1 + 2^-|z|) = max(beta, 1 - beta), so that a is r 2^-(max(z, 0) + A softplus).
+// Where the gate is closed (z < 0) the exponent is A softplus alone: a z in the sum
+// would round off the slow decay of a state that is held for long (at zb = -80 and
+// 65536 rows the state was 19% off, now 0.5%, as with every step apart in float32).
 __device__ __forceinline__ void sigmoid_pair(const Constants& K, float2 zb, float2& z, float2& eb,
                                              float2& beta) {
   z = mul2(zb, K.log2e);
-  z = make_float2(max_nan(z.x, -126.f), max_nan(z.y, -126.f));
   eb = make_float2(ex2(-z.x), ex2(-z.y));
   const float2 d = add2(eb, K.one);
   beta = make_float2(rcp(d.x), rcp(d.y));
 }
+__device__ __forceinline__ float2 decay_pair(const Constants& K, float2 A, float2 sp, float2 z,
+                                             float2 beta, float2& r) {
+  const float2 closed = sub2(K.one, beta);
+  r = make_float2(fmaxf(beta.x, closed.x), fmaxf(beta.y, closed.y));
+  const float2 l = fma2(A, sp, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+  return mul2(r, make_float2(ex2(-l.x), ex2(-l.y)));
+}
 
-// a = (1 - beta) alpha and b = beta v of two channels.  1 - beta is 2^-z' beta,
-// so that a is beta 2^-(z' + A softplus).
+// a and b = beta v of two channels.
 __device__ __forceinline__ void gate_pair(const Constants& K, float2 za, float2 zb, float2 v,
                                           float2 A, float2 bias2, float2& a, float2& b) {
-  float2 x, e, sp, z, eb, beta;
+  float2 x, e, sp, z, eb, beta, r;
   softplus_pair(K, za, bias2, x, e, sp);
   sigmoid_pair(K, zb, z, eb, beta);
-  const float2 l = fma2(A, sp, z);
-  a = mul2(beta, make_float2(ex2(-l.x), ex2(-l.y)));
+  a = decay_pair(K, A, sp, z, beta, r);
   b = mul2(beta, v);
 }
 
@@ -963,15 +972,14 @@ struct Gates2 {
 __device__ __forceinline__ Gates2 gates_pair(const Constants& K, float2 za, float2 zb, float2 A,
                                              float2 bias2) {
   Gates2 g;
-  float2 x, e, z, eb;
+  float2 x, e, z, eb, r;
   softplus_pair(K, za, bias2, x, e, g.sp);
   const float2 f = add2(e, K.one);
   g.sig = mul2(make_float2(x.x >= 0.f ? 1.f : e.x, x.y >= 0.f ? 1.f : e.y),
                make_float2(rcp(f.x), rcp(f.y)));
   sigmoid_pair(K, zb, z, eb, g.beta);
-  g.keep = mul2(eb, g.beta);
-  const float2 l = fma2(A, g.sp, z);
-  g.a = mul2(g.beta, make_float2(ex2(-l.x), ex2(-l.y)));
+  g.a = decay_pair(K, A, g.sp, z, g.beta, r);
+  g.keep = mul2(make_float2(fminf(eb.x, 1.f), fminf(eb.y, 1.f)), r);
   return g;
 }
 

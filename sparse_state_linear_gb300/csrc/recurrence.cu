@@ -82,11 +82,12 @@ __device__ __forceinline__ Constants constants() {
 }
 
 // What the exponent of alpha is made of, for two channels: x = (za + bias)
-// log2(e) from bias already times log2(e), e = 2^-|x| and
-// softplus = max(x, 0) + log2(1 + e), as log2p1_unit.
-__device__ __forceinline__ void softplus_pair(const Constants& K, float2 za, float2 bias2,
-                                              float2& x, float2& e, float2& sp) {
-  x = fma2(za, K.log2e, bias2);
+// log2(e), e = 2^-|x| and softplus = max(x, 0) + log2(1 + e), as log2p1_unit.
+// (The sum first: a bias times log2(e) would be rounded at its own size, which
+// tells where za nearly cancels it.)
+__device__ __forceinline__ void softplus_pair(const Constants& K, float2 za, float2 bias, float2& x,
+                                              float2& e, float2& sp) {
+  x = mul2(add2(za, bias), K.log2e);
   e = make_float2(ex2(-fabsf(x.x)), ex2(-fabsf(x.y)));
   const float2 d = add2(e, K.two);
   const float2 t = mul2(e, make_float2(rcp(d.x), rcp(d.y))), z = mul2(t, t);
@@ -120,9 +121,9 @@ __device__ __forceinline__ float2 decay_pair(const Constants& K, float2 A, float
 
 // a and b = beta v of two channels.
 __device__ __forceinline__ void gate_pair(const Constants& K, float2 za, float2 zb, float2 v,
-                                          float2 A, float2 bias2, float2& a, float2& b) {
+                                          float2 A, float2 bias, float2& a, float2& b) {
   float2 x, e, sp, z, eb, beta, r;
-  softplus_pair(K, za, bias2, x, e, sp);
+  softplus_pair(K, za, bias, x, e, sp);
   sigmoid_pair(K, zb, z, eb, beta);
   a = decay_pair(K, A, sp, z, beta, r);
   b = mul2(beta, v);
@@ -163,8 +164,8 @@ template <typename T>
 constexpr int kStateRows = 128 / (int)sizeof(T);
 
 // --------------------------------------------------------------------- scan
-// A (or ones) and bias (or zeros) times log2(e) of a tile's channels, brought
-// to shared memory by the warp that fetches it, two channels a lane.
+// A (or ones) and bias (or zeros) of a tile's channels, brought to shared memory
+// by the warp that fetches it, two channels a lane.
 struct Rates {
   float2 A, bias;
 };
@@ -172,7 +173,6 @@ __device__ __forceinline__ Rates rates_of(const float* A, const float* bias, int
   Rates r{both(1.f), both(0.f)};
   if (A && c < D) r.A = __ldg(reinterpret_cast<const float2*>(A + c));
   if (bias && c < D) r.bias = __ldg(reinterpret_cast<const float2*>(bias + c));
-  r.bias = mul2(r.bias, both(kLog2e));
   return r;
 }
 
@@ -970,10 +970,10 @@ struct Gates2 {
   float2 a, beta, keep, sp, sig;
 };
 __device__ __forceinline__ Gates2 gates_pair(const Constants& K, float2 za, float2 zb, float2 A,
-                                             float2 bias2) {
+                                             float2 bias) {
   Gates2 g;
   float2 x, e, z, eb, r;
-  softplus_pair(K, za, bias2, x, e, g.sp);
+  softplus_pair(K, za, bias, x, e, g.sp);
   const float2 f = add2(e, K.one);
   g.sig = mul2(make_float2(x.x >= 0.f ? 1.f : e.x, x.y >= 0.f ? 1.f : e.y),
                make_float2(rcp(f.x), rcp(f.y)));

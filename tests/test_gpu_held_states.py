@@ -1,5 +1,5 @@
 """States that are held for long: the gate a = (1 - beta) alpha of closed write
-gates (zb far below zero) and slow decays.
+gates (zb far below zero) and slow decays, and logits that cancel their bias.
 
 The bounds, from those of the operations (2^x instruction 4 U, reciprocal 2 U,
 each float32 operation U, the logarithm 6.5 U), count what each step is
@@ -58,6 +58,14 @@ def slow(D, seed=0):
     return torch.randn(D, generator=g).bfloat16().float() * 0.5, r() * 15 + 1, torch.log(torch.expm1(step))
 
 
+def cancelling(D, seed=0):
+    """x = za + bias of a few units from za and bias of some hundreds, exactly."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.round((torch.rand(D, generator=g) * 10 - 6) * 1024) / 1024
+    bias = torch.round((torch.rand(D, generator=g) - 0.5) * 1500)
+    return x - bias, torch.rand(D, generator=g) * 7 + 1, bias
+
+
 def near(got, want, rel, what):
     got, want = got.detach().cpu().double(), want.double()
     lim = rel * want.abs() + torch.finfo(torch.float32).tiny
@@ -65,7 +73,7 @@ def near(got, want, rel, what):
     assert not bad.any(), (what, int(bad.sum()), float(((got - want).abs() / lim)[bad].max()), torch.nonzero(bad)[:4].tolist())
 
 
-@pytest.mark.parametrize("inputs", [slow])
+@pytest.mark.parametrize("inputs", [slow, cancelling])
 def test_one_row_is_its_gate(inputs):
     # No input, one row: the state behind it, and the gradient in front of it, is
     # a times what it was.

@@ -405,6 +405,14 @@ sdm_status sdm_get_device_status(void* stream);
  * Results do not depend on these; only speed does. */
 sdm_status sdm_set_scan_tuning(int depth, int col_slice);
 
+/* How long a block of sdm_recurrence_forward or _backward waits for what other
+ * blocks publish, for the calling process's calls from now on: microseconds,
+ * 0..1e7; -1 = the default, 4e6.  A wait that runs out ends the call's kernels,
+ * which record SDM_ERR_TIMEOUT; the call's outputs are void then, and the next
+ * call is as good as any.  With 0 a wait that is not over at the first look runs
+ * out, which shows this on a real device. */
+sdm_status sdm_set_recurrence_wait(long long limit_us);
+
 /* Self-test of the bounded device wait: launches one CTA that waits on a
  * barrier no thread ever completes, with a limit of `timeout_ns`
  * nanoseconds (1e6..1e10), then records SDM_ERR_TIMEOUT and returns.

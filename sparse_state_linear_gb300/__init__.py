@@ -31,6 +31,7 @@ EXPORTS = ["sdm_status_string", "sdm_subscores", "sdm_select", "sdm_address",
            "sdm_forward", "sdm_forward_windows",
            "sdm_get_device_status",
            "sdm_set_scan_tuning", "sdm_selftest_wait_timeout", "sdm_measure_row_traffic",
+           "sdm_set_recurrence_wait",
            "sdm_recurrence_workspace_size", "sdm_recurrence_states_size",
            "sdm_recurrence_forward", "sdm_recurrence_backward", "sdm_recurrence_step",
            "sdm_add_rmsnorm", "sdm_add_rmsnorm_workspace_size", "sdm_add_rmsnorm_backward"]
@@ -132,6 +133,7 @@ def lib():
         "sdm_forward_windows": ([SP], I),
         "sdm_get_device_status": ([P], I),
         "sdm_set_scan_tuning": ([I, I], I),
+        "sdm_set_recurrence_wait": ([ctypes.c_longlong], I),
         "sdm_selftest_wait_timeout": ([ctypes.c_longlong, P], I),
         "sdm_measure_row_traffic": ([P, P, ctypes.c_longlong, ctypes.c_longlong, I, I, I, I, I,
                                      ctypes.c_uint, P], I),
@@ -426,6 +428,11 @@ def sdm_get_device_status(stream=None) -> int:
 
 def sdm_set_scan_tuning(depth: int = 0, col_slice: int = 0):
     _ok(lib().sdm_set_scan_tuning(int(depth), int(col_slice)), "sdm_set_scan_tuning")
+
+
+def sdm_set_recurrence_wait(limit_us: int = -1):
+    """Limit in us of the recurrence's waits for other blocks (-1: the default)."""
+    _ok(lib().sdm_set_recurrence_wait(int(limit_us)), "sdm_set_recurrence_wait")
 
 
 def sdm_selftest_wait_timeout(timeout_ns: int, stream=None):

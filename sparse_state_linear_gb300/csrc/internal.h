@@ -123,6 +123,9 @@ cudaError_t launch_decode(const Dims& d, const void* q_w, const void* q_r, const
                           const void* g, const float* gamma, float eps, void* out,
                           int out_dtype, cudaStream_t stream);
 
+// Limit in us of the recurrence's waits for other blocks (sdm_set_recurrence_wait).
+unsigned api_recurrence_wait_us();
+
 // Gated delta recurrence (recurrence.cu).  Parameters of one call, validated.
 struct RecurrenceDims {
   int n_seq, rows, D;

@@ -197,6 +197,15 @@ struct Chain {
   float* pairs;       // [numbers][D][2]
 };
 
+// What a block's warps share about giving up, in shared memory: whether one has,
+// and the limit of the waits for other blocks in us.  (Waits within the block have
+// a fixed one: with a limit to look up, every one of them, the forward pass takes
+// 2% longer and the float32 backward pass 4%.)
+struct GiveUp {
+  int done;
+  unsigned limit_us;
+};
+
 __device__ __forceinline__ unsigned next_ticket(const Chain& c) {
   return atomicAdd(c.ticket, 1u) + 1u;
 }
@@ -205,7 +214,7 @@ __device__ __forceinline__ unsigned next_ticket(const Chain& c) {
 // backward at 10007 x 1000 float32: 409 and 98 us with 6, 412 and 93 with 8, 431
 // and 115 with 12, 440 and 109 with 16 (a fold waits for and reads more).
 constexpr int kGroup = 8;
-constexpr unsigned long long kWaitNs = 4000000000ull;         // limit of every wait
+constexpr unsigned long long kWaitNs = 4000000000ull;         // limit of waits within a block
 
 __device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
   unsigned v;
@@ -254,12 +263,12 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, unsigned parity) 
 // Wait for an mbarrier phase (a whole warp calls it); false once the limit has
 // passed or another warp of the block has given up (which the first to do so
 // marks).
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, volatile int* gave_up) {
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, volatile GiveUp* give_up) {
   for (uint64_t t0 = 0; !__all_sync(0xffffffffu, mbar_sleep_wait(bar, parity));) {
     const uint64_t now = global_ns();
     if (t0 == 0) t0 = now;
-    if (__any_sync(0xffffffffu, *gave_up || now - t0 > kWaitNs)) {
-      *gave_up = 1;
+    if (__any_sync(0xffffffffu, give_up->done || now - t0 > kWaitNs)) {
+      give_up->done = 1;
       return false;
     }
   }
@@ -354,6 +363,7 @@ struct ForwardArgs {
   Chain chain;
   int D, col_tiles;
   unsigned tiles;
+  unsigned limit_us;
   unsigned* status;
 };
 
@@ -511,14 +521,17 @@ __device__ __forceinline__ bool publishes_state(int pos) {
 // wait, one multiply-add and one store.  Always in the same order: results do
 // not depend on timing.  Returns false if the wait ran out or another block
 // gave up.
-__device__ __forceinline__ bool keep_waiting(const Chain& ch, int& spin, uint64_t& t0) {
-  if ((++spin & 63) != 0) return true;
+__device__ __forceinline__ bool keep_waiting(const Chain& ch, const volatile GiveUp* give_up,
+                                             int& spin, uint64_t& t0) {
+  if ((++spin & 63) != 1) return true;
+  const unsigned limit_us = give_up->limit_us;
   const uint64_t now = global_ns();
   if (t0 == 0) t0 = now;
-  return __all_sync(0xffffffffu, now - t0 < kWaitNs && load_acquire(ch.abort) != 0);
+  return __all_sync(0xffffffffu, now - t0 < limit_us * 1000ull && load_acquire(ch.abort) != 0);
 }
 
-__device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int D, float2& h) {
+__device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int D,
+                                            const volatile GiveUp* give_up, float2& h) {
   const int lane = threadIdx.x & 31, c = t.col0 + lane * 2;
   const int n = t.pos % kGroup;            // pairs of its own group
   const bool in = c < D, grouped = t.pos >= kGroup;
@@ -544,9 +557,9 @@ __device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int 
     // If not, mostly the nearest is the last to arrive.
     while (!__all_sync(0xffffffffu, !in || largest(load_pairs(near)) != kUnset)) {
       __nanosleep(20);
-      if (!keep_waiting(ch, spin, t0)) return false;
+      if (!keep_waiting(ch, give_up, spin, t0)) return false;
     }
-    if (!keep_waiting(ch, spin, t0)) return false;
+    if (!keep_waiting(ch, give_up, spin, t0)) return false;
   }
   float2 P = both(1.f), S = both(0.f);
 #pragma unroll
@@ -558,7 +571,7 @@ __device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int 
   h = S;
   if (!grouped) return true;               // the sequence's first chunk has P = 0
   while (!__all_sync(0xffffffffu, largest(from) != kUnset)) {
-    if (!keep_waiting(ch, spin, t0)) return false;
+    if (!keep_waiting(ch, give_up, spin, t0)) return false;
     if (in) from = load_pairs(state);
   }
   h = fma2(P, make_float2(__uint_as_float(from.y), __uint_as_float(from.w)), S);
@@ -689,8 +702,8 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   __shared__ __align__(16) float carry[kSlots][kCols];         // the state in front of the tile
   __shared__ __align__(16) float rates[2][2][kCols];           // A, bias
   __shared__ uint32_t tmem_base;
-  __shared__ int quit;
-  volatile int* gave_up = &quit;
+  __shared__ GiveUp quit;
+  volatile GiveUp* give_up = &quit;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
@@ -706,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       mbar_init(&folded[s], 1);
       mbar_init(&taken[s], W);
     }
-    quit = 0;
+    quit = GiveUp{0, P.limit_us};
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   tc::fence_before_sync();
@@ -742,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       const Rates rt = rates_of(P.A, P.bias, more ? t.col0 + lane * 2 : P.D, P.D);
       // The places of the first two units held the last two of the tile two
       // before, that of the third the first of the tile before.
-      if (n >= 2 && !wait_phase(&empty[n & 1], ((n >> 1) - 1) & 1, gave_up)) break;
+      if (n >= 2 && !wait_phase(&empty[n & 1], ((n >> 1) - 1) & 1, give_up)) break;
       if (lane == 0) {
         tiles[n % kInfo] = t;
         mbar_arrive(&known[n % kInfo]);
@@ -755,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       bool there = true;
       for (int j = 0; j < 3 && more; ++j) {
         if (j == 2 && n >= 1)
-          there = wait_phase(&empty[(n - 1) & 1], ((n - 1) >> 1) & 1, gave_up);
+          there = wait_phase(&empty[(n - 1) & 1], ((n - 1) >> 1) & 1, give_up);
         // Where the block gives up (its results are void then), the copy is made
         // all the same, so that the barrier completes.
         if (lane == 0)
@@ -778,10 +791,10 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   } else if (warp == W + 1) {              // publishes
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
-      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, gave_up)) break;
+      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, give_up)) break;
       const Tile t = tiles[it % kInfo];
       if (t.rows == 0) break;
-      if (!wait_phase(&paired[slot], (it / kSlots) & 1, gave_up)) break;
+      if (!wait_phase(&paired[slot], (it / kSlots) & 1, give_up)) break;
       const int c = t.col0 + lane * 2;
       running_pairs(total[slot], lane, [&](float2 p, float2 s) {
         if (t.last) return;
@@ -800,23 +813,23 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       const int slot = it % kSlots;
       // The end may come before this warp's next tile.
       if (it > 0) {
-        if (!wait_phase(&known[(it - 1) % kInfo], ((it - 1) / kInfo) & 1, gave_up)) break;
+        if (!wait_phase(&known[(it - 1) % kInfo], ((it - 1) / kInfo) & 1, give_up)) break;
         if (tiles[(it - 1) % kInfo].rows == 0) break;
       }
-      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, gave_up)) break;
+      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, give_up)) break;
       const Tile t = tiles[it % kInfo];
       if (t.rows == 0) break;
       const int c = t.col0 + lane * 2;
       float2 h = make_float2(0.f, 0.f);
       if (t.chunk == 0) {
         if (P.h0 && c < P.D) h = *reinterpret_cast<const float2*>(P.h0 + (size_t)t.seq * P.D + c);
-      } else if (!fold_before(P.chain, t, P.D, h)) {
-        *gave_up = 1;
+      } else if (!fold_before(P.chain, t, P.D, give_up, h)) {
+        give_up->done = 1;
         break;
       }
       // (Which also means that the tile two before has been finished: its state
       // may be overwritten.)
-      if (!wait_phase(&summed[slot], (it / kSlots) & 1, gave_up)) break;
+      if (!wait_phase(&summed[slot], (it / kSlots) & 1, give_up)) break;
       *reinterpret_cast<float2*>(&carry[slot][lane * 2]) = h;
       if (!t.last && publishes_state(t.pos)) {
         const float2 p = *reinterpret_cast<const float2*>(&whole[slot][0][lane * 2]);
@@ -837,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
     for (int it = 0; it - 1 < end; ++it) {
       if (it < end) {
         const int slot = it & 1;
-        if (!wait_phase(&full[it & 1], (it >> 1) & 1, gave_up)) break;
+        if (!wait_phase(&full[it & 1], (it >> 1) & 1, give_up)) break;
         const Tile t = tiles[it % kInfo];
         if (t.rows == 0) {
           end = it;
@@ -892,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
             pl[k] = shfl_xor2(p[k], 16);
             sl[k] = shfl_xor2(s[k], 16);
           }
-          if (it >= kSlots && !wait_phase(&taken[slot], ((it >> 1) - 1) & 1, gave_up)) break;
+          if (it >= kSlots && !wait_phase(&taken[slot], ((it >> 1) - 1) & 1, give_up)) break;
           if (lane >= 16) {
             store_row(&total[slot][warp][0][c4], mul2(p[0], pl[0]), mul2(p[1], pl[1]));
             store_row(&total[slot][warp][1][c4], fma2(p[0], sl[0], s[0]), fma2(p[1], sl[1], s[1]));
@@ -910,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       const int slot = out & 1;
       const Tile t = tiles[out % kInfo];
       const int c = t.col0 + c4;
-      if (!wait_phase(&folded[slot], (out >> 1) & 1, gave_up)) break;
+      if (!wait_phase(&folded[slot], (out >> 1) & 1, give_up)) break;
       float2 h[2];
       load_row(&carry[slot][c4], h[0], h[1]);
       float2 wp[2], ws[2];
@@ -954,10 +967,13 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
       if (P.hT && t.last && first < t.rows && t.rows <= first + R && c < P.D)
         store_row(P.hT + (size_t)t.seq * P.D + c, h[0], h[1]);
     }
+    parked();    // where the block gives up: nothing is on its way when the columns are freed
   }
+  tc::fence_before_sync();
   __syncthreads();
+  tc::fence_after_sync();
   if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
-  if (quit && tid == 0) {                  // tell the other blocks
+  if (quit.done && tid == 0) {             // tell the other blocks
     record_status(P.status, SDM_ERR_TIMEOUT);
     atomicExch(P.chain.abort, 0u);
   }
@@ -1014,6 +1030,7 @@ struct BackwardArgs {
   int D, col_tiles;
   long long ld_grad;
   unsigned tiles;
+  unsigned limit_us;
   unsigned* status;
 };
 
@@ -1071,8 +1088,8 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
   __shared__ __align__(16) float sums[kOpen][W][2][kCols];     // of the gradients of A and bias
   __shared__ __align__(16) float rates[kRing][2][kCols];       // A, bias
   __shared__ uint32_t tmem_base;
-  __shared__ int quit;
-  volatile int* gave_up = &quit;
+  __shared__ GiveUp quit;
+  volatile GiveUp* give_up = &quit;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
@@ -1088,7 +1105,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
       mbar_init(&folded[s], 1);
       mbar_init(&taken[s], W);
     }
-    quit = 0;
+    quit = GiveUp{0, P.limit_us};
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   tc::fence_before_sync();
@@ -1131,7 +1148,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
       // four: its barrier of the tile four before has been waited for.
       constexpr int kBehind = kLag ? 3 : 2;
       if (n >= kBehind &&
-          !wait_phase(&empty[(n - kBehind) % kRing], ((n - kBehind) / kRing) & 1, gave_up))
+          !wait_phase(&empty[(n - kBehind) % kRing], ((n - kBehind) / kRing) & 1, give_up))
         break;
       if (lane == 0) {
         tiles[n % kInfo] = t;
@@ -1145,7 +1162,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
       bool there = true;
       for (int j = 0; j < 4 && more; ++j) {
         if (kLag && j == 3 && n >= 2)
-          there = wait_phase(&empty[(n - 2) % kRing], ((n - 2) / kRing) & 1, gave_up);
+          there = wait_phase(&empty[(n - 2) % kRing], ((n - 2) / kRing) & 1, give_up);
         // Where the block gives up (its results are void then), the copy is made
         // all the same, so that the barrier completes.
         if (lane == 0)
@@ -1186,7 +1203,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
     };
     for (int it = 0;; ++it) {
       const int slot = it % kOpen;
-      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, gave_up)) break;
+      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, give_up)) break;
       const Tile t = tiles[it % kInfo];
       const int c = t.col0 + lane * 2;
       float2 h = make_float2(0.f, 0.f);
@@ -1195,7 +1212,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
         h = __ldg(reinterpret_cast<const float2*>(
             P.states + (size_t)(begin / L + t.seq + t.chunk) * P.D + c));
       }
-      if (!wait_phase(&paired[slot], (it / kOpen) & 1, gave_up)) break;
+      if (!wait_phase(&paired[slot], (it / kOpen) & 1, give_up)) break;
       if (t.rows > 0) {
         // What others wait for goes out first.
         float2 wp[kHalves], wq[kHalves];
@@ -1257,7 +1274,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
   } else if (warp == W + 2) {              // folds
     for (int it = 0;; ++it) {
       const int slot = it % kOpen;
-      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, gave_up)) break;
+      if (!wait_phase(&known[it % kInfo], (it / kInfo) & 1, give_up)) break;
       const Tile t = tiles[it % kInfo];
       if (t.rows == 0) break;
       const int c = t.col0 + lane * 2;
@@ -1265,16 +1282,16 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
       if (t.pos == 0) {
         if (P.dhT && c < P.D)
           r = *reinterpret_cast<const float2*>(P.dhT + (size_t)t.seq * P.D + c);
-      } else if (!fold_before(P.chain, t, P.D, r)) {
-        *gave_up = 1;
+      } else if (!fold_before(P.chain, t, P.D, give_up, r)) {
+        give_up->done = 1;
         break;
       }
       // The tile that last used this carry has been finished.
       const int past = kLag ? it : it - 1;
-      if (past >= 0 && !wait_phase(&summed[past & 1], (past >> 1) & 1, gave_up)) break;
+      if (past >= 0 && !wait_phase(&summed[past & 1], (past >> 1) & 1, give_up)) break;
       *reinterpret_cast<float2*>(&carry[it & 1][lane * 2]) = r;
       if (!t.last && publishes_state(t.pos)) {
-        if (!kLag && !wait_phase(&summed[it & 1], (it >> 1) & 1, gave_up)) break;
+        if (!kLag && !wait_phase(&summed[it & 1], (it >> 1) & 1, give_up)) break;
         const float2 p = *reinterpret_cast<const float2*>(&whole[slot][0][lane * 2]);
         const float2 q = *reinterpret_cast<const float2*>(&whole[slot][1][lane * 2]);
         if (c < P.D)
@@ -1302,7 +1319,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
       unit_before = unit;
       if (it < end) {
         const int slot = it % kOpen;
-        if (!wait_phase(&full[it % kRing], (it / kRing) & 1, gave_up)) break;
+        if (!wait_phase(&full[it % kRing], (it / kRing) & 1, give_up)) break;
         const Tile t = tiles[it % kInfo];
         if (t.rows == 0) {
           end = it;
@@ -1347,7 +1364,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
               q[k] = fma2(p[k], dy[k], q[k]);
             }
           }
-          if (kLag && it >= 2 && !wait_phase(&taken[it & 1], ((it >> 1) - 1) & 1, gave_up)) break;
+          if (kLag && it >= 2 && !wait_phase(&taken[it & 1], ((it >> 1) - 1) & 1, give_up)) break;
           store_row(&half[slot][hw][0][c4], p[0], p[1]);
           store_row(&half[slot][hw][1][c4], s[0], s[1]);
           store_row(&half[slot][hw][2][c4], q[0], q[1]);
@@ -1365,7 +1382,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
       const uint32_t at_park = park + slot * Sh::kOpenCols;
       T *const bza = place(finished, 0), *const bzb = place(finished, 1),
               *const bv = place(finished, 2), *const bdy = place(finished, 3);
-      if (!wait_phase(&summed[out & 1], (out >> 1) & 1, gave_up)) break;
+      if (!wait_phase(&summed[out & 1], (out >> 1) & 1, give_up)) break;
       // w[r] = a h[r-1], the decayed state in front of each row.
       float2 h[2], w[R][2];
       load_row(&half[slot][hw][1][c4], h[0], h[1]);
@@ -1391,7 +1408,7 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
       float2 rr[2], bp[2], bq[2];
       load_row(&half[slot][hw][0][c4], bp[0], bp[1]);
       load_row(&half[slot][hw][2][c4], bq[0], bq[1]);
-      if (!wait_phase(&folded[out & 1], (out >> 1) & 1, gave_up)) break;
+      if (!wait_phase(&folded[out & 1], (out >> 1) & 1, give_up)) break;
       load_row(&carry[out & 1][c4], rr[0], rr[1]);
       rr[0] = fma2(bp[0], rr[0], bq[0]);
       rr[1] = fma2(bp[1], rr[1], bq[1]);
@@ -1455,12 +1472,15 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
       __syncwarp();
       mbar_arrive_if(lane == 0, &empty[out % kRing]);
     }
+    parked();    // where the block gives up: nothing is on its way when the columns are freed
     __syncwarp();                          // lets the last sums be written
     mbar_arrive_if(lane == 0 && it - (kOpen - 1) >= end, &paired[end % kOpen]);
   }
+  tc::fence_before_sync();
   __syncthreads();
+  tc::fence_after_sync();
   if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
-  if (quit && tid == 0) {                  // tell the other blocks
+  if (quit.done && tid == 0) {             // tell the other blocks
     record_status(P.status, SDM_ERR_TIMEOUT);
     atomicExch(P.chain.abort, 0u);
   }
@@ -1674,6 +1694,7 @@ cudaError_t forward_as(const RecurrenceDims& d, const RecurrenceInputs& in, cons
   P.col_tiles = col_tiles_of(d.D);
   P.tiles = tiles_of(d, in.offsets != nullptr, L);
   P.status = status;
+  P.limit_us = api_recurrence_wait_us();
   const auto kernel = forward_kernel<T>;
   static std::atomic<bool> allowed[64];   // false
   cudaError_t e = allow_smem(kernel, Sh::kSmem, allowed);
@@ -1748,6 +1769,7 @@ cudaError_t backward_as(const RecurrenceDims& d, const RecurrenceInputs& in, con
   P.ld_grad = d.ld_grad;
   P.tiles = tiles_of(d, in.offsets != nullptr, L);
   P.status = status;
+  P.limit_us = api_recurrence_wait_us();
   const auto kernel = backward_kernel<T, kLag>;
   static std::atomic<bool> allowed[64];   // false
   cudaError_t e = allow_smem(kernel, Sh::kSmem, allowed);

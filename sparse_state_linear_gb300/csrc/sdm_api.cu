@@ -3,6 +3,7 @@
 // allocated here; every tensor belongs to the caller.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -19,6 +20,8 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 unsigned* g_status_ptr[kMaxDevices] = {};
 int g_depth = 0, g_colslice = 0;
+constexpr unsigned kRecurrenceWaitUs = 4000000u;
+std::atomic<unsigned> g_recurrence_wait_us{kRecurrenceWaitUs};
 
 sdm_status status_ptr(unsigned** out) {
   int dev = 0;
@@ -262,6 +265,7 @@ void api_scan_tuning(int* depth, int* col_slice) {
   *depth = g_depth;
   *col_slice = g_colslice;
 }
+unsigned api_recurrence_wait_us() { return g_recurrence_wait_us.load(std::memory_order_relaxed); }
 
 }  // namespace sdm
 
@@ -705,6 +709,13 @@ sdm_status sdm_set_scan_tuning(int depth, int col_slice) {
   std::lock_guard<std::mutex> lk(g_mu);
   g_depth = depth;
   g_colslice = col_slice;
+  return SDM_OK;
+}
+
+sdm_status sdm_set_recurrence_wait(long long limit_us) {
+  if (limit_us < -1 || limit_us > 10000000ll) return SDM_ERR_INVALID_ARG;
+  g_recurrence_wait_us.store(limit_us < 0 ? kRecurrenceWaitUs : (unsigned)limit_us,
+                             std::memory_order_relaxed);
   return SDM_OK;
 }
 

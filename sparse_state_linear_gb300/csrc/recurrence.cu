@@ -706,6 +706,9 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   volatile GiveUp* give_up = &quit;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // First of all: a block that holds tensor memory must not wait for a kernel in
+  // front of it, which may want it.
+  wait_for_stream();
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -725,7 +728,6 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_const
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  wait_for_stream();
   if (!offsets_ok(P.packed)) {
     if (tid == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);
@@ -1092,6 +1094,9 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
   volatile GiveUp* give_up = &quit;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // First of all: a block that holds tensor memory must not wait for a kernel in
+  // front of it, which may want it.
+  wait_for_stream();
   if (warp == W + 1) tc::tmem_alloc(&tmem_base, Sh::kTmemCols);
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
@@ -1111,7 +1116,6 @@ __global__ void __launch_bounds__(kBackThreads, BackwardShape<T, kLag>::kBlocks)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  wait_for_stream();
   if (!offsets_ok(P.packed)) {
     if (tid == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     if (warp == W + 1) tc::tmem_dealloc(tmem_base, Sh::kTmemCols);

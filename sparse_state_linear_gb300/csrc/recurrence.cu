@@ -1592,6 +1592,105 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const Args P, float*
   }
 }
 
+// The same for many rows with slots, where looking through all earlier slots row
+// by row would be most of the work: a block takes kManyGroup rows by 512 channels,
+// puts the group's slots into a hash table in shared memory and looks all earlier
+// ones up in it once.  Its kManyLanes groups of 128 threads then take a row each,
+// two at a time, their loads on the way together.
+// From kStepMany blocks of step_kernel on.  Measured, step_kernel and this one, us:
+// bf16, 1920 channels: 2048 rows 17.9 and 24.5, 4096 33.5 and 30.6, 16384 138 and 122,
+// 70000 1468 and 594 (without slots 441); bf16, 256 channels: 8192 rows 13.8 and 20.0,
+// 16384 32.2 and 32.9, 70000 336 and 157 (74).  With 128 rows a group 24 us at least, and
+// 559 and 154 in the last; four rows at a time are short of registers.
+constexpr int kStepMany = 16384;
+constexpr int kManyGroup = 64, kManyLanes = 4, kManyThreads = kManyLanes * kStepThreads;
+constexpr int kManyTable = 512, kManyAhead = 2;
+
+__device__ __forceinline__ int place_of(int slot) {
+  return (int)((unsigned)slot * 2654435769u >> 23);          // golden ratio, 9 bits
+}
+
+__global__ void __launch_bounds__(kManyThreads) step_many_kernel(const Args P, float* state,
+                                                                 int n_slots, const int32_t* slots,
+                                                                 int parts) {
+  static_assert(kManyTable == 512 && kManyGroup < kManyTable, "place_of gives 9 bits");
+  wait_for_stream();
+  __shared__ int key[kManyTable], first[kManyTable], seen[kManyTable], group[kManyGroup];
+  const int D = P.d.D, dt = P.d.dtype, tid = threadIdx.x, lane = tid / kStepThreads;
+  const long long blocks = ((long long)P.d.rows + kManyGroup - 1) / kManyGroup * parts;
+  for (long long w = blockIdx.x; w < blocks; w += gridDim.x) {
+    const int row0 = (int)(w / parts) * kManyGroup, n = min(kManyGroup, P.d.rows - row0);
+    const int c = ((int)(w % parts) * kStepThreads + tid % kStepThreads) * 4;
+    for (int i = tid; i < kManyTable; i += kManyThreads) {
+      key[i] = -1;
+      first[i] = kManyGroup;
+      seen[i] = 0;
+    }
+    __syncthreads();
+    int slot = tid < n ? __ldg(slots + row0 + tid) : -1, at = 0;
+    if (slot >= n_slots) {
+      record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+      slot = -1;
+    }
+    if (slot >= 0) {                       // ends: the table has more places than the group rows
+      at = place_of(slot);
+      for (int k; (k = atomicCAS(&key[at], -1, slot)) != -1 && k != slot;) at = (at + 1) % kManyTable;
+      atomicMin(&first[at], tid);
+    }
+    __syncthreads();
+    const int4* s4 = reinterpret_cast<const int4*>(slots);
+#pragma unroll 4
+    for (int k = tid; k < row0 / 4; k += kManyThreads) {
+      const int4 q = __ldg(s4 + k);
+      const int e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        int p = place_of(e[j]), there;
+        while ((there = key[p]) != -1 && there != e[j]) p = (p + 1) % kManyTable;
+        if (there != -1) seen[p] = 1;      // (a negative slot, were it -1, finds an empty place)
+      }
+    }
+    __syncthreads();
+    if (slot >= 0 && (seen[at] || first[at] != tid)) {
+      record_status(P.status, SDM_ERR_DUPLICATE_SLOT);
+      slot = -1;
+    }
+    if (tid < kManyGroup) group[tid] = slot;
+    __syncthreads();
+    if (c < D) {
+      float4 A = make_float4(1.f, 1.f, 1.f, 1.f), bias = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (P.in.A) A = __ldg(reinterpret_cast<const float4*>(P.in.A) + (c >> 2));
+      if (P.in.bias) bias = __ldg(reinterpret_cast<const float4*>(P.in.bias) + (c >> 2));
+      for (int i0 = lane; i0 < n; i0 += kManyLanes * kManyAhead) {
+        float4 za[kManyAhead], zb[kManyAhead], v[kManyAhead], h[kManyAhead];
+        float4* hp[kManyAhead];
+#pragma unroll
+        for (int j = 0; j < kManyAhead; ++j) {
+          const int r = i0 + j * kManyLanes, s = r < n ? group[r] : -1;
+          hp[j] = s < 0 ? nullptr : reinterpret_cast<float4*>(state) + (((size_t)s * D + c) >> 2);
+          if (s < 0) continue;
+          const size_t i = ((size_t)(row0 + r) * P.d.ld + c) >> 2;
+          za[j] = load4(P.in.za, i, dt);
+          zb[j] = load4(P.in.zb, i, dt);
+          v[j] = load4(P.in.v, i, dt);
+          h[j] = *hp[j];
+        }
+#pragma unroll
+        for (int j = 0; j < kManyAhead; ++j) {
+          if (!hp[j]) continue;
+          const float4 y = make_float4(step_one(h[j].x, za[j].x, zb[j].x, v[j].x, A.x, bias.x),
+                                       step_one(h[j].y, za[j].y, zb[j].y, v[j].y, A.y, bias.y),
+                                       step_one(h[j].z, za[j].z, zb[j].z, v[j].z, A.z, bias.z),
+                                       step_one(h[j].w, za[j].w, zb[j].w, v[j].w, A.w, bias.w));
+          *hp[j] = y;
+          store4(P.y, ((size_t)(row0 + i0 + j * kManyLanes) * D + c) >> 2, dt, y);
+        }
+      }
+    }
+    __syncthreads();                       // the tables are filled again
+  }
+}
+
 }  // namespace
 
 namespace {
@@ -1814,8 +1913,12 @@ cudaError_t launch_recurrence_step(const RecurrenceDims& d, const RecurrenceInpu
   P.y = y;
   P.status = status;
   const int parts = (d.D / 4 + kStepThreads - 1) / kStepThreads;
-  const long long want = (long long)d.rows * parts;
+  const long long rows = (long long)d.rows * parts;           // by 512 channels
+  const bool many = slots && rows >= kStepMany;
+  const long long want = many ? ((long long)d.rows + kManyGroup - 1) / kManyGroup * parts : rows;
   const unsigned blocks = (unsigned)(want < (1 << 20) ? want : (1 << 20));
+  if (many)
+    return launch_behind(step_many_kernel, blocks, kManyThreads, 0, stream, P, state, n_slots, slots, parts);
   return launch_behind(step_kernel, blocks, kStepThreads, 0, stream, P, state, n_slots, slots, parts);
 }
 

@@ -617,6 +617,7 @@ sdm_status sdm_recurrence_step(const sdm_recurrence* shape, const void* za, cons
   sdm_status st = check_recurrence(shape, false, &d);
   if (st != SDM_OK) return st;
   if (n_slots < 0 || (!slots && d.rows > n_slots)) return SDM_ERR_INVALID_ARG;
+  if (slots && d.rows > (1 << 22)) return SDM_ERR_UNSUPPORTED;   // see the header
   if (d.rows == 0) return SDM_OK;   // no work: pointers are not looked at
   SDM_CHECK_PTR(za);
   SDM_CHECK_PTR(zb);

@@ -629,10 +629,10 @@ __device__ __forceinline__ void here(float2 (&v)[N]) {
 // gates, put a and b aside in tensor memory (which nothing else here uses),
 // go on to the next tile, and only then come back to finish the one before.
 //
-// Measured at 131072 x 2048 bf16: 379 us, 2.15 GB once = 0.85 of the copy rate;
+// Measured at 131072 x 2048 bf16: 384 us, 2.15 GB once = 0.84 of the copy rate;
 // at 9001 x 1920 float32 in 13 sequences 50 us, 0.82.  With every gate left out
 // (a = za + zb, b = v) the first takes 336 us: what bounds it is the arithmetic,
-// about 20 instructions of every element's 38, on 65% of the issue slots.  A first
+// about 19 instructions of every element's 36, on 60% of the issue slots.  A first
 // form in which the block waited for each tile's state took 791 us.
 //
 // Inputs come in units of one tensor's tile (16 KB), in a ring of kUnits.
@@ -1048,8 +1048,8 @@ struct BackwardArgs {
 //
 // kLag: a tile is finished after the next one's gates, as in the forward pass,
 // so that a fold has a tile's time to come; otherwise at once, which takes less
-// memory and, in float32, leaves room for three blocks (75 us with two, 69 with
-// three at 10007 x 1000; bf16, 32768 x 1024: 108 with two and 113 with three, which
+// memory and, in float32, leaves room for three blocks (75 us with two, 68 with
+// three at 10007 x 1000; bf16, 32768 x 1024: 109 with two and 113 with three, which
 // are short of registers).  See lags.
 constexpr int kBackWarps = 4;
 constexpr int kHalves = 2 * kBackWarps;
@@ -1539,8 +1539,8 @@ struct Args {
 // Four channels per thread (8 or 16 bytes of each input, 16 of the state), a
 // block of 128 threads per 512 channels of a row.  The inputs and the state
 // are on their way while the block looks for its slot among the earlier rows'.
-// Bound by the bytes: 1024 x 3840 float32 on a pool of 1500 rows in 17.2 us (0.82 of
-// the copy rate); 64 x 1920 bf16 is one launch's latency, 2.6 us.
+// Bound by the bytes: 1024 x 3840 float32 on a pool of 1500 rows in 16.5 us (0.86 of
+// the copy rate); 64 x 1920 bf16 is one launch's latency, 2.2 us.
 constexpr int kStepThreads = 128;
 
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const Args P, float* state,

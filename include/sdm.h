@@ -61,7 +61,7 @@ typedef enum {
 } sdm_status;
 
 /* SDM_E4M3 (8-bit float, 4 exponent bits, largest value 448) is an output
- * type of sdm_add_rmsnorm only; every other argument takes the first two. */
+ * type of the residual norms only; every other argument takes the first two. */
 typedef enum { SDM_F32 = 0, SDM_BF16 = 1, SDM_E4M3 = 2 } sdm_dtype;
 typedef enum { SDM_SCORE_DOT = 0, SDM_SCORE_IDW = 1 } sdm_score_kind;
 typedef enum { SDM_UPDATE_EQ4 = 0, SDM_UPDATE_SHARED_RESIDUAL = 1 } sdm_update_form;
@@ -397,6 +397,190 @@ sdm_status sdm_add_rmsnorm_backward(const sdm_norm* shape, const void* s, const 
                                     const float* gamma, const void* ds, float eps, void* dx,
                                     float* dgamma, void* workspace, size_t ws_bytes,
                                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * Residual addition and layer norm: sdm_add_rmsnorm with the mean taken off and
+ * an offset added, everything else as there:
+ *   s = x + residual, rounded to the shape's dtype;  c = s - mean_c s_c;
+ *   n = c / sqrt(mean_c c_c^2 + eps) * gamma + beta, in float32;
+ *   out = n, or in 8 bits with scales.
+ * The mean is taken first and the squares are those of c.
+ *   beta: [D] float32 or NULL for zeros. */
+sdm_status sdm_add_layernorm(const sdm_norm* shape, const void* x, const void* residual,
+                             const float* gamma, const float* beta, float eps, void* s, void* out,
+                             sdm_dtype out_dtype, int group, float* scale, void* stream);
+
+/* Bytes of device workspace sdm_add_layernorm_backward needs (0 for an invalid
+ * shape). */
+size_t sdm_add_layernorm_workspace_size(const sdm_norm* shape);
+
+/* Backward of the 16/32-bit forward from the s it wrote, as
+ * sdm_add_rmsnorm_backward:
+ *   w = dout gamma;  inv = 1 / sqrt(mean c^2 + eps);
+ *   dx = ds + inv (w - mean_c w - c inv mean_c(w c inv));
+ *   dgamma = sum_rows dout c inv;  dbeta = sum_rows dout.
+ *   dgamma, dbeta: [D] float32 out, written, or NULL; workspace: needed if one
+ *   of them is given, one per overlapping call.
+ * Results are the same from run to run, bit for bit. */
+sdm_status sdm_add_layernorm_backward(const sdm_norm* shape, const void* s, const void* dout,
+                                      const float* gamma, const void* ds, float eps, void* dx,
+                                      float* dgamma, float* dbeta, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Short causal convolution of every channel with its own taps, in front of a
+ * recurrence.  For every sequence, row t and channel c:
+ *   pre = bias[c] + sum_{k < taps} w[c, taps-1-k] x[t-k, c];
+ *   y[t,c] = pre, or silu(pre) = pre / (1 + exp(-pre)),
+ * in float32, rounded once.  Rows before a sequence are those of its start x0.
+ * Packing, offsets, row strides and the treatment of bad offsets are those of
+ * the recurrence above. */
+typedef enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1 } sdm_activation;
+
+typedef struct {
+  int n_seq;              /* sequences, 0..65535                                 */
+  int rows;               /* rows of the packed tensors, at most 2^30            */
+  int D;                  /* channels, a multiple of 8, at most 65536            */
+  int taps;               /* 2, 3 or 4                                           */
+  sdm_activation act;
+  int ld;                 /* elements between rows of x; a multiple of 8, at     */
+                          /* least D; 0 = D                                      */
+  int ld_grad;            /* the same of dx; 0 = D                               */
+  sdm_dtype dtype;        /* of x, y, x0, xT, state and their gradients:         */
+                          /* SDM_F32 / SDM_BF16                                  */
+} sdm_conv;
+
+/* Forward pass.
+ *   x: [rows, D] (rows ld apart);  w: [D, taps] float32, the last tap that of
+ *   the row itself;  bias: [D] float32 or NULL for zeros;  offsets: as in
+ *   sdm_recurrence_forward, or NULL;
+ *   x0: [n_seq, taps-1, D] the rows in front of every sequence, oldest first,
+ *   or NULL for zeros;
+ *   y: [rows, D] out;  xT: [n_seq, taps-1, D] out, the last taps-1 rows of
+ *   every sequence (of its start, where it is shorter), or NULL (may be x0
+ *   itself: states updated in place).
+ * Apart from xT = x0, outputs must not overlap inputs or one another. */
+sdm_status sdm_short_conv_forward(const sdm_conv* shape, const void* x, const float* w,
+                                  const float* bias, const int32_t* offsets, const void* x0,
+                                  void* y, void* xT, void* stream);
+
+/* Bytes of device workspace sdm_short_conv_backward needs (0 for an invalid
+ * shape). */
+size_t sdm_short_conv_workspace_size(const sdm_conv* shape);
+
+/* Backward pass for the same shape and inputs.
+ *   dy: [rows, D] gradient of y;  dxT: [n_seq, taps-1, D] gradient of xT, or
+ *   NULL for zeros;
+ *   dx: [rows, D] out (rows ld_grad apart);  dw: [D, taps], dbias: [D] float32
+ *   out, sums over every row of every sequence, or NULL;  dx0: [n_seq, taps-1,
+ *   D] out, or NULL;
+ *   workspace: at least sdm_short_conv_workspace_size bytes if dw or dbias is
+ *   given (else it may be NULL), one per overlapping call.
+ * Gradients are written, not added to what the arrays held; outputs must not
+ * overlap inputs or one another.  With n_seq = 0 only dw and dbias are written
+ * (zeros).  Results are the same from run to run, bit for bit. */
+sdm_status sdm_short_conv_backward(const sdm_conv* shape, const void* x, const float* w,
+                                   const float* bias, const int32_t* offsets, const void* x0,
+                                   const void* dy, const void* dxT, void* dx, float* dw,
+                                   float* dbias, void* dx0, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/* One token per sequence on a pool of windows (decode): row i of x goes
+ * through the window slots[i], which loses its oldest row and gains x's.
+ *   state: [n_slots, taps-1, D] in the shape's dtype, in place;  slots, n_slots
+ *   and what is skipped and recorded: as in sdm_recurrence_step.
+ * Needs no workspace.  y must not overlap an input. */
+sdm_status sdm_short_conv_step(const sdm_conv* shape, const void* x, const float* w,
+                               const float* bias, void* state, int n_slots, const int32_t* slots,
+                               void* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Selective state space scan: a diagonal recurrence with N states per channel
+ * whose time step, input and output vectors depend on the token.  For every
+ * sequence, row t, channel c of group g and state n:
+ *   delta = softplus(dt[t,c] + bias[c]);
+ *   h[c,n] = exp(-A[c,n] delta) h[c,n] + delta x[t,c] B[t,g,n];
+ *   inner = sum_n C[t,g,n] h[c,n] + skip[c] x[t,c];
+ *   y[t,c] = inner, or inner z / (1 + exp(-z)) with z = z[t,c].
+ * Groups are of D / groups neighbouring channels.  The state h is float32
+ * throughout; y is rounded once.  Packing, offsets and the treatment of bad
+ * offsets are those of the recurrence above. */
+typedef struct {
+  int n_seq;              /* sequences, 0..65535                                 */
+  int rows;               /* rows of the packed tensors, at most 2^30            */
+  int D;                  /* channels, at most 65536                             */
+  int N;                  /* states per channel: 8, 16, 32 or 64                 */
+  int groups;             /* dividing D into multiples of 8 channels             */
+  int ld;                 /* elements between rows of x and of dt; every stride  */
+                          /* is a multiple of 8 and at least the row; 0 = dense  */
+  int ld_z;               /* of z                                                */
+  int ld_bc;              /* of B and of C (rows of groups * N)                  */
+  int ld_grad;            /* of dx and of ddt                                    */
+  int ld_z_grad;          /* of dz                                               */
+  int ld_bc_grad;         /* of dB and of dC                                     */
+  sdm_dtype dtype;        /* of x, dt, B, C, z, y, dy and the gradients of the   */
+                          /* rows: SDM_F32 / SDM_BF16                            */
+} sdm_selective;
+
+/* Bytes of device workspace the forward and the backward pass need, and of the
+ * `states` array that carries what the backward pass needs from the forward one
+ * (a state every 16 rows; 0 for an invalid shape). */
+size_t sdm_selective_scan_workspace_size(const sdm_selective* shape);
+size_t sdm_selective_scan_backward_workspace_size(const sdm_selective* shape);
+size_t sdm_selective_scan_states_size(const sdm_selective* shape);
+
+/* Forward pass.
+ *   x, dt: [rows, D];  A: [D, N] float32, not negative;  B, C: [rows, groups,
+ *   N];  skip, bias: [D] float32 or NULL for zeros;  z: [rows, D] or NULL for
+ *   no gate;  offsets: as in sdm_recurrence_forward, or NULL;
+ *   h0: [n_seq, D, N] float32 initial states, or NULL for zeros;
+ *   y: [rows, D] out;  hT: [n_seq, D, N] float32 final states out, or NULL (may
+ *   be h0 itself: states updated in place);
+ *   states: NULL, or caller-owned scratch of sdm_selective_scan_states_size
+ *   bytes that sdm_selective_scan_backward reads;
+ *   workspace: at least sdm_selective_scan_workspace_size bytes, contents
+ *   irrelevant on entry and on return; calls that may overlap on the GPU (other
+ *   streams, captured graphs that run at the same time) need one each.
+ * Apart from hT = h0, outputs must not overlap inputs or one another.  Results
+ * are the same from run to run, bit for bit. */
+sdm_status sdm_selective_scan_forward(const sdm_selective* shape, const void* x, const void* dt,
+                                      const float* A, const void* B, const void* C,
+                                      const float* skip, const float* bias, const void* z,
+                                      const int32_t* offsets, const float* h0, void* y, float* hT,
+                                      float* states, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/* Backward pass for the same shape, inputs and offsets and the `states` that
+ * the forward pass wrote.
+ *   dy: [rows, D] gradient of y;  dhT: [n_seq, D, N] float32 gradient of hT, or
+ *   NULL for zeros;
+ *   dx, ddt: [rows, D], dB, dC: [rows, groups, N], dz: [rows, D] (with z only)
+ *   out;  dA: [D, N], dskip, dbias: [D] float32 out, sums over every row of
+ *   every sequence, or NULL;  dh0: [n_seq, D, N] float32 out, or NULL (may be
+ *   dhT itself);
+ *   workspace: at least sdm_selective_scan_backward_workspace_size bytes.
+ * Gradients are written, not added to what the arrays held.  Overlap and
+ * repeatability as in the forward pass.  With n_seq = 0 only dA, dskip and
+ * dbias are written (zeros). */
+sdm_status sdm_selective_scan_backward(const sdm_selective* shape, const void* x, const void* dt,
+                                       const float* A, const void* B, const void* C,
+                                       const float* skip, const float* bias, const void* z,
+                                       const int32_t* offsets, const float* states,
+                                       const void* dy, const float* dhT, void* dx, void* ddt,
+                                       float* dA, void* dB, void* dC, float* dskip, float* dbias,
+                                       void* dz, float* dh0, void* workspace, size_t ws_bytes,
+                                       void* stream);
+
+/* One token per sequence on a pool of states (decode): row i of the inputs
+ * steps state slots[i] in place and writes y row i.
+ *   state: [n_slots, D, N] float32, in place;  slots, n_slots and what is
+ *   skipped and recorded: as in sdm_recurrence_step.
+ * Needs no workspace.  y must not overlap an input. */
+sdm_status sdm_selective_scan_step(const sdm_selective* shape, const void* x, const void* dt,
+                                   const float* A, const void* B, const void* C,
+                                   const float* skip, const float* bias, const void* z,
+                                   float* state, int n_slots, const int32_t* slots, void* y,
+                                   void* stream);
 
 /* Synchronizes `stream`, then returns and clears the device status word of
  * the current device (SDM_OK if no device-side failure was recorded). */

@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_PKG, "_build", "libsdm_gb300.so")
 SDM_F32, SDM_BF16, SDM_E4M3 = 0, 1, 2
 SDM_SCORE_DOT, SDM_SCORE_IDW = 0, 1
 SDM_UPDATE_EQ4, SDM_UPDATE_SHARED_RESIDUAL = 0, 1
+SDM_ACT_NONE, SDM_ACT_SILU = 0, 1
 
 STATUS = {0: "SDM_OK", 1: "SDM_ERR_INVALID_ARG", 2: "SDM_ERR_UNSUPPORTED", 3: "SDM_ERR_CUDA",
           4: "SDM_ERR_TIMEOUT", 5: "SDM_ERR_DEVICE_BOUNDS", 6: "SDM_ERR_DUPLICATE_SLOT"}
@@ -34,7 +35,13 @@ EXPORTS = ["sdm_status_string", "sdm_subscores", "sdm_select", "sdm_address",
            "sdm_set_recurrence_wait",
            "sdm_recurrence_workspace_size", "sdm_recurrence_states_size",
            "sdm_recurrence_forward", "sdm_recurrence_backward", "sdm_recurrence_step",
-           "sdm_add_rmsnorm", "sdm_add_rmsnorm_workspace_size", "sdm_add_rmsnorm_backward"]
+           "sdm_add_rmsnorm", "sdm_add_rmsnorm_workspace_size", "sdm_add_rmsnorm_backward",
+           "sdm_add_layernorm", "sdm_add_layernorm_workspace_size", "sdm_add_layernorm_backward",
+           "sdm_short_conv_workspace_size", "sdm_short_conv_forward", "sdm_short_conv_backward",
+           "sdm_short_conv_step",
+           "sdm_selective_scan_workspace_size", "sdm_selective_scan_backward_workspace_size",
+           "sdm_selective_scan_states_size", "sdm_selective_scan_forward",
+           "sdm_selective_scan_backward", "sdm_selective_scan_step"]
 
 
 class SdmUnavailable(RuntimeError):
@@ -86,12 +93,42 @@ class Norm(ctypes.Structure):
         return "Norm(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class Conv(ctypes.Structure):
+    """Mirror of ``sdm_conv`` in include/sdm.h."""
+    _fields_ = [("n_seq", ctypes.c_int), ("rows", ctypes.c_int), ("D", ctypes.c_int),
+                ("taps", ctypes.c_int), ("act", ctypes.c_int), ("ld", ctypes.c_int),
+                ("ld_grad", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+    def __repr__(self):
+        return "Conv(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class Selective(ctypes.Structure):
+    """Mirror of ``sdm_selective`` in include/sdm.h."""
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "n_seq", "rows", "D", "N", "groups", "ld", "ld_z", "ld_bc", "ld_grad", "ld_z_grad",
+        "ld_bc_grad", "dtype")]
+
+    def __repr__(self):
+        return "Selective(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
 def make_recurrence(n_seq, rows, D, dtype=SDM_BF16, ld=0, ld_grad=0) -> Recurrence:
     return Recurrence(n_seq, rows, D, ld, ld_grad, dtype)
 
 
 def make_norm(rows, D, dtype=SDM_BF16) -> Norm:
     return Norm(rows, D, dtype)
+
+
+def make_conv(n_seq, rows, D, taps=4, act=SDM_ACT_SILU, dtype=SDM_BF16, ld=0, ld_grad=0) -> Conv:
+    return Conv(n_seq, rows, D, taps, act, ld, ld_grad, dtype)
+
+
+def make_selective(n_seq, rows, D, N=16, groups=1, dtype=SDM_BF16, ld=0, ld_z=0, ld_bc=0,
+                   ld_grad=0, ld_z_grad=0, ld_bc_grad=0) -> Selective:
+    return Selective(n_seq, rows, D, N, groups, ld, ld_z, ld_bc, ld_grad, ld_z_grad, ld_bc_grad,
+                     dtype)
 
 
 def make_shape(B, H, T, n_sub, d_h, d_v, W, R, k_w=0, k_r=0, in_dtype=SDM_BF16,
@@ -116,6 +153,7 @@ def lib():
         raise SdmUnavailable(f"cannot load {LIB_PATH}: {e}") from e
     P, SP, I = ctypes.c_void_p, ctypes.POINTER(Shape), ctypes.c_int
     RP, NP, Z = ctypes.POINTER(Recurrence), ctypes.POINTER(Norm), ctypes.c_size_t
+    CP, XP = ctypes.POINTER(Conv), ctypes.POINTER(Selective)
     sig = {
         "sdm_status_string": ([I], ctypes.c_char_p),
         "sdm_subscores": ([SP, P, P, P, P], I),
@@ -145,6 +183,19 @@ def lib():
         "sdm_add_rmsnorm": ([NP, P, P, P, ctypes.c_float, P, P, I, I, P, P], I),
         "sdm_add_rmsnorm_workspace_size": ([NP], Z),
         "sdm_add_rmsnorm_backward": ([NP, P, P, P, P, ctypes.c_float, P, P, P, Z, P], I),
+        "sdm_add_layernorm": ([NP, P, P, P, P, ctypes.c_float, P, P, I, I, P, P], I),
+        "sdm_add_layernorm_workspace_size": ([NP], Z),
+        "sdm_add_layernorm_backward": ([NP, P, P, P, P, ctypes.c_float, P, P, P, P, Z, P], I),
+        "sdm_short_conv_workspace_size": ([CP], Z),
+        "sdm_short_conv_forward": ([CP] + [P] * 8, I),
+        "sdm_short_conv_backward": ([CP] + [P] * 12 + [Z, P], I),
+        "sdm_short_conv_step": ([CP] + [P] * 4 + [I, P, P, P], I),
+        "sdm_selective_scan_workspace_size": ([XP], Z),
+        "sdm_selective_scan_backward_workspace_size": ([XP], Z),
+        "sdm_selective_scan_states_size": ([XP], Z),
+        "sdm_selective_scan_forward": ([XP] + [P] * 14 + [Z, P], I),
+        "sdm_selective_scan_backward": ([XP] + [P] * 22 + [Z, P], I),
+        "sdm_selective_scan_step": ([XP] + [P] * 9 + [I, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -724,3 +775,306 @@ def sdm_add_rmsnorm_backward(sh: Norm, s, dout, gamma=None, ds=None, eps: float 
     if rc:
         raise SdmError(rc, "sdm_add_rmsnorm_backward")
     return dict(dx=dx, dgamma=dgamma)
+
+
+def sdm_add_layernorm(sh: Norm, x, residual=None, gamma=None, beta=None, eps: float = 1e-5, s=None,
+                      out=None, out_dtype=SDM_BF16, group: int = 0, scale=None, stream=None):
+    """Residual addition and layer norm of x [rows, D]; returns dict(s, out,
+    scale) as sdm_add_rmsnorm does; gamma, beta [D] float32 or None."""
+    L = lib()
+    dev, raw, ts = _where(x, stream)
+    dt, odt = _torch_dtype(sh.dtype, "sdm_add_layernorm"), _torch_dtype(out_dtype, "sdm_add_layernorm")
+    rows, D = sh.rows, sh.D
+    n, n_scale = rows * D, 0
+    if s is None and residual is not None:
+        s = _make((rows, D), dt, x, ts)
+    if out is None:
+        out = _make((rows, D), odt, x, ts)
+    if out_dtype == SDM_E4M3:
+        if group < 0 or (group and D % group):
+            raise SdmError(1, "sdm_add_layernorm")
+        n_scale = rows * (D // group if group else 1)
+        if scale is None:
+            scale = _make((rows, D // group) if group else (rows,), _F32, x, ts)
+    rc = L.sdm_add_layernorm(
+        ctypes.byref(sh), _at(x, "x", dt, n, dev),
+        None if residual is None else _at(residual, "residual", dt, n, dev),
+        None if gamma is None else _at(gamma, "gamma", _F32, D, dev),
+        None if beta is None else _at(beta, "beta", _F32, D, dev), eps,
+        None if s is None else _at(s, "s", dt, n, dev), _at(out, "out", odt, n, dev), out_dtype,
+        group, None if scale is None else _at(scale, "scale", _F32, n_scale, dev), raw)
+    if rc:
+        raise SdmError(rc, "sdm_add_layernorm")
+    return dict(s=s, out=out, scale=scale)
+
+
+def sdm_add_layernorm_workspace_size(sh: Norm) -> int:
+    """Bytes of device workspace sdm_add_layernorm_backward needs."""
+    return int(lib().sdm_add_layernorm_workspace_size(ctypes.byref(sh)))
+
+
+def sdm_add_layernorm_backward(sh: Norm, s, dout, gamma=None, ds=None, eps: float = 1e-5, dx=None,
+                               dgamma=None, dbeta=None, workspace=None, stream=None):
+    """Gradients of sdm_add_layernorm from dout [rows, D] and ds [rows, D] (the
+    gradient that reaches s from elsewhere, or None).  Returns dict(dx, dgamma,
+    dbeta); dx is the gradient of x and of residual, dgamma and dbeta are made
+    only where gamma is given."""
+    L = lib()
+    dev, raw, ts = _where(s, stream)
+    dt, rows, D = _torch_dtype(sh.dtype, "sdm_add_layernorm_backward"), sh.rows, sh.D
+    n = rows * D
+    if dx is None:
+        dx = _make((rows, D), dt, s, ts)
+    if gamma is not None:
+        dgamma = _make((D,), _F32, s, ts) if dgamma is None else dgamma
+        dbeta = _make((D,), _F32, s, ts) if dbeta is None else dbeta
+    ws, wsp, nws = None, None, 0
+    if dgamma is not None or dbeta is not None:
+        ws, wsp, nws = _scratch(workspace, L.sdm_add_layernorm_workspace_size(ctypes.byref(sh)), s,
+                                ts, dev)
+    rc = L.sdm_add_layernorm_backward(
+        ctypes.byref(sh), _at(s, "s", dt, n, dev), _at(dout, "dout", dt, n, dev),
+        None if gamma is None else _at(gamma, "gamma", _F32, D, dev),
+        None if ds is None else _at(ds, "ds", dt, n, dev), eps, _at(dx, "dx", dt, n, dev),
+        None if dgamma is None else _at(dgamma, "dgamma", _F32, D, dev),
+        None if dbeta is None else _at(dbeta, "dbeta", _F32, D, dev), wsp, nws, raw)
+    if rc:
+        raise SdmError(rc, "sdm_add_layernorm_backward")
+    return dict(dx=dx, dgamma=dgamma, dbeta=dbeta)
+
+
+# ------------------------------------------- short convolution, selective scan
+
+def sdm_short_conv_workspace_size(sh: Conv) -> int:
+    """Bytes of device workspace sdm_short_conv_backward needs."""
+    return int(lib().sdm_short_conv_workspace_size(ctypes.byref(sh)))
+
+
+def sdm_short_conv_forward(sh: Conv, x, w, bias=None, offsets=None, x0=None, y=None, xT=None,
+                           stream=None):
+    """Short causal convolution over packed sequences.  x [rows, D] (row stride
+    ``sh.ld``); w [D, taps], bias [D] float32; offsets [n_seq + 1] int32 on the
+    device or None for equal parts; x0 [n_seq, taps - 1, D] the rows in front.
+    Returns dict(y, xT), xT [n_seq, taps - 1, D] the last rows."""
+    L = lib()
+    dev, raw, ts = _where(x, stream)
+    dt, rows, D, n = _torch_dtype(sh.dtype, "sdm_short_conv_forward"), sh.rows, sh.D, sh.n_seq
+    n_ends = n * (sh.taps - 1) * D
+    if y is None:
+        y = _make((rows, D), dt, x, ts)
+    if xT is None:
+        xT = _make((n, max(sh.taps - 1, 0), D), dt, x, ts)
+    rc = L.sdm_short_conv_forward(
+        ctypes.byref(sh), _rows_at(x, "x", dt, rows, D, sh.ld or D, dev),
+        _at(w, "w", _F32, D * sh.taps, dev),
+        None if bias is None else _at(bias, "bias", _F32, D, dev),
+        None if offsets is None else _at(offsets, "offsets", _I32, n + 1, dev),
+        None if x0 is None else _at(x0, "x0", dt, n_ends, dev), _at(y, "y", dt, rows * D, dev),
+        _at(xT, "xT", dt, n_ends, dev), raw)
+    if rc:
+        raise SdmError(rc, "sdm_short_conv_forward")
+    return dict(y=y, xT=xT)
+
+
+def sdm_short_conv_backward(sh: Conv, x, w, dy, bias=None, offsets=None, x0=None, dxT=None, dx=None,
+                            dw=None, dbias=None, dx0=None, workspace=None, stream=None):
+    """Gradients of sdm_short_conv_forward from dy [rows, D] and dxT [n_seq,
+    taps - 1, D] (None = zeros).  dx has row stride ``sh.ld_grad`` and must be
+    given where that is not D.  Returns dict(dx, dw, dbias, dx0); dbias is made
+    only where bias is given."""
+    L = lib()
+    dev, raw, ts = _where(x, stream)
+    dt, rows, D, n = _torch_dtype(sh.dtype, "sdm_short_conv_backward"), sh.rows, sh.D, sh.n_seq
+    ldg, n_ends = sh.ld_grad or D, n * (sh.taps - 1) * D
+    if dx is None and ldg == D:
+        dx = _make((rows, D), dt, x, ts)
+    if dw is None:
+        dw = _make((D, sh.taps), _F32, x, ts)
+    if dbias is None and bias is not None:
+        dbias = _make((D,), _F32, x, ts)
+    if dx0 is None:
+        dx0 = _make((n, max(sh.taps - 1, 0), D), dt, x, ts)
+    ws, wsp, nws = _scratch(workspace, L.sdm_short_conv_workspace_size(ctypes.byref(sh)), x, ts, dev)
+    rc = L.sdm_short_conv_backward(
+        ctypes.byref(sh), _rows_at(x, "x", dt, rows, D, sh.ld or D, dev),
+        _at(w, "w", _F32, D * sh.taps, dev),
+        None if bias is None else _at(bias, "bias", _F32, D, dev),
+        None if offsets is None else _at(offsets, "offsets", _I32, n + 1, dev),
+        None if x0 is None else _at(x0, "x0", dt, n_ends, dev), _at(dy, "dy", dt, rows * D, dev),
+        None if dxT is None else _at(dxT, "dxT", dt, n_ends, dev),
+        _rows_at(dx, "dx", dt, rows, D, ldg, dev), _at(dw, "dw", _F32, D * sh.taps, dev),
+        None if dbias is None else _at(dbias, "dbias", _F32, D, dev),
+        _at(dx0, "dx0", dt, n_ends, dev), wsp, nws, raw)
+    if rc:
+        raise SdmError(rc, "sdm_short_conv_backward")
+    return dict(dx=dx, dw=dw, dbias=dbias, dx0=dx0)
+
+
+def _pool_slots(state, name, shape):
+    if tuple(state.shape[1:]) != shape:
+        raise ValueError(f"{name} has shape {tuple(state.shape)}, expected (n_slots, "
+                         + ", ".join(map(str, shape)) + ")")
+    return state.shape[0]
+
+
+def sdm_short_conv_step(sh: Conv, x, w, state, bias=None, slots=None, y=None, stream=None):
+    """One token per sequence: row i of x [rows, D] goes through the window
+    slots[i] (int32; negative = padding; None = row i) of state [n_slots,
+    taps - 1, D] in place.  Returns y [rows, D]."""
+    L = lib()
+    dev, raw, ts = _where(x, stream)
+    dt, rows, D = _torch_dtype(sh.dtype, "sdm_short_conv_step"), sh.rows, sh.D
+    if y is None:
+        y = _make((rows, D), dt, x, ts)
+    n_slots = _pool_slots(state, "state", (sh.taps - 1, D))
+    rc = L.sdm_short_conv_step(
+        ctypes.byref(sh), _rows_at(x, "x", dt, rows, D, sh.ld or D, dev),
+        _at(w, "w", _F32, D * sh.taps, dev),
+        None if bias is None else _at(bias, "bias", _F32, D, dev),
+        _at(state, "state", dt, 0, dev), n_slots,
+        None if slots is None else _at(slots, "slots", _I32, rows, dev),
+        _at(y, "y", dt, rows * D, dev), raw)
+    if rc:
+        raise SdmError(rc, "sdm_short_conv_step")
+    return y
+
+
+def sdm_selective_scan_workspace_size(sh: Selective) -> int:
+    """Bytes of device workspace sdm_selective_scan_forward needs."""
+    return int(lib().sdm_selective_scan_workspace_size(ctypes.byref(sh)))
+
+
+def sdm_selective_scan_backward_workspace_size(sh: Selective) -> int:
+    """Bytes of device workspace sdm_selective_scan_backward needs."""
+    return int(lib().sdm_selective_scan_backward_workspace_size(ctypes.byref(sh)))
+
+
+def sdm_selective_scan_states_size(sh: Selective) -> int:
+    """Bytes of the states the forward pass saves for the backward pass."""
+    return int(lib().sdm_selective_scan_states_size(ctypes.byref(sh)))
+
+
+def _selective_inputs(sh, dt, dev, x, dt_, A, B, C, skip, bias, z):
+    """Addresses of the inputs that every selective scan call has, in order."""
+    rows, D, bc = sh.rows, sh.D, sh.groups * sh.N
+    ld, ld_bc = sh.ld or D, sh.ld_bc or bc
+    return (_rows_at(x, "x", dt, rows, D, ld, dev), _rows_at(dt_, "dt", dt, rows, D, ld, dev),
+            _at(A, "A", _F32, D * sh.N, dev), _bc_at(B, "B", dt, rows, bc, ld_bc, dev),
+            _bc_at(C, "C", dt, rows, bc, ld_bc, dev),
+            None if skip is None else _at(skip, "skip", _F32, D, dev),
+            None if bias is None else _at(bias, "bias", _F32, D, dev),
+            None if z is None else _rows_at(z, "z", dt, rows, D, sh.ld_z or D, dev))
+
+
+def _bc_at(t, name, dtype, rows, width, ld, dev):
+    """Address of B or C, [rows, groups, N] or [rows, groups * N]."""
+    if ld != width and t is not None and t.dim() == 3:
+        if t.shape[1] * t.shape[2] != width or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError(f"{name} has shape {tuple(t.shape)} and strides {t.stride()}, "
+                             f"expected rows of {width} neighbouring elements")
+        t = t.flatten(1)
+    return _rows_at(t, name, dtype, rows, width, ld, dev)
+
+
+def sdm_selective_scan_forward(sh: Selective, x, dt, A, B, C, skip=None, bias=None, z=None,
+                               offsets=None, h0=None, y=None, hT=None, states=None,
+                               save_states=False, workspace=None, stream=None):
+    """Selective state space scan over packed sequences.  x, dt [rows, D] (row
+    stride ``sh.ld``), z [rows, D] (``sh.ld_z``) or None; B, C [rows, groups, N]
+    (``sh.ld_bc``); A [D, N], skip, bias [D] float32; offsets [n_seq + 1] int32
+    on the device or None for equal parts; h0 [n_seq, D, N] float32.  Returns
+    dict(y, hT, states); states (for the backward pass) only if given or
+    ``save_states``."""
+    L = lib()
+    dev, raw, ts = _where(x, stream)
+    ty, rows, D, n, ref = _torch_dtype(sh.dtype, "sdm_selective_scan_forward"), sh.rows, sh.D, sh.n_seq, ctypes.byref(sh)
+    if y is None:
+        y = _make((rows, D), ty, x, ts)
+    if hT is None:
+        hT = _make((n, D, sh.N), _F32, x, ts)
+    n_states = 0
+    if save_states or states is not None:
+        n_states = L.sdm_selective_scan_states_size(ref) // 4
+        if states is None:
+            states = _make((n_states,), _F32, x, ts)
+    ws, wsp, nws = _scratch(workspace, L.sdm_selective_scan_workspace_size(ref), x, ts, dev)
+    rc = L.sdm_selective_scan_forward(
+        ref, *_selective_inputs(sh, ty, dev, x, dt, A, B, C, skip, bias, z),
+        None if offsets is None else _at(offsets, "offsets", _I32, n + 1, dev),
+        None if h0 is None else _at(h0, "h0", _F32, n * D * sh.N, dev),
+        _at(y, "y", ty, rows * D, dev), _at(hT, "hT", _F32, n * D * sh.N, dev),
+        None if states is None else _at(states, "states", _F32, n_states, dev), wsp, nws, raw)
+    if rc:
+        raise SdmError(rc, "sdm_selective_scan_forward")
+    return dict(y=y, hT=hT, states=states)
+
+
+def sdm_selective_scan_backward(sh: Selective, x, dt, A, B, C, states, dy, skip=None, bias=None,
+                                z=None, offsets=None, dhT=None, dx=None, ddt=None, dA=None, dB=None,
+                                dC=None, dskip=None, dbias=None, dz=None, dh0=None, workspace=None,
+                                stream=None):
+    """Gradients of sdm_selective_scan_forward from dy [rows, D] and dhT [n_seq,
+    D, N] float32 (None = zeros) with the states it saved.  dx, ddt have row
+    stride ``sh.ld_grad``, dz ``sh.ld_z_grad``, dB and dC ``sh.ld_bc_grad``;
+    those that are not dense must be given.  Returns dict(dx, ddt, dA, dB, dC,
+    dskip, dbias, dz, dh0); dskip, dbias, dz are made only where skip, bias, z
+    are given."""
+    L = lib()
+    dev, raw, ts = _where(x, stream)
+    ty, rows, D, n, ref = _torch_dtype(sh.dtype, "sdm_selective_scan_backward"), sh.rows, sh.D, sh.n_seq, ctypes.byref(sh)
+    bc = sh.groups * sh.N
+    ldg, ldzg, ldbg = sh.ld_grad or D, sh.ld_z_grad or D, sh.ld_bc_grad or bc
+    if ldg == D:
+        dx = _make((rows, D), ty, x, ts) if dx is None else dx
+        ddt = _make((rows, D), ty, x, ts) if ddt is None else ddt
+    if ldzg == D and z is not None and dz is None:
+        dz = _make((rows, D), ty, x, ts)
+    if ldbg == bc:
+        dB = _make((rows, sh.groups, sh.N), ty, x, ts) if dB is None else dB
+        dC = _make((rows, sh.groups, sh.N), ty, x, ts) if dC is None else dC
+    if dA is None:
+        dA = _make((D, sh.N), _F32, x, ts)
+    if dskip is None and skip is not None:
+        dskip = _make((D,), _F32, x, ts)
+    if dbias is None and bias is not None:
+        dbias = _make((D,), _F32, x, ts)
+    if dh0 is None:
+        dh0 = _make((n, D, sh.N), _F32, x, ts)
+    ws, wsp, nws = _scratch(workspace, L.sdm_selective_scan_backward_workspace_size(ref), x, ts, dev)
+    rc = L.sdm_selective_scan_backward(
+        ref, *_selective_inputs(sh, ty, dev, x, dt, A, B, C, skip, bias, z),
+        None if offsets is None else _at(offsets, "offsets", _I32, n + 1, dev),
+        _at(states, "states", _F32, L.sdm_selective_scan_states_size(ref) // 4, dev),
+        _at(dy, "dy", ty, rows * D, dev),
+        None if dhT is None else _at(dhT, "dhT", _F32, n * D * sh.N, dev),
+        _rows_at(dx, "dx", ty, rows, D, ldg, dev), _rows_at(ddt, "ddt", ty, rows, D, ldg, dev),
+        _at(dA, "dA", _F32, D * sh.N, dev), _bc_at(dB, "dB", ty, rows, bc, ldbg, dev),
+        _bc_at(dC, "dC", ty, rows, bc, ldbg, dev),
+        None if dskip is None else _at(dskip, "dskip", _F32, D, dev),
+        None if dbias is None else _at(dbias, "dbias", _F32, D, dev),
+        None if z is None else _rows_at(dz, "dz", ty, rows, D, ldzg, dev),
+        _at(dh0, "dh0", _F32, n * D * sh.N, dev), wsp, nws, raw)
+    if rc:
+        raise SdmError(rc, "sdm_selective_scan_backward")
+    return dict(dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dskip=dskip, dbias=dbias, dz=dz, dh0=dh0)
+
+
+def sdm_selective_scan_step(sh: Selective, x, dt, A, B, C, state, skip=None, bias=None, z=None,
+                            slots=None, y=None, stream=None):
+    """One token per sequence: row i of the inputs steps state row slots[i]
+    (int32; negative = padding; None = row i) of state [n_slots, D, N] float32
+    in place.  Returns y [rows, D]."""
+    L = lib()
+    dev, raw, ts = _where(x, stream)
+    ty, rows, D = _torch_dtype(sh.dtype, "sdm_selective_scan_step"), sh.rows, sh.D
+    if y is None:
+        y = _make((rows, D), ty, x, ts)
+    n_slots = _pool_slots(state, "state", (D, sh.N))
+    rc = L.sdm_selective_scan_step(
+        ctypes.byref(sh), *_selective_inputs(sh, ty, dev, x, dt, A, B, C, skip, bias, z),
+        _at(state, "state", _F32, 0, dev), n_slots,
+        None if slots is None else _at(slots, "slots", _I32, rows, dev),
+        _at(y, "y", ty, rows * D, dev), raw)
+    if rc:
+        raise SdmError(rc, "sdm_selective_scan_step")
+    return y

@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libsdm_gb300.so")
 SOURCES = ["sdm_api.cu", "address.cu", "plan.cu", "scan.cu", "undo.cu", "epilogue.cu",
            "decode.cu", "sdm_noalloc.cu", "rowtraffic.cu", "recurrence.cu",
-           "residual_norm.cu"]
+           "residual_norm.cu", "short_conv.cu", "selective_scan.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

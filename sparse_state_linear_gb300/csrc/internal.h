@@ -166,6 +166,85 @@ cudaError_t launch_add_rmsnorm_backward(const NormDims& d, const void* s, const 
                                         const float* gamma, const void* ds, float eps, void* dx,
                                         float* dgamma, void* workspace, cudaStream_t stream);
 
+// Residual addition and layer norm (residual_norm.cu).
+size_t add_layernorm_workspace_bytes(const NormDims& d);
+cudaError_t launch_add_layernorm(const NormDims& d, const void* x, const void* residual,
+                                 const float* gamma, const float* beta, float eps, void* s,
+                                 void* out, int out_dtype, int group, float* scale,
+                                 cudaStream_t stream);
+cudaError_t launch_add_layernorm_backward(const NormDims& d, const void* s, const void* dout,
+                                          const float* gamma, const void* ds, float eps, void* dx,
+                                          float* dgamma, float* dbeta, void* workspace,
+                                          cudaStream_t stream);
+
+// Short causal convolution (short_conv.cu).  Parameters of one call, validated.
+struct ConvDims {
+  int n_seq, rows, D, taps, act;
+  long long ld, ld_grad;
+  int dtype;
+};
+struct ConvInputs {
+  const void* x;
+  const float* w;
+  const float* bias;
+  const int32_t* offsets;
+  const void* x0;
+};
+size_t short_conv_workspace_bytes(const ConvDims& d);
+cudaError_t launch_short_conv_forward(const ConvDims& d, const ConvInputs& in, void* y, void* xT,
+                                      unsigned* status, cudaStream_t stream);
+cudaError_t launch_short_conv_backward(const ConvDims& d, const ConvInputs& in, const void* dy,
+                                       const void* dxT, void* dx, float* dw, float* dbias,
+                                       void* dx0, void* workspace, unsigned* status,
+                                       cudaStream_t stream);
+cudaError_t launch_short_conv_step(const ConvDims& d, const ConvInputs& in, void* state,
+                                   int n_slots, const int32_t* slots, void* y, unsigned* status,
+                                   cudaStream_t stream);
+
+// Selective state space scan (selective_scan.cu).
+struct SelectiveDims {
+  int n_seq, rows, D, N, groups;
+  long long ld, ld_z, ld_bc, ld_grad, ld_z_grad, ld_bc_grad;
+  int dtype;
+};
+struct SelectiveInputs {
+  const void* x;
+  const void* dt;
+  const float* A;
+  const void* B;
+  const void* C;
+  const float* skip;
+  const float* bias;
+  const void* z;
+  const int32_t* offsets;
+};
+struct SelectiveGrads {
+  void* dx;
+  void* ddt;
+  float* dA;
+  void* dB;
+  void* dC;
+  float* dskip;
+  float* dbias;
+  void* dz;
+  float* dh0;
+};
+// Tiles of channels (the blocks of a chunk).
+int selective_scan_tiles(const SelectiveDims& d);
+size_t selective_scan_workspace_bytes(const SelectiveDims& d);
+size_t selective_scan_backward_workspace_bytes(const SelectiveDims& d);
+size_t selective_scan_states_bytes(const SelectiveDims& d);
+cudaError_t launch_selective_scan_forward(const SelectiveDims& d, const SelectiveInputs& in,
+                                          const float* h0, void* y, float* hT, float* states,
+                                          void* workspace, unsigned* status, cudaStream_t stream);
+cudaError_t launch_selective_scan_backward(const SelectiveDims& d, const SelectiveInputs& in,
+                                           const float* states, const void* dy, const float* dhT,
+                                           const SelectiveGrads& out, void* workspace,
+                                           unsigned* status, cudaStream_t stream);
+cudaError_t launch_selective_scan_step(const SelectiveDims& d, const SelectiveInputs& in,
+                                       float* state, int n_slots, const int32_t* slots, void* y,
+                                       unsigned* status, cudaStream_t stream);
+
 // Limits of the current device, queried once per device (sdm_api.cu): SM
 // count, shared memory per SM, and the opt-in maximum per CTA.
 struct DeviceLimits {

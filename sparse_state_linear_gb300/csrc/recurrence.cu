@@ -15,28 +15,19 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "gates.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "packed.cuh"
+#include "packing.cuh"
+#include "park.cuh"
+#include "rows.cuh"
 #include "tcgen05.cuh"
 
 namespace sdm {
 namespace {
 
 // ------------------------------------------------------------------- gates
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// log2(1 + e) for e in [0, 1]: 2 log2(e) atanh(t) with t = e / (2 + e), as t
-// times the degree-4 polynomial in t^2 that interpolates the rest at the
-// Chebyshev points of [0, 1/9] (relative error 4e-9).  With the roundings the
-// relative error is below 6.5 half steps for every e; the logarithm instruction
-// has an absolute bound, which is not enough where the gate hardly decays.
-constexpr float kLog0 = 2.88539004f, kLog1 = 0.961791694f, kLog2 = 0.577432871f,
-                kLog3 = 0.403451949f, kLog4 = 0.406230867f;
-__device__ __forceinline__ float log2p1_unit(float e) {
-  const float t = e * rcp(e + 2.f), z = t * t;
-  return t * fmaf(fmaf(fmaf(fmaf(kLog4, z, kLog3), z, kLog2), z, kLog1), z, kLog0);
-}
 // One row of one channel: the state behind it.
 __device__ __forceinline__ float step_one(float h, float za, float zb, float v, float A,
                                           float bias) {
@@ -62,40 +53,6 @@ __device__ __forceinline__ void store4(void* base, size_t i, int dt, float4 v) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(v.z, v.w);
   reinterpret_cast<uint2*>(base)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
                                                  *reinterpret_cast<const uint32_t*>(&b));
-}
-
-// ------------------------------------------------------------- pairs of floats
-// The packed forms take no immediates.  Their constants are made once, out of
-// the compiler's sight: it would otherwise move them into registers again
-// before every use (about seven of 42 instructions per element).
-struct Constants {
-  float2 log2e, one, two, k0, k1, k2, k3, k4;
-};
-__device__ __forceinline__ float2 hidden(float x) {
-  uint64_t r;
-  asm volatile("mov.b64 %0, {%1, %1};\n" : "=l"(r) : "f"(x));
-  return float2_of(r);
-}
-__device__ __forceinline__ Constants constants() {
-  return Constants{hidden(kLog2e), hidden(1.f),   hidden(2.f),   hidden(kLog0),
-                   hidden(kLog1),  hidden(kLog2), hidden(kLog3), hidden(kLog4)};
-}
-
-// What the exponent of alpha is made of, for two channels: x = (za + bias)
-// log2(e), e = 2^-|x| and softplus = max(x, 0) + log2(1 + e), as log2p1_unit.
-// (The sum first: a bias times log2(e) would be rounded at its own size, which
-// tells where za nearly cancels it.)
-__device__ __forceinline__ void softplus_pair(const Constants& K, float2 za, float2 bias, float2& x,
-                                              float2& e, float2& sp) {
-  x = mul2(add2(za, bias), K.log2e);
-  e = make_float2(ex2(-fabsf(x.x)), ex2(-fabsf(x.y)));
-  const float2 d = add2(e, K.two);
-  const float2 t = mul2(e, make_float2(rcp(d.x), rcp(d.y))), z = mul2(t, t);
-  float2 p = fma2(K.k4, z, K.k3);
-  p = fma2(p, z, K.k2);
-  p = fma2(p, z, K.k1);
-  p = fma2(p, z, K.k0);
-  sp = fma2(p, t, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
 
 // beta = sigmoid(zb) = 1 / (1 + 2^-z) with z = zb log2(e) (2^-z may be infinite:
@@ -130,34 +87,8 @@ __device__ __forceinline__ void gate_pair(const Constants& K, float2 za, float2 
 }
 
 // ------------------------------------------------------------------ packing
-// A tile is L rows of one sequence by 64 channels.  Chunk c (of L rows) of
-// sequence s whose first row is o has number o / L + s + c: distinct for all
-// chunks of all sequences, below rows / L + n_seq, and growing with s and c.
+// A tile is L rows of one sequence by 64 channels.
 constexpr int kCols = 64;
-
-__host__ __device__ inline long long chunk_numbers(int rows, int n_seq, int L) {
-  return (long long)rows / L + n_seq;
-}
-
-struct Packed {
-  const int32_t* offsets;
-  int n_seq, rows;
-  __device__ int begin(int s) const {
-    return offsets ? __ldg(offsets + s) : (int)((long long)rows / n_seq * s);
-  }
-};
-
-// Whether the offsets stay within [0, rows] and never decrease (all threads
-// of the block call it).
-__device__ bool offsets_ok(const Packed& P) {
-  if (!P.offsets) return true;
-  bool bad = false;
-  for (int s = threadIdx.x; s <= P.n_seq; s += blockDim.x) {
-    const int o = P.begin(s);
-    bad |= o < 0 || o > P.rows || (s > 0 && o < P.begin(s - 1));
-  }
-  return !__syncthreads_or(bad);
-}
 
 // Rows between saved states = rows of a backward tile.
 template <typename T>
@@ -293,43 +224,6 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
       : "memory");
 }
 
-// The sequence a chunk number belongs to (a whole warp calls it): the last s
-// with base(s) = begin(s) / L + s <= number, or -1.
-template <int L>
-__device__ int sequence_of(const Packed& P, int number) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = P.n_seq;
-  if (P.begin(0) / L > number) return -1;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, s = lo + lane * step;
-    const bool below = s < hi && P.begin(s) / L + s <= number;
-    const int n = __popc(__ballot_sync(0xffffffffu, below));
-    const int next = lo + n * step;
-    lo += (n - 1) * step;
-    hi = next < hi ? next : hi;
-  }
-  return lo;
-}
-
-// Four channels of a row in shared memory or registers.
-__device__ __forceinline__ void load_row(const float* p, float2& lo, float2& hi) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  lo = make_float2(v.x, v.y);
-  hi = make_float2(v.z, v.w);
-}
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float2& lo, float2& hi) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  lo = make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
-  hi = make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-}
-__device__ __forceinline__ void store_row(float* p, float2 lo, float2 hi) {
-  *reinterpret_cast<float4*>(p) = make_float4(lo.x, lo.y, hi.x, hi.y);
-}
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, float2 lo, float2 hi) {
-  const __nv_bfloat162 a = __float22bfloat162_rn(lo), b = __float22bfloat162_rn(hi);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                            *reinterpret_cast<const uint32_t*>(&b));
-}
 // The same to global memory where `p` holds, without a branch.
 __device__ __forceinline__ void store_row_if(bool p, float* at, float2 lo, float2 hi) {
   asm volatile(
@@ -396,7 +290,7 @@ __device__ Order order_of(const Packed& P, int numbers, bool many) {
   }
 #pragma unroll
   for (int j = 1; j < kParts; ++j) {
-    const int aim = (int)((long long)numbers * j / kParts), s = sequence_of<L>(P, aim);
+    const int aim = (int)((long long)numbers * j / kParts), s = sequence_of(P, L, aim);
     const int lo = s < 0 ? 0 : P.begin(s) / L + s, hi = s < 0 ? P.begin(0) / L : P.begin(s + 1) / L + s + 1;
     at[j] = aim - lo < hi - aim ? lo : min(hi, numbers);
   }
@@ -465,7 +359,7 @@ __device__ __forceinline__ bool fetch(const Packed& packed, const Order& order, 
     t.chunk = 0;
     if (packed.offsets) {
       t.number = number_at<kReverse>(order, q);
-      t.seq = sequence_of<L>(packed, t.number);
+      t.seq = sequence_of(packed, L, t.number);
       if (t.seq >= 0) {
         o = packed.begin(t.seq);
         len = packed.begin(t.seq + 1) - o;
@@ -576,47 +470,6 @@ __device__ __forceinline__ bool fold_before(const Chain& ch, const Tile& t, int 
   }
   h = fma2(P, make_float2(__uint_as_float(from.y), __uint_as_float(from.w)), S);
   return true;
-}
-
-// Registers parked in tensor memory: the calling warp's 32 lanes of it, one
-// 32-bit column per register, read back by the same threads.
-__device__ __forceinline__ void park16(uint32_t taddr, const float2 (&v)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
-      "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x),
-      "f"(v[3].y), "f"(v[4].x), "f"(v[4].y), "f"(v[5].x), "f"(v[5].y), "f"(v[6].x), "f"(v[6].y),
-      "f"(v[7].x), "f"(v[7].y)
-      : "memory");
-}
-__device__ __forceinline__ void parked() {
-  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-}
-// Asked for; there after the wait, which the registers pass through so that no
-// use of them precedes it.
-__device__ __forceinline__ void ask16(uint32_t taddr, float2 (&v)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y), "=f"(v[2].x), "=f"(v[2].y),
-        "=f"(v[3].x), "=f"(v[3].y), "=f"(v[4].x), "=f"(v[4].y), "=f"(v[5].x), "=f"(v[5].y),
-        "=f"(v[6].x), "=f"(v[6].y), "=f"(v[7].x), "=f"(v[7].y)
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void ask4(uint32_t taddr, float2& lo, float2& hi) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n"
-               : "=f"(lo.x), "=f"(lo.y), "=f"(hi.x), "=f"(hi.y)
-               : "r"(taddr)
-               : "memory");
-}
-__device__ __forceinline__ void asked() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void here(float2 (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i].x), "+f"(v[i].y) : : "memory");
 }
 
 // A block is eight warps for the arithmetic (a half-warp takes R rows by 64

@@ -1,17 +1,22 @@
-// residual_norm.cu -- residual addition and RMS-Norm, forward (16-, 32- or
-// 8-bit output with scales) and backward.
+// residual_norm.cu -- residual addition and norm, forward (16-, 32- or 8-bit
+// output with scales) and backward: the RMS-Norm and, with kCentred, the layer norm.
 //
-//   s = round(x + residual),  inv = 1 / sqrt(mean s^2 + eps),  n = s inv gamma;
+//   s = round(x + residual);
+//   RMS-Norm:   inv = 1 / sqrt(mean s^2 + eps),  n = s inv gamma;
+//   layer norm: c = s - mean s,  inv = 1 / sqrt(mean c^2 + eps),  n = c inv gamma + beta;
 //   8 bits: scale = max(max|n| / 448, 2^-126) of a row or a group of channels,
 //   out = n / scale rounded to e4m3.
-//   backward: w = dout gamma,  dx = ds + inv (w - s inv mean(w s inv)),
-//   dgamma = sum over rows of dout s inv.
+//   backward: w = dout gamma,  RMS-Norm dx = ds + inv (w - s inv mean(w s inv)),
+//   layer norm dx = ds + inv (w - mean w - c inv mean(w c inv));
+//   dgamma = sum over rows of dout s inv (dout c inv),  dbeta = sum of dout.
 //
-// Measured at 32768 x 1024 bf16: forward 39.9 us (the copy rate), backward 46.7 us
-// (0.86); 8-bit output at 16384 x 3840, groups of 128, 75.1 us (0.88).
+// Measured at 32768 x 1024 bf16, RMS-Norm: forward 39.9 us (the copy rate), backward
+// 46.7 us (0.86); 8-bit output at 16384 x 3840, groups of 128, 75.1 us (0.88).
 // All of it is bound by the bytes of the rows, each read and written once: a
 // row is held in the registers of a team of warps (eight channels a thread and
-// step, 16 bytes of a bf16 tensor) between the reduction and the output.
+// step, 16 bytes of a bf16 tensor) between the reduction and the output.  The
+// layer norm reduces twice, the mean before the squares of what differs from it:
+// sums of s and s^2 in one go would cancel where the mean is large.
 #include <atomic>
 #include <type_traits>
 
@@ -156,6 +161,7 @@ struct ForwardArgs {
   const void* x;
   const void* residual;
   const float* gamma;
+  const float* beta;   // layer norm only
   float eps;
   void* s;
   void* out;
@@ -165,7 +171,7 @@ struct ForwardArgs {
   float one_over_D;
 };
 
-template <typename T, int TW, int NV, int kOut>
+template <typename T, int TW, int NV, int kOut, bool kCentred>
 __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P) {
   wait_for_stream();
   __shared__ float red[2][kTeams<TW>][TW][1];
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
         if (P.residual) res[j].load(static_cast<const T*>(P.residual) + base + c);
       }
     }
-    float2 ss2 = both(0.f);
+    float2 ss2 = both(0.f), sum2 = both(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
@@ -202,11 +208,32 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
         }
         if (P.s) s[j].store(static_cast<T*>(P.s) + base + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ss2 = fma2(f[i], f[i], ss2);
+        for (int i = 0; i < 4; ++i) {
+          if (kCentred) sum2 = add2(sum2, f[i]);
+          else ss2 = fma2(f[i], f[i], ss2);
+        }
+      }
+    }
+    float2 mean = both(0.f);
+    if (kCentred) {
+      float sum[1] = {sum2.x + sum2.y};
+      team_sum<TW, 1>(sum, red[0][team], team);
+      mean = both(sum[0] * P.one_over_D);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if ((j * TW * 32 + lane) * kVec < D) {
+          float2 f[4];
+          s[j].get(f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[i] = sub2(f[i], mean);
+            ss2 = fma2(f[i], f[i], ss2);
+          }
+        }
       }
     }
     float ss[1] = {ss2.x + ss2.y};
-    team_sum<TW, 1>(ss, red[flip][team], team);
+    team_sum<TW, 1>(ss, red[kCentred ? 1 : flip][team], team);
     const float2 inv = both(rsqrtf(fmaf(ss[0], P.one_over_D, P.eps)));
     // n, kept where the scale of the 8-bit output has yet to be found.
     float2 n[NV][4];
@@ -217,7 +244,7 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
       if (c < D) {
         s[j].get(n[j]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) n[j][i] = mul2(n[j][i], inv);
+        for (int i = 0; i < 4; ++i) n[j][i] = mul2(kCentred ? sub2(n[j][i], mean) : n[j][i], inv);
         if (P.gamma) {
           Eight<float> g;
           float2 gm[4];
@@ -225,6 +252,14 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
           g.get(gm);
 #pragma unroll
           for (int i = 0; i < 4; ++i) n[j][i] = mul2(n[j][i], gm[i]);
+        }
+        if (kCentred && P.beta) {
+          Eight<float> b;
+          float2 bt[4];
+          b.load(P.beta + c);
+          b.get(bt);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) n[j][i] = add2(n[j][i], bt[i]);
         }
         if (kOut == SDM_BF16) {
           Eight<__nv_bfloat16> o;
@@ -277,7 +312,7 @@ struct BackwardArgs {
   const void* ds;
   float eps;
   void* dx;
-  float* partial;      // [blocks][D], or null
+  float* partial;      // [blocks][D] of dgamma (layer norm: [2][D], and dbeta), or null
   int rows, D;
   float one_over_D;
 };
@@ -285,17 +320,23 @@ struct BackwardArgs {
 // Threads keep their channels from row to row, so that the gradient of gamma
 // is summed in registers; the teams of a block are added in shared memory at
 // the end, the blocks by column_sums_kernel.
-template <typename T, int TW, int NV>
+template <typename T, int TW, int NV, bool kCentred>
 __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs P) {
   wait_for_stream();
-  __shared__ float red[2][kTeams<TW>][TW][2];
-  extern __shared__ __align__(16) float teams[];   // [kTeams - 1][TW * NV * 256]
+  // (A row's two sums of the layer norm each have their own slots: between two
+  // writes to one there is the other's barrier.)
+  __shared__ float red[2][kTeams<TW>][TW][kCentred ? 3 : 2];
+  __shared__ float red_mean[kTeams<TW>][TW][1];
+  extern __shared__ __align__(16) float teams[];   // [sums][kTeams - 1][TW * NV * 256]
+  constexpr int kSums = kCentred ? 2 : 1;          // gamma's, and beta's
   const int team = threadIdx.x / (TW * 32), lane = threadIdx.x % (TW * 32), D = P.D;
-  float2 acc[NV][4];
+  float2 acc[kSums][NV][4];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int k = 0; k < kSums; ++k)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = both(0.f);
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[k][j][i] = both(0.f);
   int flip = 0;
   const long long step = (long long)gridDim.x * kTeams<TW>;
   // The next row's loads are under way while a row is worked on (not with 64
@@ -327,7 +368,23 @@ __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs
       more[j] = ahead_more[j];
     }
     if (kAhead) ask(row + step);
-    float2 ss = both(0.f), ws = both(0.f);
+    float2 centre = both(0.f);
+    if (kCentred) {
+      float2 sum2 = both(0.f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if ((j * TW * 32 + lane) * kVec < D) {
+          float2 fs[4];
+          s[j].get(fs);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum2 = add2(sum2, fs[i]);
+        }
+      }
+      float sum[1] = {sum2.x + sum2.y};
+      team_sum<TW, 1>(sum, red_mean[team], team);
+      centre = both(sum[0] * P.one_over_D);
+    }
+    float2 ss = both(0.f), ws = both(0.f), w_sum = both(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
@@ -345,15 +402,21 @@ __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          if (kCentred) {
+            fs[i] = sub2(fs[i], centre);
+            w_sum = add2(w_sum, w[i]);
+          }
           ss = fma2(fs[i], fs[i], ss);
           ws = fma2(w[i], fs[i], ws);
         }
       }
     }
-    float v[2] = {ss.x + ss.y, ws.x + ws.y};
-    team_sum<TW, 2>(v, red[flip][team], team);
+    float v[kCentred ? 3 : 2] = {ss.x + ss.y, ws.x + ws.y};
+    if (kCentred) v[kCentred ? 2 : 0] = w_sum.x + w_sum.y;
+    team_sum<TW, kCentred ? 3 : 2>(v, red[kCentred ? 0 : flip][team], team);
     const float inv1 = rsqrtf(fmaf(v[0], P.one_over_D, P.eps));
     const float2 inv = both(inv1), mean = both(-v[1] * inv1 * P.one_over_D);
+    const float2 w_mean = both(kCentred ? v[kCentred ? 2 : 0] * P.one_over_D : 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
@@ -380,8 +443,12 @@ __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 hat = mul2(fs[i], inv);
-          acc[j][i] = fma2(fd[i], hat, acc[j][i]);
+          const float2 hat = mul2(kCentred ? sub2(fs[i], centre) : fs[i], inv);
+          acc[0][j][i] = fma2(fd[i], hat, acc[0][j][i]);
+          if (kCentred) {
+            acc[kSums - 1][j][i] = add2(acc[kSums - 1][j][i], fd[i]);
+            w[i] = sub2(w[i], w_mean);
+          }
           dx[i] = fma2(inv, fma2(hat, mean, w[i]), dx[i]);
         }
         Eight<T> o;
@@ -396,48 +463,58 @@ __global__ void __launch_bounds__(kBlock<TW>) backward_kernel(const BackwardArgs
     float2* const mine = reinterpret_cast<float2*>(teams) + lane * 4;
     if (team > 0) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int k = 0; k < kSums; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mine[((team - 1) * kRow + j * TW * 256) / 2 + i] = acc[j][i];
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mine[((k * (kTeams<TW> - 1) + team - 1) * kRow + j * TW * 256) / 2 + i] = acc[k][j][i];
     }
     __syncthreads();
     if (team > 0) return;
-    for (int k = 0; k < kTeams<TW> - 1; ++k)
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+    for (int k = 0; k < kSums; ++k)
+      for (int n = 0; n < kTeams<TW> - 1; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[j][i] = add2(acc[j][i], mine[(k * kRow + j * TW * 256) / 2 + i]);
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[k][j][i] = add2(acc[k][j][i],
+                                mine[((k * (kTeams<TW> - 1) + n) * kRow + j * TW * 256) / 2 + i]);
   }
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * TW * 32 + lane) * kVec;
-    if (c < D) {
-      Eight<float> o;
-      o.set(acc[j]);
-      o.store(P.partial + (size_t)blockIdx.x * D + c);
+  for (int k = 0; k < kSums; ++k)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TW * 32 + lane) * kVec;
+      if (c < D) {
+        Eight<float> o;
+        o.set(acc[k][j]);
+        o.store(P.partial + ((size_t)blockIdx.x * kSums + k) * D + c);
+      }
     }
-  }
 }
 
-// Sums of [parts][D] over the parts, always in the same order: 32 channels a
-// block, each of 32 warps every 32nd part, then the warps.
+// Sums of [parts][width] over the parts, always in the same order: 32 columns a
+// block, each of 32 warps every 32nd part, then the warps.  The first D columns
+// go to `out`, those behind them to `more`; either may be null.
 __global__ void __launch_bounds__(1024)
-    column_sums_kernel(const float* partial, int parts, int D, float* out) {
+    column_sums_kernel(const float* partial, int parts, int width, int D, float* out, float* more) {
   wait_for_stream();
   __shared__ float warps[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float a = 0.f;
-  if (c < D) {
+  if (c < width) {
 #pragma unroll 4
-    for (int n = warp; n < parts; n += 32) a += __ldg(partial + (size_t)n * D + c);
+    for (int n = warp; n < parts; n += 32) a += __ldg(partial + (size_t)n * width + c);
   }
   warps[warp][lane] = a;
   __syncthreads();
-  if (warp == 0 && c < D) {
+  float* const to = c < D ? out : more;
+  if (warp == 0 && c < width && to) {
     float sum = 0.f;
     for (int w = 0; w < 32; ++w) sum += warps[w][lane];
-    out[c] = sum;
+    to[c < D ? c : c - D] = sum;
   }
 }
 
@@ -460,29 +537,30 @@ int blocks_per_sm(K kernel, int threads, int smem, std::atomic<int>* cache) {
   return n;
 }
 
-template <typename T, int TW, int NV>
+template <typename T, int TW, int NV, bool kCentred>
 cudaError_t forward_as(const ForwardArgs& P, int out_dtype, cudaStream_t stream) {
   const long long want = ((long long)P.rows + kTeams<TW> - 1) / kTeams<TW>;
   const long long most = 1 << 20;
   const unsigned blocks = (unsigned)(want < most ? want : most);
-  const auto kernel = out_dtype == SDM_E4M3   ? forward_kernel<T, TW, NV, SDM_E4M3>
-                      : out_dtype == SDM_BF16 ? forward_kernel<T, TW, NV, SDM_BF16>
-                                              : forward_kernel<T, TW, NV, SDM_F32>;
+  const auto kernel = out_dtype == SDM_E4M3   ? forward_kernel<T, TW, NV, SDM_E4M3, kCentred>
+                      : out_dtype == SDM_BF16 ? forward_kernel<T, TW, NV, SDM_BF16, kCentred>
+                                              : forward_kernel<T, TW, NV, SDM_F32, kCentred>;
   return launch_behind(kernel, blocks, kBlock<TW>, 0, stream, P);
 }
 
-template <typename T, int TW, int NV>
-cudaError_t backward_as(const BackwardArgs& P, float* dgamma, cudaStream_t stream) {
+template <typename T, int TW, int NV, bool kCentred>
+cudaError_t backward_as(const BackwardArgs& P, float* dgamma, float* dbeta, cudaStream_t stream) {
   static std::atomic<int> cache[64];       // zeros
-  const auto kernel = backward_kernel<T, TW, NV>;
-  const int smem = (kTeams<TW> - 1) * TW * NV * 256 * (int)sizeof(float);
+  const auto kernel = backward_kernel<T, TW, NV, kCentred>;
+  constexpr int kSums = kCentred ? 2 : 1;
+  const int smem = kSums * (kTeams<TW> - 1) * TW * NV * 256 * (int)sizeof(float);
   const long long want = ((long long)P.rows + kTeams<TW> - 1) / kTeams<TW>;
   const int most = blocks_per_sm(kernel, kBlock<TW>, smem, cache) * device_limits().sms;
   const int blocks = (int)(want < most ? want : most);
   const cudaError_t e = launch_behind(kernel, blocks, kBlock<TW>, smem, stream, P);
-  if (e != cudaSuccess || !dgamma) return e;
-  return launch_behind(column_sums_kernel, (P.D + 31) / 32, 1024, 0, stream, P.partial, blocks, P.D,
-                       dgamma);
+  if (e != cudaSuccess || !P.partial) return e;
+  return launch_behind(column_sums_kernel, (kSums * P.D + 31) / 32, 1024, 0, stream,
+                       (const float*)P.partial, blocks, kSums * P.D, P.D, dgamma, dbeta);
 }
 
 // Calls f with the team for rows of D channels: a thread takes 32 bytes of a
@@ -514,6 +592,31 @@ cudaError_t with_team(int D, bool few, F f) {
 
 bool few_rows(int rows) { return rows < 8 * device_limits().sms; }
 
+// Either norm of a call.
+template <bool kCentred>
+cudaError_t forward_of(const ForwardArgs& P, int dtype, int out_dtype, cudaStream_t stream) {
+  const bool few = few_rows(P.rows);
+  if (dtype == SDM_BF16)
+    return with_team<__nv_bfloat16>(P.D, few, [&](auto tw, auto nv) {
+      return forward_as<__nv_bfloat16, decltype(tw)::value, decltype(nv)::value, kCentred>(P, out_dtype, stream);
+    });
+  return with_team<float>(P.D, few, [&](auto tw, auto nv) {
+    return forward_as<float, decltype(tw)::value, decltype(nv)::value, kCentred>(P, out_dtype, stream);
+  });
+}
+template <bool kCentred>
+cudaError_t backward_of(const BackwardArgs& P, int dtype, float* dgamma, float* dbeta,
+                        cudaStream_t stream) {
+  const bool few = few_rows(P.rows);
+  if (dtype == SDM_BF16)
+    return with_team<__nv_bfloat16>(P.D, few, [&](auto tw, auto nv) {
+      return backward_as<__nv_bfloat16, decltype(tw)::value, decltype(nv)::value, kCentred>(P, dgamma, dbeta, stream);
+    });
+  return with_team<float>(P.D, few, [&](auto tw, auto nv) {
+    return backward_as<float, decltype(tw)::value, decltype(nv)::value, kCentred>(P, dgamma, dbeta, stream);
+  });
+}
+
 }  // namespace
 
 size_t add_rmsnorm_workspace_bytes(const NormDims& d) {
@@ -523,15 +626,8 @@ size_t add_rmsnorm_workspace_bytes(const NormDims& d) {
 cudaError_t launch_add_rmsnorm(const NormDims& d, const void* x, const void* residual,
                                const float* gamma, float eps, void* s, void* out, int out_dtype,
                                int group, float* scale, cudaStream_t stream) {
-  const ForwardArgs P{x, residual, gamma, eps, s, out, group, scale, d.rows, d.D, 1.f / (float)d.D};
-  const bool few = few_rows(d.rows);
-  if (d.dtype == SDM_BF16)
-    return with_team<__nv_bfloat16>(d.D, few, [&](auto tw, auto nv) {
-      return forward_as<__nv_bfloat16, decltype(tw)::value, decltype(nv)::value>(P, out_dtype, stream);
-    });
-  return with_team<float>(d.D, few, [&](auto tw, auto nv) {
-    return forward_as<float, decltype(tw)::value, decltype(nv)::value>(P, out_dtype, stream);
-  });
+  const ForwardArgs P{x, residual, gamma, nullptr, eps, s, out, group, scale, d.rows, d.D, 1.f / (float)d.D};
+  return forward_of<false>(P, d.dtype, out_dtype, stream);
 }
 
 cudaError_t launch_add_rmsnorm_backward(const NormDims& d, const void* s, const void* dout,
@@ -540,14 +636,34 @@ cudaError_t launch_add_rmsnorm_backward(const NormDims& d, const void* s, const 
   if (d.rows == 0) return cudaMemsetAsync(dgamma, 0, (size_t)d.D * sizeof(float), stream);
   const BackwardArgs P{s,  dout,   gamma, ds, eps, dx, dgamma ? static_cast<float*>(workspace) : nullptr,
                        d.rows, d.D, 1.f / (float)d.D};
-  const bool few = few_rows(d.rows);
-  if (d.dtype == SDM_BF16)
-    return with_team<__nv_bfloat16>(d.D, few, [&](auto tw, auto nv) {
-      return backward_as<__nv_bfloat16, decltype(tw)::value, decltype(nv)::value>(P, dgamma, stream);
-    });
-  return with_team<float>(d.D, few, [&](auto tw, auto nv) {
-    return backward_as<float, decltype(tw)::value, decltype(nv)::value>(P, dgamma, stream);
-  });
+  return backward_of<false>(P, d.dtype, dgamma, nullptr, stream);
+}
+
+size_t add_layernorm_workspace_bytes(const NormDims& d) {
+  return (size_t)most_parts() * 2 * d.D * sizeof(float);
+}
+
+cudaError_t launch_add_layernorm(const NormDims& d, const void* x, const void* residual,
+                                 const float* gamma, const float* beta, float eps, void* s,
+                                 void* out, int out_dtype, int group, float* scale,
+                                 cudaStream_t stream) {
+  const ForwardArgs P{x, residual, gamma, beta, eps, s, out, group, scale, d.rows, d.D, 1.f / (float)d.D};
+  return forward_of<true>(P, d.dtype, out_dtype, stream);
+}
+
+cudaError_t launch_add_layernorm_backward(const NormDims& d, const void* s, const void* dout,
+                                          const float* gamma, const void* ds, float eps, void* dx,
+                                          float* dgamma, float* dbeta, void* workspace,
+                                          cudaStream_t stream) {
+  if (d.rows == 0) {                       // sums over nothing
+    cudaError_t e = cudaSuccess;
+    if (dgamma) e = cudaMemsetAsync(dgamma, 0, (size_t)d.D * sizeof(float), stream);
+    if (e == cudaSuccess && dbeta) e = cudaMemsetAsync(dbeta, 0, (size_t)d.D * sizeof(float), stream);
+    return e;
+  }
+  const BackwardArgs P{s,  dout,   gamma, ds, eps, dx, dgamma || dbeta ? static_cast<float*>(workspace) : nullptr,
+                       d.rows, d.D, 1.f / (float)d.D};
+  return backward_of<true>(P, d.dtype, dgamma, dbeta, stream);
 }
 
 }  // namespace sdm

@@ -110,6 +110,56 @@ sdm_status check_norm(const sdm_norm* sh, NormDims* d) {
   return SDM_OK;
 }
 
+sdm_status check_conv(const sdm_conv* sh, bool equal_parts, ConvDims* d) {
+  if (!sh) return SDM_ERR_INVALID_ARG;
+  if (sh->n_seq < 0 || sh->rows < 0 || sh->D < 1 || sh->taps < 1 || sh->ld < 0 || sh->ld_grad < 0)
+    return SDM_ERR_INVALID_ARG;
+  if (sh->act != SDM_ACT_NONE && sh->act != SDM_ACT_SILU) return SDM_ERR_INVALID_ARG;
+  if (sh->dtype != SDM_F32 && sh->dtype != SDM_BF16) return SDM_ERR_INVALID_ARG;
+  if ((sh->ld && sh->ld < sh->D) || (sh->ld_grad && sh->ld_grad < sh->D))
+    return SDM_ERR_INVALID_ARG;
+  if (equal_parts && sh->n_seq > 0 && sh->rows % sh->n_seq != 0) return SDM_ERR_INVALID_ARG;
+  if (sh->n_seq > 65535 || sh->D > 65536 || sh->taps < 2 || sh->taps > 4)
+    return SDM_ERR_UNSUPPORTED;
+  if (sh->D % 8 != 0 || sh->ld % 8 != 0 || sh->ld_grad % 8 != 0) return SDM_ERR_UNSUPPORTED;
+  if (sh->rows > (1 << 30) || ((long long)sh->rows / 32 + 1) * ((sh->D + 127) / 128) >= (1ll << 31))
+    return SDM_ERR_UNSUPPORTED;            // blocks of 32 rows or more by 128 channels
+  *d = ConvDims{sh->n_seq, sh->rows, sh->D, sh->taps, (int)sh->act, sh->ld ? sh->ld : sh->D,
+                sh->ld_grad ? sh->ld_grad : sh->D, (int)sh->dtype};
+  return SDM_OK;
+}
+
+sdm_status check_selective(const sdm_selective* sh, bool equal_parts, SelectiveDims* d) {
+  if (!sh) return SDM_ERR_INVALID_ARG;
+  if (sh->n_seq < 0 || sh->rows < 0 || sh->D < 1 || sh->N < 1 || sh->groups < 1)
+    return SDM_ERR_INVALID_ARG;
+  if (sh->dtype != SDM_F32 && sh->dtype != SDM_BF16) return SDM_ERR_INVALID_ARG;
+  if (sh->D % sh->groups != 0) return SDM_ERR_INVALID_ARG;
+  if (equal_parts && sh->n_seq > 0 && sh->rows % sh->n_seq != 0) return SDM_ERR_INVALID_ARG;
+  // Row strides: 0 is dense; each is checked against the row's own width.
+  const long long bc = (long long)sh->groups * sh->N;
+  const int given[6] = {sh->ld, sh->ld_z, sh->ld_bc, sh->ld_grad, sh->ld_z_grad, sh->ld_bc_grad};
+  long long ld[6];
+  bool uneven = false;
+  for (int i = 0; i < 6; ++i) {
+    const long long width = i % 3 == 2 ? bc : sh->D;
+    if (given[i] < 0 || (given[i] && given[i] < width)) return SDM_ERR_INVALID_ARG;
+    ld[i] = given[i] ? given[i] : width;
+    uneven |= ld[i] % 8 != 0;
+  }
+  if (sh->n_seq > 65535 || sh->D > 65536) return SDM_ERR_UNSUPPORTED;
+  if (sh->N != 8 && sh->N != 16 && sh->N != 32 && sh->N != 64) return SDM_ERR_UNSUPPORTED;
+  if (uneven || sh->D / sh->groups % 8 != 0) return SDM_ERR_UNSUPPORTED;
+  const SelectiveDims r{sh->n_seq, sh->rows, sh->D, sh->N, sh->groups, ld[0], ld[1], ld[2],
+                        ld[3], ld[4], ld[5], (int)sh->dtype};
+  // Blocks of a chunk's 16 rows or more by a tile of channels, counted in 32 bits.
+  if (sh->rows > (1 << 30) ||
+      ((long long)sh->rows / 16 + sh->n_seq) * selective_scan_tiles(r) >= (1ll << 31))
+    return SDM_ERR_UNSUPPORTED;
+  *d = r;
+  return SDM_OK;
+}
+
 bool empty_work(const Dims& d) { return (long long)d.B * d.H * d.T == 0; }
 
 sdm_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA; }
@@ -687,6 +737,276 @@ sdm_status sdm_add_rmsnorm_backward(const sdm_norm* shape, const void* s, const 
   SDM_CHECK_OPTIONAL(dgamma);
   return from_cuda(launch_add_rmsnorm_backward(d, s, dout, gamma, ds, eps, dx, dgamma, workspace,
                                                static_cast<cudaStream_t>(stream)));
+}
+
+sdm_status sdm_add_layernorm(const sdm_norm* shape, const void* x, const void* residual,
+                             const float* gamma, const float* beta, float eps, void* s, void* out,
+                             sdm_dtype out_dtype, int group, float* scale, void* stream) {
+  NormDims d;
+  sdm_status st = check_norm(shape, &d);
+  if (st != SDM_OK) return st;
+  if (!(eps > 0.f) || !(eps < INFINITY)) return SDM_ERR_INVALID_ARG;
+  if (out_dtype != SDM_F32 && out_dtype != SDM_BF16 && out_dtype != SDM_E4M3)
+    return SDM_ERR_INVALID_ARG;
+  if (group != 0) {
+    if (out_dtype != SDM_E4M3 || group < 0 || d.D % group != 0) return SDM_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return SDM_ERR_UNSUPPORTED;
+  }
+  if (d.rows == 0) return SDM_OK;   // no work: pointers are not looked at
+  SDM_CHECK_PTR(x);
+  SDM_CHECK_PTR(out);
+  SDM_CHECK_OPTIONAL(residual);
+  SDM_CHECK_OPTIONAL(gamma);
+  SDM_CHECK_OPTIONAL(beta);
+  SDM_CHECK_OPTIONAL(s);
+  if (out_dtype == SDM_E4M3) SDM_CHECK_PTR(scale);
+  return from_cuda(launch_add_layernorm(d, x, residual, gamma, beta, eps, s, out, out_dtype, group,
+                                        scale, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sdm_add_layernorm_workspace_size(const sdm_norm* shape) {
+  NormDims d;
+  if (check_norm(shape, &d) != SDM_OK) return 0;
+  return add_layernorm_workspace_bytes(d);
+}
+
+sdm_status sdm_add_layernorm_backward(const sdm_norm* shape, const void* s, const void* dout,
+                                      const float* gamma, const void* ds, float eps, void* dx,
+                                      float* dgamma, float* dbeta, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  NormDims d;
+  sdm_status st = check_norm(shape, &d);
+  if (st != SDM_OK) return st;
+  if (!(eps > 0.f) || !(eps < INFINITY)) return SDM_ERR_INVALID_ARG;
+  if (d.rows == 0 && !dgamma && !dbeta) return SDM_OK;
+  if (d.rows > 0) {
+    SDM_CHECK_PTR(s);
+    SDM_CHECK_PTR(dout);
+    SDM_CHECK_PTR(dx);
+    SDM_CHECK_OPTIONAL(gamma);
+    SDM_CHECK_OPTIONAL(ds);
+    if (dgamma || dbeta) {
+      SDM_CHECK_PTR(workspace);
+      if (ws_bytes < add_layernorm_workspace_bytes(d)) return SDM_ERR_INVALID_ARG;
+    }
+  }
+  SDM_CHECK_OPTIONAL(dgamma);
+  SDM_CHECK_OPTIONAL(dbeta);
+  return from_cuda(launch_add_layernorm_backward(d, s, dout, gamma, ds, eps, dx, dgamma, dbeta,
+                                                 workspace, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sdm_short_conv_workspace_size(const sdm_conv* shape) {
+  ConvDims d;
+  if (check_conv(shape, false, &d) != SDM_OK) return 0;
+  return short_conv_workspace_bytes(d);
+}
+
+sdm_status sdm_short_conv_forward(const sdm_conv* shape, const void* x, const float* w,
+                                  const float* bias, const int32_t* offsets, const void* x0,
+                                  void* y, void* xT, void* stream) {
+  ConvDims d;
+  sdm_status st = check_conv(shape, !offsets, &d);
+  if (st != SDM_OK) return st;
+  if (d.n_seq == 0) return SDM_OK;   // no work: pointers are not looked at
+  if (d.rows > 0) {
+    SDM_CHECK_PTR(x);
+    SDM_CHECK_PTR(y);
+  }
+  SDM_CHECK_PTR(w);
+  SDM_CHECK_OPTIONAL(bias);
+  SDM_CHECK_OPTIONAL(offsets);
+  SDM_CHECK_OPTIONAL(x0);
+  SDM_CHECK_OPTIONAL(xT);
+  unsigned* sp = nullptr;
+  if ((st = status_ptr(&sp)) != SDM_OK) return st;
+  return from_cuda(launch_short_conv_forward(d, ConvInputs{x, w, bias, offsets, x0}, y, xT, sp,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+sdm_status sdm_short_conv_backward(const sdm_conv* shape, const void* x, const float* w,
+                                   const float* bias, const int32_t* offsets, const void* x0,
+                                   const void* dy, const void* dxT, void* dx, float* dw,
+                                   float* dbias, void* dx0, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  ConvDims d;
+  sdm_status st = check_conv(shape, !offsets, &d);
+  if (st != SDM_OK) return st;
+  if (d.n_seq == 0 && !dw && !dbias) return SDM_OK;
+  if (d.n_seq > 0) {
+    if (d.rows > 0) {
+      SDM_CHECK_PTR(x);
+      SDM_CHECK_PTR(dy);
+      SDM_CHECK_PTR(dx);
+    }
+    SDM_CHECK_PTR(w);
+    SDM_CHECK_OPTIONAL(bias);
+    SDM_CHECK_OPTIONAL(offsets);
+    SDM_CHECK_OPTIONAL(x0);
+    SDM_CHECK_OPTIONAL(dxT);
+    SDM_CHECK_OPTIONAL(dx0);
+    if (dw || dbias) {
+      SDM_CHECK_PTR(workspace);
+      if (ws_bytes < short_conv_workspace_bytes(d)) return SDM_ERR_INVALID_ARG;
+    }
+  }
+  SDM_CHECK_OPTIONAL(dw);
+  SDM_CHECK_OPTIONAL(dbias);
+  unsigned* sp = nullptr;
+  if ((st = status_ptr(&sp)) != SDM_OK) return st;
+  return from_cuda(launch_short_conv_backward(d, ConvInputs{x, w, bias, offsets, x0}, dy, dxT, dx,
+                                              dw, dbias, dx0, workspace, sp,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+sdm_status sdm_short_conv_step(const sdm_conv* shape, const void* x, const float* w,
+                               const float* bias, void* state, int n_slots, const int32_t* slots,
+                               void* y, void* stream) {
+  ConvDims d;
+  sdm_status st = check_conv(shape, false, &d);
+  if (st != SDM_OK) return st;
+  if (n_slots < 0 || (!slots && d.rows > n_slots)) return SDM_ERR_INVALID_ARG;
+  if (slots && d.rows > (1 << 22)) return SDM_ERR_UNSUPPORTED;   // see the header
+  if (d.rows == 0) return SDM_OK;   // no work: pointers are not looked at
+  SDM_CHECK_PTR(x);
+  SDM_CHECK_PTR(w);
+  SDM_CHECK_PTR(y);
+  if (n_slots > 0) SDM_CHECK_PTR(state);
+  SDM_CHECK_OPTIONAL(bias);
+  SDM_CHECK_OPTIONAL(slots);
+  unsigned* sp = nullptr;
+  if ((st = status_ptr(&sp)) != SDM_OK) return st;
+  return from_cuda(launch_short_conv_step(d, ConvInputs{x, w, bias, nullptr, nullptr}, state,
+                                          n_slots, slots, y, sp,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+size_t sdm_selective_scan_workspace_size(const sdm_selective* shape) {
+  SelectiveDims d;
+  if (check_selective(shape, false, &d) != SDM_OK) return 0;
+  return selective_scan_workspace_bytes(d);
+}
+
+size_t sdm_selective_scan_backward_workspace_size(const sdm_selective* shape) {
+  SelectiveDims d;
+  if (check_selective(shape, false, &d) != SDM_OK) return 0;
+  return selective_scan_backward_workspace_bytes(d);
+}
+
+size_t sdm_selective_scan_states_size(const sdm_selective* shape) {
+  SelectiveDims d;
+  if (check_selective(shape, false, &d) != SDM_OK) return 0;
+  return selective_scan_states_bytes(d);
+}
+
+sdm_status sdm_selective_scan_forward(const sdm_selective* shape, const void* x, const void* dt,
+                                      const float* A, const void* B, const void* C,
+                                      const float* skip, const float* bias, const void* z,
+                                      const int32_t* offsets, const float* h0, void* y, float* hT,
+                                      float* states, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+  SelectiveDims d;
+  sdm_status st = check_selective(shape, !offsets, &d);
+  if (st != SDM_OK) return st;
+  if (d.n_seq == 0) return SDM_OK;   // no work: pointers are not looked at
+  if (d.rows > 0) {
+    SDM_CHECK_PTR(x);
+    SDM_CHECK_PTR(dt);
+    SDM_CHECK_PTR(B);
+    SDM_CHECK_PTR(C);
+    SDM_CHECK_PTR(y);
+    SDM_CHECK_OPTIONAL(z);
+  }
+  SDM_CHECK_PTR(A);
+  SDM_CHECK_OPTIONAL(skip);
+  SDM_CHECK_OPTIONAL(bias);
+  SDM_CHECK_OPTIONAL(offsets);
+  SDM_CHECK_OPTIONAL(h0);
+  SDM_CHECK_OPTIONAL(hT);
+  SDM_CHECK_OPTIONAL(states);
+  SDM_CHECK_PTR(workspace);
+  if (ws_bytes < selective_scan_workspace_bytes(d)) return SDM_ERR_INVALID_ARG;
+  unsigned* sp = nullptr;
+  if ((st = status_ptr(&sp)) != SDM_OK) return st;
+  return from_cuda(launch_selective_scan_forward(
+      d, SelectiveInputs{x, dt, A, B, C, skip, bias, z, offsets}, h0, y, hT, states, workspace, sp,
+      static_cast<cudaStream_t>(stream)));
+}
+
+sdm_status sdm_selective_scan_backward(const sdm_selective* shape, const void* x, const void* dt,
+                                       const float* A, const void* B, const void* C,
+                                       const float* skip, const float* bias, const void* z,
+                                       const int32_t* offsets, const float* states,
+                                       const void* dy, const float* dhT, void* dx, void* ddt,
+                                       float* dA, void* dB, void* dC, float* dskip, float* dbias,
+                                       void* dz, float* dh0, void* workspace, size_t ws_bytes,
+                                       void* stream) {
+  SelectiveDims d;
+  sdm_status st = check_selective(shape, !offsets, &d);
+  if (st != SDM_OK) return st;
+  if (d.n_seq == 0 && !dA && !dskip && !dbias) return SDM_OK;
+  if (d.n_seq > 0) {
+    if (d.rows > 0) {
+      SDM_CHECK_PTR(x);
+      SDM_CHECK_PTR(dt);
+      SDM_CHECK_PTR(B);
+      SDM_CHECK_PTR(C);
+      SDM_CHECK_PTR(dy);
+      SDM_CHECK_PTR(dx);
+      SDM_CHECK_PTR(ddt);
+      SDM_CHECK_PTR(dB);
+      SDM_CHECK_PTR(dC);
+      SDM_CHECK_OPTIONAL(z);
+      if (z) SDM_CHECK_PTR(dz);
+    }
+    SDM_CHECK_PTR(A);
+    SDM_CHECK_PTR(states);
+    SDM_CHECK_OPTIONAL(skip);
+    SDM_CHECK_OPTIONAL(bias);
+    SDM_CHECK_OPTIONAL(offsets);
+    SDM_CHECK_OPTIONAL(dhT);
+    SDM_CHECK_OPTIONAL(dh0);
+    SDM_CHECK_PTR(workspace);
+    if (ws_bytes < selective_scan_backward_workspace_bytes(d)) return SDM_ERR_INVALID_ARG;
+  }
+  SDM_CHECK_OPTIONAL(dA);
+  SDM_CHECK_OPTIONAL(dskip);
+  SDM_CHECK_OPTIONAL(dbias);
+  unsigned* sp = nullptr;
+  if ((st = status_ptr(&sp)) != SDM_OK) return st;
+  return from_cuda(launch_selective_scan_backward(
+      d, SelectiveInputs{x, dt, A, B, C, skip, bias, z, offsets}, states, dy, dhT,
+      SelectiveGrads{dx, ddt, dA, dB, dC, dskip, dbias, dz, dh0}, workspace, sp,
+      static_cast<cudaStream_t>(stream)));
+}
+
+sdm_status sdm_selective_scan_step(const sdm_selective* shape, const void* x, const void* dt,
+                                   const float* A, const void* B, const void* C,
+                                   const float* skip, const float* bias, const void* z,
+                                   float* state, int n_slots, const int32_t* slots, void* y,
+                                   void* stream) {
+  SelectiveDims d;
+  sdm_status st = check_selective(shape, false, &d);
+  if (st != SDM_OK) return st;
+  if (n_slots < 0 || (!slots && d.rows > n_slots)) return SDM_ERR_INVALID_ARG;
+  if (slots && d.rows > (1 << 22)) return SDM_ERR_UNSUPPORTED;   // see the header
+  if (d.rows == 0) return SDM_OK;   // no work: pointers are not looked at
+  SDM_CHECK_PTR(x);
+  SDM_CHECK_PTR(dt);
+  SDM_CHECK_PTR(A);
+  SDM_CHECK_PTR(B);
+  SDM_CHECK_PTR(C);
+  SDM_CHECK_PTR(y);
+  if (n_slots > 0) SDM_CHECK_PTR(state);
+  SDM_CHECK_OPTIONAL(skip);
+  SDM_CHECK_OPTIONAL(bias);
+  SDM_CHECK_OPTIONAL(z);
+  SDM_CHECK_OPTIONAL(slots);
+  unsigned* sp = nullptr;
+  if ((st = status_ptr(&sp)) != SDM_OK) return st;
+  return from_cuda(launch_selective_scan_step(
+      d, SelectiveInputs{x, dt, A, B, C, skip, bias, z, nullptr}, state, n_slots, slots, y, sp,
+      static_cast<cudaStream_t>(stream)));
 }
 
 sdm_status sdm_get_device_status(void* stream) {

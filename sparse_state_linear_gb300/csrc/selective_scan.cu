@@ -1,0 +1,1101 @@
+// selective_scan.cu -- selective state space scan over packed sequences:
+// forward, backward and single-token step.
+//
+// Per channel c, state n and row t, with one B and C for the channels of a group:
+//   delta = softplus(dt + bias),  a = exp(-A delta),  u = delta x,
+//   h[t] = a h[t-1] + u B[n],  inner = sum_n C[n] h[t] + skip x,  y = inner silu(z).
+// Backward, from the last row to the first, with dinner = dy silu(z):
+//   g = dinner C[n] + r,  r = a g (r starts as the gradient of the final state),
+//   p = r h[t-1],  du = sum_n g B[n],  ddelta = du x - sum_n A p,
+//   dx = du delta + dinner skip,  ddt = ddelta sigmoid(dt + bias),  dz = dy inner silu'(z),
+//   dB[n] = sum_c g u,  dC[n] = sum_c dinner h[t],  dA = -sum_t delta p,
+//   dskip = sum_t dinner x,  dbias = sum_t ddt.
+//
+// Sequences are cut into chunks of L rows where the GPU would not be filled
+// otherwise.  The state behind a chunk is S + exp(-A sum delta) h with S the state
+// behind it from zeros: one kernel finds S and the sum of every chunk, one folds
+// them along each sequence, and the third walks every chunk from the state in
+// front of it (backward: behind it, from the last row to the first).
+#include <atomic>
+#include <type_traits>
+
+#include "common.cuh"
+#include "gates.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "packed.cuh"
+#include "packing.cuh"
+#include "park.cuh"
+#include "rows.cuh"
+#include "slots.cuh"
+
+namespace sdm {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int R = 16;                      // rows at a time; also between saved states
+
+// A thread holds four states of four channels, as pairs of channels.  Of a warp's
+// lanes NL neighbours share channels, CL groups of them have channels of their own.
+template <int N>
+struct Lanes {
+  static constexpr int NL = N / 4, CL = 32 / NL, kCols = CL * 4, kBlockCols = kWarps * kCols;
+  static constexpr int kItems = R * CL / 32;   // of four channels of a row, per lane
+  static constexpr int kNBits = NL == 2 ? 1 : NL == 4 ? 2 : NL == 8 ? 3 : 4, kCBits = 5 - kNBits;
+};
+
+struct ScanArgs {
+  Packed packed;
+  const void* x;
+  const void* dt;
+  const void* z;
+  const void* B;
+  const void* C;
+  const float* A;
+  const float* skip;
+  const float* bias;
+  long long ld, ld_z, ld_bc;
+  int D, G, per;         // channels, groups, channels of a group
+  int tiles, group_tiles;
+  int L, chunks;         // rows of a chunk; of a sequence where all are equal
+  unsigned indexes;      // chunks to look at, see Span
+  float* carry;          // [numbers][D][N]: S, then the state in front of (behind) the chunk
+  float* sums;           // [numbers][D]: sum of delta log2(e)
+  bool split;            // whether there are chunks to be carried between
+  const float* h0;       // (dhT)
+  float* hT;             // (dh0)
+  float* states;         // [numbers of R rows][D][N]
+  void* y;
+  // backward
+  const void* dy;
+  void* dx;
+  void* ddt;
+  void* dz;
+  long long ld_grad, ld_z_grad;
+  float* partial;        // [parts][D (N + 2)]: dA, dskip, dbias
+  float* partial_bc;     // [rows][tiles][2 N]
+  unsigned* status;
+};
+
+// A chunk of a sequence.
+struct Span {
+  int seq, number, row0, rows, begin;
+  bool first, last;
+};
+// The chunk of an index: its number, or where sequences are equal the place among
+// all of them.  False where there is none.  A whole warp calls it.
+__device__ __forceinline__ bool span_of(const Packed& P, int L, int chunks, int index, Span& s) {
+  int chunk;
+  if (P.offsets) {
+    s.seq = sequence_of(P, L, index);
+    if (s.seq < 0) return false;
+    s.begin = P.begin(s.seq);
+    chunk = index - (s.begin / L + s.seq);
+  } else {
+    s.seq = index / chunks;
+    chunk = index % chunks;
+    s.begin = P.begin(s.seq);
+  }
+  const int end = P.begin(s.seq + 1);
+  const long long row0 = s.begin + (long long)chunk * L;
+  if (chunk > 0 && row0 >= end) return false;
+  s.row0 = (int)row0;
+  s.rows = min(L, end - s.row0);
+  s.number = s.begin / L + s.seq + chunk;
+  s.first = chunk == 0;
+  s.last = s.row0 + s.rows == end;
+  return true;
+}
+
+// What a thread's channels are: those of its states, and the four it stages.
+template <int N>
+struct Place {
+  int lane, warp, nl, cl, group, c0, c_end;     // c0: the warp's first channel
+  __device__ __forceinline__ Place(const ScanArgs& P, int tile) {
+    lane = threadIdx.x & 31;
+    warp = threadIdx.x >> 5;
+    nl = lane % Lanes<N>::NL;
+    cl = lane / Lanes<N>::NL;
+    group = tile / P.group_tiles;
+    c0 = group * P.per + tile % P.group_tiles * Lanes<N>::kBlockCols + warp * Lanes<N>::kCols;
+    c_end = (group + 1) * P.per;
+  }
+  __device__ __forceinline__ int mine() const { return c0 + cl * 4; }
+  __device__ __forceinline__ int staged() const { return c0 + lane % Lanes<N>::CL * 4; }
+  __device__ __forceinline__ int staged_row(int i) const { return lane / Lanes<N>::CL + i * Lanes<N>::NL; }
+};
+
+// State registers: v[cp * 4 + n] holds state n of channels 2 cp and 2 cp + 1.
+__device__ __forceinline__ void zero8(float2 (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = both(0.f);
+}
+// From / to [D][N] at the thread's channels and states.
+template <int N>
+__device__ __forceinline__ void load_states(const float* p, float2 (&v)[8]) {
+#pragma unroll
+  for (int cp = 0; cp < 2; ++cp) {
+    const float4 a = *reinterpret_cast<const float4*>(p + (2 * cp) * N);
+    const float4 b = *reinterpret_cast<const float4*>(p + (2 * cp + 1) * N);
+    v[cp * 4 + 0] = make_float2(a.x, b.x);
+    v[cp * 4 + 1] = make_float2(a.y, b.y);
+    v[cp * 4 + 2] = make_float2(a.z, b.z);
+    v[cp * 4 + 3] = make_float2(a.w, b.w);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_states(float* p, const float2 (&v)[8]) {
+#pragma unroll
+  for (int cp = 0; cp < 2; ++cp) {
+    const float2* w = v + cp * 4;
+    *reinterpret_cast<float4*>(p + (2 * cp) * N) = make_float4(w[0].x, w[1].x, w[2].x, w[3].x);
+    *reinterpret_cast<float4*>(p + (2 * cp + 1) * N) = make_float4(w[0].y, w[1].y, w[2].y, w[3].y);
+  }
+}
+
+// Sums of V values over 2^kBits lanes, lane bits kBase on: each step a lane keeps
+// half of the values and gives away the other.  In the end it has kLeft of them, from
+// index() on, and one of the lanes that have the same ones is chosen().
+template <int V, int kBits, int kBase>
+struct Halving {
+  static constexpr int kHalvings = V >= 8 ? (kBits < 3 ? kBits : 3) : V >= 4 ? (kBits < 2 ? kBits : 2) : 0;
+  static constexpr int kLeft = V >> kHalvings;
+  static __device__ __forceinline__ void sum(float (&v)[V], int lane) {
+    int n = V;
+#pragma unroll
+    for (int b = kBits - 1; b >= 0; --b) {
+      const int mask = 1 << (kBase + b);
+      if (n > kLeft) {
+        n /= 2;
+        const bool upper = lane & mask;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+          if (i < n) {
+            const float keep = upper ? v[n + i] : v[i], give = upper ? v[i] : v[n + i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, mask);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLeft; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], mask);
+      }
+    }
+  }
+  static __device__ __forceinline__ int index(int lane) {
+    return (lane >> (kBase + kBits - kHalvings) & ((1 << kHalvings) - 1)) * kLeft;
+  }
+  static __device__ __forceinline__ bool chosen(int lane) {
+    return (lane >> kBase & ((1 << (kBits - kHalvings)) - 1)) == 0;
+  }
+};
+
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<__nv_bfloat16> {
+  uint2 w;
+};
+template <>
+struct Raw4<float> {
+  float4 w;
+};
+template <typename T>
+__device__ __forceinline__ void get4(const Raw4<T>& r, float2 (&f)[2]) {
+  load_row(reinterpret_cast<const T*>(&r), f[0], f[1]);
+}
+template <typename T>
+__device__ __forceinline__ Raw4<T> raw4(const void* base, size_t i) {
+  return *reinterpret_cast<const Raw4<T>*>(static_cast<const T*>(base) + i);
+}
+__device__ __forceinline__ void load_four(const float* p, bool in, float none, float2 (&f)[2]) {
+  f[0] = f[1] = both(none);
+  if (p && in) load_row(p, f[0], f[1]);
+}
+
+// sigmoid(v); 0 where exp(-v) overflows.
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  const float2 z = mul2(v, both(-kLog2e));
+  return make_float2(rcp(1.f + ex2(z.x)), rcp(1.f + ex2(z.y)));
+}
+
+// Rows row0 .. row0 + n - 1 of B (of C) to shared memory, every number twice, zeros
+// behind them.
+template <typename T, int N>
+__device__ __forceinline__ void stage_bc(const void* from, long long ld, int group, int row0, int n,
+                                         float2 (*to)[N]) {
+  for (int i = threadIdx.x; i < R * N / 4; i += kThreads) {
+    const int t = i / (N / 4), q = i % (N / 4) * 4;
+    float2 f[2] = {both(0.f), both(0.f)};
+    if (t < n) get4(raw4<T>(from, (size_t)(row0 + t) * ld + (size_t)group * N + q), f);
+    float4* const at = reinterpret_cast<float4*>(&to[t][q]);
+    at[0] = make_float4(f[0].x, f[0].x, f[0].y, f[0].y);
+    at[1] = make_float4(f[1].x, f[1].x, f[1].y, f[1].y);
+  }
+}
+template <int N>
+__device__ __forceinline__ void four_of(const float2 (*from)[N], int t, int nl, float2 (&v)[4]) {
+  const float4* const at = reinterpret_cast<const float4*>(&from[t][nl * 4]);
+  const float4 a = at[0], b = at[1];
+  v[0] = make_float2(a.x, a.y);
+  v[1] = make_float2(a.z, a.w);
+  v[2] = make_float2(b.x, b.y);
+  v[3] = make_float2(b.z, b.w);
+}
+__device__ __forceinline__ float2 ex2_pair(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+
+template <int N>
+struct ForwardSmem {
+  float2 B[R][N], C[R][N];
+  struct {
+    float sp[R][Lanes<N>::kCols], u[R][Lanes<N>::kCols], y[R][Lanes<N>::kCols];
+  } warp[kWarps];
+};
+
+// ------------------------------------------------------------------- forward
+// kSummary: S and the sum of the chunk only.
+template <typename T, int N, bool kSummary>
+__global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
+  using Ln = Lanes<N>;
+  extern __shared__ __align__(16) char smem[];
+  ForwardSmem<N>& sh = *reinterpret_cast<ForwardSmem<N>*>(smem);
+  wait_for_stream();
+  if (!offsets_ok(P.packed)) {
+    if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  Span s;
+  if (!span_of(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s)) return;
+  if (kSummary && s.last) return;          // what is behind it nobody needs
+  const Place<N> at(P, blockIdx.x % P.tiles);
+  auto& mem = sh.warp[at.warp];
+  const Constants K = constants();
+  const int c = at.mine(), cs = at.staged();
+  const bool in = c < at.c_end, in_s = cs < at.c_end;
+  const size_t state = (size_t)c * N + at.nl * 4;
+  float2 nA[8], h[8];
+  zero8(nA);
+  zero8(h);
+  if (in) {
+    load_states<N>(P.A + state, nA);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
+    if (!kSummary) {
+      const size_t DN = (size_t)P.D * N;
+      if (P.split) load_states<N>(P.carry + s.number * DN + state, h);
+      else if (P.h0) load_states<N>(P.h0 + s.seq * DN + state, h);
+    }
+  }
+  float2 bias[2], skip[2], sum[2] = {both(0.f), both(0.f)};
+  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
+  load_four(P.skip ? P.skip + cs : nullptr, in_s, 0.f, skip);
+
+  for (int r = 0; r < s.rows; r += R) {
+    const int row0 = s.row0 + r, n = min(R, s.rows - r);
+    __syncthreads();                       // the rows before are done with
+    stage_bc<T, N>(P.B, P.ld_bc, at.group, row0, n, sh.B);
+    if (!kSummary) stage_bc<T, N>(P.C, P.ld_bc, at.group, row0, n, sh.C);
+    Raw4<T> x[Ln::kItems], z[Ln::kItems];
+#pragma unroll
+    for (int i = 0; i < Ln::kItems; ++i) {
+      const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
+      float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)};
+      if (t < n && in_s) {
+        x[i] = raw4<T>(P.x, (size_t)(row0 + t) * P.ld + cs);
+        const Raw4<T> dt = raw4<T>(P.dt, (size_t)(row0 + t) * P.ld + cs);
+        if (!kSummary && P.z) z[i] = raw4<T>(P.z, (size_t)(row0 + t) * P.ld_z + cs);
+        float2 f[2], d[2];
+        get4(x[i], f);
+        get4(dt, d);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float2 unused, e;
+          softplus_pair(K, d[p], bias[p], unused, e, sp[p]);
+          u[p] = mul2(mul2(sp[p], both(kLn2)), f[p]);
+          if (kSummary) sum[p] = add2(sum[p], sp[p]);
+        }
+      }
+      store_row(&mem.sp[t][q], sp[0], sp[1]);
+      store_row(&mem.u[t][q], u[0], u[1]);
+    }
+    __syncthreads();
+    if (!kSummary && P.states && in)
+      store_states<N>(P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * P.D * N + state, h);
+#pragma unroll 2
+    for (int t = 0; t < R; ++t) {
+      float2 sp[2], u[2], B[4], C[4], y[2];
+      load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
+      load_row(&mem.u[t][at.cl * 4], u[0], u[1]);
+      four_of<N>(sh.B, t, at.nl, B);
+      if (!kSummary) four_of<N>(sh.C, t, at.nl, C);
+#pragma unroll
+      for (int cp = 0; cp < 2; ++cp) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = cp * 4 + k;
+          h[i] = fma2(ex2_pair(mul2(nA[i], sp[cp])), h[i], mul2(u[cp], B[k]));
+          if (!kSummary) y[cp] = k ? fma2(C[k], h[i], y[cp]) : mul2(C[k], h[i]);
+        }
+      }
+      if (kSummary) continue;
+      using Sum = Halving<4, Ln::kNBits, 0>;
+      float v[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
+      Sum::sum(v, at.lane);
+      if (Sum::chosen(at.lane)) {
+        float* const to = &mem.y[t][at.cl * 4 + Sum::index(at.lane)];
+        if (Sum::kLeft == 2) *reinterpret_cast<float2*>(to) = make_float2(v[0], v[1]);
+        else *to = v[0];
+      }
+    }
+    if (kSummary) continue;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < Ln::kItems; ++i) {
+      const int t = at.staged_row(i);
+      if (t >= n || !in_s) continue;
+      float2 y[2], f[2], g[2];
+      load_row(&mem.y[t][at.lane % Ln::CL * 4], y[0], y[1]);
+      get4(x[i], f);
+      if (P.z) get4(z[i], g);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        y[p] = fma2(skip[p], f[p], y[p]);
+        if (P.z) y[p] = mul2(y[p], mul2(g[p], sigmoid2(g[p])));
+      }
+      store_row(static_cast<T*>(P.y) + (size_t)(row0 + t) * P.D + cs, y[0], y[1]);
+    }
+  }
+  if (kSummary) {
+    if (in) store_states<N>(P.carry + (size_t)s.number * P.D * N + state, h);
+    float v[4] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y};
+#pragma unroll
+    for (int o = Ln::CL; o < 32; o *= 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (at.lane < Ln::CL && in_s)
+      store_row(P.sums + (size_t)s.number * P.D + cs, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
+  } else if (P.hT && s.last && in) {
+    store_states<N>(P.hT + (size_t)s.seq * P.D * N + state, h);
+  }
+}
+
+// The state in front of every chunk from those behind the chunks before it; with
+// kBack the gradient of the state behind every chunk.  Four states a thread.
+template <bool kBack>
+__global__ void __launch_bounds__(kThreads) fold_kernel(const ScanArgs P, int N, int blocks) {
+  wait_for_stream();
+  if (!offsets_ok(P.packed)) return;
+  const int seq = blockIdx.x / blocks;
+  const long long i = (long long)(blockIdx.x % blocks) * kThreads + threadIdx.x;
+  const size_t DN = (size_t)P.D * N;
+  if (i * 4 >= (long long)DN) return;
+  const int begin = P.packed.begin(seq), end = P.packed.begin(seq + 1), c = (int)(i * 4 / N);
+  const int chunks = max(1, (int)(((long long)end - begin + P.L - 1) / P.L));
+  const float4 A = *reinterpret_cast<const float4*>(P.A + i * 4);
+  float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (P.h0) h = *reinterpret_cast<const float4*>(P.h0 + seq * DN + i * 4);
+  const size_t number = (size_t)(begin / P.L + seq);
+  constexpr int kAhead = 8;
+  for (int k0 = 0; k0 < chunks; k0 += kAhead) {
+    float4 S[kAhead];
+    float sum[kAhead];
+    float* at[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j;
+      if (k >= chunks) break;
+      const size_t m = number + (kBack ? chunks - 1 - k : k);
+      at[j] = P.carry + m * DN + i * 4;
+      if (k + 1 < chunks) {
+        S[j] = *reinterpret_cast<const float4*>(at[j]);
+        sum[j] = P.sums[m * P.D + c];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (k0 + j >= chunks) break;
+      *reinterpret_cast<float4*>(at[j]) = h;
+      if (k0 + j + 1 < chunks) {
+        h.x = fmaf(ex2(-A.x * sum[j]), h.x, S[j].x);
+        h.y = fmaf(ex2(-A.y * sum[j]), h.y, S[j].y);
+        h.z = fmaf(ex2(-A.z * sum[j]), h.z, S[j].z);
+        h.w = fmaf(ex2(-A.w * sum[j]), h.w, S[j].w);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ backward
+template <int N>
+struct BackwardSmem {
+  float2 B[R][N], C[R][N];
+  float bc[kWarps][R][2 * N];              // a warp's channels' shares of dB and dC
+  struct {
+    float sp[R][Lanes<N>::kCols], u[R][Lanes<N>::kCols], d[R][Lanes<N>::kCols];
+    float du[R][Lanes<N>::kCols], dl[R][Lanes<N>::kCols], y[R][Lanes<N>::kCols];
+  } warp[kWarps];
+  uint32_t tmem;
+};
+
+// dinner = dy silu(z) of four channels.
+template <typename T>
+__device__ __forceinline__ void dinner_of(const Raw4<T>& dy, const Raw4<T>& z, bool gated, float2 (&d)[2]) {
+  get4(dy, d);
+  if (!gated) return;
+  float2 g[2];
+  get4(z, g);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) d[p] = mul2(d[p], mul2(g[p], sigmoid2(g[p])));
+}
+
+// The gradient of the state in front of a chunk from zeros behind it, and the sum.
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) back_summary_kernel(const ScanArgs P) {
+  using Ln = Lanes<N>;
+  extern __shared__ __align__(16) char smem[];
+  ForwardSmem<N>& sh = *reinterpret_cast<ForwardSmem<N>*>(smem);   // u: dinner
+  wait_for_stream();
+  if (!offsets_ok(P.packed)) {
+    if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  Span s;
+  if (!span_of(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s)) return;
+  if (s.first) return;
+  const Place<N> at(P, blockIdx.x % P.tiles);
+  auto& mem = sh.warp[at.warp];
+  const Constants K = constants();
+  const int c = at.mine(), cs = at.staged();
+  const bool in = c < at.c_end, in_s = cs < at.c_end;
+  const size_t state = (size_t)c * N + at.nl * 4;
+  float2 nA[8], r[8];
+  zero8(nA);
+  zero8(r);
+  if (in) {
+    load_states<N>(P.A + state, nA);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
+  }
+  float2 bias[2], sum[2] = {both(0.f), both(0.f)};
+  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
+
+  for (int r0 = (s.rows - 1) / R * R; r0 >= 0; r0 -= R) {
+    const int row0 = s.row0 + r0, n = min(R, s.rows - r0);
+    __syncthreads();
+    stage_bc<T, N>(P.C, P.ld_bc, at.group, row0, n, sh.C);
+#pragma unroll
+    for (int i = 0; i < Ln::kItems; ++i) {
+      const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
+      float2 sp[2] = {both(0.f), both(0.f)}, d[2] = {both(0.f), both(0.f)};
+      if (t < n && in_s) {
+        const Raw4<T> dt = raw4<T>(P.dt, (size_t)(row0 + t) * P.ld + cs);
+        const Raw4<T> dy = raw4<T>(P.dy, (size_t)(row0 + t) * P.D + cs);
+        Raw4<T> z = dy;
+        if (P.z) z = raw4<T>(P.z, (size_t)(row0 + t) * P.ld_z + cs);
+        float2 f[2];
+        get4(dt, f);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float2 unused, e;
+          softplus_pair(K, f[p], bias[p], unused, e, sp[p]);
+          sum[p] = add2(sum[p], sp[p]);
+        }
+        dinner_of(dy, z, P.z != nullptr, d);
+      }
+      store_row(&mem.sp[t][q], sp[0], sp[1]);
+      store_row(&mem.u[t][q], d[0], d[1]);
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int t = R - 1; t >= 0; --t) {
+      float2 sp[2], d[2], C[4];
+      load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
+      load_row(&mem.u[t][at.cl * 4], d[0], d[1]);
+      four_of<N>(sh.C, t, at.nl, C);
+#pragma unroll
+      for (int cp = 0; cp < 2; ++cp)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = cp * 4 + k;
+          r[i] = mul2(ex2_pair(mul2(nA[i], sp[cp])), fma2(d[cp], C[k], r[i]));
+        }
+    }
+  }
+  if (in) store_states<N>(P.carry + (size_t)s.number * P.D * N + state, r);
+  float v[4] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y};
+#pragma unroll
+  for (int o = Ln::CL; o < 32; o *= 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (at.lane < Ln::CL && in_s)
+    store_row(P.sums + (size_t)s.number * P.D + cs, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
+}
+
+// A block takes a tile of channels and every parts-th chunk, from its last rows to
+// its first, R at a time: forward from the saved state with the state in front of
+// every row parked in tensor memory, then back.
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
+  using Ln = Lanes<N>;
+  extern __shared__ __align__(16) char smem[];
+  BackwardSmem<N>& sh = *reinterpret_cast<BackwardSmem<N>*>(smem);
+  constexpr uint32_t kTmemCols = R * 16;
+  // A block that holds tensor memory must not wait for a kernel in front of it.
+  wait_for_stream();
+  if (!offsets_ok(P.packed)) {
+    if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  const Place<N> at(P, blockIdx.x % P.tiles);
+  if (at.warp == 0) tc::tmem_alloc(&sh.tmem, kTmemCols);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t park = sh.tmem + ((uint32_t)at.warp << 21);
+  auto& mem = sh.warp[at.warp];
+  const Constants K = constants();
+  const int c = at.mine(), cs = at.staged();
+  const bool in = c < at.c_end, in_s = cs < at.c_end;
+  const size_t state = (size_t)c * N + at.nl * 4, DN = (size_t)P.D * N;
+  float2 nA[8], dA[8];
+  zero8(nA);
+  zero8(dA);
+  if (in) {
+    load_states<N>(P.A + state, nA);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
+  }
+  float2 bias[2], skip[2], dskip[2] = {both(0.f), both(0.f)}, dbias[2] = {both(0.f), both(0.f)};
+  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
+  load_four(P.skip ? P.skip + cs : nullptr, in_s, 0.f, skip);
+
+  const unsigned parts = gridDim.x / P.tiles, part = blockIdx.x / P.tiles;
+  for (unsigned index = part; index < P.indexes; index += parts) {
+    Span s;
+    if (!span_of(P.packed, P.L, P.chunks, (int)index, s)) continue;
+    float2 r[8];
+    zero8(r);
+    if (in) {
+      if (P.split) load_states<N>(P.carry + s.number * DN + state, r);
+      else if (P.h0) load_states<N>(P.h0 + s.seq * DN + state, r);
+    }
+    for (int r0 = (s.rows - 1) / R * R; r0 >= 0 && s.rows > 0; r0 -= R) {
+      const int row0 = s.row0 + r0, n = min(R, s.rows - r0);
+      __syncthreads();                     // the rows behind are done with
+      float2 h[8];
+      zero8(h);
+      if (in)
+        load_states<N>(P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * DN + state, h);
+      stage_bc<T, N>(P.B, P.ld_bc, at.group, row0, n, sh.B);
+      stage_bc<T, N>(P.C, P.ld_bc, at.group, row0, n, sh.C);
+#pragma unroll
+      for (int i = 0; i < Ln::kItems; ++i) {
+        const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
+        float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)}, d[2] = {both(0.f), both(0.f)};
+        if (t < n && in_s) {
+          const Raw4<T> x = raw4<T>(P.x, (size_t)(row0 + t) * P.ld + cs);
+          const Raw4<T> dt = raw4<T>(P.dt, (size_t)(row0 + t) * P.ld + cs);
+          const Raw4<T> dy = raw4<T>(P.dy, (size_t)(row0 + t) * P.D + cs);
+          Raw4<T> z = dy;
+          if (P.z) z = raw4<T>(P.z, (size_t)(row0 + t) * P.ld_z + cs);
+          float2 f[2], v[2];
+          get4(x, f);
+          get4(dt, v);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            float2 unused, e;
+            softplus_pair(K, v[p], bias[p], unused, e, sp[p]);
+            u[p] = mul2(mul2(sp[p], both(kLn2)), f[p]);
+          }
+          dinner_of(dy, z, P.z != nullptr, d);
+        }
+        store_row(&mem.sp[t][q], sp[0], sp[1]);
+        store_row(&mem.u[t][q], u[0], u[1]);
+        store_row(&mem.d[t][q], d[0], d[1]);
+      }
+      __syncthreads();
+#pragma unroll 2
+      for (int t = 0; t < R; ++t) {
+        float2 sp[2], u[2], B[4];
+        park16(park + t * 16, h);
+        load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
+        load_row(&mem.u[t][at.cl * 4], u[0], u[1]);
+        four_of<N>(sh.B, t, at.nl, B);
+#pragma unroll
+        for (int cp = 0; cp < 2; ++cp)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = cp * 4 + k;
+            h[i] = fma2(ex2_pair(mul2(nA[i], sp[cp])), h[i], mul2(u[cp], B[k]));
+          }
+      }
+      parked();
+#pragma unroll 2
+      for (int t = R - 1; t >= 0; --t) {
+        float2 before[8], sp[2], u[2], d[2], B[4], C[4];
+        ask16(park + t * 16, before);
+        load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
+        load_row(&mem.u[t][at.cl * 4], u[0], u[1]);
+        load_row(&mem.d[t][at.cl * 4], d[0], d[1]);
+        four_of<N>(sh.B, t, at.nl, B);
+        four_of<N>(sh.C, t, at.nl, C);
+        asked();
+        here(before);
+        float2 du[2], dl[2], y[2], dB[4], dC[4];
+#pragma unroll
+        for (int cp = 0; cp < 2; ++cp)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = cp * 4 + k;
+            const float2 g = fma2(d[cp], C[k], r[i]);
+            r[i] = mul2(g, ex2_pair(mul2(nA[i], sp[cp])));
+            const float2 p = mul2(r[i], before[i]);
+            dA[i] = fma2(p, sp[cp], dA[i]);
+            du[cp] = k ? fma2(g, B[k], du[cp]) : mul2(g, B[k]);
+            dl[cp] = k ? fma2(p, nA[i], dl[cp]) : mul2(p, nA[i]);
+            y[cp] = k ? fma2(C[k], h[i], y[cp]) : mul2(C[k], h[i]);
+            dB[k] = cp ? fma2(g, u[cp], dB[k]) : mul2(g, u[cp]);
+            dC[k] = cp ? fma2(d[cp], h[i], dC[k]) : mul2(d[cp], h[i]);
+            h[i] = before[i];
+          }
+        using Sum = Halving<4, Ln::kNBits, 0>;
+        float v[4] = {du[0].x, du[0].y, du[1].x, du[1].y};
+        float w[4] = {dl[0].x, dl[0].y, dl[1].x, dl[1].y};
+        float o[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
+        Sum::sum(v, at.lane);
+        Sum::sum(w, at.lane);
+        Sum::sum(o, at.lane);
+        if (Sum::chosen(at.lane)) {
+          const int to = at.cl * 4 + Sum::index(at.lane);
+#pragma unroll
+          for (int j = 0; j < Sum::kLeft; ++j) {
+            mem.du[t][to + j] = v[j];
+            mem.dl[t][to + j] = w[j];
+            mem.y[t][to + j] = o[j];
+          }
+        }
+        using Over = Halving<8, Ln::kCBits, Ln::kNBits>;
+        float q[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          q[k] = dB[k].x + dB[k].y;
+          q[4 + k] = dC[k].x + dC[k].y;
+        }
+        Over::sum(q, at.lane);
+        if (Over::chosen(at.lane)) {
+#pragma unroll
+          for (int j = 0; j < Over::kLeft; ++j) {
+            const int to = Over::index(at.lane) + j;
+            sh.bc[at.warp][t][(to >> 2) * N + at.nl * 4 + (to & 3)] = q[j];
+          }
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < n * 2 * N; i += kThreads) {
+        const int t = i / (2 * N), k = i % (2 * N);
+        float v = sh.bc[0][t][k];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v += sh.bc[w][t][k];
+        P.partial_bc[((size_t)(row0 + t) * P.tiles + blockIdx.x % P.tiles) * (2 * N) + k] = v;
+      }
+#pragma unroll
+      for (int i = 0; i < Ln::kItems; ++i) {
+        const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
+        if (t >= n || !in_s) continue;
+        const size_t row = row0 + t;
+        float2 x[2], dt[2], d[2], sp[2], du[2], dl[2], y[2], dx[2], ddt[2];
+        get4(raw4<T>(P.x, row * P.ld + cs), x);
+        get4(raw4<T>(P.dt, row * P.ld + cs), dt);
+        load_row(&mem.sp[t][q], sp[0], sp[1]);
+        load_row(&mem.d[t][q], d[0], d[1]);
+        load_row(&mem.du[t][q], du[0], du[1]);
+        load_row(&mem.dl[t][q], dl[0], dl[1]);
+        load_row(&mem.y[t][q], y[0], y[1]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          dx[p] = fma2(du[p], mul2(sp[p], both(kLn2)), mul2(d[p], skip[p]));
+          ddt[p] = mul2(fma2(du[p], x[p], dl[p]), sigmoid2(add2(dt[p], bias[p])));
+          dskip[p] = fma2(d[p], x[p], dskip[p]);
+          dbias[p] = add2(dbias[p], ddt[p]);
+        }
+        store_row(static_cast<T*>(P.dx) + row * P.ld_grad + cs, dx[0], dx[1]);
+        store_row(static_cast<T*>(P.ddt) + row * P.ld_grad + cs, ddt[0], ddt[1]);
+        if (P.z) {
+          float2 z[2], dy[2];
+          get4(raw4<T>(P.z, row * P.ld_z + cs), z);
+          get4(raw4<T>(P.dy, row * P.D + cs), dy);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float2 sig = sigmoid2(z[p]), inner = fma2(skip[p], x[p], y[p]);
+            // silu' = sig (1 + z (1 - sig)).
+            z[p] = mul2(mul2(dy[p], inner), mul2(sig, fma2(z[p], sub2(both(1.f), sig), both(1.f))));
+          }
+          store_row(static_cast<T*>(P.dz) + row * P.ld_z_grad + cs, z[0], z[1]);
+        }
+      }
+    }
+    if (P.hT && s.first && in) store_states<N>(P.hT + s.seq * DN + state, r);
+  }
+  // The chunks' sums.  dA = -sum delta p, and sp is delta log2(e).
+  float* const to = P.partial + (size_t)part * P.D * (N + 2);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dA[i] = mul2(dA[i], both(-kLn2));
+  if (in) store_states<N>(to + state, dA);
+  float v[8] = {dskip[0].x, dskip[0].y, dskip[1].x, dskip[1].y, dbias[0].x, dbias[0].y, dbias[1].x, dbias[1].y};
+#pragma unroll
+  for (int o = Ln::CL; o < 32; o *= 2)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (at.lane < Ln::CL && in_s) {
+    store_row(to + DN + cs, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
+    store_row(to + DN + P.D + cs, make_float2(v[4], v[5]), make_float2(v[6], v[7]));
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (at.warp == 0) tc::tmem_dealloc(sh.tmem, kTmemCols);
+}
+
+// dB and dC of every row of a sequence: the tiles' shares of a group, in their order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    bc_sums_kernel(const ScanArgs P, int N, T* dB, T* dC, long long ld) {
+  wait_for_stream();
+  if (!offsets_ok(P.packed)) return;
+  const int width = P.G * 2 * N;
+  const long long first = P.packed.begin(0), n = (long long)(P.packed.begin(P.packed.n_seq) - first) * width;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    const long long row = first + i / width;
+    const int k = (int)(i % width), g = k / (2 * N), j = k % (2 * N);
+    const float* at = P.partial_bc + ((size_t)row * P.tiles + (size_t)g * P.group_tiles) * (2 * N) + j;
+    float v = 0.f;
+    for (int t = 0; t < P.group_tiles; ++t) v += __ldg(at + (size_t)t * (2 * N));
+    T* const to = j < N ? dB : dC;
+    to[(size_t)row * ld + (size_t)g * N + j % N] = (T)v;
+  }
+}
+
+// Sums of [parts][D (N + 2)] over the parts, always in the same order: 32 columns a
+// block, each of 32 warps every 32nd part, then the warps.
+__global__ void __launch_bounds__(1024)
+    scan_sums_kernel(const Packed packed, const float* partial, int parts, long long D, int N,
+                     float* dA, float* dskip, float* dbias) {
+  wait_for_stream();
+  if (!offsets_ok(packed)) return;
+  __shared__ float warps[32][33];
+  const long long width = D * (N + 2), i = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float a = 0.f;
+  if (i < width) {
+#pragma unroll 4
+    for (int n = warp; n < parts; n += 32) a += __ldg(partial + n * width + i);
+  }
+  warps[warp][lane] = a;
+  __syncthreads();
+  if (warp != 0 || i >= width) return;
+  float sum = 0.f;
+  for (int w = 0; w < 32; ++w) sum += warps[w][lane];
+  if (i < D * N) {
+    if (dA) dA[i] = sum;
+  } else if (i < D * (N + 1)) {
+    if (dskip) dskip[i - D * N] = sum;
+  } else if (dbias) {
+    dbias[i - D * (N + 1)] = sum;
+  }
+}
+
+// ----------------------------------------------------------------- one token
+// A block takes kGroup tokens by a tile of channels, as the chunks do.
+template <typename T, int N, int kGroup>
+__global__ void __launch_bounds__(kThreads) step_kernel(const ScanArgs P, float* pool, int n_slots,
+                                                        const int32_t* slots) {
+  using Ln = Lanes<N>;
+  wait_for_stream();
+  __shared__ SlotTable<kGroup, kThreads> table;
+  const int row0 = (int)(blockIdx.x / P.tiles) * kGroup, rows = min(kGroup, P.packed.rows - row0);
+  const Place<N> at(P, blockIdx.x % P.tiles);
+  table.find(slots, row0, rows, n_slots, P.status);
+  const Constants K = constants();
+  const int c = at.mine();
+  const unsigned lanes = __ballot_sync(0xffffffffu, c < at.c_end);   // whole groups of NL lanes
+  if (c >= at.c_end) return;
+  const size_t state = (size_t)c * N + at.nl * 4;
+  float2 nA[8], bias[2], skip[2];
+  load_states<N>(P.A + state, nA);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
+  load_four(P.bias ? P.bias + c : nullptr, true, 0.f, bias);
+  load_four(P.skip ? P.skip + c : nullptr, true, 0.f, skip);
+  for (int j = 0; j < rows; ++j) {
+    const int slot = table.own[j];
+    if (slot < 0) continue;
+    const size_t row = row0 + j;
+    float* const p = pool + (size_t)slot * P.D * N + state;
+    float2 h[8], x[2], dt[2], z[2], B[2], C[2], y[2];
+    load_states<N>(p, h);
+    get4(raw4<T>(P.x, row * P.ld + c), x);
+    get4(raw4<T>(P.dt, row * P.ld + c), dt);
+    get4(raw4<T>(P.B, row * P.ld_bc + (size_t)at.group * N + at.nl * 4), B);
+    get4(raw4<T>(P.C, row * P.ld_bc + (size_t)at.group * N + at.nl * 4), C);
+    if (P.z) get4(raw4<T>(P.z, row * P.ld_z + c), z);
+    const float b[4] = {B[0].x, B[0].y, B[1].x, B[1].y}, o[4] = {C[0].x, C[0].y, C[1].x, C[1].y};
+#pragma unroll
+    for (int cp = 0; cp < 2; ++cp) {
+      float2 unused, e, sp;
+      softplus_pair(K, dt[cp], bias[cp], unused, e, sp);
+      const float2 u = mul2(mul2(sp, both(kLn2)), x[cp]);
+      y[cp] = both(0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = cp * 4 + k;
+        h[i] = fma2(ex2_pair(mul2(nA[i], sp)), h[i], mul2(u, both(b[k])));
+        y[cp] = fma2(both(o[k]), h[i], y[cp]);
+      }
+    }
+    store_states<N>(p, h);
+    float v[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
+#pragma unroll
+    for (int m = 1; m < Ln::NL; m *= 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(lanes, v[i], m);
+    if (at.nl != 0) continue;
+    y[0] = make_float2(v[0], v[1]);
+    y[1] = make_float2(v[2], v[3]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      y[q] = fma2(skip[q], x[q], y[q]);
+      if (P.z) y[q] = mul2(y[q], mul2(z[q], sigmoid2(z[q])));
+    }
+    store_row(static_cast<T*>(P.y) + row * P.D + c, y[0], y[1]);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+int tile_cols(int N) { return kWarps * 4 * 32 / (N / 4); }
+int group_tiles_of(const SelectiveDims& d) {
+  return (d.D / d.groups + tile_cols(d.N) - 1) / tile_cols(d.N);
+}
+
+// How the sequences are cut: rows of a chunk, a multiple of R, and whether any
+// sequence has more than one.
+struct Cut {
+  int L;
+  bool split;
+};
+constexpr int kLeastChunk = 64, kMostChunk = 1 << 20;
+Cut cut_of(const SelectiveDims& d, bool equal) {
+  const long long tiles = (long long)group_tiles_of(d) * d.groups, fill = 4ll * device_limits().sms;
+  const int longest = equal && d.n_seq > 0 ? d.rows / d.n_seq : d.rows;
+  const long long whole = ((long long)longest + R - 1) / R * R;
+  long long L = whole;
+  if (!equal || d.n_seq * tiles < fill) {
+    L = (long long)d.rows * tiles / fill / R * R;
+    if (L < kLeastChunk) L = kLeastChunk;
+    if (L > whole) L = whole;
+  }
+  if (L > kMostChunk) L = kMostChunk;
+  if (L < R) L = R;
+  return Cut{(int)L, longest > L};
+}
+size_t numbers_of(const SelectiveDims& d, int L) { return (size_t)chunk_numbers(d.rows, d.n_seq, L); }
+size_t carry_bytes(const SelectiveDims& d, const Cut& cut) {
+  return cut.split ? round256(numbers_of(d, cut.L) * d.D * d.N * 4) + round256(numbers_of(d, cut.L) * d.D * 4) : 0;
+}
+// Parts of the sums over rows: at most what fills the GPU.
+size_t most_parts(const SelectiveDims& d) {
+  const size_t tiles = (size_t)group_tiles_of(d) * d.groups, fill = 2 * (size_t)device_limits().sms;
+  return (fill + tiles - 1) / tiles;
+}
+
+ScanArgs args_of(const SelectiveDims& d, const SelectiveInputs& in, const Cut& cut, void* workspace,
+                 unsigned* status) {
+  ScanArgs P{};
+  P.packed = Packed{in.offsets, d.n_seq, d.rows};
+  P.x = in.x;
+  P.dt = in.dt;
+  P.z = in.z;
+  P.B = in.B;
+  P.C = in.C;
+  P.A = in.A;
+  P.skip = in.skip;
+  P.bias = in.bias;
+  P.ld = d.ld;
+  P.ld_z = d.ld_z;
+  P.ld_bc = d.ld_bc;
+  P.D = d.D;
+  P.G = d.groups;
+  P.per = d.D / d.groups;
+  P.group_tiles = group_tiles_of(d);
+  P.tiles = P.group_tiles * d.groups;
+  P.L = cut.L;
+  P.split = cut.split;
+  P.chunks = 1;
+  if (in.offsets || d.n_seq == 0) {
+    P.indexes = (unsigned)numbers_of(d, cut.L);
+  } else {
+    const int len = d.rows / d.n_seq;
+    P.chunks = len > cut.L ? (int)(((long long)len + cut.L - 1) / cut.L) : 1;
+    P.indexes = (unsigned)P.chunks * d.n_seq;
+  }
+  if (cut.split) {
+    P.carry = static_cast<float*>(workspace);
+    P.sums = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                      round256(numbers_of(d, cut.L) * d.D * d.N * 4));
+  }
+  P.status = status;
+  return P;
+}
+
+// Dynamic shared memory of a kernel, allowed once per device.
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (f == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  return f;
+}
+template <class K>
+cudaError_t launch_with(K kernel, std::atomic<bool>* allowed, unsigned blocks, size_t smem,
+                        cudaStream_t stream, const ScanArgs& P) {
+  const cudaError_t e = allow_smem(kernel, (int)smem, allowed);
+  return e != cudaSuccess ? e : launch_behind(kernel, blocks, kThreads, smem, stream, P);
+}
+
+template <class F>
+cudaError_t with_kind(const SelectiveDims& d, F f) {
+  using std::integral_constant;
+  auto states = [&](auto t) {
+    if (d.N == 8) return f(t, integral_constant<int, 8>{});
+    if (d.N == 16) return f(t, integral_constant<int, 16>{});
+    if (d.N == 32) return f(t, integral_constant<int, 32>{});
+    return f(t, integral_constant<int, 64>{});
+  };
+  return d.dtype == SDM_BF16 ? states(__nv_bfloat16{}) : states(float{});
+}
+
+template <bool kBack>
+cudaError_t launch_fold(const SelectiveDims& d, const ScanArgs& P, cudaStream_t stream) {
+  const int blocks = (int)(((long long)d.D * d.N / 4 + kThreads - 1) / kThreads);
+  return launch_behind(fold_kernel<kBack>, (unsigned)blocks * d.n_seq, kThreads, 0, stream, P, d.N, blocks);
+}
+
+}  // namespace
+
+int selective_scan_tiles(const SelectiveDims& d) { return group_tiles_of(d) * d.groups; }
+
+size_t selective_scan_workspace_bytes(const SelectiveDims& d) {
+  const size_t a = carry_bytes(d, cut_of(d, false));
+  const size_t b = d.n_seq > 0 && d.rows % d.n_seq == 0 ? carry_bytes(d, cut_of(d, true)) : 0;
+  return 256 + (a > b ? a : b);
+}
+size_t selective_scan_backward_workspace_bytes(const SelectiveDims& d) {
+  const size_t tiles = (size_t)group_tiles_of(d) * d.groups;
+  return selective_scan_workspace_bytes(d) + round256(most_parts(d) * d.D * (d.N + 2) * 4) +
+         (size_t)d.rows * tiles * 2 * d.N * 4;
+}
+
+size_t selective_scan_states_bytes(const SelectiveDims& d) {
+  return numbers_of(d, R) * d.D * d.N * sizeof(float);
+}
+
+cudaError_t launch_selective_scan_forward(const SelectiveDims& d, const SelectiveInputs& in,
+                                          const float* h0, void* y, float* hT, float* states,
+                                          void* workspace, unsigned* status, cudaStream_t stream) {
+  const Cut cut = cut_of(d, !in.offsets);
+  ScanArgs P = args_of(d, in, cut, workspace, status);
+  P.h0 = h0;
+  P.hT = hT;
+  P.y = y;
+  P.states = states;
+  return with_kind(d, [&](auto t, auto n) {
+    using T = decltype(t);
+    constexpr int N = decltype(n)::value;
+    static std::atomic<bool> allowed[2][64];
+    const unsigned blocks = P.indexes * P.tiles;
+    cudaError_t e = cudaSuccess;
+    if (cut.split) {
+      e = launch_with(forward_kernel<T, N, true>, allowed[0], blocks, sizeof(ForwardSmem<N>), stream, P);
+      if (e == cudaSuccess) e = launch_fold<false>(d, P, stream);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_with(forward_kernel<T, N, false>, allowed[1], blocks, sizeof(ForwardSmem<N>), stream, P);
+  });
+}
+
+cudaError_t launch_selective_scan_backward(const SelectiveDims& d, const SelectiveInputs& in,
+                                           const float* states, const void* dy, const float* dhT,
+                                           const SelectiveGrads& out, void* workspace,
+                                           unsigned* status, cudaStream_t stream) {
+  if (d.n_seq == 0) {                      // sums over nothing
+    cudaError_t e = cudaSuccess;
+    if (out.dA) e = cudaMemsetAsync(out.dA, 0, (size_t)d.D * d.N * 4, stream);
+    if (e == cudaSuccess && out.dskip) e = cudaMemsetAsync(out.dskip, 0, (size_t)d.D * 4, stream);
+    if (e == cudaSuccess && out.dbias) e = cudaMemsetAsync(out.dbias, 0, (size_t)d.D * 4, stream);
+    return e;
+  }
+  const Cut cut = cut_of(d, !in.offsets);
+  ScanArgs P = args_of(d, in, cut, workspace, status);
+  char* w = static_cast<char*>(workspace) + carry_bytes(d, cut);
+  P.partial = reinterpret_cast<float*>(w);
+  P.partial_bc = reinterpret_cast<float*>(w + round256(most_parts(d) * d.D * (d.N + 2) * 4));
+  P.h0 = dhT;
+  P.hT = out.dh0;
+  P.states = const_cast<float*>(states);
+  P.dy = dy;
+  P.dx = out.dx;
+  P.ddt = out.ddt;
+  P.dz = out.dz;
+  P.ld_grad = d.ld_grad;
+  P.ld_z_grad = d.ld_z_grad;
+  const unsigned parts = (unsigned)(P.indexes < most_parts(d) ? P.indexes : most_parts(d));
+  cudaError_t e = with_kind(d, [&](auto t, auto n) {
+    using T = decltype(t);
+    constexpr int N = decltype(n)::value;
+    static std::atomic<bool> allowed[2][64];
+    cudaError_t e = cudaSuccess;
+    if (cut.split) {
+      e = launch_with(back_summary_kernel<T, N>, allowed[0], P.indexes * P.tiles, sizeof(ForwardSmem<N>), stream, P);
+      if (e == cudaSuccess) e = launch_fold<true>(d, P, stream);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_with(backward_kernel<T, N>, allowed[1], parts * P.tiles, sizeof(BackwardSmem<N>), stream, P);
+  });
+  if (e == cudaSuccess && d.rows > 0) {
+    const long long want = ((long long)d.rows * d.groups * 2 * d.N + 255) / 256, most = 16ll * device_limits().sms;
+    const unsigned blocks = (unsigned)(want < most ? want : most);
+    e = d.dtype == SDM_BF16
+            ? launch_behind(bc_sums_kernel<__nv_bfloat16>, blocks, 256, 0, stream, P, d.N,
+                            static_cast<__nv_bfloat16*>(out.dB), static_cast<__nv_bfloat16*>(out.dC), d.ld_bc_grad)
+            : launch_behind(bc_sums_kernel<float>, blocks, 256, 0, stream, P, d.N,
+                            static_cast<float*>(out.dB), static_cast<float*>(out.dC), d.ld_bc_grad);
+  }
+  if (e != cudaSuccess || (!out.dA && !out.dskip && !out.dbias)) return e;
+  const unsigned blocks = (unsigned)(((long long)d.D * (d.N + 2) + 31) / 32);
+  return launch_behind(scan_sums_kernel, blocks, 1024, 0, stream, P.packed, (const float*)P.partial,
+                       (int)parts, (long long)d.D, d.N, out.dA, out.dskip, out.dbias);
+}
+
+// Blocks of single tokens from which on a block takes kMany tokens (see SlotTable).
+constexpr long long kManyBlocks = 1 << 17;
+constexpr int kMany = 64;
+
+cudaError_t launch_selective_scan_step(const SelectiveDims& d, const SelectiveInputs& in,
+                                       float* state, int n_slots, const int32_t* slots, void* y,
+                                       unsigned* status, cudaStream_t stream) {
+  ScanArgs P = args_of(d, in, Cut{R, false}, nullptr, status);
+  P.y = y;
+  return with_kind(d, [&](auto t, auto n) {
+    using T = decltype(t);
+    constexpr int N = decltype(n)::value;
+    if ((long long)d.rows * P.tiles >= kManyBlocks)
+      return launch_behind(step_kernel<T, N, kMany>, (unsigned)((d.rows + kMany - 1) / kMany) * P.tiles,
+                           kThreads, 0, stream, P, state, n_slots, slots);
+    return launch_behind(step_kernel<T, N, 1>, (unsigned)d.rows * P.tiles, kThreads, 0, stream, P, state,
+                         n_slots, slots);
+  });
+}
+
+}  // namespace sdm

@@ -1,0 +1,97 @@
+// slots.cuh -- the rows of a pool of states that a batch of single tokens steps:
+// which of a block's tokens step their slot.
+//
+// A negative slot is padding, one at or beyond n_slots is out of bounds, and of
+// the tokens that name one slot only the first steps it; what is skipped for the
+// last two reasons is recorded.
+#pragma once
+
+#include "common.cuh"
+
+namespace sdm {
+
+// kGroup tokens from row0 on (n of them valid).  `own[i]` is token i's slot or -1.
+// All threads of the block call it; it ends with a barrier.  A group is looked up
+// in a hash table of its slots, by all earlier slots once; a single token compares
+// its own with them.
+template <int kGroup, int kThreads>
+struct SlotTable {
+  static constexpr int kPlaces = kGroup == 1 ? 1 : 8 * kGroup;
+  int own[kGroup];
+  int key[kPlaces], first[kPlaces], seen[kPlaces];
+
+  static __device__ __forceinline__ int place_of(int slot) {
+    return (int)(((unsigned)slot * 2654435769u >> 16) & (unsigned)(kPlaces - 1));   // golden ratio
+  }
+
+  __device__ __forceinline__ void find(const int32_t* slots, int row0, int n, int n_slots,
+                                       unsigned* status) {
+    static_assert((kPlaces & (kPlaces - 1)) == 0 && kGroup <= kThreads, "");
+    const int tid = threadIdx.x;
+    const int4* s4 = reinterpret_cast<const int4*>(slots);
+    int slot = -1;
+    if (tid < n) {
+      slot = slots ? __ldg(slots + row0 + tid) : row0 + tid;
+      if (slot >= n_slots) {
+        record_status(status, SDM_ERR_DEVICE_BOUNDS);
+        slot = -1;
+      }
+    }
+    if (!slots) {
+      if (tid < kGroup) own[tid] = slot;
+      __syncthreads();
+      return;
+    }
+    if (kGroup == 1) {
+      const int mine = __ldg(slots + row0);
+      bool twice = false;
+      if (mine >= 0) {
+        for (int k = tid; k < row0 >> 2; k += kThreads) {
+          const int4 q = __ldg(s4 + k);
+          twice |= q.x == mine || q.y == mine || q.z == mine || q.w == mine;
+        }
+        if (tid < (row0 & 3)) twice |= __ldg(slots + (row0 & ~3) + tid) == mine;
+      }
+      twice = __syncthreads_or(twice);
+      if (tid == 0) {
+        if (twice && slot >= 0) record_status(status, SDM_ERR_DUPLICATE_SLOT);
+        own[0] = twice ? -1 : slot;
+      }
+      __syncthreads();
+      return;
+    }
+    for (int i = tid; i < kPlaces; i += kThreads) {
+      key[i] = -1;
+      first[i] = kGroup;
+      seen[i] = 0;
+    }
+    __syncthreads();
+    int at = 0;
+    if (slot >= 0) {                       // ends: there are more places than tokens
+      at = place_of(slot);
+      for (int k; (k = atomicCAS(&key[at], -1, slot)) != -1 && k != slot;) at = (at + 1) % kPlaces;
+      atomicMin(&first[at], tid);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int k = tid; k < row0 / 4; k += kThreads) {          // row0 is a multiple of kGroup
+      const int4 q = __ldg(s4 + k);
+      const int e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        int p = place_of(e[j]), there;
+        while ((there = key[p]) != -1 && there != e[j]) p = (p + 1) % kPlaces;
+        if (there != -1) seen[p] = 1;      // (a negative slot finds an empty place)
+      }
+    }
+    __syncthreads();
+    if (slot >= 0 && (seen[at] || first[at] != tid)) {
+      record_status(status, SDM_ERR_DUPLICATE_SLOT);
+      slot = -1;
+    }
+    if (tid < kGroup) own[tid] = slot;
+    __syncthreads();
+  }
+};
+
+}  // namespace sdm

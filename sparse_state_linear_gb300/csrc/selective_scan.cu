@@ -217,20 +217,68 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
   return make_float2(rcp(1.f + ex2(z.x)), rcp(1.f + ex2(z.y)));
 }
 
-// Rows row0 .. row0 + n - 1 of B (of C) to shared memory, every number twice, zeros
-// behind them.
-template <typename T, int N>
-__device__ __forceinline__ void stage_bc(const void* from, long long ld, int group, int row0, int n,
-                                         float2 (*to)[N]) {
-  for (int i = threadIdx.x; i < R * N / 4; i += kThreads) {
-    const int t = i / (N / 4), q = i % (N / 4) * 4;
-    float2 f[2] = {both(0.f), both(0.f)};
-    if (t < n) get4(raw4<T>(from, (size_t)(row0 + t) * ld + (size_t)group * N + q), f);
-    float4* const at = reinterpret_cast<float4*>(&to[t][q]);
-    at[0] = make_float4(f[0].x, f[0].x, f[0].y, f[0].y);
-    at[1] = make_float4(f[1].x, f[1].x, f[1].y, f[1].y);
-  }
+// Inputs are copied to shared memory R rows ahead, every thread what it will itself
+// take from there: its items of the tensors of channels, and of B and C.
+__device__ __forceinline__ void copy_item(void* to, const void* from, bool in, int bytes) {
+  if (!in) return;
+  if (bytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(to)), "l"(from) : "memory");
+  else
+    cp_async16(to, from);
 }
+template <typename T, int N, int kTensors>
+struct RawRows {
+  static constexpr int kBC = (2 * R * N / 4 + kThreads - 1) / kThreads;
+  Raw4<T> rows[kTensors][Lanes<N>::kItems][kThreads];
+  Raw4<T> bc[kBC][kThreads];
+
+  // n rows from row0 on; kB, kC: which of B and C.
+  template <bool kB, bool kC>
+  __device__ __forceinline__ void ask(const ScanArgs& P, const Place<N>& at, bool in,
+                                      const void* const (&from)[kTensors], const long long (&ld)[kTensors],
+                                      int row0, int n) {
+#pragma unroll
+    for (int i = 0; i < Lanes<N>::kItems; ++i) {
+      const int t = at.staged_row(i);
+#pragma unroll
+      for (int k = 0; k < kTensors; ++k)
+        if (from[k])
+          copy_item(&rows[k][i][threadIdx.x],
+                    static_cast<const T*>(from[k]) + (size_t)(row0 + t) * ld[k] + at.staged(), in && t < n,
+                    sizeof(Raw4<T>));
+    }
+#pragma unroll
+    for (int i = 0; i < kBC; ++i) {
+      const int j = i * kThreads + threadIdx.x, t = j % (R * N / 4) / (N / 4), q = j % (N / 4) * 4;
+      const bool c = j >= R * N / 4;
+      const bool wanted = j < 2 * R * N / 4 && t < n && (c ? kC : kB);
+      copy_item(&bc[i][threadIdx.x],
+                static_cast<const T*>(c ? P.C : P.B) + (size_t)(row0 + t) * P.ld_bc + (size_t)at.group * N + q,
+                wanted, sizeof(Raw4<T>));
+    }
+    cp_async_commit();
+  }
+  // B and C to where all threads read them, zeros behind row n; as float2 every number
+  // twice.
+  template <bool kB, bool kC, class Out>
+  __device__ __forceinline__ void spread(int n, Out (*B)[N], Out (*C)[N]) const {
+#pragma unroll
+    for (int i = 0; i < kBC; ++i) {
+      const int j = i * kThreads + threadIdx.x, t = j % (R * N / 4) / (N / 4), q = j % (N / 4) * 4;
+      const bool c = j >= R * N / 4;
+      if (j >= 2 * R * N / 4 || !(c ? kC : kB)) continue;
+      float2 f[2] = {both(0.f), both(0.f)};
+      if (t < n) get4(bc[i][threadIdx.x], f);
+      float4* const to = reinterpret_cast<float4*>(&(c ? C : B)[t][q]);
+      if (std::is_same<Out, float2>::value) {
+        to[0] = make_float4(f[0].x, f[0].x, f[0].y, f[0].y);
+        to[1] = make_float4(f[1].x, f[1].x, f[1].y, f[1].y);
+      } else {
+        to[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+      }
+    }
+  }
+};
 template <int N>
 __device__ __forceinline__ void four_of(const float2 (*from)[N], int t, int nl, float2 (&v)[4]) {
   const float4* const at = reinterpret_cast<const float4*>(&from[t][nl * 4]);
@@ -242,21 +290,34 @@ __device__ __forceinline__ void four_of(const float2 (*from)[N], int t, int nl, 
 }
 __device__ __forceinline__ float2 ex2_pair(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
 
-template <int N>
-struct ForwardSmem {
-  float2 B[R][N], C[R][N];
+// dinner = dy silu(z) of four channels.
+template <typename T>
+__device__ __forceinline__ void dinner_of(const Raw4<T>& dy, const Raw4<T>& z, bool gated, float2 (&d)[2]) {
+  get4(dy, d);
+  if (!gated) return;
+  float2 g[2];
+  get4(z, g);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) d[p] = mul2(d[p], mul2(g[p], sigmoid2(g[p])));
+}
+
+// ------------------------------------------------------------------ summaries
+template <typename T, int N>
+struct SummarySmem {
+  float2 v[2][R][N];                       // B, or C; of two times R rows in turn
   struct {
-    float sp[R][Lanes<N>::kCols], u[R][Lanes<N>::kCols], y[R][Lanes<N>::kCols];
+    float sp[R][Lanes<N>::kCols], u[R][Lanes<N>::kCols];   // (dinner in the place of u)
   } warp[kWarps];
+  RawRows<T, N, 3> raw;
 };
 
-// ------------------------------------------------------------------- forward
-// kSummary: S and the sum of the chunk only.
-template <typename T, int N, bool kSummary>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
+// The state behind a chunk from zeros in front of it, and the sum of delta; with
+// kBack the gradient of the state in front of it from zeros behind it.
+template <typename T, int N, bool kBack>
+__global__ void __launch_bounds__(kThreads, 6) summary_kernel(const ScanArgs P) {
   using Ln = Lanes<N>;
   extern __shared__ __align__(16) char smem[];
-  ForwardSmem<N>& sh = *reinterpret_cast<ForwardSmem<N>*>(smem);
+  SummarySmem<T, N>& sh = *reinterpret_cast<SummarySmem<T, N>*>(smem);
   wait_for_stream();
   if (!offsets_ok(P.packed)) {
     if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
@@ -264,7 +325,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
   }
   Span s;
   if (!span_of(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s)) return;
-  if (kSummary && s.last) return;          // what is behind it nobody needs
+  if (kBack ? s.first : s.last) return;    // nobody needs it
   const Place<N> at(P, blockIdx.x % P.tiles);
   auto& mem = sh.warp[at.warp];
   const Constants K = constants();
@@ -278,74 +339,195 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
     load_states<N>(P.A + state, nA);
 #pragma unroll
     for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
-    if (!kSummary) {
-      const size_t DN = (size_t)P.D * N;
-      if (P.split) load_states<N>(P.carry + s.number * DN + state, h);
-      else if (P.h0) load_states<N>(P.h0 + s.seq * DN + state, h);
-    }
   }
-  float2 bias[2], skip[2], sum[2] = {both(0.f), both(0.f)};
+  float2 bias[2], sum[2] = {both(0.f), both(0.f)};
+  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
+
+  const void* const from[3] = {kBack ? P.dy : P.x, P.dt, kBack ? P.z : nullptr};
+  const long long ld[3] = {kBack ? P.D : P.ld, P.ld, P.ld_z};
+  // (What is left has rows.)
+  const int last = (s.rows - 1) / R * R, step = kBack ? -R : R;
+  int r = kBack ? last : 0;
+  sh.raw.template ask<!kBack, kBack>(P, at, in_s, from, ld, s.row0 + r, min(R, s.rows - r));
+  for (int turn = 0; r >= 0 && r <= last; r += step, turn ^= 1) {
+    const int n = min(R, s.rows - r), next = r + step;
+    cp_async_wait_all();
+    sh.raw.template spread<!kBack, kBack>(n, sh.v[turn], sh.v[turn]);
+#pragma unroll
+    for (int i = 0; i < Ln::kItems; ++i) {
+      const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
+      float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)};
+      if (t < n && in_s) {
+        float2 d[2];
+        get4(sh.raw.rows[1][i][threadIdx.x], d);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float2 unused, e;
+          softplus_pair(K, d[p], bias[p], unused, e, sp[p]);
+          sum[p] = add2(sum[p], sp[p]);
+        }
+        if (kBack) {
+          dinner_of(sh.raw.rows[0][i][threadIdx.x], sh.raw.rows[2][i][threadIdx.x], P.z != nullptr, u);
+        } else {
+          get4(sh.raw.rows[0][i][threadIdx.x], d);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) u[p] = mul2(mul2(sp[p], both(kLn2)), d[p]);
+        }
+      }
+      store_row(&mem.sp[t][q], sp[0], sp[1]);
+      store_row(&mem.u[t][q], u[0], u[1]);
+    }
+    if (next >= 0 && next <= last)
+      sh.raw.template ask<!kBack, kBack>(P, at, in_s, from, ld, s.row0 + next, min(R, s.rows - next));
+    __syncthreads();                       // (v of the turn before is done with)
+#pragma unroll 4
+    for (int j = 0; j < R; ++j) {
+      const int t = kBack ? R - 1 - j : j;
+      float2 sp[2], u[2], v[4];
+      load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
+      load_row(&mem.u[t][at.cl * 4], u[0], u[1]);
+      four_of<N>(sh.v[turn], t, at.nl, v);
+#pragma unroll
+      for (int cp = 0; cp < 2; ++cp)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = cp * 4 + k;
+          const float2 a = ex2_pair(mul2(nA[i], sp[cp]));
+          h[i] = kBack ? mul2(a, fma2(u[cp], v[k], h[i])) : fma2(a, h[i], mul2(u[cp], v[k]));
+        }
+    }
+    __syncwarp();                          // the warp's rows are done with
+  }
+  if (in) store_states<N>(P.carry + (size_t)s.number * P.D * N + state, h);
+  float v[4] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y};
+#pragma unroll
+  for (int o = Ln::CL; o < 32; o *= 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (at.lane < Ln::CL && in_s)
+    store_row(P.sums + (size_t)s.number * P.D + cs, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
+}
+
+// ------------------------------------------------------------------- forward
+// Here a thread holds 16 neighbouring states (of two channels where N = 8), as pairs of
+// states, so that y is summed within it (over 2 or 4 lanes where N is 32 or 64).
+template <int N>
+struct RowLanes {
+  static constexpr int NT = N < 16 ? N : 16, CH = 16 / NT, NL = N / NT;
+};
+
+template <typename T, int N>
+struct ForwardSmem {
+  float B[2][R][N], C[2][R][N];            // of two times R rows in turn
+  struct {
+    float2 in[R][Lanes<N>::kCols];         // delta log2(e), u
+    float y[R][Lanes<N>::kCols];
+  } warp[kWarps];
+  RawRows<T, N, 3> raw;
+};
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
+  using Ln = Lanes<N>;
+  using Rl = RowLanes<N>;
+  extern __shared__ __align__(16) char smem[];
+  ForwardSmem<T, N>& sh = *reinterpret_cast<ForwardSmem<T, N>*>(smem);
+  wait_for_stream();
+  if (!offsets_ok(P.packed)) {
+    if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  Span s;
+  if (!span_of(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s)) return;
+  const Place<N> at(P, blockIdx.x % P.tiles);
+  auto& mem = sh.warp[at.warp];
+  const Constants K = constants();
+  const int nl = at.lane % Rl::NL, col = at.lane / Rl::NL * Rl::CH, cs = at.staged();
+  const bool in = at.c0 + col < at.c_end, in_s = cs < at.c_end;
+  const size_t state = (size_t)(at.c0 + col) * N + nl * Rl::NT, DN = (size_t)P.D * N;
+  auto load16 = [&](const float* p, float2 (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_row(p + 4 * i, v[2 * i], v[2 * i + 1]);
+  };
+  auto store16 = [&](float* p, const float2 (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_row(p + 4 * i, v[2 * i], v[2 * i + 1]);
+  };
+  float2 nA[8], h[8];
+  zero8(nA);
+  zero8(h);
+  if (in) {
+    load16(P.A + state, nA);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
+    if (P.split) load16(P.carry + s.number * DN + state, h);
+    else if (P.h0) load16(P.h0 + s.seq * DN + state, h);
+  }
+  float2 bias[2], skip[2];
   load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
   load_four(P.skip ? P.skip + cs : nullptr, in_s, 0.f, skip);
 
-  for (int r = 0; r < s.rows; r += R) {
+  const void* const from[3] = {P.x, P.dt, P.z};
+  const long long ld[3] = {P.ld, P.ld, P.ld_z};
+  if (s.rows > 0) sh.raw.template ask<true, true>(P, at, in_s, from, ld, s.row0, min(R, s.rows));
+  for (int r = 0, turn = 0; r < s.rows; r += R, turn ^= 1) {
     const int row0 = s.row0 + r, n = min(R, s.rows - r);
-    __syncthreads();                       // the rows before are done with
-    stage_bc<T, N>(P.B, P.ld_bc, at.group, row0, n, sh.B);
-    if (!kSummary) stage_bc<T, N>(P.C, P.ld_bc, at.group, row0, n, sh.C);
+    cp_async_wait_all();
+    sh.raw.template spread<true, true>(n, sh.B[turn], sh.C[turn]);
     Raw4<T> x[Ln::kItems], z[Ln::kItems];
 #pragma unroll
     for (int i = 0; i < Ln::kItems; ++i) {
       const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
       float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)};
       if (t < n && in_s) {
-        x[i] = raw4<T>(P.x, (size_t)(row0 + t) * P.ld + cs);
-        const Raw4<T> dt = raw4<T>(P.dt, (size_t)(row0 + t) * P.ld + cs);
-        if (!kSummary && P.z) z[i] = raw4<T>(P.z, (size_t)(row0 + t) * P.ld_z + cs);
+        x[i] = sh.raw.rows[0][i][threadIdx.x];
+        if (P.z) z[i] = sh.raw.rows[2][i][threadIdx.x];
         float2 f[2], d[2];
         get4(x[i], f);
-        get4(dt, d);
+        get4(sh.raw.rows[1][i][threadIdx.x], d);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           float2 unused, e;
           softplus_pair(K, d[p], bias[p], unused, e, sp[p]);
           u[p] = mul2(mul2(sp[p], both(kLn2)), f[p]);
-          if (kSummary) sum[p] = add2(sum[p], sp[p]);
         }
       }
-      store_row(&mem.sp[t][q], sp[0], sp[1]);
-      store_row(&mem.u[t][q], u[0], u[1]);
+      float4* const to = reinterpret_cast<float4*>(&mem.in[t][q]);
+      to[0] = make_float4(sp[0].x, u[0].x, sp[0].y, u[0].y);
+      to[1] = make_float4(sp[1].x, u[1].x, sp[1].y, u[1].y);
     }
-    __syncthreads();
-    if (!kSummary && P.states && in)
-      store_states<N>(P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * P.D * N + state, h);
-#pragma unroll 2
+    if (r + R < s.rows)
+      sh.raw.template ask<true, true>(P, at, in_s, from, ld, row0 + R, min(R, s.rows - r - R));
+    __syncthreads();                       // (B and C of the turn before are done with)
+    if (P.states && in)
+      store16(P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * DN + state, h);
+#pragma unroll 4
     for (int t = 0; t < R; ++t) {
-      float2 sp[2], u[2], B[4], C[4], y[2];
-      load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
-      load_row(&mem.u[t][at.cl * 4], u[0], u[1]);
-      four_of<N>(sh.B, t, at.nl, B);
-      if (!kSummary) four_of<N>(sh.C, t, at.nl, C);
+      float2 su[Rl::CH], B[Rl::NT / 2], C[Rl::NT / 2];
+      float y[Rl::CH];
+      if (Rl::CH == 2) load_row(&mem.in[t][col].x, su[0], su[Rl::CH - 1]);
+      else su[0] = mem.in[t][col];
 #pragma unroll
-      for (int cp = 0; cp < 2; ++cp) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = cp * 4 + k;
-          h[i] = fma2(ex2_pair(mul2(nA[i], sp[cp])), h[i], mul2(u[cp], B[k]));
-          if (!kSummary) y[cp] = k ? fma2(C[k], h[i], y[cp]) : mul2(C[k], h[i]);
-        }
+      for (int k = 0; k < Rl::NT / 4; ++k) {
+        load_row(&sh.B[turn][t][nl * Rl::NT + 4 * k], B[2 * k], B[2 * k + 1]);
+        load_row(&sh.C[turn][t][nl * Rl::NT + 4 * k], C[2 * k], C[2 * k + 1]);
       }
-      if (kSummary) continue;
-      using Sum = Halving<4, Ln::kNBits, 0>;
-      float v[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
-      Sum::sum(v, at.lane);
-      if (Sum::chosen(at.lane)) {
-        float* const to = &mem.y[t][at.cl * 4 + Sum::index(at.lane)];
-        if (Sum::kLeft == 2) *reinterpret_cast<float2*>(to) = make_float2(v[0], v[1]);
-        else *to = v[0];
+#pragma unroll
+      for (int j = 0; j < Rl::CH; ++j) {
+        const float2 sp = both(su[j].x), u = both(su[j].y);
+        float2 sum = both(0.f);
+#pragma unroll
+        for (int k = 0; k < Rl::NT / 2; ++k) {
+          const int i = j * (Rl::NT / 2) + k;
+          h[i] = fma2(ex2_pair(mul2(nA[i], sp)), h[i], mul2(u, B[k]));
+          sum = k ? fma2(C[k], h[i], sum) : mul2(C[k], h[i]);
+        }
+        y[j] = sum.x + sum.y;
+#pragma unroll
+        for (int m = 1; m < Rl::NL; m *= 2) y[j] += __shfl_xor_sync(0xffffffffu, y[j], m);
+        if (nl == 0) mem.y[t][col + j] = y[j];
       }
     }
-    if (kSummary) continue;
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < Ln::kItems; ++i) {
@@ -362,19 +544,9 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
       }
       store_row(static_cast<T*>(P.y) + (size_t)(row0 + t) * P.D + cs, y[0], y[1]);
     }
+    __syncwarp();                          // the warp's rows are done with
   }
-  if (kSummary) {
-    if (in) store_states<N>(P.carry + (size_t)s.number * P.D * N + state, h);
-    float v[4] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y};
-#pragma unroll
-    for (int o = Ln::CL; o < 32; o *= 2)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (at.lane < Ln::CL && in_s)
-      store_row(P.sums + (size_t)s.number * P.D + cs, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
-  } else if (P.hT && s.last && in) {
-    store_states<N>(P.hT + (size_t)s.seq * P.D * N + state, h);
-  }
+  if (P.hT && s.last && in) store16(P.hT + (size_t)s.seq * DN + state, h);
 }
 
 // The state in front of every chunk from those behind the chunks before it; with
@@ -424,120 +596,27 @@ __global__ void __launch_bounds__(kThreads) fold_kernel(const ScanArgs P, int N,
 }
 
 // ------------------------------------------------------------------ backward
-template <int N>
+template <typename T, int N>
 struct BackwardSmem {
   float2 B[R][N], C[R][N];
   float bc[kWarps][R][2 * N];              // a warp's channels' shares of dB and dC
-  struct {
-    float sp[R][Lanes<N>::kCols], u[R][Lanes<N>::kCols], d[R][Lanes<N>::kCols];
-    float du[R][Lanes<N>::kCols], dl[R][Lanes<N>::kCols], y[R][Lanes<N>::kCols];
+  struct {                                 // u becomes du row by row, d (where gated) inner
+    float sp[R][Lanes<N>::kCols], u[R][Lanes<N>::kCols], d[R][Lanes<N>::kCols], dl[R][Lanes<N>::kCols];
   } warp[kWarps];
+  RawRows<T, N, 4> raw[2];                 // of these and the next R rows
   uint32_t tmem;
 };
-
-// dinner = dy silu(z) of four channels.
-template <typename T>
-__device__ __forceinline__ void dinner_of(const Raw4<T>& dy, const Raw4<T>& z, bool gated, float2 (&d)[2]) {
-  get4(dy, d);
-  if (!gated) return;
-  float2 g[2];
-  get4(z, g);
-#pragma unroll
-  for (int p = 0; p < 2; ++p) d[p] = mul2(d[p], mul2(g[p], sigmoid2(g[p])));
-}
-
-// The gradient of the state in front of a chunk from zeros behind it, and the sum.
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) back_summary_kernel(const ScanArgs P) {
-  using Ln = Lanes<N>;
-  extern __shared__ __align__(16) char smem[];
-  ForwardSmem<N>& sh = *reinterpret_cast<ForwardSmem<N>*>(smem);   // u: dinner
-  wait_for_stream();
-  if (!offsets_ok(P.packed)) {
-    if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
-    return;
-  }
-  Span s;
-  if (!span_of(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s)) return;
-  if (s.first) return;
-  const Place<N> at(P, blockIdx.x % P.tiles);
-  auto& mem = sh.warp[at.warp];
-  const Constants K = constants();
-  const int c = at.mine(), cs = at.staged();
-  const bool in = c < at.c_end, in_s = cs < at.c_end;
-  const size_t state = (size_t)c * N + at.nl * 4;
-  float2 nA[8], r[8];
-  zero8(nA);
-  zero8(r);
-  if (in) {
-    load_states<N>(P.A + state, nA);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
-  }
-  float2 bias[2], sum[2] = {both(0.f), both(0.f)};
-  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
-
-  for (int r0 = (s.rows - 1) / R * R; r0 >= 0; r0 -= R) {
-    const int row0 = s.row0 + r0, n = min(R, s.rows - r0);
-    __syncthreads();
-    stage_bc<T, N>(P.C, P.ld_bc, at.group, row0, n, sh.C);
-#pragma unroll
-    for (int i = 0; i < Ln::kItems; ++i) {
-      const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
-      float2 sp[2] = {both(0.f), both(0.f)}, d[2] = {both(0.f), both(0.f)};
-      if (t < n && in_s) {
-        const Raw4<T> dt = raw4<T>(P.dt, (size_t)(row0 + t) * P.ld + cs);
-        const Raw4<T> dy = raw4<T>(P.dy, (size_t)(row0 + t) * P.D + cs);
-        Raw4<T> z = dy;
-        if (P.z) z = raw4<T>(P.z, (size_t)(row0 + t) * P.ld_z + cs);
-        float2 f[2];
-        get4(dt, f);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          float2 unused, e;
-          softplus_pair(K, f[p], bias[p], unused, e, sp[p]);
-          sum[p] = add2(sum[p], sp[p]);
-        }
-        dinner_of(dy, z, P.z != nullptr, d);
-      }
-      store_row(&mem.sp[t][q], sp[0], sp[1]);
-      store_row(&mem.u[t][q], d[0], d[1]);
-    }
-    __syncthreads();
-#pragma unroll 2
-    for (int t = R - 1; t >= 0; --t) {
-      float2 sp[2], d[2], C[4];
-      load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
-      load_row(&mem.u[t][at.cl * 4], d[0], d[1]);
-      four_of<N>(sh.C, t, at.nl, C);
-#pragma unroll
-      for (int cp = 0; cp < 2; ++cp)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = cp * 4 + k;
-          r[i] = mul2(ex2_pair(mul2(nA[i], sp[cp])), fma2(d[cp], C[k], r[i]));
-        }
-    }
-  }
-  if (in) store_states<N>(P.carry + (size_t)s.number * P.D * N + state, r);
-  float v[4] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y};
-#pragma unroll
-  for (int o = Ln::CL; o < 32; o *= 2)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (at.lane < Ln::CL && in_s)
-    store_row(P.sums + (size_t)s.number * P.D + cs, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
-}
 
 // A block takes a tile of channels and every parts-th chunk, from its last rows to
 // its first, R at a time: forward from the saved state with the state in front of
 // every row parked in tensor memory, then back.
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
+__global__ void __launch_bounds__(kThreads, 2) backward_kernel(const ScanArgs P) {
   using Ln = Lanes<N>;
   extern __shared__ __align__(16) char smem[];
-  BackwardSmem<N>& sh = *reinterpret_cast<BackwardSmem<N>*>(smem);
+  BackwardSmem<T, N>& sh = *reinterpret_cast<BackwardSmem<T, N>*>(smem);
   constexpr uint32_t kTmemCols = R * 16;
+  static_assert(sizeof(BackwardSmem<T, N>) <= 227 * 1024, "shared memory of a block");
   // A block that holds tensor memory must not wait for a kernel in front of it.
   wait_for_stream();
   if (!offsets_ok(P.packed)) {
@@ -567,6 +646,9 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
   load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
   load_four(P.skip ? P.skip + cs : nullptr, in_s, 0.f, skip);
 
+  const void* const from[4] = {P.x, P.dt, P.dy, P.z};
+  const long long ld[4] = {P.ld, P.ld, P.D, P.ld_z};
+  int turn = 0;
   const unsigned parts = gridDim.x / P.tiles, part = blockIdx.x / P.tiles;
   for (unsigned index = part; index < P.indexes; index += parts) {
     Span s;
@@ -577,35 +659,34 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
       if (P.split) load_states<N>(P.carry + s.number * DN + state, r);
       else if (P.h0) load_states<N>(P.h0 + s.seq * DN + state, r);
     }
-    for (int r0 = (s.rows - 1) / R * R; r0 >= 0 && s.rows > 0; r0 -= R) {
+    const int last = s.rows > 0 ? (s.rows - 1) / R * R : -1;
+    if (last >= 0) sh.raw[turn].template ask<true, true>(P, at, in_s, from, ld, s.row0 + last, s.rows - last);
+    for (int r0 = last; r0 >= 0; r0 -= R, turn ^= 1) {
       const int row0 = s.row0 + r0, n = min(R, s.rows - r0);
-      __syncthreads();                     // the rows behind are done with
+      auto& raw = sh.raw[turn];
       float2 h[8];
       zero8(h);
       if (in)
         load_states<N>(P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * DN + state, h);
-      stage_bc<T, N>(P.B, P.ld_bc, at.group, row0, n, sh.B);
-      stage_bc<T, N>(P.C, P.ld_bc, at.group, row0, n, sh.C);
+      cp_async_wait_all();
+      if (r0 > 0) sh.raw[turn ^ 1].template ask<true, true>(P, at, in_s, from, ld, row0 - R, R);
+      __syncthreads();                     // the rows behind are done with
+      raw.template spread<true, true>(n, sh.B, sh.C);
 #pragma unroll
       for (int i = 0; i < Ln::kItems; ++i) {
         const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
         float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)}, d[2] = {both(0.f), both(0.f)};
         if (t < n && in_s) {
-          const Raw4<T> x = raw4<T>(P.x, (size_t)(row0 + t) * P.ld + cs);
-          const Raw4<T> dt = raw4<T>(P.dt, (size_t)(row0 + t) * P.ld + cs);
-          const Raw4<T> dy = raw4<T>(P.dy, (size_t)(row0 + t) * P.D + cs);
-          Raw4<T> z = dy;
-          if (P.z) z = raw4<T>(P.z, (size_t)(row0 + t) * P.ld_z + cs);
           float2 f[2], v[2];
-          get4(x, f);
-          get4(dt, v);
+          get4(raw.rows[0][i][threadIdx.x], f);
+          get4(raw.rows[1][i][threadIdx.x], v);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             float2 unused, e;
             softplus_pair(K, v[p], bias[p], unused, e, sp[p]);
             u[p] = mul2(mul2(sp[p], both(kLn2)), f[p]);
           }
-          dinner_of(dy, z, P.z != nullptr, d);
+          dinner_of(raw.rows[2][i][threadIdx.x], raw.rows[3][i][threadIdx.x], P.z != nullptr, d);
         }
         store_row(&mem.sp[t][q], sp[0], sp[1]);
         store_row(&mem.u[t][q], u[0], u[1]);
@@ -628,9 +709,9 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
           }
       }
       parked();
-#pragma unroll 2
-      for (int t = R - 1; t >= 0; --t) {
-        float2 before[8], sp[2], u[2], d[2], B[4], C[4];
+      // Row t: h is the state behind it, and the state in front of it comes to `before`.
+      auto back = [&](int t, float2 (&before)[8], float2 (&h)[8]) {
+        float2 sp[2], u[2], d[2], B[4], C[4];
         ask16(park + t * 16, before);
         load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
         load_row(&mem.u[t][at.cl * 4], u[0], u[1]);
@@ -654,7 +735,6 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
             y[cp] = k ? fma2(C[k], h[i], y[cp]) : mul2(C[k], h[i]);
             dB[k] = cp ? fma2(g, u[cp], dB[k]) : mul2(g, u[cp]);
             dC[k] = cp ? fma2(d[cp], h[i], dC[k]) : mul2(d[cp], h[i]);
-            h[i] = before[i];
           }
         using Sum = Halving<4, Ln::kNBits, 0>;
         float v[4] = {du[0].x, du[0].y, du[1].x, du[1].y};
@@ -663,13 +743,14 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
         Sum::sum(v, at.lane);
         Sum::sum(w, at.lane);
         Sum::sum(o, at.lane);
+        __syncwarp();                      // row t of u and d has been read
         if (Sum::chosen(at.lane)) {
           const int to = at.cl * 4 + Sum::index(at.lane);
 #pragma unroll
           for (int j = 0; j < Sum::kLeft; ++j) {
-            mem.du[t][to + j] = v[j];
+            mem.u[t][to + j] = v[j];
             mem.dl[t][to + j] = w[j];
-            mem.y[t][to + j] = o[j];
+            if (P.z) mem.d[t][to + j] = o[j];
           }
         }
         using Over = Halving<8, Ln::kCBits, Ln::kNBits>;
@@ -687,6 +768,12 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
             sh.bc[at.warp][t][(to >> 2) * N + at.nl * 4 + (to & 3)] = q[j];
           }
         }
+      };
+      float2 other[8];
+#pragma unroll 1
+      for (int t = R - 1; t >= 0; t -= 2) {
+        back(t, other, h);
+        back(t - 1, h, other);
       }
       __syncthreads();
       for (int i = threadIdx.x; i < n * 2 * N; i += kThreads) {
@@ -701,14 +788,26 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
         const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
         if (t >= n || !in_s) continue;
         const size_t row = row0 + t;
-        float2 x[2], dt[2], d[2], sp[2], du[2], dl[2], y[2], dx[2], ddt[2];
-        get4(raw4<T>(P.x, row * P.ld + cs), x);
-        get4(raw4<T>(P.dt, row * P.ld + cs), dt);
+        float2 x[2], dt[2], d[2], sp[2], du[2], dl[2], dx[2], ddt[2];
+        get4(raw.rows[0][i][threadIdx.x], x);
+        get4(raw.rows[1][i][threadIdx.x], dt);
         load_row(&mem.sp[t][q], sp[0], sp[1]);
-        load_row(&mem.d[t][q], d[0], d[1]);
-        load_row(&mem.du[t][q], du[0], du[1]);
+        load_row(&mem.u[t][q], du[0], du[1]);
         load_row(&mem.dl[t][q], dl[0], dl[1]);
-        load_row(&mem.y[t][q], y[0], y[1]);
+        load_row(&mem.d[t][q], d[0], d[1]);
+        if (P.z) {
+          float2 z[2], dy[2], dz[2];
+          get4(raw.rows[2][i][threadIdx.x], dy);
+          get4(raw.rows[3][i][threadIdx.x], z);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float2 sig = sigmoid2(z[p]), inner = fma2(skip[p], x[p], d[p]);
+            d[p] = mul2(dy[p], mul2(z[p], sig));
+            // silu' = sig (1 + z (1 - sig)).
+            dz[p] = mul2(mul2(dy[p], inner), mul2(sig, fma2(z[p], sub2(both(1.f), sig), both(1.f))));
+          }
+          store_row(static_cast<T*>(P.dz) + row * P.ld_z_grad + cs, dz[0], dz[1]);
+        }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           dx[p] = fma2(du[p], mul2(sp[p], both(kLn2)), mul2(d[p], skip[p]));
@@ -718,18 +817,6 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ScanArgs P) {
         }
         store_row(static_cast<T*>(P.dx) + row * P.ld_grad + cs, dx[0], dx[1]);
         store_row(static_cast<T*>(P.ddt) + row * P.ld_grad + cs, ddt[0], ddt[1]);
-        if (P.z) {
-          float2 z[2], dy[2];
-          get4(raw4<T>(P.z, row * P.ld_z + cs), z);
-          get4(raw4<T>(P.dy, row * P.D + cs), dy);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const float2 sig = sigmoid2(z[p]), inner = fma2(skip[p], x[p], y[p]);
-            // silu' = sig (1 + z (1 - sig)).
-            z[p] = mul2(mul2(dy[p], inner), mul2(sig, fma2(z[p], sub2(both(1.f), sig), both(1.f))));
-          }
-          store_row(static_cast<T*>(P.dz) + row * P.ld_z_grad + cs, z[0], z[1]);
-        }
       }
     }
     if (P.hT && s.first && in) store_states<N>(P.hT + s.seq * DN + state, r);
@@ -882,9 +969,9 @@ struct Cut {
   int L;
   bool split;
 };
-constexpr int kLeastChunk = 64, kMostChunk = 1 << 20;
+constexpr int kLeastChunk = 16, kMostChunk = 1 << 20;
 Cut cut_of(const SelectiveDims& d, bool equal) {
-  const long long tiles = (long long)group_tiles_of(d) * d.groups, fill = 4ll * device_limits().sms;
+  const long long tiles = (long long)group_tiles_of(d) * d.groups, fill = 16ll * device_limits().sms;
   const int longest = equal && d.n_seq > 0 ? d.rows / d.n_seq : d.rows;
   const long long whole = ((long long)longest + R - 1) / R * R;
   long long L = whole;
@@ -1017,11 +1104,11 @@ cudaError_t launch_selective_scan_forward(const SelectiveDims& d, const Selectiv
     const unsigned blocks = P.indexes * P.tiles;
     cudaError_t e = cudaSuccess;
     if (cut.split) {
-      e = launch_with(forward_kernel<T, N, true>, allowed[0], blocks, sizeof(ForwardSmem<N>), stream, P);
+      e = launch_with(summary_kernel<T, N, false>, allowed[0], blocks, sizeof(SummarySmem<T, N>), stream, P);
       if (e == cudaSuccess) e = launch_fold<false>(d, P, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_with(forward_kernel<T, N, false>, allowed[1], blocks, sizeof(ForwardSmem<N>), stream, P);
+    return launch_with(forward_kernel<T, N>, allowed[1], blocks, sizeof(ForwardSmem<T, N>), stream, P);
   });
 }
 
@@ -1057,11 +1144,11 @@ cudaError_t launch_selective_scan_backward(const SelectiveDims& d, const Selecti
     static std::atomic<bool> allowed[2][64];
     cudaError_t e = cudaSuccess;
     if (cut.split) {
-      e = launch_with(back_summary_kernel<T, N>, allowed[0], P.indexes * P.tiles, sizeof(ForwardSmem<N>), stream, P);
+      e = launch_with(summary_kernel<T, N, true>, allowed[0], P.indexes * P.tiles, sizeof(SummarySmem<T, N>), stream, P);
       if (e == cudaSuccess) e = launch_fold<true>(d, P, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_with(backward_kernel<T, N>, allowed[1], parts * P.tiles, sizeof(BackwardSmem<N>), stream, P);
+    return launch_with(backward_kernel<T, N>, allowed[1], parts * P.tiles, sizeof(BackwardSmem<T, N>), stream, P);
   });
   if (e == cudaSuccess && d.rows > 0) {
     const long long want = ((long long)d.rows * d.groups * 2 * d.N + 255) / 256, most = 16ll * device_limits().sms;

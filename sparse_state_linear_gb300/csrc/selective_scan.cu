@@ -29,19 +29,57 @@
 #include "rows.cuh"
 #include "slots.cuh"
 
+#ifndef FILL
+#define FILL 16
+#endif
+#ifndef FILL_E
+#define FILL_E 24
+#endif
+#ifndef SB
+#define SB 8
+#endif
+#ifndef SU
+#define SU 4
+#endif
+#ifndef FB
+#define FB 7
+#endif
+#ifndef FU
+#define FU 4
+#endif
+#ifndef BU
+#define BU 4
+#endif
 namespace sdm {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int R = 16;                      // rows at a time; also between saved states
+constexpr int kSU = SU, kFU = FU, kBU = BU;
+constexpr int kStateRows = 16;             // rows between saved states
 
-// A thread holds four states of four channels, as pairs of channels.  Of a warp's
-// lanes NL neighbours share channels, CL groups of them have channels of their own.
+// Blocks of the forward pass and of the summaries: two warps, eight rows at a time.  A
+// thread holds 16 neighbouring states (all 8 where N = 8) of CH channels, as pairs of
+// states, so that what a row of B and C brings from shared memory serves CH channels
+// and y is summed within a thread (over 2 or 4 lanes where N is 32 or 64).
 template <int N>
-struct Lanes {
-  static constexpr int NL = N / 4, CL = 32 / NL, kCols = CL * 4, kBlockCols = kWarps * kCols;
-  static constexpr int kItems = R * CL / 32;   // of four channels of a row, per lane
+struct Wide {
+  static constexpr int kWarps = 2, kRows = 8, kCols = 1024 / N;   // channels of a warp
+  static constexpr int NT = N < 16 ? N : 16, CH = 32 / NT, NL = N / NT;
+};
+// Blocks of the backward pass: four warps, 16 rows at a time.  A thread holds four
+// states of four channels, as pairs of channels, so that the sums over states and those
+// over channels are both half done within it.  NL neighbouring lanes share channels, CL
+// groups of them have channels of their own.
+template <int N>
+struct Square {
+  static constexpr int kWarps = 4, kRows = 16, kCols = 512 / N;
+  static constexpr int NL = N / 4, CL = 32 / NL;
   static constexpr int kNBits = NL == 2 ? 1 : NL == 4 ? 2 : NL == 8 ? 3 : 4, kCBits = 5 - kNBits;
+};
+constexpr int kBlockStates = 2048;         // a block's states: its channels are 2048 / N
+// How a warp goes through rows of its channels: four channels a lane and step.
+template <class S>
+struct Steps {
+  static constexpr int kThreads = 32 * S::kWarps, QL = S::kCols / 4, kItems = S::kRows * QL / 32;
 };
 
 struct ScanArgs {
@@ -107,22 +145,20 @@ __device__ __forceinline__ bool span_of(const Packed& P, int L, int chunks, int 
   return true;
 }
 
-// What a thread's channels are: those of its states, and the four it stages.
-template <int N>
+// Which channels a block's warps and threads work on.
+template <int N, class S>
 struct Place {
-  int lane, warp, nl, cl, group, c0, c_end;     // c0: the warp's first channel
+  int lane, warp, group, c0, c_end;        // c0: the warp's first channel; c_end: behind the group's last
   __device__ __forceinline__ Place(const ScanArgs& P, int tile) {
     lane = threadIdx.x & 31;
     warp = threadIdx.x >> 5;
-    nl = lane % Lanes<N>::NL;
-    cl = lane / Lanes<N>::NL;
     group = tile / P.group_tiles;
-    c0 = group * P.per + tile % P.group_tiles * Lanes<N>::kBlockCols + warp * Lanes<N>::kCols;
+    c0 = group * P.per + tile % P.group_tiles * (kBlockStates / N) + warp * S::kCols;
     c_end = (group + 1) * P.per;
   }
-  __device__ __forceinline__ int mine() const { return c0 + cl * 4; }
-  __device__ __forceinline__ int staged() const { return c0 + lane % Lanes<N>::CL * 4; }
-  __device__ __forceinline__ int staged_row(int i) const { return lane / Lanes<N>::CL + i * Lanes<N>::NL; }
+  // The four channels and the rows that a thread takes from the inputs.
+  __device__ __forceinline__ int quad() const { return lane % Steps<S>::QL * 4; }
+  __device__ __forceinline__ int row(int i) const { return lane / Steps<S>::QL + i * (32 / Steps<S>::QL); }
 };
 
 // State registers: v[cp * 4 + n] holds state n of channels 2 cp and 2 cp + 1.
@@ -226,32 +262,33 @@ __device__ __forceinline__ void copy_item(void* to, const void* from, bool in, i
   else
     cp_async16(to, from);
 }
-template <typename T, int N, int kTensors>
+template <typename T, int N, class S, int kTensors>
 struct RawRows {
-  static constexpr int kBC = (2 * R * N / 4 + kThreads - 1) / kThreads;
-  Raw4<T> rows[kTensors][Lanes<N>::kItems][kThreads];
+  static constexpr int kThreads = Steps<S>::kThreads, kItems = Steps<S>::kItems, kQuads = S::kRows * N / 4;
+  static constexpr int kBC = (2 * kQuads + kThreads - 1) / kThreads;
+  Raw4<T> rows[kTensors][kItems][kThreads];
   Raw4<T> bc[kBC][kThreads];
 
   // n rows from row0 on; kB, kC: which of B and C.
   template <bool kB, bool kC>
-  __device__ __forceinline__ void ask(const ScanArgs& P, const Place<N>& at, bool in,
+  __device__ __forceinline__ void ask(const ScanArgs& P, const Place<N, S>& at, bool in,
                                       const void* const (&from)[kTensors], const long long (&ld)[kTensors],
                                       int row0, int n) {
 #pragma unroll
-    for (int i = 0; i < Lanes<N>::kItems; ++i) {
-      const int t = at.staged_row(i);
+    for (int i = 0; i < kItems; ++i) {
+      const int t = at.row(i);
 #pragma unroll
       for (int k = 0; k < kTensors; ++k)
         if (from[k])
           copy_item(&rows[k][i][threadIdx.x],
-                    static_cast<const T*>(from[k]) + (size_t)(row0 + t) * ld[k] + at.staged(), in && t < n,
+                    static_cast<const T*>(from[k]) + (size_t)(row0 + t) * ld[k] + at.c0 + at.quad(), in && t < n,
                     sizeof(Raw4<T>));
     }
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
-      const int j = i * kThreads + threadIdx.x, t = j % (R * N / 4) / (N / 4), q = j % (N / 4) * 4;
-      const bool c = j >= R * N / 4;
-      const bool wanted = j < 2 * R * N / 4 && t < n && (c ? kC : kB);
+      const int j = i * kThreads + threadIdx.x, t = j % kQuads / (N / 4), q = j % (N / 4) * 4;
+      const bool c = j >= kQuads;
+      const bool wanted = j < 2 * kQuads && t < n && (c ? kC : kB);
       copy_item(&bc[i][threadIdx.x],
                 static_cast<const T*>(c ? P.C : P.B) + (size_t)(row0 + t) * P.ld_bc + (size_t)at.group * N + q,
                 wanted, sizeof(Raw4<T>));
@@ -264,9 +301,9 @@ struct RawRows {
   __device__ __forceinline__ void spread(int n, Out (*B)[N], Out (*C)[N]) const {
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
-      const int j = i * kThreads + threadIdx.x, t = j % (R * N / 4) / (N / 4), q = j % (N / 4) * 4;
-      const bool c = j >= R * N / 4;
-      if (j >= 2 * R * N / 4 || !(c ? kC : kB)) continue;
+      const int j = i * kThreads + threadIdx.x, t = j % kQuads / (N / 4), q = j % (N / 4) * 4;
+      const bool c = j >= kQuads;
+      if (j >= 2 * kQuads || !(c ? kC : kB)) continue;
       float2 f[2] = {both(0.f), both(0.f)};
       if (t < n) get4(bc[i][threadIdx.x], f);
       float4* const to = reinterpret_cast<float4*>(&(c ? C : B)[t][q]);
@@ -279,15 +316,6 @@ struct RawRows {
     }
   }
 };
-template <int N>
-__device__ __forceinline__ void four_of(const float2 (*from)[N], int t, int nl, float2 (&v)[4]) {
-  const float4* const at = reinterpret_cast<const float4*>(&from[t][nl * 4]);
-  const float4 a = at[0], b = at[1];
-  v[0] = make_float2(a.x, a.y);
-  v[1] = make_float2(a.z, a.w);
-  v[2] = make_float2(b.x, b.y);
-  v[3] = make_float2(b.z, b.w);
-}
 __device__ __forceinline__ float2 ex2_pair(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
 
 // dinner = dy silu(z) of four channels.
@@ -302,20 +330,67 @@ __device__ __forceinline__ void dinner_of(const Raw4<T>& dy, const Raw4<T>& z, b
 }
 
 // ------------------------------------------------------------------ summaries
+// Sixteen or more neighbouring numbers.
+template <int V>
+__device__ __forceinline__ void load_pairs(const float* p, float2 (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) load_row(p + 4 * i, v[2 * i], v[2 * i + 1]);
+}
+// A thread's states from or to [D][N]: NT of each of its CH channels.
+template <int N>
+__device__ __forceinline__ void load_wide(const float* p, float2 (&v)[16]) {
+  using W = Wide<N>;
+#pragma unroll
+  for (int j = 0; j < W::CH; ++j)
+#pragma unroll
+    for (int k = 0; k < W::NT / 4; ++k)
+      load_row(p + j * N + 4 * k, v[j * (W::NT / 2) + 2 * k], v[j * (W::NT / 2) + 2 * k + 1]);
+}
+template <int N>
+__device__ __forceinline__ void store_wide(float* p, const float2 (&v)[16]) {
+  using W = Wide<N>;
+#pragma unroll
+  for (int j = 0; j < W::CH; ++j)
+#pragma unroll
+    for (int k = 0; k < W::NT / 4; ++k)
+      store_row(p + j * N + 4 * k, v[j * (W::NT / 2) + 2 * k], v[j * (W::NT / 2) + 2 * k + 1]);
+}
+template <int N>
+__device__ __forceinline__ void load_rates(const float* p, bool in, float2 (&nA)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) nA[i] = both(0.f);
+  if (in) load_wide<N>(p, nA);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
+}
+// A thread's CH channels of a row of shared memory.
+template <int CH>
+__device__ __forceinline__ void load_channels(const float* p, float (&v)[CH]) {
+  if (CH == 4) {
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    v[0] = w.x, v[1] = w.y, v[CH - 2] = w.z, v[CH - 1] = w.w;
+  } else {
+    const float2 w = *reinterpret_cast<const float2*>(p);
+    v[0] = w.x, v[1] = w.y;
+  }
+}
+
 template <typename T, int N>
 struct SummarySmem {
-  float2 v[2][R][N];                       // B, or C; of two times R rows in turn
+  float v[2][Wide<N>::kRows][N];           // B, or C; of two times so many rows in turn
   struct {
-    float sp[R][Lanes<N>::kCols], u[R][Lanes<N>::kCols];   // (dinner in the place of u)
-  } warp[kWarps];
-  RawRows<T, N, 3> raw;
+    float sp[Wide<N>::kRows][Wide<N>::kCols], u[Wide<N>::kRows][Wide<N>::kCols];   // (dinner in the place of u)
+  } warp[Wide<N>::kWarps];
+  RawRows<T, N, Wide<N>, 3> raw;
 };
 
 // The state behind a chunk from zeros in front of it, and the sum of delta; with
 // kBack the gradient of the state in front of it from zeros behind it.
 template <typename T, int N, bool kBack>
-__global__ void __launch_bounds__(kThreads, 6) summary_kernel(const ScanArgs P) {
-  using Ln = Lanes<N>;
+__global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, SB) summary_kernel(const ScanArgs P) {
+  using W = Wide<N>;
+  using St = Steps<W>;
+  constexpr int R = W::kRows;
   extern __shared__ __align__(16) char smem[];
   SummarySmem<T, N>& sh = *reinterpret_cast<SummarySmem<T, N>*>(smem);
   wait_for_stream();
@@ -326,36 +401,31 @@ __global__ void __launch_bounds__(kThreads, 6) summary_kernel(const ScanArgs P) 
   Span s;
   if (!span_of(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s)) return;
   if (kBack ? s.first : s.last) return;    // nobody needs it
-  const Place<N> at(P, blockIdx.x % P.tiles);
+  const Place<N, W> at(P, blockIdx.x % P.tiles);
   auto& mem = sh.warp[at.warp];
-  const Constants K = constants();
-  const int c = at.mine(), cs = at.staged();
-  const bool in = c < at.c_end, in_s = cs < at.c_end;
-  const size_t state = (size_t)c * N + at.nl * 4;
-  float2 nA[8], h[8];
-  zero8(nA);
-  zero8(h);
-  if (in) {
-    load_states<N>(P.A + state, nA);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
-  }
-  float2 bias[2], sum[2] = {both(0.f), both(0.f)};
-  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
-
+  const int nl = at.lane % W::NL, col = at.lane / W::NL * W::CH, cs = at.c0 + at.quad();
+  const bool in = at.c0 + col < at.c_end, in_s = cs < at.c_end;
+  const size_t state = (size_t)(at.c0 + col) * N + nl * W::NT;
   const void* const from[3] = {kBack ? P.dy : P.x, P.dt, kBack ? P.z : nullptr};
   const long long ld[3] = {kBack ? P.D : P.ld, P.ld, P.ld_z};
   // (What is left has rows.)
   const int last = (s.rows - 1) / R * R, step = kBack ? -R : R;
   int r = kBack ? last : 0;
   sh.raw.template ask<!kBack, kBack>(P, at, in_s, from, ld, s.row0 + r, min(R, s.rows - r));
+  const Constants K = constants();
+  float2 nA[16], h[16];
+  load_rates<N>(P.A + state, in, nA);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) h[i] = both(0.f);
+  float2 bias[2], sum[2] = {both(0.f), both(0.f)};
+  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
   for (int turn = 0; r >= 0 && r <= last; r += step, turn ^= 1) {
     const int n = min(R, s.rows - r), next = r + step;
     cp_async_wait_all();
     sh.raw.template spread<!kBack, kBack>(n, sh.v[turn], sh.v[turn]);
 #pragma unroll
-    for (int i = 0; i < Ln::kItems; ++i) {
-      const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
+    for (int i = 0; i < St::kItems; ++i) {
+      const int t = at.row(i), q = at.quad();
       float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)};
       if (t < n && in_s) {
         float2 d[2];
@@ -380,56 +450,48 @@ __global__ void __launch_bounds__(kThreads, 6) summary_kernel(const ScanArgs P) 
     if (next >= 0 && next <= last)
       sh.raw.template ask<!kBack, kBack>(P, at, in_s, from, ld, s.row0 + next, min(R, s.rows - next));
     __syncthreads();                       // (v of the turn before is done with)
-#pragma unroll 4
+#pragma unroll kSU
     for (int j = 0; j < R; ++j) {
       const int t = kBack ? R - 1 - j : j;
-      float2 sp[2], u[2], v[4];
-      load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
-      load_row(&mem.u[t][at.cl * 4], u[0], u[1]);
-      four_of<N>(sh.v[turn], t, at.nl, v);
+      float sp[W::CH], u[W::CH];
+      float2 v[W::NT / 2];
+      load_channels(&mem.sp[t][col], sp);
+      load_channels(&mem.u[t][col], u);
+      load_pairs(&sh.v[turn][t][nl * W::NT], v);
 #pragma unroll
-      for (int cp = 0; cp < 2; ++cp)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = cp * 4 + k;
-          const float2 a = ex2_pair(mul2(nA[i], sp[cp]));
-          h[i] = kBack ? mul2(a, fma2(u[cp], v[k], h[i])) : fma2(a, h[i], mul2(u[cp], v[k]));
-        }
+      for (int i = 0; i < 16; ++i) {
+        const int ch = i / (W::NT / 2), k = i % (W::NT / 2);
+        const float2 a = ex2_pair(mul2(nA[i], both(sp[ch])));
+        h[i] = kBack ? mul2(a, fma2(both(u[ch]), v[k], h[i])) : fma2(a, h[i], mul2(both(u[ch]), v[k]));
+      }
     }
     __syncwarp();                          // the warp's rows are done with
   }
-  if (in) store_states<N>(P.carry + (size_t)s.number * P.D * N + state, h);
+  if (in) store_wide<N>(P.carry + (size_t)s.number * P.D * N + state, h);
   float v[4] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y};
 #pragma unroll
-  for (int o = Ln::CL; o < 32; o *= 2)
+  for (int o = St::QL; o < 32; o *= 2)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (at.lane < Ln::CL && in_s)
+  if (at.lane < St::QL && in_s)
     store_row(P.sums + (size_t)s.number * P.D + cs, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
 }
 
 // ------------------------------------------------------------------- forward
-// Here a thread holds 16 neighbouring states (of two channels where N = 8), as pairs of
-// states, so that y is summed within it (over 2 or 4 lanes where N is 32 or 64).
-template <int N>
-struct RowLanes {
-  static constexpr int NT = N < 16 ? N : 16, CH = 16 / NT, NL = N / NT;
-};
-
 template <typename T, int N>
 struct ForwardSmem {
-  float B[2][R][N], C[2][R][N];            // of two times R rows in turn
-  struct {
-    float2 in[R][Lanes<N>::kCols];         // delta log2(e), u
-    float y[R][Lanes<N>::kCols];
-  } warp[kWarps];
-  RawRows<T, N, 3> raw;
+  float B[2][Wide<N>::kRows][N], C[2][Wide<N>::kRows][N];   // of two times so many rows in turn
+  struct {                                 // sp becomes y row by row
+    float sp[Wide<N>::kRows][Wide<N>::kCols], u[Wide<N>::kRows][Wide<N>::kCols];
+  } warp[Wide<N>::kWarps];
+  RawRows<T, N, Wide<N>, 3> raw[2];
 };
 
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
-  using Ln = Lanes<N>;
-  using Rl = RowLanes<N>;
+__global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, FB) forward_kernel(const ScanArgs P) {
+  using W = Wide<N>;
+  using St = Steps<W>;
+  constexpr int R = W::kRows;
   extern __shared__ __align__(16) char smem[];
   ForwardSmem<T, N>& sh = *reinterpret_cast<ForwardSmem<T, N>*>(smem);
   wait_for_stream();
@@ -439,52 +501,41 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
   }
   Span s;
   if (!span_of(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s)) return;
-  const Place<N> at(P, blockIdx.x % P.tiles);
+  const Place<N, W> at(P, blockIdx.x % P.tiles);
   auto& mem = sh.warp[at.warp];
-  const Constants K = constants();
-  const int nl = at.lane % Rl::NL, col = at.lane / Rl::NL * Rl::CH, cs = at.staged();
+  const int nl = at.lane % W::NL, col = at.lane / W::NL * W::CH, cs = at.c0 + at.quad();
   const bool in = at.c0 + col < at.c_end, in_s = cs < at.c_end;
-  const size_t state = (size_t)(at.c0 + col) * N + nl * Rl::NT, DN = (size_t)P.D * N;
-  auto load16 = [&](const float* p, float2 (&v)[8]) {
+  const size_t state = (size_t)(at.c0 + col) * N + nl * W::NT, DN = (size_t)P.D * N;
+  const void* const from[3] = {P.x, P.dt, P.z};
+  const long long ld[3] = {P.ld, P.ld, P.ld_z};
+  if (s.rows > 0) sh.raw[0].template ask<true, true>(P, at, in_s, from, ld, s.row0, min(R, s.rows));
+  const Constants K = constants();
+  float2 nA[16], h[16];
+  load_rates<N>(P.A + state, in, nA);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_row(p + 4 * i, v[2 * i], v[2 * i + 1]);
-  };
-  auto store16 = [&](float* p, const float2 (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) store_row(p + 4 * i, v[2 * i], v[2 * i + 1]);
-  };
-  float2 nA[8], h[8];
-  zero8(nA);
-  zero8(h);
+  for (int i = 0; i < 16; ++i) h[i] = both(0.f);
   if (in) {
-    load16(P.A + state, nA);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
-    if (P.split) load16(P.carry + s.number * DN + state, h);
-    else if (P.h0) load16(P.h0 + s.seq * DN + state, h);
+    if (P.split) load_wide<N>(P.carry + s.number * DN + state, h);
+    else if (P.h0) load_wide<N>(P.h0 + s.seq * DN + state, h);
   }
   float2 bias[2], skip[2];
   load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
   load_four(P.skip ? P.skip + cs : nullptr, in_s, 0.f, skip);
-
-  const void* const from[3] = {P.x, P.dt, P.z};
-  const long long ld[3] = {P.ld, P.ld, P.ld_z};
-  if (s.rows > 0) sh.raw.template ask<true, true>(P, at, in_s, from, ld, s.row0, min(R, s.rows));
   for (int r = 0, turn = 0; r < s.rows; r += R, turn ^= 1) {
     const int row0 = s.row0 + r, n = min(R, s.rows - r);
+    auto& raw = sh.raw[turn];
     cp_async_wait_all();
-    sh.raw.template spread<true, true>(n, sh.B[turn], sh.C[turn]);
-    Raw4<T> x[Ln::kItems], z[Ln::kItems];
+    if (r + R < s.rows)
+      sh.raw[turn ^ 1].template ask<true, true>(P, at, in_s, from, ld, row0 + R, min(R, s.rows - r - R));
+    raw.template spread<true, true>(n, sh.B[turn], sh.C[turn]);
 #pragma unroll
-    for (int i = 0; i < Ln::kItems; ++i) {
-      const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
+    for (int i = 0; i < St::kItems; ++i) {
+      const int t = at.row(i), q = at.quad();
       float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)};
       if (t < n && in_s) {
-        x[i] = sh.raw.rows[0][i][threadIdx.x];
-        if (P.z) z[i] = sh.raw.rows[2][i][threadIdx.x];
         float2 f[2], d[2];
-        get4(x[i], f);
-        get4(sh.raw.rows[1][i][threadIdx.x], d);
+        get4(raw.rows[0][i][threadIdx.x], f);
+        get4(raw.rows[1][i][threadIdx.x], d);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           float2 unused, e;
@@ -492,51 +543,48 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
           u[p] = mul2(mul2(sp[p], both(kLn2)), f[p]);
         }
       }
-      float4* const to = reinterpret_cast<float4*>(&mem.in[t][q]);
-      to[0] = make_float4(sp[0].x, u[0].x, sp[0].y, u[0].y);
-      to[1] = make_float4(sp[1].x, u[1].x, sp[1].y, u[1].y);
+      store_row(&mem.sp[t][q], sp[0], sp[1]);
+      store_row(&mem.u[t][q], u[0], u[1]);
     }
-    if (r + R < s.rows)
-      sh.raw.template ask<true, true>(P, at, in_s, from, ld, row0 + R, min(R, s.rows - r - R));
     __syncthreads();                       // (B and C of the turn before are done with)
-    if (P.states && in)
-      store16(P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * DN + state, h);
-#pragma unroll 4
+    if (P.states && in && (row0 - s.begin) % kStateRows == 0)
+      store_wide<N>(P.states + ((size_t)(s.begin / kStateRows + s.seq) + (row0 - s.begin) / kStateRows) * DN + state, h);
+#pragma unroll kFU
     for (int t = 0; t < R; ++t) {
-      float2 su[Rl::CH], B[Rl::NT / 2], C[Rl::NT / 2];
-      float y[Rl::CH];
-      if (Rl::CH == 2) load_row(&mem.in[t][col].x, su[0], su[Rl::CH - 1]);
-      else su[0] = mem.in[t][col];
+      float sp[W::CH], u[W::CH], y[W::CH];
+      float2 B[W::NT / 2], C[W::NT / 2];
+      load_channels(&mem.sp[t][col], sp);
+      load_channels(&mem.u[t][col], u);
+      load_pairs(&sh.B[turn][t][nl * W::NT], B);
+      load_pairs(&sh.C[turn][t][nl * W::NT], C);
 #pragma unroll
-      for (int k = 0; k < Rl::NT / 4; ++k) {
-        load_row(&sh.B[turn][t][nl * Rl::NT + 4 * k], B[2 * k], B[2 * k + 1]);
-        load_row(&sh.C[turn][t][nl * Rl::NT + 4 * k], C[2 * k], C[2 * k + 1]);
-      }
-#pragma unroll
-      for (int j = 0; j < Rl::CH; ++j) {
-        const float2 sp = both(su[j].x), u = both(su[j].y);
+      for (int j = 0; j < W::CH; ++j) {
         float2 sum = both(0.f);
 #pragma unroll
-        for (int k = 0; k < Rl::NT / 2; ++k) {
-          const int i = j * (Rl::NT / 2) + k;
-          h[i] = fma2(ex2_pair(mul2(nA[i], sp)), h[i], mul2(u, B[k]));
+        for (int k = 0; k < W::NT / 2; ++k) {
+          const int i = j * (W::NT / 2) + k;
+          h[i] = fma2(ex2_pair(mul2(nA[i], both(sp[j]))), h[i], mul2(both(u[j]), B[k]));
           sum = k ? fma2(C[k], h[i], sum) : mul2(C[k], h[i]);
         }
         y[j] = sum.x + sum.y;
 #pragma unroll
-        for (int m = 1; m < Rl::NL; m *= 2) y[j] += __shfl_xor_sync(0xffffffffu, y[j], m);
-        if (nl == 0) mem.y[t][col + j] = y[j];
+        for (int m = 1; m < W::NL; m *= 2) y[j] += __shfl_xor_sync(0xffffffffu, y[j], m);
+      }
+      if (W::NL > 1) __syncwarp();         // row t of sp has been read
+      if (nl == 0) {
+        if (W::CH == 4) store_row(&mem.sp[t][col], make_float2(y[0], y[1]), make_float2(y[W::CH - 2], y[W::CH - 1]));
+        else *reinterpret_cast<float2*>(&mem.sp[t][col]) = make_float2(y[0], y[1]);
       }
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < Ln::kItems; ++i) {
-      const int t = at.staged_row(i);
+    for (int i = 0; i < St::kItems; ++i) {
+      const int t = at.row(i);
       if (t >= n || !in_s) continue;
       float2 y[2], f[2], g[2];
-      load_row(&mem.y[t][at.lane % Ln::CL * 4], y[0], y[1]);
-      get4(x[i], f);
-      if (P.z) get4(z[i], g);
+      load_row(&mem.sp[t][at.quad()], y[0], y[1]);
+      get4(raw.rows[0][i][threadIdx.x], f);
+      if (P.z) get4(raw.rows[2][i][threadIdx.x], g);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         y[p] = fma2(skip[p], f[p], y[p]);
@@ -546,17 +594,18 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ScanArgs P) {
     }
     __syncwarp();                          // the warp's rows are done with
   }
-  if (P.hT && s.last && in) store16(P.hT + (size_t)s.seq * DN + state, h);
+  if (P.hT && s.last && in) store_wide<N>(P.hT + (size_t)s.seq * DN + state, h);
 }
 
 // The state in front of every chunk from those behind the chunks before it; with
 // kBack the gradient of the state behind every chunk.  Four states a thread.
+constexpr int kFoldThreads = 128;
 template <bool kBack>
-__global__ void __launch_bounds__(kThreads) fold_kernel(const ScanArgs P, int N, int blocks) {
+__global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs P, int N, int blocks) {
   wait_for_stream();
   if (!offsets_ok(P.packed)) return;
   const int seq = blockIdx.x / blocks;
-  const long long i = (long long)(blockIdx.x % blocks) * kThreads + threadIdx.x;
+  const long long i = (long long)(blockIdx.x % blocks) * kFoldThreads + threadIdx.x;
   const size_t DN = (size_t)P.D * N;
   if (i * 4 >= (long long)DN) return;
   const int begin = P.packed.begin(seq), end = P.packed.begin(seq + 1), c = (int)(i * 4 / N);
@@ -596,14 +645,61 @@ __global__ void __launch_bounds__(kThreads) fold_kernel(const ScanArgs P, int N,
 }
 
 // ------------------------------------------------------------------ backward
+// (Held as float2 through the loops of the backward pass pairs are taken apart and put
+// together again at every turn: 76 moves per row of 32 channels.)
+__device__ __forceinline__ Pair ex2_pair(Pair v) {
+  Pair r;
+  asm("{\n .reg .f32 a, b;\n mov.b64 {a, b}, %1;\n ex2.approx.ftz.f32 a, a;\n"
+      " ex2.approx.ftz.f32 b, b;\n mov.b64 %0, {a, b};\n}\n"
+      : "=l"(r)
+      : "l"(v));
+  return r;
+}
+__device__ __forceinline__ void load_pairs(const void* p, Pair& a, Pair& b) {
+  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+  a = v.x;
+  b = v.y;
+}
+// As park16 and ask16, the latter with its wait.
+__device__ __forceinline__ void park_pairs(uint32_t taddr, const Pair (&v)[8]) {
+  asm volatile(
+      "{\n .reg .b32 a<16>;\n"
+      " mov.b64 {a0, a1}, %1;\n mov.b64 {a2, a3}, %2;\n mov.b64 {a4, a5}, %3;\n mov.b64 {a6, a7}, %4;\n"
+      " mov.b64 {a8, a9}, %5;\n mov.b64 {a10, a11}, %6;\n mov.b64 {a12, a13}, %7;\n mov.b64 {a14, a15}, %8;\n"
+      " tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{a0, a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15};\n}\n" ::"r"(taddr),
+      "l"(v[0]), "l"(v[1]), "l"(v[2]), "l"(v[3]), "l"(v[4]), "l"(v[5]), "l"(v[6]), "l"(v[7])
+      : "memory");
+}
+__device__ __forceinline__ void fetch_pairs(uint32_t taddr, Pair (&v)[8]) {
+  asm volatile(
+      "{\n .reg .b32 a<16>;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{a0, a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15}, [%8];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      " mov.b64 %0, {a0, a1};\n mov.b64 %1, {a2, a3};\n mov.b64 %2, {a4, a5};\n mov.b64 %3, {a6, a7};\n"
+      " mov.b64 %4, {a8, a9};\n mov.b64 %5, {a10, a11};\n mov.b64 %6, {a12, a13};\n mov.b64 %7, {a14, a15};\n}\n"
+      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void pairs_of(const float2 (&v)[8], Pair (&p)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = bits2(v[i]);
+}
+__device__ __forceinline__ void floats_of(const Pair (&p)[8], float2 (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = float2_of(p[i]);
+}
+
 template <typename T, int N>
 struct BackwardSmem {
-  float2 B[R][N], C[R][N];
-  float bc[kWarps][R][2 * N];              // a warp's channels' shares of dB and dC
+  float2 B[kStateRows][N], C[kStateRows][N];
+  float bc[Square<N>::kWarps][kStateRows][2 * N];              // a warp's channels' shares of dB and dC
   struct {                                 // u becomes du row by row, d (where gated) inner
-    float sp[R][Lanes<N>::kCols], u[R][Lanes<N>::kCols], d[R][Lanes<N>::kCols], dl[R][Lanes<N>::kCols];
-  } warp[kWarps];
-  RawRows<T, N, 4> raw[2];                 // of these and the next R rows
+    float sp[kStateRows][Square<N>::kCols], u[kStateRows][Square<N>::kCols], d[kStateRows][Square<N>::kCols], dl[kStateRows][Square<N>::kCols];
+  } warp[Square<N>::kWarps];
+  RawRows<T, N, Square<N>, 4> raw[2];                 // of these and the next R rows
   uint32_t tmem;
 };
 
@@ -611,8 +707,11 @@ struct BackwardSmem {
 // its first, R at a time: forward from the saved state with the state in front of
 // every row parked in tensor memory, then back.
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads, 2) backward_kernel(const ScanArgs P) {
-  using Ln = Lanes<N>;
+__global__ void __launch_bounds__(Steps<Square<N>>::kThreads, 2) backward_kernel(const ScanArgs P) {
+  using Sq = Square<N>;
+  using St = Steps<Sq>;
+  constexpr int R = Sq::kRows;
+  static_assert(R == kStateRows, "");
   extern __shared__ __align__(16) char smem[];
   BackwardSmem<T, N>& sh = *reinterpret_cast<BackwardSmem<T, N>*>(smem);
   constexpr uint32_t kTmemCols = R * 16;
@@ -623,7 +722,8 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const ScanArgs P)
     if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     return;
   }
-  const Place<N> at(P, blockIdx.x % P.tiles);
+  const Place<N, Sq> at(P, blockIdx.x % P.tiles);
+  const int nl = at.lane % Sq::NL, cl = at.lane / Sq::NL;
   if (at.warp == 0) tc::tmem_alloc(&sh.tmem, kTmemCols);
   tc::fence_before_sync();
   __syncthreads();
@@ -631,17 +731,16 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const ScanArgs P)
   const uint32_t park = sh.tmem + ((uint32_t)at.warp << 21);
   auto& mem = sh.warp[at.warp];
   const Constants K = constants();
-  const int c = at.mine(), cs = at.staged();
+  const int c = at.c0 + cl * 4, cs = at.c0 + at.quad();
   const bool in = c < at.c_end, in_s = cs < at.c_end;
-  const size_t state = (size_t)c * N + at.nl * 4, DN = (size_t)P.D * N;
-  float2 nA[8], dA[8];
-  zero8(nA);
-  zero8(dA);
-  if (in) {
-    load_states<N>(P.A + state, nA);
+  const size_t state = (size_t)c * N + nl * 4, DN = (size_t)P.D * N;
+  float2 some[8];                          // states on their way to or from memory
+  Pair nA[8], dA[8];
+  zero8(some);
+  pairs_of(some, dA);
+  if (in) load_states<N>(P.A + state, some);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
-  }
+  for (int i = 0; i < 8; ++i) nA[i] = bits2(make_float2(-some[i].x, -some[i].y));
   float2 bias[2], skip[2], dskip[2] = {both(0.f), both(0.f)}, dbias[2] = {both(0.f), both(0.f)};
   load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
   load_four(P.skip ? P.skip + cs : nullptr, in_s, 0.f, skip);
@@ -653,28 +752,28 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const ScanArgs P)
   for (unsigned index = part; index < P.indexes; index += parts) {
     Span s;
     if (!span_of(P.packed, P.L, P.chunks, (int)index, s)) continue;
-    float2 r[8];
-    zero8(r);
+    Pair r[8];
+    zero8(some);
     if (in) {
-      if (P.split) load_states<N>(P.carry + s.number * DN + state, r);
-      else if (P.h0) load_states<N>(P.h0 + s.seq * DN + state, r);
+      if (P.split) load_states<N>(P.carry + s.number * DN + state, some);
+      else if (P.h0) load_states<N>(P.h0 + s.seq * DN + state, some);
     }
+    pairs_of(some, r);
     const int last = s.rows > 0 ? (s.rows - 1) / R * R : -1;
     if (last >= 0) sh.raw[turn].template ask<true, true>(P, at, in_s, from, ld, s.row0 + last, s.rows - last);
     for (int r0 = last; r0 >= 0; r0 -= R, turn ^= 1) {
       const int row0 = s.row0 + r0, n = min(R, s.rows - r0);
       auto& raw = sh.raw[turn];
-      float2 h[8];
-      zero8(h);
+      zero8(some);
       if (in)
-        load_states<N>(P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * DN + state, h);
+        load_states<N>(P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * DN + state, some);
       cp_async_wait_all();
       if (r0 > 0) sh.raw[turn ^ 1].template ask<true, true>(P, at, in_s, from, ld, row0 - R, R);
       __syncthreads();                     // the rows behind are done with
       raw.template spread<true, true>(n, sh.B, sh.C);
 #pragma unroll
-      for (int i = 0; i < Ln::kItems; ++i) {
-        const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
+      for (int i = 0; i < St::kItems; ++i) {
+        const int t = at.row(i), q = at.quad();
         float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)}, d[2] = {both(0.f), both(0.f)};
         if (t < n && in_s) {
           float2 f[2], v[2];
@@ -693,13 +792,16 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const ScanArgs P)
         store_row(&mem.d[t][q], d[0], d[1]);
       }
       __syncthreads();
-#pragma unroll 2
+      Pair h[8], other[8];
+      pairs_of(some, h);
+#pragma unroll kBU
       for (int t = 0; t < R; ++t) {
-        float2 sp[2], u[2], B[4];
-        park16(park + t * 16, h);
-        load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
-        load_row(&mem.u[t][at.cl * 4], u[0], u[1]);
-        four_of<N>(sh.B, t, at.nl, B);
+        Pair sp[2], u[2], B[4];
+        park_pairs(park + t * 16, h);
+        load_pairs(&mem.sp[t][cl * 4], sp[0], sp[1]);
+        load_pairs(&mem.u[t][cl * 4], u[0], u[1]);
+        load_pairs(&sh.B[t][nl * 4], B[0], B[1]);
+        load_pairs(&sh.B[t][nl * 4 + 2], B[2], B[3]);
 #pragma unroll
         for (int cp = 0; cp < 2; ++cp)
 #pragma unroll
@@ -709,26 +811,30 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const ScanArgs P)
           }
       }
       parked();
+      // A row's sums: over a thread's states of four channels (du, what delta gets by the
+      // decay, inner), and over its channels of four states (dB, dC).
+      struct Sums {
+        float du[4], dl[4], y[4], bc[8];
+      };
       // Row t: h is the state behind it, and the state in front of it comes to `before`.
-      auto back = [&](int t, float2 (&before)[8], float2 (&h)[8]) {
-        float2 sp[2], u[2], d[2], B[4], C[4];
-        ask16(park + t * 16, before);
-        load_row(&mem.sp[t][at.cl * 4], sp[0], sp[1]);
-        load_row(&mem.u[t][at.cl * 4], u[0], u[1]);
-        load_row(&mem.d[t][at.cl * 4], d[0], d[1]);
-        four_of<N>(sh.B, t, at.nl, B);
-        four_of<N>(sh.C, t, at.nl, C);
-        asked();
-        here(before);
-        float2 du[2], dl[2], y[2], dB[4], dC[4];
+      auto back = [&](int t, Pair (&before)[8], const Pair (&h)[8], Sums& out) {
+        Pair sp[2], u[2], d[2], B[4], C[4], du[2], dl[2], y[2], dB[4], dC[4];
+        load_pairs(&mem.sp[t][cl * 4], sp[0], sp[1]);
+        load_pairs(&mem.u[t][cl * 4], u[0], u[1]);
+        load_pairs(&mem.d[t][cl * 4], d[0], d[1]);
+        load_pairs(&sh.B[t][nl * 4], B[0], B[1]);
+        load_pairs(&sh.B[t][nl * 4 + 2], B[2], B[3]);
+        load_pairs(&sh.C[t][nl * 4], C[0], C[1]);
+        load_pairs(&sh.C[t][nl * 4 + 2], C[2], C[3]);
+        fetch_pairs(park + t * 16, before);
 #pragma unroll
         for (int cp = 0; cp < 2; ++cp)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int i = cp * 4 + k;
-            const float2 g = fma2(d[cp], C[k], r[i]);
+            const Pair g = fma2(d[cp], C[k], r[i]);
             r[i] = mul2(g, ex2_pair(mul2(nA[i], sp[cp])));
-            const float2 p = mul2(r[i], before[i]);
+            const Pair p = mul2(r[i], before[i]);
             dA[i] = fma2(p, sp[cp], dA[i]);
             du[cp] = k ? fma2(g, B[k], du[cp]) : mul2(g, B[k]);
             dl[cp] = k ? fma2(p, nA[i], dl[cp]) : mul2(p, nA[i]);
@@ -736,56 +842,69 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const ScanArgs P)
             dB[k] = cp ? fma2(g, u[cp], dB[k]) : mul2(g, u[cp]);
             dC[k] = cp ? fma2(d[cp], h[i], dC[k]) : mul2(d[cp], h[i]);
           }
-        using Sum = Halving<4, Ln::kNBits, 0>;
-        float v[4] = {du[0].x, du[0].y, du[1].x, du[1].y};
-        float w[4] = {dl[0].x, dl[0].y, dl[1].x, dl[1].y};
-        float o[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
-        Sum::sum(v, at.lane);
-        Sum::sum(w, at.lane);
-        Sum::sum(o, at.lane);
-        __syncwarp();                      // row t of u and d has been read
-        if (Sum::chosen(at.lane)) {
-          const int to = at.cl * 4 + Sum::index(at.lane);
-#pragma unroll
-          for (int j = 0; j < Sum::kLeft; ++j) {
-            mem.u[t][to + j] = v[j];
-            mem.dl[t][to + j] = w[j];
-            if (P.z) mem.d[t][to + j] = o[j];
-          }
-        }
-        using Over = Halving<8, Ln::kCBits, Ln::kNBits>;
-        float q[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          q[k] = dB[k].x + dB[k].y;
-          q[4 + k] = dC[k].x + dC[k].y;
+          const float2 b = float2_of(dB[k]), c = float2_of(dC[k]);
+          out.bc[k] = b.x + b.y;
+          out.bc[4 + k] = c.x + c.y;
+          const float2 e = float2_of(du[k / 2]), f = float2_of(dl[k / 2]), g = float2_of(y[k / 2]);
+          out.du[k] = k % 2 ? e.y : e.x;
+          out.dl[k] = k % 2 ? f.y : f.x;
+          out.y[k] = k % 2 ? g.y : g.x;
         }
-        Over::sum(q, at.lane);
+      };
+      // The sums over the lanes, one row later: between their steps there is the next row's
+      // arithmetic.
+      auto finish = [&](int t, Sums& v) {
+        using Sum = Halving<4, Sq::kNBits, 0>;
+        using Over = Halving<8, Sq::kCBits, Sq::kNBits>;
+        Over::sum(v.bc, at.lane);
+        Sum::sum(v.du, at.lane);
+        Sum::sum(v.dl, at.lane);
+        Sum::sum(v.y, at.lane);
+        if (Sum::chosen(at.lane)) {        // (all lanes have read row t of u and d)
+          const int to = cl * 4 + Sum::index(at.lane);
+#pragma unroll
+          for (int j = 0; j < Sum::kLeft; ++j) {
+            mem.u[t][to + j] = v.du[j];
+            mem.dl[t][to + j] = v.dl[j];
+            if (P.z) mem.d[t][to + j] = v.y[j];
+          }
+        }
         if (Over::chosen(at.lane)) {
 #pragma unroll
           for (int j = 0; j < Over::kLeft; ++j) {
             const int to = Over::index(at.lane) + j;
-            sh.bc[at.warp][t][(to >> 2) * N + at.nl * 4 + (to & 3)] = q[j];
+            sh.bc[at.warp][t][(to >> 2) * N + nl * 4 + (to & 3)] = v.bc[j];
           }
         }
       };
-      float2 other[8];
+      Sums even, odd;
+      back(R - 1, other, h, odd);
 #pragma unroll 1
-      for (int t = R - 1; t >= 0; t -= 2) {
-        back(t, other, h);
-        back(t - 1, h, other);
+      for (int t = R - 2; t > 0; t -= 2) {
+        __syncwarp();                      // row t + 1 has been read
+        back(t, h, other, even);
+        finish(t + 1, odd);
+        __syncwarp();
+        back(t - 1, other, h, odd);
+        finish(t, even);
       }
+      back(0, h, other, even);
+      __syncwarp();
+      finish(1, odd);
+      finish(0, even);
       __syncthreads();
-      for (int i = threadIdx.x; i < n * 2 * N; i += kThreads) {
+      for (int i = threadIdx.x; i < n * 2 * N; i += St::kThreads) {
         const int t = i / (2 * N), k = i % (2 * N);
         float v = sh.bc[0][t][k];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v += sh.bc[w][t][k];
+        for (int w = 1; w < Sq::kWarps; ++w) v += sh.bc[w][t][k];
         P.partial_bc[((size_t)(row0 + t) * P.tiles + blockIdx.x % P.tiles) * (2 * N) + k] = v;
       }
 #pragma unroll
-      for (int i = 0; i < Ln::kItems; ++i) {
-        const int t = at.staged_row(i), q = at.lane % Ln::CL * 4;
+      for (int i = 0; i < St::kItems; ++i) {
+        const int t = at.row(i), q = at.quad();
         if (t >= n || !in_s) continue;
         const size_t row = row0 + t;
         float2 x[2], dt[2], d[2], sp[2], du[2], dl[2], dx[2], ddt[2];
@@ -819,19 +938,21 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const ScanArgs P)
         store_row(static_cast<T*>(P.ddt) + row * P.ld_grad + cs, ddt[0], ddt[1]);
       }
     }
-    if (P.hT && s.first && in) store_states<N>(P.hT + s.seq * DN + state, r);
+    floats_of(r, some);
+    if (P.hT && s.first && in) store_states<N>(P.hT + s.seq * DN + state, some);
   }
   // The chunks' sums.  dA = -sum delta p, and sp is delta log2(e).
   float* const to = P.partial + (size_t)part * P.D * (N + 2);
+  floats_of(dA, some);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dA[i] = mul2(dA[i], both(-kLn2));
-  if (in) store_states<N>(to + state, dA);
+  for (int i = 0; i < 8; ++i) some[i] = mul2(some[i], both(-kLn2));
+  if (in) store_states<N>(to + state, some);
   float v[8] = {dskip[0].x, dskip[0].y, dskip[1].x, dskip[1].y, dbias[0].x, dbias[0].y, dbias[1].x, dbias[1].y};
 #pragma unroll
-  for (int o = Ln::CL; o < 32; o *= 2)
+  for (int o = Sq::CL; o < 32; o *= 2)
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (at.lane < Ln::CL && in_s) {
+  if (at.lane < Sq::CL && in_s) {
     store_row(to + DN + cs, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
     store_row(to + DN + P.D + cs, make_float2(v[4], v[5]), make_float2(v[6], v[7]));
   }
@@ -890,21 +1011,22 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ----------------------------------------------------------------- one token
-// A block takes kGroup tokens by a tile of channels, as the chunks do.
+// A block takes kGroup tokens by a tile of channels, with the lanes of the backward pass.
 template <typename T, int N, int kGroup>
-__global__ void __launch_bounds__(kThreads) step_kernel(const ScanArgs P, float* pool, int n_slots,
+__global__ void __launch_bounds__(Steps<Square<N>>::kThreads) step_kernel(const ScanArgs P, float* pool, int n_slots,
                                                         const int32_t* slots) {
-  using Ln = Lanes<N>;
+  using Sq = Square<N>;
   wait_for_stream();
-  __shared__ SlotTable<kGroup, kThreads> table;
+  __shared__ SlotTable<kGroup, Steps<Sq>::kThreads> table;
   const int row0 = (int)(blockIdx.x / P.tiles) * kGroup, rows = min(kGroup, P.packed.rows - row0);
-  const Place<N> at(P, blockIdx.x % P.tiles);
+  const Place<N, Sq> at(P, blockIdx.x % P.tiles);
+  const int nl = at.lane % Sq::NL;
   table.find(slots, row0, rows, n_slots, P.status);
   const Constants K = constants();
-  const int c = at.mine();
+  const int c = at.c0 + at.lane / Sq::NL * 4;
   const unsigned lanes = __ballot_sync(0xffffffffu, c < at.c_end);   // whole groups of NL lanes
   if (c >= at.c_end) return;
-  const size_t state = (size_t)c * N + at.nl * 4;
+  const size_t state = (size_t)c * N + nl * 4;
   float2 nA[8], bias[2], skip[2];
   load_states<N>(P.A + state, nA);
 #pragma unroll
@@ -920,8 +1042,8 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const ScanArgs P, float*
     load_states<N>(p, h);
     get4(raw4<T>(P.x, row * P.ld + c), x);
     get4(raw4<T>(P.dt, row * P.ld + c), dt);
-    get4(raw4<T>(P.B, row * P.ld_bc + (size_t)at.group * N + at.nl * 4), B);
-    get4(raw4<T>(P.C, row * P.ld_bc + (size_t)at.group * N + at.nl * 4), C);
+    get4(raw4<T>(P.B, row * P.ld_bc + (size_t)at.group * N + nl * 4), B);
+    get4(raw4<T>(P.C, row * P.ld_bc + (size_t)at.group * N + nl * 4), C);
     if (P.z) get4(raw4<T>(P.z, row * P.ld_z + c), z);
     const float b[4] = {B[0].x, B[0].y, B[1].x, B[1].y}, o[4] = {C[0].x, C[0].y, C[1].x, C[1].y};
 #pragma unroll
@@ -940,10 +1062,10 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const ScanArgs P, float*
     store_states<N>(p, h);
     float v[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
 #pragma unroll
-    for (int m = 1; m < Ln::NL; m *= 2)
+    for (int m = 1; m < Sq::NL; m *= 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(lanes, v[i], m);
-    if (at.nl != 0) continue;
+    if (nl != 0) continue;
     y[0] = make_float2(v[0], v[1]);
     y[1] = make_float2(v[2], v[3]);
 #pragma unroll
@@ -958,12 +1080,12 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const ScanArgs P, float*
 // ---------------------------------------------------------------- host side
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-int tile_cols(int N) { return kWarps * 4 * 32 / (N / 4); }
+int tile_cols(int N) { return kBlockStates / N; }
 int group_tiles_of(const SelectiveDims& d) {
   return (d.D / d.groups + tile_cols(d.N) - 1) / tile_cols(d.N);
 }
 
-// How the sequences are cut: rows of a chunk, a multiple of R, and whether any
+// How the sequences are cut: rows of a chunk, a multiple of kStateRows, and whether any
 // sequence has more than one.
 struct Cut {
   int L;
@@ -971,17 +1093,15 @@ struct Cut {
 };
 constexpr int kLeastChunk = 16, kMostChunk = 1 << 20;
 Cut cut_of(const SelectiveDims& d, bool equal) {
-  const long long tiles = (long long)group_tiles_of(d) * d.groups, fill = 16ll * device_limits().sms;
+  const long long tiles = (long long)group_tiles_of(d) * d.groups;
+  const long long slots = (long long)(equal ? FILL_E : FILL) * device_limits().sms / tiles;
   const int longest = equal && d.n_seq > 0 ? d.rows / d.n_seq : d.rows;
-  const long long whole = ((long long)longest + R - 1) / R * R;
-  long long L = whole;
-  if (!equal || d.n_seq * tiles < fill) {
-    L = (long long)d.rows * tiles / fill / R * R;
-    if (L < kLeastChunk) L = kLeastChunk;
-    if (L > whole) L = whole;
-  }
+  long long chunks = equal && d.n_seq > 0 ? slots / d.n_seq : slots;   // of `longest` rows
+  if (chunks < 1) chunks = 1;
+  long long L = (longest + chunks - 1) / chunks;
+  L = (L + kStateRows - 1) / kStateRows * kStateRows;
   if (L > kMostChunk) L = kMostChunk;
-  if (L < R) L = R;
+  if (L < kLeastChunk) L = kLeastChunk;
   return Cut{(int)L, longest > L};
 }
 size_t numbers_of(const SelectiveDims& d, int L) { return (size_t)chunk_numbers(d.rows, d.n_seq, L); }
@@ -1045,10 +1165,10 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool>* done) {
   return f;
 }
 template <class K>
-cudaError_t launch_with(K kernel, std::atomic<bool>* allowed, unsigned blocks, size_t smem,
+cudaError_t launch_with(K kernel, std::atomic<bool>* allowed, unsigned blocks, int threads, size_t smem,
                         cudaStream_t stream, const ScanArgs& P) {
   const cudaError_t e = allow_smem(kernel, (int)smem, allowed);
-  return e != cudaSuccess ? e : launch_behind(kernel, blocks, kThreads, smem, stream, P);
+  return e != cudaSuccess ? e : launch_behind(kernel, blocks, threads, smem, stream, P);
 }
 
 template <class F>
@@ -1065,8 +1185,8 @@ cudaError_t with_kind(const SelectiveDims& d, F f) {
 
 template <bool kBack>
 cudaError_t launch_fold(const SelectiveDims& d, const ScanArgs& P, cudaStream_t stream) {
-  const int blocks = (int)(((long long)d.D * d.N / 4 + kThreads - 1) / kThreads);
-  return launch_behind(fold_kernel<kBack>, (unsigned)blocks * d.n_seq, kThreads, 0, stream, P, d.N, blocks);
+  const int blocks = (int)(((long long)d.D * d.N / 4 + kFoldThreads - 1) / kFoldThreads);
+  return launch_behind(fold_kernel<kBack>, (unsigned)blocks * d.n_seq, kFoldThreads, 0, stream, P, d.N, blocks);
 }
 
 }  // namespace
@@ -1085,7 +1205,7 @@ size_t selective_scan_backward_workspace_bytes(const SelectiveDims& d) {
 }
 
 size_t selective_scan_states_bytes(const SelectiveDims& d) {
-  return numbers_of(d, R) * d.D * d.N * sizeof(float);
+  return numbers_of(d, kStateRows) * d.D * d.N * sizeof(float);
 }
 
 cudaError_t launch_selective_scan_forward(const SelectiveDims& d, const SelectiveInputs& in,
@@ -1104,11 +1224,11 @@ cudaError_t launch_selective_scan_forward(const SelectiveDims& d, const Selectiv
     const unsigned blocks = P.indexes * P.tiles;
     cudaError_t e = cudaSuccess;
     if (cut.split) {
-      e = launch_with(summary_kernel<T, N, false>, allowed[0], blocks, sizeof(SummarySmem<T, N>), stream, P);
+      e = launch_with(summary_kernel<T, N, false>, allowed[0], blocks, Steps<Wide<N>>::kThreads, sizeof(SummarySmem<T, N>), stream, P);
       if (e == cudaSuccess) e = launch_fold<false>(d, P, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_with(forward_kernel<T, N>, allowed[1], blocks, sizeof(ForwardSmem<T, N>), stream, P);
+    return launch_with(forward_kernel<T, N>, allowed[1], blocks, Steps<Wide<N>>::kThreads, sizeof(ForwardSmem<T, N>), stream, P);
   });
 }
 
@@ -1144,11 +1264,11 @@ cudaError_t launch_selective_scan_backward(const SelectiveDims& d, const Selecti
     static std::atomic<bool> allowed[2][64];
     cudaError_t e = cudaSuccess;
     if (cut.split) {
-      e = launch_with(summary_kernel<T, N, true>, allowed[0], P.indexes * P.tiles, sizeof(SummarySmem<T, N>), stream, P);
+      e = launch_with(summary_kernel<T, N, true>, allowed[0], P.indexes * P.tiles, Steps<Wide<N>>::kThreads, sizeof(SummarySmem<T, N>), stream, P);
       if (e == cudaSuccess) e = launch_fold<true>(d, P, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_with(backward_kernel<T, N>, allowed[1], parts * P.tiles, sizeof(BackwardSmem<T, N>), stream, P);
+    return launch_with(backward_kernel<T, N>, allowed[1], parts * P.tiles, Steps<Square<N>>::kThreads, sizeof(BackwardSmem<T, N>), stream, P);
   });
   if (e == cudaSuccess && d.rows > 0) {
     const long long want = ((long long)d.rows * d.groups * 2 * d.N + 255) / 256, most = 16ll * device_limits().sms;
@@ -1172,15 +1292,15 @@ constexpr int kMany = 64;
 cudaError_t launch_selective_scan_step(const SelectiveDims& d, const SelectiveInputs& in,
                                        float* state, int n_slots, const int32_t* slots, void* y,
                                        unsigned* status, cudaStream_t stream) {
-  ScanArgs P = args_of(d, in, Cut{R, false}, nullptr, status);
+  ScanArgs P = args_of(d, in, Cut{kStateRows, false}, nullptr, status);
   P.y = y;
   return with_kind(d, [&](auto t, auto n) {
     using T = decltype(t);
     constexpr int N = decltype(n)::value;
     if ((long long)d.rows * P.tiles >= kManyBlocks)
       return launch_behind(step_kernel<T, N, kMany>, (unsigned)((d.rows + kMany - 1) / kMany) * P.tiles,
-                           kThreads, 0, stream, P, state, n_slots, slots);
-    return launch_behind(step_kernel<T, N, 1>, (unsigned)d.rows * P.tiles, kThreads, 0, stream, P, state,
+                           Steps<Square<N>>::kThreads, 0, stream, P, state, n_slots, slots);
+    return launch_behind(step_kernel<T, N, 1>, (unsigned)d.rows * P.tiles, Steps<Square<N>>::kThreads, 0, stream, P, state,
                          n_slots, slots);
   });
 }

@@ -42,7 +42,7 @@ struct SlotTable {
       __syncthreads();
       return;
     }
-    if (kGroup == 1) {
+    if constexpr (kGroup == 1) {
       const int mine = __ldg(slots + row0);
       bool twice = false;
       if (mine >= 0) {
@@ -58,39 +58,39 @@ struct SlotTable {
         own[0] = twice ? -1 : slot;
       }
       __syncthreads();
-      return;
-    }
-    for (int i = tid; i < kPlaces; i += kThreads) {
-      key[i] = -1;
-      first[i] = kGroup;
-      seen[i] = 0;
-    }
-    __syncthreads();
-    int at = 0;
-    if (slot >= 0) {                       // ends: there are more places than tokens
-      at = place_of(slot);
-      for (int k; (k = atomicCAS(&key[at], -1, slot)) != -1 && k != slot;) at = (at + 1) % kPlaces;
-      atomicMin(&first[at], tid);
-    }
-    __syncthreads();
-#pragma unroll 4
-    for (int k = tid; k < row0 / 4; k += kThreads) {          // row0 is a multiple of kGroup
-      const int4 q = __ldg(s4 + k);
-      const int e[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        int p = place_of(e[j]), there;
-        while ((there = key[p]) != -1 && there != e[j]) p = (p + 1) % kPlaces;
-        if (there != -1) seen[p] = 1;      // (a negative slot finds an empty place)
+    } else {
+      for (int i = tid; i < kPlaces; i += kThreads) {
+        key[i] = -1;
+        first[i] = kGroup;
+        seen[i] = 0;
       }
+      __syncthreads();
+      int at = 0;
+      if (slot >= 0) {                       // ends: there are more places than tokens
+        at = place_of(slot);
+        for (int k; (k = atomicCAS(&key[at], -1, slot)) != -1 && k != slot;) at = (at + 1) % kPlaces;
+        atomicMin(&first[at], tid);
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int k = tid; k < row0 / 4; k += kThreads) {          // row0 is a multiple of kGroup
+        const int4 q = __ldg(s4 + k);
+        const int e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          int p = place_of(e[j]), there;
+          while ((there = key[p]) != -1 && there != e[j]) p = (p + 1) % kPlaces;
+          if (there != -1) seen[p] = 1;      // (a negative slot finds an empty place)
+        }
+      }
+      __syncthreads();
+      if (slot >= 0 && (seen[at] || first[at] != tid)) {
+        record_status(status, SDM_ERR_DUPLICATE_SLOT);
+        slot = -1;
+      }
+      if (tid < kGroup) own[tid] = slot;
+      __syncthreads();
     }
-    __syncthreads();
-    if (slot >= 0 && (seen[at] || first[at] != tid)) {
-      record_status(status, SDM_ERR_DUPLICATE_SLOT);
-      slot = -1;
-    }
-    if (tid < kGroup) own[tid] = slot;
-    __syncthreads();
   }
 };
 

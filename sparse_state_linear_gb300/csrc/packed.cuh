@@ -42,6 +42,7 @@ __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
   asm("sub.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
   return float2_of(r);
 }
+__device__ __forceinline__ float2 ex2_pair(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
 // The same on pairs that stay in one 64-bit register.
 using Pair = uint64_t;
 __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
@@ -52,6 +53,27 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 __device__ __forceinline__ Pair mul2(Pair a, Pair b) {
   Pair r;
   asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair ex2_pair(Pair v) {
+  Pair r;
+  asm("{\n .reg .f32 a, b;\n mov.b64 {a, b}, %1;\n ex2.approx.ftz.f32 a, a;\n"
+      " ex2.approx.ftz.f32 b, b;\n mov.b64 %0, {a, b};\n}\n"
+      : "=l"(r)
+      : "l"(v));
+  return r;
+}
+__device__ __forceinline__ Pair rcp_pair(Pair v) {
+  Pair r;
+  asm("{\n .reg .f32 a, b;\n mov.b64 {a, b}, %1;\n rcp.approx.ftz.f32 a, a;\n"
+      " rcp.approx.ftz.f32 b, b;\n mov.b64 %0, {a, b};\n}\n"
+      : "=l"(r)
+      : "l"(v));
   return r;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }

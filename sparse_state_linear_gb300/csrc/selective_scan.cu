@@ -29,6 +29,9 @@
 #include "rows.cuh"
 #include "slots.cuh"
 
+#ifndef LC
+#define LC 16
+#endif
 #ifndef FILL
 #define FILL 16
 #endif
@@ -316,7 +319,6 @@ struct RawRows {
     }
   }
 };
-__device__ __forceinline__ float2 ex2_pair(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
 
 // dinner = dy silu(z) of four channels.
 template <typename T>
@@ -647,14 +649,6 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs P, in
 // ------------------------------------------------------------------ backward
 // (Held as float2 through the loops of the backward pass pairs are taken apart and put
 // together again at every turn: 76 moves per row of 32 channels.)
-__device__ __forceinline__ Pair ex2_pair(Pair v) {
-  Pair r;
-  asm("{\n .reg .f32 a, b;\n mov.b64 {a, b}, %1;\n ex2.approx.ftz.f32 a, a;\n"
-      " ex2.approx.ftz.f32 b, b;\n mov.b64 %0, {a, b};\n}\n"
-      : "=l"(r)
-      : "l"(v));
-  return r;
-}
 __device__ __forceinline__ void load_pairs(const void* p, Pair& a, Pair& b) {
   const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
   a = v.x;
@@ -1033,47 +1027,64 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads) step_kernel(const 
   for (int i = 0; i < 8; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
   load_four(P.bias ? P.bias + c : nullptr, true, 0.f, bias);
   load_four(P.skip ? P.skip + c : nullptr, true, 0.f, skip);
-  for (int j = 0; j < rows; ++j) {
-    const int slot = table.own[j];
-    if (slot < 0) continue;
-    const size_t row = row0 + j;
-    float* const p = pool + (size_t)slot * P.D * N + state;
-    float2 h[8], x[2], dt[2], z[2], B[2], C[2], y[2];
-    load_states<N>(p, h);
-    get4(raw4<T>(P.x, row * P.ld + c), x);
-    get4(raw4<T>(P.dt, row * P.ld + c), dt);
-    get4(raw4<T>(P.B, row * P.ld_bc + (size_t)at.group * N + nl * 4), B);
-    get4(raw4<T>(P.C, row * P.ld_bc + (size_t)at.group * N + nl * 4), C);
-    if (P.z) get4(raw4<T>(P.z, row * P.ld_z + c), z);
-    const float b[4] = {B[0].x, B[0].y, B[1].x, B[1].y}, o[4] = {C[0].x, C[0].y, C[1].x, C[1].y};
+  constexpr int kAhead = kGroup == 1 ? 1 : 2;                // tokens at a time
+  for (int j0 = 0; j0 < rows; j0 += kAhead) {
+    float2 h[kAhead][8];
+    float* at_pool[kAhead];
+    Raw4<T> raw_x[kAhead], raw_dt[kAhead], raw_z[kAhead], raw_B[kAhead], raw_C[kAhead];
 #pragma unroll
-    for (int cp = 0; cp < 2; ++cp) {
-      float2 unused, e, sp;
-      softplus_pair(K, dt[cp], bias[cp], unused, e, sp);
-      const float2 u = mul2(mul2(sp, both(kLn2)), x[cp]);
-      y[cp] = both(0.f);
+    for (int j = 0; j < kAhead; ++j) {
+      const int slot = j0 + j < rows ? table.own[j0 + j] : -1;
+      at_pool[j] = slot < 0 ? nullptr : pool + (size_t)slot * P.D * N + state;
+      if (slot < 0) continue;
+      const size_t row = row0 + j0 + j;
+      load_states<N>(at_pool[j], h[j]);
+      raw_x[j] = raw4<T>(P.x, row * P.ld + c);
+      raw_dt[j] = raw4<T>(P.dt, row * P.ld + c);
+      raw_B[j] = raw4<T>(P.B, row * P.ld_bc + (size_t)at.group * N + nl * 4);
+      raw_C[j] = raw4<T>(P.C, row * P.ld_bc + (size_t)at.group * N + nl * 4);
+      if (P.z) raw_z[j] = raw4<T>(P.z, row * P.ld_z + c);
+    }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = cp * 4 + k;
-        h[i] = fma2(ex2_pair(mul2(nA[i], sp)), h[i], mul2(u, both(b[k])));
-        y[cp] = fma2(both(o[k]), h[i], y[cp]);
+    for (int j = 0; j < kAhead; ++j) {
+      if (!at_pool[j]) continue;           // (the whole block has the same tokens)
+      float2 x[2], dt[2], z[2], B[2], C[2], y[2];
+      get4(raw_x[j], x);
+      get4(raw_dt[j], dt);
+      get4(raw_B[j], B);
+      get4(raw_C[j], C);
+      if (P.z) get4(raw_z[j], z);
+      const float b[4] = {B[0].x, B[0].y, B[1].x, B[1].y}, o[4] = {C[0].x, C[0].y, C[1].x, C[1].y};
+#pragma unroll
+      for (int cp = 0; cp < 2; ++cp) {
+        float2 unused, e, sp;
+        softplus_pair(K, dt[cp], bias[cp], unused, e, sp);
+        const float2 u = mul2(mul2(sp, both(kLn2)), x[cp]);
+        y[cp] = both(0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = cp * 4 + k;
+          h[j][i] = fma2(ex2_pair(mul2(nA[i], sp)), h[j][i], mul2(u, both(b[k])));
+          y[cp] = fma2(both(o[k]), h[j][i], y[cp]);
+        }
+      }
+      store_states<N>(at_pool[j], h[j]);
+      float v[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
+#pragma unroll
+      for (int m = 1; m < Sq::NL; m *= 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(lanes, v[i], m);
+      if (nl == 0) {
+        y[0] = make_float2(v[0], v[1]);
+        y[1] = make_float2(v[2], v[3]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          y[q] = fma2(skip[q], x[q], y[q]);
+          if (P.z) y[q] = mul2(y[q], mul2(z[q], sigmoid2(z[q])));
+        }
+        store_row(static_cast<T*>(P.y) + (size_t)(row0 + j0 + j) * P.D + c, y[0], y[1]);
       }
     }
-    store_states<N>(p, h);
-    float v[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
-#pragma unroll
-    for (int m = 1; m < Sq::NL; m *= 2)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(lanes, v[i], m);
-    if (nl != 0) continue;
-    y[0] = make_float2(v[0], v[1]);
-    y[1] = make_float2(v[2], v[3]);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      y[q] = fma2(skip[q], x[q], y[q]);
-      if (P.z) y[q] = mul2(y[q], mul2(z[q], sigmoid2(z[q])));
-    }
-    store_row(static_cast<T*>(P.y) + row * P.D + c, y[0], y[1]);
   }
 }
 
@@ -1091,7 +1102,7 @@ struct Cut {
   int L;
   bool split;
 };
-constexpr int kLeastChunk = 16, kMostChunk = 1 << 20;
+constexpr int kLeastChunk = LC, kMostChunk = 1 << 20;
 Cut cut_of(const SelectiveDims& d, bool equal) {
   const long long tiles = (long long)group_tiles_of(d) * d.groups;
   const long long slots = (long long)(equal ? FILL_E : FILL) * device_limits().sms / tiles;
@@ -1285,10 +1296,6 @@ cudaError_t launch_selective_scan_backward(const SelectiveDims& d, const Selecti
                        (int)parts, (long long)d.D, d.N, out.dA, out.dskip, out.dbias);
 }
 
-// Blocks of single tokens from which on a block takes kMany tokens (see SlotTable).
-constexpr long long kManyBlocks = 1 << 17;
-constexpr int kMany = 64;
-
 cudaError_t launch_selective_scan_step(const SelectiveDims& d, const SelectiveInputs& in,
                                        float* state, int n_slots, const int32_t* slots, void* y,
                                        unsigned* status, cudaStream_t stream) {
@@ -1297,11 +1304,11 @@ cudaError_t launch_selective_scan_step(const SelectiveDims& d, const SelectiveIn
   return with_kind(d, [&](auto t, auto n) {
     using T = decltype(t);
     constexpr int N = decltype(n)::value;
-    if ((long long)d.rows * P.tiles >= kManyBlocks)
-      return launch_behind(step_kernel<T, N, kMany>, (unsigned)((d.rows + kMany - 1) / kMany) * P.tiles,
+    return with_group(d.rows, (long long)d.rows * P.tiles, 16384, [&](auto group) {
+      constexpr int G = decltype(group)::value;
+      return launch_behind(step_kernel<T, N, G>, (unsigned)(((long long)d.rows + G - 1) / G * P.tiles),
                            Steps<Square<N>>::kThreads, 0, stream, P, state, n_slots, slots);
-    return launch_behind(step_kernel<T, N, 1>, (unsigned)d.rows * P.tiles, Steps<Square<N>>::kThreads, 0, stream, P, state,
-                         n_slots, slots);
+    });
   });
 }
 

@@ -23,6 +23,11 @@
 namespace sdm {
 namespace {
 
+// Blocks a multiprocessor of the forward and the backward pass, and rows whose loads are
+// under way together.  Measured at 32768 x 2048 bf16, us: forward with 3, 4, 5, 6 blocks
+// 51, 48, 49, 61; backward with 3 blocks 95, with 2 and 8 rows 97, with 4 the registers do
+// not suffice (207).  At 10007 x 1000 float32 backward with 2 blocks 29, 3 37.
+constexpr int kPerSm = 4, kBackPerSm = 3, kBackPerSmF32 = 2;
 constexpr int kThreads = 128, kWarps = kThreads / 32, kWarpCols = 128;
 
 struct ConvArgs {
@@ -50,18 +55,18 @@ struct Raw;
 template <>
 struct Raw<__nv_bfloat16> {
   uint2 w;
-  __device__ __forceinline__ void get(float2 (&f)[2]) const {
-    f[0] = make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
-    f[1] = make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  __device__ __forceinline__ void get(Pair (&f)[2]) const {
+    f[0] = bits2(make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u)));
+    f[1] = bits2(make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)));
   }
   __device__ __forceinline__ void zero() { w = make_uint2(0u, 0u); }
 };
 template <>
 struct Raw<float> {
   float4 w;
-  __device__ __forceinline__ void get(float2 (&f)[2]) const {
-    f[0] = make_float2(w.x, w.y);
-    f[1] = make_float2(w.z, w.w);
+  __device__ __forceinline__ void get(Pair (&f)[2]) const {
+    f[0] = bits2(make_float2(w.x, w.y));
+    f[1] = bits2(make_float2(w.z, w.w));
   }
   __device__ __forceinline__ void zero() { w = make_float4(0.f, 0.f, 0.f, 0.f); }
 };
@@ -74,33 +79,54 @@ __device__ __forceinline__ void put_raw(T* p, Raw<T> v) {
   *reinterpret_cast<Raw<T>*>(p) = v;
 }
 
-// Taps of four channels: w[j] of [D][K] as pairs of channels.
+template <typename T>
+__device__ __forceinline__ void put(T* p, const Pair (&f)[2]) {
+  store_row(p, float2_of(f[0]), float2_of(f[1]));
+}
+
+// Taps of four channels: w[j] of [D][K] as pairs of channels; and constants of the
+// activation, made out of the compiler's sight (see Constants).
 template <int K>
 struct Taps {
-  float2 w[K][2], bias[2];
-  __device__ __forceinline__ void load(const float* at, const float* b, int c, bool in) {
+  Pair w[K][2], bias[2], minus_log2e, one;
+  __device__ __forceinline__ void load(const float* at, const float* b, int c) {
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        w[j][p] = both(0.f);
-        if (in)
-          w[j][p] = make_float2(__ldg(at + (size_t)(c + 2 * p) * K + j),
-                                __ldg(at + (size_t)(c + 2 * p + 1) * K + j));
-      }
-    bias[0] = bias[1] = both(0.f);
-    if (b && in) {
+      for (int p = 0; p < 2; ++p)
+        w[j][p] = bits2(make_float2(__ldg(at + (size_t)(c + 2 * p) * K + j),
+                                    __ldg(at + (size_t)(c + 2 * p + 1) * K + j)));
+    bias[0] = bias[1] = 0;
+    if (b) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(b + c));
-      bias[0] = make_float2(v.x, v.y);
-      bias[1] = make_float2(v.z, v.w);
+      bias[0] = bits2(make_float2(v.x, v.y));
+      bias[1] = bits2(make_float2(v.z, v.w));
     }
+    minus_log2e = bits2(hidden(-kLog2e));
+    one = bits2(hidden(1.f));
+  }
+  // 1 / (1 + exp(-v)); where exp overflows it is 0.
+  __device__ __forceinline__ Pair sigmoid(Pair v) const {
+    return rcp_pair(add2(one, ex2_pair(mul2(v, minus_log2e))));
+  }
+  // bias + sum w[j] row[j], of one pair of channels.
+  template <class Rows>
+  __device__ __forceinline__ Pair pre(const Rows& rows, Pair now, int p) const {
+    Pair v = bias[p];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) v = fma2(w[j][p], rows[j][p], v);
+    return fma2(w[K - 1][p], now, v);
   }
 };
-
-// 1 / (1 + exp(-v)); where exp overflows it is 0.
-__device__ __forceinline__ float2 sigmoid2(float2 v) {
-  const float2 z = mul2(v, both(-kLog2e));
-  return make_float2(rcp(1.f + ex2(z.x)), rcp(1.f + ex2(z.y)));
+// A new row behind the others, the first one leaves.
+template <int M>
+__device__ __forceinline__ void shift(Pair (&rows)[M][2], const Pair (&now)[2]) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+#pragma unroll
+    for (int j = 0; j + 1 < M; ++j) rows[j][p] = rows[j + 1][p];
+    rows[M - 1][p] = now[p];
+  }
 }
 
 // The first s in [0, n_seq] with begin(s) >= row (a whole warp calls it), or
@@ -123,7 +149,7 @@ __device__ __forceinline__ int first_from(const Packed& P, int row) {
 // that its first row lies in, which therefore alone reads the sequence's start
 // and may overwrite it with the final rows (xT = x0).
 template <typename T, int K, bool kSilu>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const ConvArgs P) {
+__global__ void __launch_bounds__(kThreads, kPerSm) forward_kernel(const ConvArgs P) {
   wait_for_stream();
   if (!offsets_ok(P.packed)) {
     if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
@@ -131,8 +157,9 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ConvArgs P) {
   }
   const int lane = threadIdx.x & 31, run = blockIdx.x / P.col_tiles * kWarps + (threadIdx.x >> 5);
   if (run >= P.runs) return;
-  const int c = (blockIdx.x % P.col_tiles * 32 + lane) * 4, D = P.D;
-  const bool in = c < D;
+  const int D = P.D, col = (blockIdx.x % P.col_tiles * 32 + lane) * 4;
+  const bool in = col < D;
+  const int c = min(col, D - 4);           // (lanes without channels go along with the last)
   const int r0 = run * P.run, r1 = min(r0 + P.run, P.packed.rows);
   const bool last_run = run == P.runs - 1;
   const T* const x = static_cast<const T*>(P.x) + c;
@@ -140,37 +167,42 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ConvArgs P) {
   T* const y = static_cast<T*>(P.y) + c;
   T* const xT = static_cast<T*>(P.xT) + c;
   Taps<K> taps;
-  taps.load(P.w, P.bias, c, in);
+  taps.load(P.w, P.bias, c);
 
-  Raw<T> window[K - 1];                    // the rows before the next, oldest first
+  Pair window[K - 1][2];                   // the rows before the next, oldest first
+  auto row = [&](int t, const Raw<T>& raw) {
+    Pair now[2], out[2];
+    raw.get(now);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      out[p] = taps.pre(window, now[p], p);
+      if (kSilu) out[p] = mul2(out[p], taps.sigmoid(out[p]));
+    }
+    if (in) put(y + (size_t)t * D, out);
+    shift(window, now);
+  };
+  // Batches of rows, the next one's loads on their way during one's arithmetic.
   auto rows = [&](int a, int e) {
-    constexpr int kBatch = 32 / (int)sizeof(Raw<T>) * 2;      // 8 rows of bf16, 4 of float32
+    constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;
+    Raw<T> next[kBatch];
+    auto ask = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (t + i < e) next[i] = raw_at(x + (size_t)(t + i) * P.ld);
+    };
+    ask(a);
     for (int t = a; t < e; t += kBatch) {
       Raw<T> now[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (in && t + i < e) now[i] = raw_at(x + (size_t)(t + i) * P.ld);
+      for (int i = 0; i < kBatch; ++i) now[i] = next[i];
+      ask(t + kBatch);
+      if (t + kBatch <= e) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (t + i >= e) break;
-        float2 pre[2] = {taps.bias[0], taps.bias[1]}, f[2];
+        for (int i = 0; i < kBatch; ++i) row(t + i, now[i]);
+      } else {
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) {
-          window[j].get(f);
-          pre[0] = fma2(taps.w[j][0], f[0], pre[0]);
-          pre[1] = fma2(taps.w[j][1], f[1], pre[1]);
-        }
-        now[i].get(f);
-        pre[0] = fma2(taps.w[K - 1][0], f[0], pre[0]);
-        pre[1] = fma2(taps.w[K - 1][1], f[1], pre[1]);
-        if (kSilu) {
-          pre[0] = mul2(pre[0], sigmoid2(pre[0]));
-          pre[1] = mul2(pre[1], sigmoid2(pre[1]));
-        }
-        if (in) store_row(y + (size_t)(t + i) * D, pre[0], pre[1]);
-#pragma unroll
-        for (int j = 0; j + 1 < K - 1; ++j) window[j] = window[j + 1];
-        window[K - 2] = now[i];
+        for (int i = 0; i < kBatch; ++i)
+          if (t + i < e) row(t + i, now[i]);
       }
     }
   };
@@ -182,8 +214,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ConvArgs P) {
     const int a = max(r0, begin + K - 1), e = min(end, r1);
     if (a < e) {
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j)
-        if (in) window[j] = raw_at(x + (size_t)(a - (K - 1) + j) * P.ld);
+      for (int j = 0; j < K - 1; ++j) raw_at(x + (size_t)(a - (K - 1) + j) * P.ld).get(window[j]);
       rows(a, e);
     }
   }
@@ -193,18 +224,20 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ConvArgs P) {
     Raw<T> last[K - 1];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
-      window[j].zero();
-      if (P.x0 && in) window[j] = raw_at(x0 + ((size_t)s * (K - 1) + j) * D);
+      Raw<T> w;
+      w.zero();
+      if (P.x0) w = raw_at(x0 + ((size_t)s * (K - 1) + j) * D);
+      w.get(window[j]);
     }
     if (P.xT) {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) {
         const int at = end - (K - 1) + j;
         last[j].zero();
-        if (!in) continue;
         if (at >= begin) last[j] = raw_at(x + (size_t)at * P.ld);
         else if (P.x0) last[j] = raw_at(x0 + ((size_t)s * (K - 1) + (K - 1) + at - begin) * D);
       }
+      __syncwarp();                        // (lanes that go along have read it too)
 #pragma unroll
       for (int j = 0; j < K - 1; ++j)
         if (in) put_raw(xT + ((size_t)s * (K - 1) + j) * D, last[j]);
@@ -219,17 +252,18 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ConvArgs P) {
 // rows t are walked to taps - 1 rows behind its last one: dx of a row is whole
 // once dpre of the taps - 1 rows behind it is known.
 template <typename T, int K, bool kSilu>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const ConvArgs P) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackPerSmF32) backward_kernel(const ConvArgs P) {
   wait_for_stream();
   if (!offsets_ok(P.packed)) {
     if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     return;
   }
-  __shared__ float2 sums[kWarps - 1][K + 1][2][32];
+  __shared__ Pair sums[kWarps - 1][K + 1][2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = P.D;
   const int part = blockIdx.x / P.col_tiles, parts = gridDim.x / P.col_tiles;
-  const int c = (blockIdx.x % P.col_tiles * 32 + lane) * 4;
-  const bool in = c < D;
+  const int col = (blockIdx.x % P.col_tiles * 32 + lane) * 4;
+  const bool in = col < D;
+  const int c = min(col, D - 4);           // (lanes without channels go along with the last)
   const T* const x = static_cast<const T*>(P.x) + c;
   const T* const x0 = static_cast<const T*>(P.x0) + c;
   const T* const dy = static_cast<const T*>(P.dy) + c;
@@ -237,87 +271,97 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ConvArgs P) {
   T* const dx = static_cast<T*>(P.dx) + c;
   T* const dx0 = static_cast<T*>(P.dx0) + c;
   Taps<K> taps;
-  taps.load(P.w, P.bias, c, in);
-  float2 dw[K][2], dbias[2] = {both(0.f), both(0.f)};
+  taps.load(P.w, P.bias, c);
+  const Pair minus_one = bits2(hidden(-1.f));
+  Pair dw[K][2], dbias[2] = {0, 0};
 #pragma unroll
-  for (int j = 0; j < K; ++j) dw[j][0] = dw[j][1] = both(0.f);
+  for (int j = 0; j < K; ++j) dw[j][0] = dw[j][1] = 0;
 
   // Rows a .. e - 1 of sequence s (rows begin .. end - 1).
   auto rows = [&](int s, int begin, int end, int a, int e) {
-    Raw<T> window[K - 1];
-    float2 acc[K][2];                      // of dx rows t, t - 1, .. as far as known
+    Pair window[K - 1][2], dpre[K - 1][2]; // x and dpre of the rows before t, oldest first
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       const int at = a - (K - 1) + j;
-      window[j].zero();
-      if (!in) continue;
-      if (at >= begin) window[j] = raw_at(x + (size_t)at * P.ld);
-      else if (P.x0) window[j] = raw_at(x0 + ((size_t)s * (K - 1) + (K - 1) + at - begin) * D);
+      Raw<T> w;
+      w.zero();
+      if (at >= begin) w = raw_at(x + (size_t)at * P.ld);
+      else if (P.x0) w = raw_at(x0 + ((size_t)s * (K - 1) + (K - 1) + at - begin) * D);
+      w.get(window[j]);
+      dpre[j][0] = dpre[j][1] = 0;
     }
-#pragma unroll
-    for (int k = 0; k < K; ++k) acc[k][0] = acc[k][1] = both(0.f);
     constexpr int kBatch = 4;
     const int stop = e + K - 1;            // dx of row t - (K - 1) leaves at t
-    for (int t0 = a; t0 < stop; t0 += kBatch) {
-      Raw<T> now[kBatch], grad[kBatch];
+    Raw<T> next_x[kBatch], next_dy[kBatch];
+    auto ask = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        now[i].zero();
-        grad[i].zero();
-        if (in && t0 + i < stop && t0 + i < end) {
-          now[i] = raw_at(x + (size_t)(t0 + i) * P.ld);
-          grad[i] = raw_at(dy + (size_t)(t0 + i) * D);
+      for (int i = 0; i < kBatch; ++i)
+        if (t + i < stop && t + i < end) {
+          next_x[i] = raw_at(x + (size_t)(t + i) * P.ld);
+          next_dy[i] = raw_at(dy + (size_t)(t + i) * D);
+        }
+    };
+    // One row: kInside where it and the row that leaves are rows a .. e - 1.
+    auto row = [&](int t, const Raw<T>& raw_x, const Raw<T>& raw_dy, auto inside) {
+      constexpr bool kInside = decltype(inside)::value;
+      Pair now[2] = {0, 0}, g[2] = {0, 0}, leaves[2];
+      if (kInside || t < end) {
+        raw_x.get(now);
+        raw_dy.get(g);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          if (kSilu) {
+            // silu' = sig (1 + pre (1 - sig)).
+            const Pair pre = taps.pre(window, now[p], p), sig = taps.sigmoid(pre);
+            const Pair rest = fma2(sig, minus_one, taps.one);
+            g[p] = mul2(g[p], mul2(sig, fma2(pre, rest, taps.one)));
+          }
+          if (kInside || t < e) {
+            dbias[p] = add2(dbias[p], g[p]);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) dw[j][p] = fma2(g[p], window[j][p], dw[j][p]);
+            dw[K - 1][p] = fma2(g[p], now[p], dw[K - 1][p]);
+          }
         }
       }
 #pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        leaves[p] = mul2(taps.w[0][p], g[p]);
+#pragma unroll
+        for (int j = K - 2; j >= 0; --j) leaves[p] = fma2(taps.w[K - 1 - j][p], dpre[j][p], leaves[p]);
+      }
+      shift(window, now);
+      shift(dpre, g);
+      const int out = t - (K - 1);
+      if (kInside) {
+        if (in) put(dx + (size_t)out * P.ld_grad, leaves);
+      } else if (in && (out >= a || (a == begin && P.dx0))) {
+        if (P.dxT && out >= end - (K - 1)) {
+          Pair f[2];
+          raw_at(dxT + ((size_t)s * (K - 1) + out - (end - (K - 1))) * D).get(f);
+          leaves[0] = add2(leaves[0], f[0]);
+          leaves[1] = add2(leaves[1], f[1]);
+        }
+        put(out >= a ? dx + (size_t)out * P.ld_grad
+                     : dx0 + ((size_t)s * (K - 1) + (K - 1) + out - begin) * D, leaves);
+      }
+    };
+    ask(a);
+    for (int t = a; t < stop; t += kBatch) {
+      Raw<T> now[kBatch], grad[kBatch];
+#pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int t = t0 + i;
-        if (t >= stop) break;
-        if (t < end) {
-          float2 f[K][2], g[2], pre[2] = {taps.bias[0], taps.bias[1]};
-          now[i].get(f[K - 1]);
-          grad[i].get(g);
+        now[i] = next_x[i];
+        grad[i] = next_dy[i];
+      }
+      ask(t + kBatch);
+      if (t > a && t + kBatch <= e) {      // (kBatch >= K - 1: what leaves is at least row a)
 #pragma unroll
-          for (int j = 0; j < K - 1; ++j) window[j].get(f[j]);
+        for (int i = 0; i < kBatch; ++i) row(t + i, now[i], grad[i], std::true_type{});
+      } else {
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            if (kSilu) {
-#pragma unroll
-              for (int j = 0; j < K; ++j) pre[p] = fma2(taps.w[j][p], f[j][p], pre[p]);
-              // silu' = sig (1 + pre (1 - sig)).
-              const float2 sig = sigmoid2(pre[p]);
-              g[p] = mul2(g[p], mul2(sig, fma2(pre[p], sub2(both(1.f), sig), both(1.f))));
-            }
-#pragma unroll
-            for (int k = 0; k < K; ++k) acc[k][p] = fma2(taps.w[K - 1 - k][p], g[p], acc[k][p]);
-            if (t < e) {
-              dbias[p] = add2(dbias[p], g[p]);
-#pragma unroll
-              for (int j = 0; j < K; ++j) dw[j][p] = fma2(g[p], f[j][p], dw[j][p]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j + 1 < K - 1; ++j) window[j] = window[j + 1];
-          window[K - 2] = now[i];
-        }
-        const int out = t - (K - 1);       // whole now
-        if (in && (out >= a || (a == begin && P.dx0))) {
-          if (P.dxT && out >= end - (K - 1)) {
-            float2 f[2];
-            raw_at(dxT + ((size_t)s * (K - 1) + out - (end - (K - 1))) * D).get(f);
-            acc[K - 1][0] = add2(acc[K - 1][0], f[0]);
-            acc[K - 1][1] = add2(acc[K - 1][1], f[1]);
-          }
-          T* const at = out >= a ? dx + (size_t)out * P.ld_grad
-                                 : dx0 + ((size_t)s * (K - 1) + (K - 1) + out - begin) * D;
-          store_row(at, acc[K - 1][0], acc[K - 1][1]);
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-#pragma unroll
-          for (int k = K - 1; k > 0; --k) acc[k][p] = acc[k - 1][p];
-          acc[0][p] = both(0.f);
-        }
+        for (int i = 0; i < kBatch; ++i)
+          if (t + i < stop) row(t + i, now[i], grad[i], std::false_type{});
       }
     }
   };
@@ -350,13 +394,14 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const ConvArgs P) {
   float* const to = P.partial + (size_t)part * (K + 1) * D + c;
 #pragma unroll
   for (int j = 0; j <= K; ++j) {
-    float2 v[2] = {j < K ? dw[j < K ? j : 0][0] : dbias[0], j < K ? dw[j < K ? j : 0][1] : dbias[1]};
+    Pair v[2];
 #pragma unroll
-    for (int q = 0; q < kWarps - 1; ++q) {
-      v[0] = add2(v[0], sums[q][j][0][lane]);
-      v[1] = add2(v[1], sums[q][j][1][lane]);
+    for (int p = 0; p < 2; ++p) {
+      v[p] = j < K ? dw[j < K ? j : 0][p] : dbias[p];
+#pragma unroll
+      for (int q = 0; q < kWarps - 1; ++q) v[p] = add2(v[p], sums[q][j][p][lane]);
     }
-    store_row(to + (size_t)j * D, v[0], v[1]);
+    put(to + (size_t)j * D, v);
   }
 }
 
@@ -389,59 +434,68 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ----------------------------------------------------------------- one token
-// A block takes kGroup tokens and all of their channels, four a thread.
+// A block takes kGroup tokens by 512 channels, four a thread.  What does not depend on
+// the slots is on its way while they are looked at.
 template <typename T, int K, bool kSilu, int kGroup>
 __global__ void __launch_bounds__(kThreads) step_kernel(const ConvArgs P, T* state, int n_slots,
-                                                        const int32_t* slots) {
+                                                        const int32_t* slots, int parts) {
   wait_for_stream();
   __shared__ SlotTable<kGroup, kThreads> table;
-  const int row0 = blockIdx.x * kGroup, n = min(kGroup, P.packed.rows - row0), D = P.D;
+  const int row0 = (int)(blockIdx.x / parts) * kGroup, n = min(kGroup, P.packed.rows - row0), D = P.D;
+  const int col = ((int)(blockIdx.x % parts) * kThreads + threadIdx.x) * 4, c = min(col, D - 4);
+  const T* const x = static_cast<const T*>(P.x) + (size_t)row0 * P.ld + c;
+  Taps<K> taps;
+  taps.load(P.w, P.bias, c);
+  constexpr int kAhead = kGroup < 4 ? kGroup : 4;            // tokens at a time
+  Raw<T> first = raw_at(x);
   table.find(slots, row0, n, n_slots, P.status);
-  for (int c = threadIdx.x * 4; c < D; c += kThreads * 4) {
-    Taps<K> taps;
-    taps.load(P.w, P.bias, c, true);
-    for (int i = 0; i < n; ++i) {
-      const int slot = table.own[i];
+  if (col >= D) return;
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    Raw<T> raw[kAhead][K];
+    T* at[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int slot = i0 + i < n ? table.own[i0 + i] : -1;
+      at[i] = slot < 0 ? nullptr : state + (size_t)slot * (K - 1) * D + c;
       if (slot < 0) continue;
-      const int row = row0 + i;
-      T* const at = state + (size_t)slot * (K - 1) * D + c;
-      Raw<T> window[K];
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) window[j] = raw_at(at + (size_t)j * D);
-      window[K - 1] = raw_at(static_cast<const T*>(P.x) + (size_t)row * P.ld + c);
-      float2 pre[2] = {taps.bias[0], taps.bias[1]};
+      for (int j = 0; j < K - 1; ++j) raw[i][j] = raw_at(at[i] + (size_t)j * D);
+      raw[i][K - 1] = kGroup == 1 ? first : raw_at(x + (size_t)(i0 + i) * P.ld);
+    }
 #pragma unroll
-      for (int j = 0; j < K; ++j) {
-        float2 f[2];
-        window[j].get(f);
-        pre[0] = fma2(taps.w[j][0], f[0], pre[0]);
-        pre[1] = fma2(taps.w[j][1], f[1], pre[1]);
-      }
-      if (kSilu) {
-        pre[0] = mul2(pre[0], sigmoid2(pre[0]));
-        pre[1] = mul2(pre[1], sigmoid2(pre[1]));
+    for (int i = 0; i < kAhead; ++i) {
+      if (!at[i]) continue;
+      Pair window[K - 1][2], now[2], out[2];
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) raw[i][j].get(window[j]);
+      raw[i][K - 1].get(now);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        out[p] = taps.pre(window, now[p], p);
+        if (kSilu) out[p] = mul2(out[p], taps.sigmoid(out[p]));
       }
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) put_raw(at + (size_t)j * D, window[j + 1]);
-      store_row(static_cast<T*>(P.y) + (size_t)row * D + c, pre[0], pre[1]);
+      for (int j = 0; j < K - 1; ++j) put_raw(at[i] + (size_t)j * D, raw[i][j + 1]);
+      put(static_cast<T*>(P.y) + (size_t)(row0 + i0 + i) * D + c, out);
     }
   }
 }
 
 int col_tiles_of(int D) { return (D + kWarpCols - 1) / kWarpCols; }
 
-// Rows of a run: at most kMostRun, fewer where the GPU would not be filled.
-constexpr int kMostRun = 32, kLeastRun = 8;
-int run_of(int rows, int D) {
-  const long long warps = (long long)device_limits().sms * 32;
-  const long long run = (long long)rows * col_tiles_of(D) / warps;
+// Rows of a run, so that the runs' blocks of kWarps runs fill the GPU once with
+// `per_sm` blocks a multiprocessor.
+constexpr int kLeastRun = 8, kMostRun = 1 << 16;
+int groups_of(int D, int per_sm) {
+  const int n = per_sm * device_limits().sms / col_tiles_of(D);
+  return n > 0 ? n : 1;
+}
+int run_of(int rows, int D, int per_sm) {
+  const long long warps = (long long)groups_of(D, per_sm) * kWarps, run = (rows + warps - 1) / warps;
   return run >= kMostRun ? kMostRun : run <= kLeastRun ? kLeastRun : (int)run;
 }
 
-// Parts of the sums over rows: at most what fills the GPU.
-int most_parts(int D) { return 4 * device_limits().sms / col_tiles_of(D) + 1; }
-
-ConvArgs args_of(const ConvDims& d, const ConvInputs& in, unsigned* status) {
+ConvArgs args_of(const ConvDims& d, const ConvInputs& in, int per_sm, unsigned* status) {
   ConvArgs P{};
   P.packed = Packed{in.offsets, d.n_seq, d.rows};
   P.x = in.x;
@@ -452,7 +506,7 @@ ConvArgs args_of(const ConvDims& d, const ConvInputs& in, unsigned* status) {
   P.ld_grad = d.ld_grad;
   P.D = d.D;
   P.col_tiles = col_tiles_of(d.D);
-  P.run = run_of(d.rows, d.D);
+  P.run = run_of(d.rows, d.D, per_sm);
   P.runs = d.rows > 0 ? (d.rows + P.run - 1) / P.run : 1;
   P.status = status;
   return P;
@@ -477,12 +531,12 @@ cudaError_t with_kind(const ConvDims& d, F f) {
 }  // namespace
 
 size_t short_conv_workspace_bytes(const ConvDims& d) {
-  return (size_t)most_parts(d.D) * (d.taps + 1) * d.D * sizeof(float);
+  return (size_t)groups_of(d.D, kBackPerSm) * (d.taps + 1) * d.D * sizeof(float);
 }
 
 cudaError_t launch_short_conv_forward(const ConvDims& d, const ConvInputs& in, void* y, void* xT,
                                       unsigned* status, cudaStream_t stream) {
-  ConvArgs P = args_of(d, in, status);
+  ConvArgs P = args_of(d, in, kPerSm, status);
   P.y = y;
   P.xT = xT;
   const unsigned blocks = (unsigned)((P.runs + kWarps - 1) / kWarps) * P.col_tiles;
@@ -502,13 +556,13 @@ cudaError_t launch_short_conv_backward(const ConvDims& d, const ConvInputs& in, 
     if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)d.D * 4, stream);
     return e;
   }
-  ConvArgs P = args_of(d, in, status);
+  ConvArgs P = args_of(d, in, d.dtype == SDM_BF16 ? kBackPerSm : kBackPerSmF32, status);
   P.dy = dy;
   P.dxT = dxT;
   P.dx = dx;
   P.dx0 = dx0;
   P.partial = dw || dbias ? static_cast<float*>(workspace) : nullptr;
-  const int most = most_parts(d.D), want = (P.runs + kWarps - 1) / kWarps;
+  const int most = groups_of(d.D, kBackPerSm), want = (P.runs + kWarps - 1) / kWarps;
   const int parts = want < most ? want : most;
   const cudaError_t e = with_kind(d, [&](auto t, auto k, auto silu) {
     return launch_behind(backward_kernel<decltype(t), decltype(k)::value, decltype(silu)::value>,
@@ -520,24 +574,21 @@ cudaError_t launch_short_conv_backward(const ConvDims& d, const ConvInputs& in, 
                        parts, d.D, d.taps, dw, dbias);
 }
 
-// Tokens from which on a block takes kMany of them (see SlotTable).
-constexpr int kManyRows = 16384, kMany = 64;
-
 cudaError_t launch_short_conv_step(const ConvDims& d, const ConvInputs& in, void* state,
                                    int n_slots, const int32_t* slots, void* y, unsigned* status,
                                    cudaStream_t stream) {
-  ConvArgs P = args_of(d, in, status);
+  ConvArgs P = args_of(d, in, 1, status);
   P.y = y;
-  const bool many = slots && d.rows >= kManyRows;
+  const int parts = (d.D / 4 + kThreads - 1) / kThreads;
   return with_kind(d, [&](auto t, auto k, auto silu) {
     using T = decltype(t);
     constexpr int K = decltype(k)::value;
     constexpr bool kSilu = decltype(silu)::value;
-    if (many)
-      return launch_behind(step_kernel<T, K, kSilu, kMany>, (unsigned)((d.rows + kMany - 1) / kMany),
-                           kThreads, 0, stream, P, static_cast<T*>(state), n_slots, slots);
-    return launch_behind(step_kernel<T, K, kSilu, 1>, (unsigned)d.rows, kThreads, 0, stream, P,
-                         static_cast<T*>(state), n_slots, slots);
+    return with_group(d.rows, (long long)d.rows * parts, 2048, [&](auto group) {
+      constexpr int G = decltype(group)::value;
+      return launch_behind(step_kernel<T, K, kSilu, G>, (unsigned)(((long long)d.rows + G - 1) / G * parts),
+                           kThreads, 0, stream, P, static_cast<T*>(state), n_slots, slots, parts);
+    });
   });
 }
 

@@ -178,19 +178,57 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
   __shared__ uint32_t redmax[2][kTeams<TW>][TW];
   const int team = threadIdx.x / (TW * 32), lane = threadIdx.x % (TW * 32), D = P.D;
   const int group_log = 31 - __clz(P.group | 1);
+  // The layer norm's blocks go through many rows: gamma and beta stay in registers (four
+  // loads of 16 bytes per eight channels and row otherwise, as many as all else), and the
+  // next row's loads are under way while a row is worked on.  The RMS-Norm's take one row.
+  constexpr bool kHold = kCentred && NV <= 2, kAhead = kCentred && NV * sizeof(T) <= 4;
+  float2 held_gamma[kHold ? NV : 1][4], held_beta[kHold ? NV : 1][4];
+  if (kHold) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TW * 32 + lane) * kVec, k = kHold ? j : 0;
+      Eight<float> v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        held_gamma[k][i] = both(1.f);
+        held_beta[k][i] = both(0.f);
+      }
+      if (c < D && P.gamma) {
+        v.load(P.gamma + c);
+        v.get(held_gamma[k]);
+      }
+      if (c < D && P.beta) {
+        v.load(P.beta + c);
+        v.get(held_beta[k]);
+      }
+    }
+  }
   int flip = 0;
-  for (long long row = (long long)blockIdx.x * kTeams<TW> + team; row < P.rows;
-       row += (long long)gridDim.x * kTeams<TW>, flip ^= 1) {
+  const long long step = (long long)gridDim.x * kTeams<TW>;
+  Eight<T> ahead_s[NV], ahead_res[NV];
+  auto ask = [&](long long row) {
     const size_t base = (size_t)row * D;
-    Eight<T> s[NV], res[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
-      if (c < D) {
-        s[j].load(static_cast<const T*>(P.x) + base + c);
-        if (P.residual) res[j].load(static_cast<const T*>(P.residual) + base + c);
+      if (c < D && row < P.rows) {
+        ahead_s[j].load(static_cast<const T*>(P.x) + base + c);
+        if (P.residual) ahead_res[j].load(static_cast<const T*>(P.residual) + base + c);
       }
     }
+  };
+  long long row = (long long)blockIdx.x * kTeams<TW> + team;
+  if (kAhead) ask(row);
+  for (; row < P.rows; row += step, flip ^= 1) {
+    const size_t base = (size_t)row * D;
+    if (!kAhead) ask(row);
+    Eight<T> s[NV], res[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      s[j] = ahead_s[j];
+      res[j] = ahead_res[j];
+    }
+    if (kAhead) ask(row + step);
     float2 ss2 = both(0.f), sum2 = both(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -214,20 +252,19 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
         }
       }
     }
-    float2 mean = both(0.f);
+    float2 n[NV][4];
     if (kCentred) {
       float sum[1] = {sum2.x + sum2.y};
       team_sum<TW, 1>(sum, red[0][team], team);
-      mean = both(sum[0] * P.one_over_D);
+      const float2 mean = both(sum[0] * P.one_over_D);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if ((j * TW * 32 + lane) * kVec < D) {
-          float2 f[4];
-          s[j].get(f);
+          s[j].get(n[j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            f[i] = sub2(f[i], mean);
-            ss2 = fma2(f[i], f[i], ss2);
+            n[j][i] = sub2(n[j][i], mean);
+            ss2 = fma2(n[j][i], n[j][i], ss2);
           }
         }
       }
@@ -236,16 +273,20 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
     team_sum<TW, 1>(ss, red[kCentred ? 1 : flip][team], team);
     const float2 inv = both(rsqrtf(fmaf(ss[0], P.one_over_D, P.eps)));
     // n, kept where the scale of the 8-bit output has yet to be found.
-    float2 n[NV][4];
     float most = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TW * 32 + lane) * kVec;
       if (c < D) {
-        s[j].get(n[j]);
+        if (!kCentred) s[j].get(n[j]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) n[j][i] = mul2(kCentred ? sub2(n[j][i], mean) : n[j][i], inv);
-        if (P.gamma) {
+        for (int i = 0; i < 4; ++i) n[j][i] = mul2(n[j][i], inv);
+        if (kHold) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            n[j][i] = fma2(n[j][i], held_gamma[kHold ? j : 0][i], held_beta[kHold ? j : 0][i]);
+        }
+        if (!kHold && P.gamma) {
           Eight<float> g;
           float2 gm[4];
           g.load(P.gamma + c);
@@ -253,7 +294,7 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
 #pragma unroll
           for (int i = 0; i < 4; ++i) n[j][i] = mul2(n[j][i], gm[i]);
         }
-        if (kCentred && P.beta) {
+        if (kCentred && !kHold && P.beta) {
           Eight<float> b;
           float2 bt[4];
           b.load(P.beta + c);
@@ -524,14 +565,14 @@ constexpr int kMostPerSm = 4;
 int most_parts() { return kMostPerSm * device_limits().sms; }
 
 template <class K>
-int blocks_per_sm(K kernel, int threads, int smem, std::atomic<int>* cache) {
+int blocks_per_sm(K kernel, int threads, int smem, int most, std::atomic<int>* cache) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
   int n = cache[dev].load(std::memory_order_relaxed);
   if (n == 0) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1)
       n = 1;
-    if (n > kMostPerSm) n = kMostPerSm;
+    if (n > most) n = most;
     cache[dev].store(n, std::memory_order_relaxed);
   }
   return n;
@@ -539,12 +580,14 @@ int blocks_per_sm(K kernel, int threads, int smem, std::atomic<int>* cache) {
 
 template <typename T, int TW, int NV, bool kCentred>
 cudaError_t forward_as(const ForwardArgs& P, int out_dtype, cudaStream_t stream) {
-  const long long want = ((long long)P.rows + kTeams<TW> - 1) / kTeams<TW>;
-  const long long most = 1 << 20;
-  const unsigned blocks = (unsigned)(want < most ? want : most);
+  static std::atomic<int> cache[3][64];    // zeros
   const auto kernel = out_dtype == SDM_E4M3   ? forward_kernel<T, TW, NV, SDM_E4M3, kCentred>
                       : out_dtype == SDM_BF16 ? forward_kernel<T, TW, NV, SDM_BF16, kCentred>
                                               : forward_kernel<T, TW, NV, SDM_F32, kCentred>;
+  const long long want = ((long long)P.rows + kTeams<TW> - 1) / kTeams<TW>;
+  const long long most = kCentred ? (long long)blocks_per_sm(kernel, kBlock<TW>, 0, 8, cache[out_dtype]) * device_limits().sms
+                                  : 1 << 20;
+  const unsigned blocks = (unsigned)(want < most ? want : most);
   return launch_behind(kernel, blocks, kBlock<TW>, 0, stream, P);
 }
 
@@ -555,7 +598,7 @@ cudaError_t backward_as(const BackwardArgs& P, float* dgamma, float* dbeta, cuda
   constexpr int kSums = kCentred ? 2 : 1;
   const int smem = kSums * (kTeams<TW> - 1) * TW * NV * 256 * (int)sizeof(float);
   const long long want = ((long long)P.rows + kTeams<TW> - 1) / kTeams<TW>;
-  const int most = blocks_per_sm(kernel, kBlock<TW>, smem, cache) * device_limits().sms;
+  const int most = blocks_per_sm(kernel, kBlock<TW>, smem, kMostPerSm, cache) * device_limits().sms;
   const int blocks = (int)(want < most ? want : most);
   const cudaError_t e = launch_behind(kernel, blocks, kBlock<TW>, smem, stream, P);
   if (e != cudaSuccess || !P.partial) return e;

@@ -29,34 +29,9 @@
 #include "rows.cuh"
 #include "slots.cuh"
 
-#ifndef LC
-#define LC 16
-#endif
-#ifndef FILL
-#define FILL 16
-#endif
-#ifndef FILL_E
-#define FILL_E 24
-#endif
-#ifndef SB
-#define SB 8
-#endif
-#ifndef SU
-#define SU 4
-#endif
-#ifndef FB
-#define FB 7
-#endif
-#ifndef FU
-#define FU 4
-#endif
-#ifndef BU
-#define BU 4
-#endif
 namespace sdm {
 namespace {
 
-constexpr int kSU = SU, kFU = FU, kBU = BU;
 constexpr int kStateRows = 16;             // rows between saved states
 
 // Blocks of the forward pass and of the summaries: two warps, eight rows at a time.  A
@@ -78,6 +53,10 @@ struct Square {
   static constexpr int NL = N / 4, CL = 32 / NL;
   static constexpr int kNBits = NL == 2 ? 1 : NL == 4 ? 2 : NL == 8 ? 3 : 4, kCBits = 5 - kNBits;
 };
+// Blocks a multiprocessor that the registers leave room for.  Measured, us: scan of 131072
+// x 1024 x 16 bf16 with 5, 6, 7, 8 forward blocks 1044, 1035, 1042, 1088; the backward
+// pass of 32768 x 1024 with 2 blocks 570, and with 3 of half the rows at a time 577.
+constexpr int kSummaryBlocks = 8, kForwardBlocks = 6, kBackBlocks = 2;
 constexpr int kBlockStates = 2048;         // a block's states: its channels are 2048 / N
 // How a warp goes through rows of its channels: four channels a lane and step.
 template <class S>
@@ -105,7 +84,7 @@ struct ScanArgs {
   bool split;            // whether there are chunks to be carried between
   const float* h0;       // (dhT)
   float* hT;             // (dh0)
-  float* states;         // [numbers of R rows][D][N]
+  float* states;         // [numbers of kStateRows rows][D][N], see save_states
   void* y;
   // backward
   const void* dy;
@@ -123,29 +102,44 @@ struct Span {
   int seq, number, row0, rows, begin;
   bool first, last;
 };
-// The chunk of an index: its number, or where sequences are equal the place among
-// all of them.  False where there is none.  A whole warp calls it.
-__device__ __forceinline__ bool span_of(const Packed& P, int L, int chunks, int index, Span& s) {
-  int chunk;
-  if (P.offsets) {
-    s.seq = sequence_of(P, L, index);
-    if (s.seq < 0) return false;
-    s.begin = P.begin(s.seq);
-    chunk = index - (s.begin / L + s.seq);
-  } else {
+enum Found { kBad, kNone, kChunk };
+// The chunk of an index: its number, or where sequences are equal the place among all
+// of them.  All threads of the block call it; kBad: the offsets break their rules.  Up
+// to 31 sequences every lane looks at one, so that there is one load's latency.
+// kChecked: the offsets are known to be good.
+template <bool kChecked>
+__device__ __forceinline__ Found find_chunk(const Packed& P, int L, int chunks, int index, Span& s) {
+  const int lane = threadIdx.x & 31;
+  int chunk, end;
+  if (!P.offsets) {
     s.seq = index / chunks;
     chunk = index % chunks;
     s.begin = P.begin(s.seq);
+    end = P.begin(s.seq + 1);
+  } else if (P.n_seq < 32) {
+    const int o = __ldg(P.offsets + min(lane, P.n_seq)), before = __shfl_up_sync(0xffffffffu, o, 1);
+    if (__any_sync(0xffffffffu, o < 0 || o > P.rows || (lane > 0 && o < before))) return kBad;
+    s.seq = __popc(__ballot_sync(0xffffffffu, lane < P.n_seq && o / L + lane <= index)) - 1;
+    if (s.seq < 0) return kNone;
+    s.begin = __shfl_sync(0xffffffffu, o, s.seq);
+    end = __shfl_sync(0xffffffffu, o, s.seq + 1);
+    chunk = index - (s.begin / L + s.seq);
+  } else {
+    if (!kChecked && !offsets_ok(P)) return kBad;
+    s.seq = sequence_of(P, L, index);
+    if (s.seq < 0) return kNone;
+    s.begin = P.begin(s.seq);
+    end = P.begin(s.seq + 1);
+    chunk = index - (s.begin / L + s.seq);
   }
-  const int end = P.begin(s.seq + 1);
   const long long row0 = s.begin + (long long)chunk * L;
-  if (chunk > 0 && row0 >= end) return false;
+  if (chunk > 0 && row0 >= end) return kNone;
   s.row0 = (int)row0;
   s.rows = min(L, end - s.row0);
   s.number = s.begin / L + s.seq + chunk;
   s.first = chunk == 0;
   s.last = s.row0 + s.rows == end;
-  return true;
+  return kChunk;
 }
 
 // Which channels a block's warps and threads work on.
@@ -245,6 +239,14 @@ template <typename T>
 __device__ __forceinline__ Raw4<T> raw4(const void* base, size_t i) {
   return *reinterpret_cast<const Raw4<T>*>(static_cast<const T*>(base) + i);
 }
+// The same, zeros where not `in`: a choice of what was loaded, not a branch, so that the
+// arithmetic of a thread's items is interleaved.
+template <typename T>
+__device__ __forceinline__ void get4_if(bool in, const Raw4<T>& r, float2 (&f)[2]) {
+  get4(r, f);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) f[p] = in ? f[p] : both(0.f);
+}
 __device__ __forceinline__ void load_four(const float* p, bool in, float none, float2 (&f)[2]) {
   f[0] = f[1] = both(none);
   if (p && in) load_row(p, f[0], f[1]);
@@ -256,7 +258,7 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
   return make_float2(rcp(1.f + ex2(z.x)), rcp(1.f + ex2(z.y)));
 }
 
-// Inputs are copied to shared memory R rows ahead, every thread what it will itself
+// Inputs are copied to shared memory one turn ahead, every thread what it will itself
 // take from there: its items of the tensors of channels, and of B and C.
 __device__ __forceinline__ void copy_item(void* to, const void* from, bool in, int bytes) {
   if (!in) return;
@@ -320,19 +322,19 @@ struct RawRows {
   }
 };
 
-// dinner = dy silu(z) of four channels.
+// dinner = dy silu(z) of four channels; zeros where not `in`.
 template <typename T>
-__device__ __forceinline__ void dinner_of(const Raw4<T>& dy, const Raw4<T>& z, bool gated, float2 (&d)[2]) {
-  get4(dy, d);
+__device__ __forceinline__ void dinner_of(bool in, const Raw4<T>& dy, const Raw4<T>& z, bool gated, float2 (&d)[2]) {
+  get4_if(in, dy, d);
   if (!gated) return;
   float2 g[2];
-  get4(z, g);
+  get4_if(in, z, g);
 #pragma unroll
   for (int p = 0; p < 2; ++p) d[p] = mul2(d[p], mul2(g[p], sigmoid2(g[p])));
 }
 
 // ------------------------------------------------------------------ summaries
-// Sixteen or more neighbouring numbers.
+// Neighbouring numbers as pairs.
 template <int V>
 __device__ __forceinline__ void load_pairs(const float* p, float2 (&v)[V]) {
 #pragma unroll
@@ -365,6 +367,26 @@ __device__ __forceinline__ void load_rates(const float* p, bool in, float2 (&nA)
 #pragma unroll
   for (int i = 0; i < 16; ++i) nA[i] = make_float2(-nA[i].x, -nA[i].y);
 }
+// Saved states lie as the forward pass's threads hold them: of every warp's channels the
+// first four states of all its threads with channels, then the next four, and so on, so
+// that a warp's stores are whole lines.  Lanes with channels of a warp that begins at c0:
+template <int N>
+__device__ __forceinline__ int lanes_from(int c0, int c_end) {
+  return min(32, max(0, c_end - c0) * Wide<N>::NL / Wide<N>::CH);
+}
+template <int N>
+__device__ __forceinline__ void save_states(float* p, int lane, int lanes, const float2 (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) store_row(p + (i * lanes + lane) * 4, v[2 * i], v[2 * i + 1]);
+}
+// Where the backward pass finds four states, from 4 nl on, of channel c.
+template <int N>
+__device__ __forceinline__ int saved_at(int c, int tile_c0, int c_end, int nl) {
+  using W = Wide<N>;
+  const int c0 = tile_c0 + (c - tile_c0) / W::kCols * W::kCols, o = c - c0;
+  const int lane = o / W::CH * W::NL + nl * 4 / W::NT, i = o % W::CH * (W::NT / 4) + nl * 4 % W::NT / 4;
+  return c0 * N + (i * lanes_from<N>(c0, c_end) + lane) * 4;
+}
 // A thread's CH channels of a row of shared memory.
 template <int CH>
 __device__ __forceinline__ void load_channels(const float* p, float (&v)[CH]) {
@@ -389,25 +411,27 @@ struct SummarySmem {
 // The state behind a chunk from zeros in front of it, and the sum of delta; with
 // kBack the gradient of the state in front of it from zeros behind it.
 template <typename T, int N, bool kBack>
-__global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, SB) summary_kernel(const ScanArgs P) {
+__global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, kSummaryBlocks) summary_kernel(const ScanArgs P) {
   using W = Wide<N>;
   using St = Steps<W>;
   constexpr int R = W::kRows;
   extern __shared__ __align__(16) char smem[];
   SummarySmem<T, N>& sh = *reinterpret_cast<SummarySmem<T, N>*>(smem);
   wait_for_stream();
-  if (!offsets_ok(P.packed)) {
-    if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
-    return;
-  }
-  Span s;
-  if (!span_of(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s)) return;
-  if (kBack ? s.first : s.last) return;    // nobody needs it
   const Place<N, W> at(P, blockIdx.x % P.tiles);
   auto& mem = sh.warp[at.warp];
   const int nl = at.lane % W::NL, col = at.lane / W::NL * W::CH, cs = at.c0 + at.quad();
   const bool in = at.c0 + col < at.c_end, in_s = cs < at.c_end;
   const size_t state = (size_t)(at.c0 + col) * N + nl * W::NT;
+  float2 nA[16], h[16];
+  load_rates<N>(P.A + state, in, nA);
+  float2 bias[2], sum[2] = {both(0.f), both(0.f)};
+  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
+  Span s;
+  const Found found = find_chunk<false>(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s);
+  if (found == kBad && threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+  if (found != kChunk) return;
+  if (kBack ? s.first : s.last) return;    // nobody needs it
   const void* const from[3] = {kBack ? P.dy : P.x, P.dt, kBack ? P.z : nullptr};
   const long long ld[3] = {kBack ? P.D : P.ld, P.ld, P.ld_z};
   // (What is left has rows.)
@@ -415,12 +439,8 @@ __global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, SB) summary_kernel(c
   int r = kBack ? last : 0;
   sh.raw.template ask<!kBack, kBack>(P, at, in_s, from, ld, s.row0 + r, min(R, s.rows - r));
   const Constants K = constants();
-  float2 nA[16], h[16];
-  load_rates<N>(P.A + state, in, nA);
 #pragma unroll
   for (int i = 0; i < 16; ++i) h[i] = both(0.f);
-  float2 bias[2], sum[2] = {both(0.f), both(0.f)};
-  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
   for (int turn = 0; r >= 0 && r <= last; r += step, turn ^= 1) {
     const int n = min(R, s.rows - r), next = r + step;
     cp_async_wait_all();
@@ -428,23 +448,22 @@ __global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, SB) summary_kernel(c
 #pragma unroll
     for (int i = 0; i < St::kItems; ++i) {
       const int t = at.row(i), q = at.quad();
-      float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)};
-      if (t < n && in_s) {
-        float2 d[2];
-        get4(sh.raw.rows[1][i][threadIdx.x], d);
+      const bool valid = t < n && in_s;
+      float2 sp[2], u[2], d[2];
+      get4_if(valid, sh.raw.rows[1][i][threadIdx.x], d);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          float2 unused, e;
-          softplus_pair(K, d[p], bias[p], unused, e, sp[p]);
-          sum[p] = add2(sum[p], sp[p]);
-        }
-        if (kBack) {
-          dinner_of(sh.raw.rows[0][i][threadIdx.x], sh.raw.rows[2][i][threadIdx.x], P.z != nullptr, u);
-        } else {
-          get4(sh.raw.rows[0][i][threadIdx.x], d);
+      for (int p = 0; p < 2; ++p) {
+        float2 unused, e;
+        softplus_pair(K, d[p], bias[p], unused, e, sp[p]);
+        sp[p] = valid ? sp[p] : both(0.f);
+        sum[p] = add2(sum[p], sp[p]);
+      }
+      if (kBack) {
+        dinner_of(valid, sh.raw.rows[0][i][threadIdx.x], sh.raw.rows[2][i][threadIdx.x], P.z != nullptr, u);
+      } else {
+        get4_if(valid, sh.raw.rows[0][i][threadIdx.x], d);
 #pragma unroll
-          for (int p = 0; p < 2; ++p) u[p] = mul2(mul2(sp[p], both(kLn2)), d[p]);
-        }
+        for (int p = 0; p < 2; ++p) u[p] = mul2(mul2(sp[p], both(kLn2)), d[p]);
       }
       store_row(&mem.sp[t][q], sp[0], sp[1]);
       store_row(&mem.u[t][q], u[0], u[1]);
@@ -452,7 +471,7 @@ __global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, SB) summary_kernel(c
     if (next >= 0 && next <= last)
       sh.raw.template ask<!kBack, kBack>(P, at, in_s, from, ld, s.row0 + next, min(R, s.rows - next));
     __syncthreads();                       // (v of the turn before is done with)
-#pragma unroll kSU
+#pragma unroll 4
     for (int j = 0; j < R; ++j) {
       const int t = kBack ? R - 1 - j : j;
       float sp[W::CH], u[W::CH];
@@ -490,39 +509,36 @@ struct ForwardSmem {
 };
 
 template <typename T, int N>
-__global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, FB) forward_kernel(const ScanArgs P) {
+__global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, kForwardBlocks) forward_kernel(const ScanArgs P) {
   using W = Wide<N>;
   using St = Steps<W>;
   constexpr int R = W::kRows;
   extern __shared__ __align__(16) char smem[];
   ForwardSmem<T, N>& sh = *reinterpret_cast<ForwardSmem<T, N>*>(smem);
   wait_for_stream();
-  if (!offsets_ok(P.packed)) {
-    if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
-    return;
-  }
-  Span s;
-  if (!span_of(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s)) return;
   const Place<N, W> at(P, blockIdx.x % P.tiles);
   auto& mem = sh.warp[at.warp];
   const int nl = at.lane % W::NL, col = at.lane / W::NL * W::CH, cs = at.c0 + at.quad();
   const bool in = at.c0 + col < at.c_end, in_s = cs < at.c_end;
   const size_t state = (size_t)(at.c0 + col) * N + nl * W::NT, DN = (size_t)P.D * N;
+  float2 nA[16], h[16], bias[2], skip[2];
+  load_rates<N>(P.A + state, in, nA);
+  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
+  load_four(P.skip ? P.skip + cs : nullptr, in_s, 0.f, skip);
+  Span s;
+  const Found found = find_chunk<false>(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s);
+  if (found == kBad && threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
+  if (found != kChunk) return;
   const void* const from[3] = {P.x, P.dt, P.z};
   const long long ld[3] = {P.ld, P.ld, P.ld_z};
   if (s.rows > 0) sh.raw[0].template ask<true, true>(P, at, in_s, from, ld, s.row0, min(R, s.rows));
   const Constants K = constants();
-  float2 nA[16], h[16];
-  load_rates<N>(P.A + state, in, nA);
 #pragma unroll
   for (int i = 0; i < 16; ++i) h[i] = both(0.f);
   if (in) {
     if (P.split) load_wide<N>(P.carry + s.number * DN + state, h);
     else if (P.h0) load_wide<N>(P.h0 + s.seq * DN + state, h);
   }
-  float2 bias[2], skip[2];
-  load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
-  load_four(P.skip ? P.skip + cs : nullptr, in_s, 0.f, skip);
   for (int r = 0, turn = 0; r < s.rows; r += R, turn ^= 1) {
     const int row0 = s.row0 + r, n = min(R, s.rows - r);
     auto& raw = sh.raw[turn];
@@ -533,25 +549,25 @@ __global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, FB) forward_kernel(c
 #pragma unroll
     for (int i = 0; i < St::kItems; ++i) {
       const int t = at.row(i), q = at.quad();
-      float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)};
-      if (t < n && in_s) {
-        float2 f[2], d[2];
-        get4(raw.rows[0][i][threadIdx.x], f);
-        get4(raw.rows[1][i][threadIdx.x], d);
+      const bool valid = t < n && in_s;
+      float2 sp[2], u[2], f[2], d[2];
+      get4_if(valid, raw.rows[0][i][threadIdx.x], f);
+      get4_if(valid, raw.rows[1][i][threadIdx.x], d);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          float2 unused, e;
-          softplus_pair(K, d[p], bias[p], unused, e, sp[p]);
-          u[p] = mul2(mul2(sp[p], both(kLn2)), f[p]);
-        }
+      for (int p = 0; p < 2; ++p) {
+        float2 unused, e;
+        softplus_pair(K, d[p], bias[p], unused, e, sp[p]);
+        sp[p] = valid ? sp[p] : both(0.f);
+        u[p] = mul2(mul2(sp[p], both(kLn2)), f[p]);
       }
       store_row(&mem.sp[t][q], sp[0], sp[1]);
       store_row(&mem.u[t][q], u[0], u[1]);
     }
     __syncthreads();                       // (B and C of the turn before are done with)
     if (P.states && in && (row0 - s.begin) % kStateRows == 0)
-      store_wide<N>(P.states + ((size_t)(s.begin / kStateRows + s.seq) + (row0 - s.begin) / kStateRows) * DN + state, h);
-#pragma unroll kFU
+      save_states<N>(P.states + ((size_t)(s.begin / kStateRows + s.seq) + (row0 - s.begin) / kStateRows) * DN +
+                         (size_t)at.c0 * N, at.lane, lanes_from<N>(at.c0, at.c_end), h);
+#pragma unroll 4
     for (int t = 0; t < R; ++t) {
       float sp[W::CH], u[W::CH], y[W::CH];
       float2 B[W::NT / 2], C[W::NT / 2];
@@ -582,17 +598,17 @@ __global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, FB) forward_kernel(c
 #pragma unroll
     for (int i = 0; i < St::kItems; ++i) {
       const int t = at.row(i);
-      if (t >= n || !in_s) continue;
       float2 y[2], f[2], g[2];
       load_row(&mem.sp[t][at.quad()], y[0], y[1]);
       get4(raw.rows[0][i][threadIdx.x], f);
-      if (P.z) get4(raw.rows[2][i][threadIdx.x], g);
+      get4(raw.rows[2][i][threadIdx.x], g);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         y[p] = fma2(skip[p], f[p], y[p]);
-        if (P.z) y[p] = mul2(y[p], mul2(g[p], sigmoid2(g[p])));
+        const float2 gated = mul2(y[p], mul2(g[p], sigmoid2(g[p])));
+        y[p] = P.z ? gated : y[p];
       }
-      store_row(static_cast<T*>(P.y) + (size_t)(row0 + t) * P.D + cs, y[0], y[1]);
+      if (t < n && in_s) store_row(static_cast<T*>(P.y) + (size_t)(row0 + t) * P.D + cs, y[0], y[1]);
     }
     __syncwarp();                          // the warp's rows are done with
   }
@@ -600,50 +616,52 @@ __global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, FB) forward_kernel(c
 }
 
 // The state in front of every chunk from those behind the chunks before it; with
-// kBack the gradient of the state behind every chunk.  Four states a thread.
+// kBack the gradient of the state behind every chunk.  Four states a thread; the loads of
+// up to 16 chunks together, since the time is their latency.
 constexpr int kFoldThreads = 128;
 template <bool kBack>
 __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs P, int N, int blocks) {
   wait_for_stream();
-  if (!offsets_ok(P.packed)) return;
-  const int seq = blockIdx.x / blocks;
-  const long long i = (long long)(blockIdx.x % blocks) * kFoldThreads + threadIdx.x;
+  const int seq = blockIdx.x / blocks, i = ((int)(blockIdx.x % blocks) * kFoldThreads + threadIdx.x) * 4;
   const size_t DN = (size_t)P.D * N;
-  if (i * 4 >= (long long)DN) return;
-  const int begin = P.packed.begin(seq), end = P.packed.begin(seq + 1), c = (int)(i * 4 / N);
+  const bool in = i < (long long)DN;
+  float4 A, h = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (in) A = *reinterpret_cast<const float4*>(P.A + i);
+  if (in && P.h0) h = *reinterpret_cast<const float4*>(P.h0 + seq * DN + i);
+  if (!offsets_ok(P.packed) || !in) return;
+  const int begin = P.packed.begin(seq), end = P.packed.begin(seq + 1);
   const int chunks = max(1, (int)(((long long)end - begin + P.L - 1) / P.L));
-  const float4 A = *reinterpret_cast<const float4*>(P.A + i * 4);
-  float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (P.h0) h = *reinterpret_cast<const float4*>(P.h0 + seq * DN + i * 4);
-  const size_t number = (size_t)(begin / P.L + seq);
-  constexpr int kAhead = 8;
-  for (int k0 = 0; k0 < chunks; k0 += kAhead) {
-    float4 S[kAhead];
-    float sum[kAhead];
-    float* at[kAhead];
+  const size_t number = (size_t)(begin / P.L + seq) + (kBack ? chunks - 1 : 0);
+  float* at = P.carry + number * DN + i;
+  const float* sums = P.sums + number * P.D + i / N;
+  const long long step = kBack ? -(long long)DN : (long long)DN, sums_step = kBack ? -P.D : P.D;
+  // n of up to M chunks.
+  auto some = [&](auto most, int n) {
+    constexpr int M = decltype(most)::value;
+    float4 S[M];
+    float sum[M];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int k = k0 + j;
-      if (k >= chunks) break;
-      const size_t m = number + (kBack ? chunks - 1 - k : k);
-      at[j] = P.carry + m * DN + i * 4;
-      if (k + 1 < chunks) {
-        S[j] = *reinterpret_cast<const float4*>(at[j]);
-        sum[j] = P.sums[m * P.D + c];
+    for (int j = 0; j < M; ++j)
+      if (j < n) {
+        S[j] = *reinterpret_cast<const float4*>(at + j * step);
+        sum[j] = sums[j * sums_step];
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (k0 + j >= chunks) break;
-      *reinterpret_cast<float4*>(at[j]) = h;
-      if (k0 + j + 1 < chunks) {
+    for (int j = 0; j < M; ++j)
+      if (j < n) {
+        *reinterpret_cast<float4*>(at + j * step) = h;
         h.x = fmaf(ex2(-A.x * sum[j]), h.x, S[j].x);
         h.y = fmaf(ex2(-A.y * sum[j]), h.y, S[j].y);
         h.z = fmaf(ex2(-A.z * sum[j]), h.z, S[j].z);
         h.w = fmaf(ex2(-A.w * sum[j]), h.w, S[j].w);
       }
-    }
-  }
+    at += n * step;
+    sums += n * sums_step;
+  };
+  int left = chunks - 1;                   // behind the last chunk nothing is needed
+  for (; left >= 16; left -= 16) some(std::integral_constant<int, 16>{}, 16);
+  for (; left > 0; left -= 8) some(std::integral_constant<int, 8>{}, min(left, 8));
+  *reinterpret_cast<float4*>(at) = h;
 }
 
 // ------------------------------------------------------------------ backward
@@ -701,7 +719,7 @@ struct BackwardSmem {
 // its first, R at a time: forward from the saved state with the state in front of
 // every row parked in tensor memory, then back.
 template <typename T, int N>
-__global__ void __launch_bounds__(Steps<Square<N>>::kThreads, 2) backward_kernel(const ScanArgs P) {
+__global__ void __launch_bounds__(Steps<Square<N>>::kThreads, kBackBlocks) backward_kernel(const ScanArgs P) {
   using Sq = Square<N>;
   using St = Steps<Sq>;
   constexpr int R = Sq::kRows;
@@ -729,6 +747,9 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, 2) backward_kernel
   const bool in = c < at.c_end, in_s = cs < at.c_end;
   const size_t state = (size_t)c * N + nl * 4, DN = (size_t)P.D * N;
   float2 some[8];                          // states on their way to or from memory
+  int saved[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) saved[j] = saved_at<N>(c + j, at.c0 - at.warp * Sq::kCols, at.c_end, nl);
   Pair nA[8], dA[8];
   zero8(some);
   pairs_of(some, dA);
@@ -745,7 +766,7 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, 2) backward_kernel
   const unsigned parts = gridDim.x / P.tiles, part = blockIdx.x / P.tiles;
   for (unsigned index = part; index < P.indexes; index += parts) {
     Span s;
-    if (!span_of(P.packed, P.L, P.chunks, (int)index, s)) continue;
+    if (find_chunk<true>(P.packed, P.L, P.chunks, (int)index, s) != kChunk) continue;
     Pair r[8];
     zero8(some);
     if (in) {
@@ -759,8 +780,18 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, 2) backward_kernel
       const int row0 = s.row0 + r0, n = min(R, s.rows - r0);
       auto& raw = sh.raw[turn];
       zero8(some);
-      if (in)
-        load_states<N>(P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * DN + state, some);
+      if (in) {
+        const float* const p = P.states + ((size_t)(s.begin / R + s.seq) + (row0 - s.begin) / R) * DN;
+#pragma unroll
+        for (int cp = 0; cp < 2; ++cp) {
+          const float4 a = *reinterpret_cast<const float4*>(p + saved[2 * cp]);
+          const float4 b = *reinterpret_cast<const float4*>(p + saved[2 * cp + 1]);
+          some[cp * 4 + 0] = make_float2(a.x, b.x);
+          some[cp * 4 + 1] = make_float2(a.y, b.y);
+          some[cp * 4 + 2] = make_float2(a.z, b.z);
+          some[cp * 4 + 3] = make_float2(a.w, b.w);
+        }
+      }
       cp_async_wait_all();
       if (r0 > 0) sh.raw[turn ^ 1].template ask<true, true>(P, at, in_s, from, ld, row0 - R, R);
       __syncthreads();                     // the rows behind are done with
@@ -768,19 +799,18 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, 2) backward_kernel
 #pragma unroll
       for (int i = 0; i < St::kItems; ++i) {
         const int t = at.row(i), q = at.quad();
-        float2 sp[2] = {both(0.f), both(0.f)}, u[2] = {both(0.f), both(0.f)}, d[2] = {both(0.f), both(0.f)};
-        if (t < n && in_s) {
-          float2 f[2], v[2];
-          get4(raw.rows[0][i][threadIdx.x], f);
-          get4(raw.rows[1][i][threadIdx.x], v);
+        const bool valid = t < n && in_s;
+        float2 sp[2], u[2], d[2], f[2], v[2];
+        get4_if(valid, raw.rows[0][i][threadIdx.x], f);
+        get4_if(valid, raw.rows[1][i][threadIdx.x], v);
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            float2 unused, e;
-            softplus_pair(K, v[p], bias[p], unused, e, sp[p]);
-            u[p] = mul2(mul2(sp[p], both(kLn2)), f[p]);
-          }
-          dinner_of(raw.rows[2][i][threadIdx.x], raw.rows[3][i][threadIdx.x], P.z != nullptr, d);
+        for (int p = 0; p < 2; ++p) {
+          float2 unused, e;
+          softplus_pair(K, v[p], bias[p], unused, e, sp[p]);
+          sp[p] = valid ? sp[p] : both(0.f);
+          u[p] = mul2(mul2(sp[p], both(kLn2)), f[p]);
         }
+        dinner_of(valid, raw.rows[2][i][threadIdx.x], raw.rows[3][i][threadIdx.x], P.z != nullptr, d);
         store_row(&mem.sp[t][q], sp[0], sp[1]);
         store_row(&mem.u[t][q], u[0], u[1]);
         store_row(&mem.d[t][q], d[0], d[1]);
@@ -788,7 +818,7 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, 2) backward_kernel
       __syncthreads();
       Pair h[8], other[8];
       pairs_of(some, h);
-#pragma unroll kBU
+#pragma unroll 8
       for (int t = 0; t < R; ++t) {
         Pair sp[2], u[2], B[4];
         park_pairs(park + t * 16, h);
@@ -899,19 +929,19 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, 2) backward_kernel
 #pragma unroll
       for (int i = 0; i < St::kItems; ++i) {
         const int t = at.row(i), q = at.quad();
-        if (t >= n || !in_s) continue;
+        const bool valid = t < n && in_s;
         const size_t row = row0 + t;
-        float2 x[2], dt[2], d[2], sp[2], du[2], dl[2], dx[2], ddt[2];
-        get4(raw.rows[0][i][threadIdx.x], x);
-        get4(raw.rows[1][i][threadIdx.x], dt);
+        float2 x[2], dt[2], d[2], sp[2], du[2], dl[2], dx[2], ddt[2], dz[2];
+        get4_if(valid, raw.rows[0][i][threadIdx.x], x);
+        get4_if(valid, raw.rows[1][i][threadIdx.x], dt);
         load_row(&mem.sp[t][q], sp[0], sp[1]);
         load_row(&mem.u[t][q], du[0], du[1]);
         load_row(&mem.dl[t][q], dl[0], dl[1]);
         load_row(&mem.d[t][q], d[0], d[1]);
         if (P.z) {
-          float2 z[2], dy[2], dz[2];
-          get4(raw.rows[2][i][threadIdx.x], dy);
-          get4(raw.rows[3][i][threadIdx.x], z);
+          float2 z[2], dy[2];
+          get4_if(valid, raw.rows[2][i][threadIdx.x], dy);
+          get4_if(valid, raw.rows[3][i][threadIdx.x], z);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const float2 sig = sigmoid2(z[p]), inner = fma2(skip[p], x[p], d[p]);
@@ -919,17 +949,19 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, 2) backward_kernel
             // silu' = sig (1 + z (1 - sig)).
             dz[p] = mul2(mul2(dy[p], inner), mul2(sig, fma2(z[p], sub2(both(1.f), sig), both(1.f))));
           }
-          store_row(static_cast<T*>(P.dz) + row * P.ld_z_grad + cs, dz[0], dz[1]);
         }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           dx[p] = fma2(du[p], mul2(sp[p], both(kLn2)), mul2(d[p], skip[p]));
           ddt[p] = mul2(fma2(du[p], x[p], dl[p]), sigmoid2(add2(dt[p], bias[p])));
           dskip[p] = fma2(d[p], x[p], dskip[p]);
-          dbias[p] = add2(dbias[p], ddt[p]);
+          dbias[p] = valid ? add2(dbias[p], ddt[p]) : dbias[p];
         }
-        store_row(static_cast<T*>(P.dx) + row * P.ld_grad + cs, dx[0], dx[1]);
-        store_row(static_cast<T*>(P.ddt) + row * P.ld_grad + cs, ddt[0], ddt[1]);
+        if (valid) {
+          store_row(static_cast<T*>(P.dx) + row * P.ld_grad + cs, dx[0], dx[1]);
+          store_row(static_cast<T*>(P.ddt) + row * P.ld_grad + cs, ddt[0], ddt[1]);
+          if (P.z) store_row(static_cast<T*>(P.dz) + row * P.ld_z_grad + cs, dz[0], dz[1]);
+        }
       }
     }
     floats_of(r, some);
@@ -1097,15 +1129,24 @@ int group_tiles_of(const SelectiveDims& d) {
 }
 
 // How the sequences are cut: rows of a chunk, a multiple of kStateRows, and whether any
-// sequence has more than one.
+// sequence has more than one.  A chunk more costs its block's start and end and a step of
+// the fold, a chunk less leaves multiprocessors idle at the end: there are as many as make
+// kFillEqual (where lengths are on the device kFillPacked) blocks a multiprocessor.
+// Measured with 6, 12, 24, 36: scan of 131072 x 1024 x 16 in one sequence 1025, 1022, 1041
+// and 1098 us, training of 32768 x 1024 in eight 1039, 1035, 1026 and 1020; packed, with 8,
+// 16, 32, 48: training of 5003 x 960 x 32 338, 328, 335 and 355.  Chunks go down to 16 rows:
+// 600 rows of 16 sequences take 28 us with them, 39 with 64 rows, 50 without any cut.
 struct Cut {
   int L;
   bool split;
 };
-constexpr int kLeastChunk = LC, kMostChunk = 1 << 20;
-Cut cut_of(const SelectiveDims& d, bool equal) {
+constexpr int kFillEqual = 12, kFillPacked = 16;
+// (In the backward pass a block takes several chunks, which more of them spread evenly.)
+constexpr int kFillEqualBack = 36;
+constexpr int kLeastChunk = 16, kMostChunk = 1 << 20;
+Cut cut_of(const SelectiveDims& d, bool equal, bool back) {
   const long long tiles = (long long)group_tiles_of(d) * d.groups;
-  const long long slots = (long long)(equal ? FILL_E : FILL) * device_limits().sms / tiles;
+  const long long slots = (long long)(!equal ? kFillPacked : back ? kFillEqualBack : kFillEqual) * device_limits().sms / tiles;
   const int longest = equal && d.n_seq > 0 ? d.rows / d.n_seq : d.rows;
   long long chunks = equal && d.n_seq > 0 ? slots / d.n_seq : slots;   // of `longest` rows
   if (chunks < 1) chunks = 1;
@@ -1117,12 +1158,13 @@ Cut cut_of(const SelectiveDims& d, bool equal) {
 }
 size_t numbers_of(const SelectiveDims& d, int L) { return (size_t)chunk_numbers(d.rows, d.n_seq, L); }
 size_t carry_bytes(const SelectiveDims& d, const Cut& cut) {
-  return cut.split ? round256(numbers_of(d, cut.L) * d.D * d.N * 4) + round256(numbers_of(d, cut.L) * d.D * 4) : 0;
+  if (!cut.split) return 0;
+  return round256(numbers_of(d, cut.L) * d.D * d.N * 4) + round256(numbers_of(d, cut.L) * d.D * 4);
 }
 // Parts of the sums over rows: at most what fills the GPU.
 size_t most_parts(const SelectiveDims& d) {
-  const size_t tiles = (size_t)group_tiles_of(d) * d.groups, fill = 2 * (size_t)device_limits().sms;
-  return (fill + tiles - 1) / tiles;
+  const size_t tiles = (size_t)group_tiles_of(d) * d.groups, fill = kBackBlocks * (size_t)device_limits().sms;
+  return fill > tiles ? fill / tiles : 1;
 }
 
 ScanArgs args_of(const SelectiveDims& d, const SelectiveInputs& in, const Cut& cut, void* workspace,
@@ -1157,8 +1199,8 @@ ScanArgs args_of(const SelectiveDims& d, const SelectiveInputs& in, const Cut& c
   }
   if (cut.split) {
     P.carry = static_cast<float*>(workspace);
-    P.sums = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                      round256(numbers_of(d, cut.L) * d.D * d.N * 4));
+    char* w = static_cast<char*>(workspace) + round256(numbers_of(d, cut.L) * d.D * d.N * 4);
+    P.sums = reinterpret_cast<float*>(w);
   }
   P.status = status;
   return P;
@@ -1204,14 +1246,19 @@ cudaError_t launch_fold(const SelectiveDims& d, const ScanArgs& P, cudaStream_t 
 
 int selective_scan_tiles(const SelectiveDims& d) { return group_tiles_of(d) * d.groups; }
 
-size_t selective_scan_workspace_bytes(const SelectiveDims& d) {
-  const size_t a = carry_bytes(d, cut_of(d, false));
-  const size_t b = d.n_seq > 0 && d.rows % d.n_seq == 0 ? carry_bytes(d, cut_of(d, true)) : 0;
-  return 256 + (a > b ? a : b);
+namespace {
+// Whatever the sequences' lengths may be given as.
+size_t most_carry_bytes(const SelectiveDims& d, bool back) {
+  const size_t a = carry_bytes(d, cut_of(d, false, back));
+  const size_t b = d.n_seq > 0 && d.rows % d.n_seq == 0 ? carry_bytes(d, cut_of(d, true, back)) : 0;
+  return a > b ? a : b;
 }
+}  // namespace
+
+size_t selective_scan_workspace_bytes(const SelectiveDims& d) { return 256 + most_carry_bytes(d, false); }
 size_t selective_scan_backward_workspace_bytes(const SelectiveDims& d) {
   const size_t tiles = (size_t)group_tiles_of(d) * d.groups;
-  return selective_scan_workspace_bytes(d) + round256(most_parts(d) * d.D * (d.N + 2) * 4) +
+  return 256 + most_carry_bytes(d, true) + round256(most_parts(d) * d.D * (d.N + 2) * 4) +
          (size_t)d.rows * tiles * 2 * d.N * 4;
 }
 
@@ -1222,7 +1269,7 @@ size_t selective_scan_states_bytes(const SelectiveDims& d) {
 cudaError_t launch_selective_scan_forward(const SelectiveDims& d, const SelectiveInputs& in,
                                           const float* h0, void* y, float* hT, float* states,
                                           void* workspace, unsigned* status, cudaStream_t stream) {
-  const Cut cut = cut_of(d, !in.offsets);
+  const Cut cut = cut_of(d, !in.offsets, false);
   ScanArgs P = args_of(d, in, cut, workspace, status);
   P.h0 = h0;
   P.hT = hT;
@@ -1254,7 +1301,7 @@ cudaError_t launch_selective_scan_backward(const SelectiveDims& d, const Selecti
     if (e == cudaSuccess && out.dbias) e = cudaMemsetAsync(out.dbias, 0, (size_t)d.D * 4, stream);
     return e;
   }
-  const Cut cut = cut_of(d, !in.offsets);
+  const Cut cut = cut_of(d, !in.offsets, true);
   ScanArgs P = args_of(d, in, cut, workspace, status);
   char* w = static_cast<char*>(workspace) + carry_bytes(d, cut);
   P.partial = reinterpret_cast<float*>(w);

@@ -103,7 +103,7 @@ struct SlotTable {
 // and 14.2, 1024 50 and 50, 4360 209 and 192, 16400 865 and 711.
 template <class F>
 cudaError_t with_group(int rows, long long blocks, int most, F f) {
-  if (blocks < most) return f(std::integral_constant<int, 1>{});
+  if (blocks < most && rows < 4096) return f(std::integral_constant<int, 1>{});
   if (rows < 16384) return f(std::integral_constant<int, 16>{});
   return f(std::integral_constant<int, 64>{});
 }

@@ -64,8 +64,14 @@ struct Steps {
   static constexpr int kThreads = 32 * S::kWarps, QL = S::kCols / 4, kItems = S::kRows * QL / 32;
 };
 
+// From this many sequences on the offsets are checked by a kernel of their own, which
+// leaves its finding in the workspace: looked through by every block they are most of the
+// work (6000 rows in 3000 sequences, 1920 channels bf16: 888 us forward, 2438 without).
+constexpr int kManySequences = 32;
+
 struct ScanArgs {
   Packed packed;
+  int* bad_offsets;      // of many sequences
   const void* x;
   const void* dt;
   const void* z;
@@ -102,21 +108,33 @@ struct Span {
   int seq, number, row0, rows, begin;
   bool first, last;
 };
+// Whether the offsets are good (all threads of the block call it).
+__device__ __forceinline__ bool offsets_good(const ScanArgs& P) {
+  if (!P.packed.offsets || P.packed.n_seq < kManySequences) return offsets_ok(P.packed);
+  return *P.bad_offsets == 0;
+}
+__global__ void __launch_bounds__(1024) check_offsets_kernel(const Packed P, int* bad) {
+  wait_for_stream();
+  const bool ok = offsets_ok(P);
+  if (threadIdx.x == 0) *bad = !ok;
+}
+
 enum Found { kBad, kNone, kChunk };
 // The chunk of an index: its number, or where sequences are equal the place among all
 // of them.  All threads of the block call it; kBad: the offsets break their rules.  Up
 // to 31 sequences every lane looks at one, so that there is one load's latency.
 // kChecked: the offsets are known to be good.
 template <bool kChecked>
-__device__ __forceinline__ Found find_chunk(const Packed& P, int L, int chunks, int index, Span& s) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ Found find_chunk(const ScanArgs& args, int index, Span& s) {
+  const Packed& P = args.packed;
+  const int lane = threadIdx.x & 31, L = args.L;
   int chunk, end;
   if (!P.offsets) {
-    s.seq = index / chunks;
-    chunk = index % chunks;
+    s.seq = index / args.chunks;
+    chunk = index % args.chunks;
     s.begin = P.begin(s.seq);
     end = P.begin(s.seq + 1);
-  } else if (P.n_seq < 32) {
+  } else if (P.n_seq < kManySequences) {   // at most 31
     const int o = __ldg(P.offsets + min(lane, P.n_seq)), before = __shfl_up_sync(0xffffffffu, o, 1);
     if (__any_sync(0xffffffffu, o < 0 || o > P.rows || (lane > 0 && o < before))) return kBad;
     s.seq = __popc(__ballot_sync(0xffffffffu, lane < P.n_seq && o / L + lane <= index)) - 1;
@@ -125,7 +143,7 @@ __device__ __forceinline__ Found find_chunk(const Packed& P, int L, int chunks, 
     end = __shfl_sync(0xffffffffu, o, s.seq + 1);
     chunk = index - (s.begin / L + s.seq);
   } else {
-    if (!kChecked && !offsets_ok(P)) return kBad;
+    if (!kChecked && !offsets_good(args)) return kBad;
     s.seq = sequence_of(P, L, index);
     if (s.seq < 0) return kNone;
     s.begin = P.begin(s.seq);
@@ -428,7 +446,7 @@ __global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, kSummaryBlocks) summ
   float2 bias[2], sum[2] = {both(0.f), both(0.f)};
   load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
   Span s;
-  const Found found = find_chunk<false>(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s);
+  const Found found = find_chunk<false>(P, blockIdx.x / P.tiles, s);
   if (found == kBad && threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
   if (found != kChunk) return;
   if (kBack ? s.first : s.last) return;    // nobody needs it
@@ -526,7 +544,7 @@ __global__ void __launch_bounds__(Steps<Wide<N>>::kThreads, kForwardBlocks) forw
   load_four(P.bias ? P.bias + cs : nullptr, in_s, 0.f, bias);
   load_four(P.skip ? P.skip + cs : nullptr, in_s, 0.f, skip);
   Span s;
-  const Found found = find_chunk<false>(P.packed, P.L, P.chunks, blockIdx.x / P.tiles, s);
+  const Found found = find_chunk<false>(P, blockIdx.x / P.tiles, s);
   if (found == kBad && threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
   if (found != kChunk) return;
   const void* const from[3] = {P.x, P.dt, P.z};
@@ -628,7 +646,7 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const ScanArgs P, in
   float4 A, h = make_float4(0.f, 0.f, 0.f, 0.f);
   if (in) A = *reinterpret_cast<const float4*>(P.A + i);
   if (in && P.h0) h = *reinterpret_cast<const float4*>(P.h0 + seq * DN + i);
-  if (!offsets_ok(P.packed) || !in) return;
+  if (!offsets_good(P) || !in) return;
   const int begin = P.packed.begin(seq), end = P.packed.begin(seq + 1);
   const int chunks = max(1, (int)(((long long)end - begin + P.L - 1) / P.L));
   const size_t number = (size_t)(begin / P.L + seq) + (kBack ? chunks - 1 : 0);
@@ -730,7 +748,7 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, kBackBlocks) backw
   static_assert(sizeof(BackwardSmem<T, N>) <= 227 * 1024, "shared memory of a block");
   // A block that holds tensor memory must not wait for a kernel in front of it.
   wait_for_stream();
-  if (!offsets_ok(P.packed)) {
+  if (!offsets_good(P)) {
     if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     return;
   }
@@ -766,7 +784,7 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, kBackBlocks) backw
   const unsigned parts = gridDim.x / P.tiles, part = blockIdx.x / P.tiles;
   for (unsigned index = part; index < P.indexes; index += parts) {
     Span s;
-    if (find_chunk<true>(P.packed, P.L, P.chunks, (int)index, s) != kChunk) continue;
+    if (find_chunk<true>(P, (int)index, s) != kChunk) continue;
     Pair r[8];
     zero8(some);
     if (in) {
@@ -993,7 +1011,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     bc_sums_kernel(const ScanArgs P, int N, T* dB, T* dC, long long ld) {
   wait_for_stream();
-  if (!offsets_ok(P.packed)) return;
+  if (!offsets_good(P)) return;
   const int width = P.G * 2 * N;
   const long long first = P.packed.begin(0), n = (long long)(P.packed.begin(P.packed.n_seq) - first) * width;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
@@ -1010,10 +1028,11 @@ __global__ void __launch_bounds__(256)
 // Sums of [parts][D (N + 2)] over the parts, always in the same order: 32 columns a
 // block, each of 32 warps every 32nd part, then the warps.
 __global__ void __launch_bounds__(1024)
-    scan_sums_kernel(const Packed packed, const float* partial, int parts, long long D, int N,
-                     float* dA, float* dskip, float* dbias) {
+    scan_sums_kernel(const ScanArgs P, int parts, int N, float* dA, float* dskip, float* dbias) {
   wait_for_stream();
-  if (!offsets_ok(packed)) return;
+  if (!offsets_good(P)) return;
+  const float* const partial = P.partial;
+  const long long D = P.D;
   __shared__ float warps[32][33];
   const long long width = D * (N + 2), i = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1156,6 +1175,7 @@ Cut cut_of(const SelectiveDims& d, bool equal, bool back) {
   if (L < kLeastChunk) L = kLeastChunk;
   return Cut{(int)L, longest > L};
 }
+constexpr size_t kHeaderBytes = 256;       // of the workspace, in front of the carry
 size_t numbers_of(const SelectiveDims& d, int L) { return (size_t)chunk_numbers(d.rows, d.n_seq, L); }
 size_t carry_bytes(const SelectiveDims& d, const Cut& cut) {
   if (!cut.split) return 0;
@@ -1197,10 +1217,11 @@ ScanArgs args_of(const SelectiveDims& d, const SelectiveInputs& in, const Cut& c
     P.chunks = len > cut.L ? (int)(((long long)len + cut.L - 1) / cut.L) : 1;
     P.indexes = (unsigned)P.chunks * d.n_seq;
   }
+  P.bad_offsets = static_cast<int*>(workspace);
   if (cut.split) {
-    P.carry = static_cast<float*>(workspace);
-    char* w = static_cast<char*>(workspace) + round256(numbers_of(d, cut.L) * d.D * d.N * 4);
-    P.sums = reinterpret_cast<float*>(w);
+    char* w = static_cast<char*>(workspace) + kHeaderBytes;
+    P.carry = reinterpret_cast<float*>(w);
+    P.sums = reinterpret_cast<float*>(w + round256(numbers_of(d, cut.L) * d.D * d.N * 4));
   }
   P.status = status;
   return P;
@@ -1236,6 +1257,11 @@ cudaError_t with_kind(const SelectiveDims& d, F f) {
   return d.dtype == SDM_BF16 ? states(__nv_bfloat16{}) : states(float{});
 }
 
+cudaError_t check_offsets(const ScanArgs& P, cudaStream_t stream) {
+  if (!P.packed.offsets || P.packed.n_seq < kManySequences) return cudaSuccess;
+  return launch_behind(check_offsets_kernel, 1, 1024, 0, stream, P.packed, P.bad_offsets);
+}
+
 template <bool kBack>
 cudaError_t launch_fold(const SelectiveDims& d, const ScanArgs& P, cudaStream_t stream) {
   const int blocks = (int)(((long long)d.D * d.N / 4 + kFoldThreads - 1) / kFoldThreads);
@@ -1255,10 +1281,10 @@ size_t most_carry_bytes(const SelectiveDims& d, bool back) {
 }
 }  // namespace
 
-size_t selective_scan_workspace_bytes(const SelectiveDims& d) { return 256 + most_carry_bytes(d, false); }
+size_t selective_scan_workspace_bytes(const SelectiveDims& d) { return kHeaderBytes + most_carry_bytes(d, false); }
 size_t selective_scan_backward_workspace_bytes(const SelectiveDims& d) {
   const size_t tiles = (size_t)group_tiles_of(d) * d.groups;
-  return 256 + most_carry_bytes(d, true) + round256(most_parts(d) * d.D * (d.N + 2) * 4) +
+  return kHeaderBytes + most_carry_bytes(d, true) + round256(most_parts(d) * d.D * (d.N + 2) * 4) +
          (size_t)d.rows * tiles * 2 * d.N * 4;
 }
 
@@ -1280,8 +1306,8 @@ cudaError_t launch_selective_scan_forward(const SelectiveDims& d, const Selectiv
     constexpr int N = decltype(n)::value;
     static std::atomic<bool> allowed[2][64];
     const unsigned blocks = P.indexes * P.tiles;
-    cudaError_t e = cudaSuccess;
-    if (cut.split) {
+    cudaError_t e = check_offsets(P, stream);
+    if (e == cudaSuccess && cut.split) {
       e = launch_with(summary_kernel<T, N, false>, allowed[0], blocks, Steps<Wide<N>>::kThreads, sizeof(SummarySmem<T, N>), stream, P);
       if (e == cudaSuccess) e = launch_fold<false>(d, P, stream);
     }
@@ -1303,7 +1329,7 @@ cudaError_t launch_selective_scan_backward(const SelectiveDims& d, const Selecti
   }
   const Cut cut = cut_of(d, !in.offsets, true);
   ScanArgs P = args_of(d, in, cut, workspace, status);
-  char* w = static_cast<char*>(workspace) + carry_bytes(d, cut);
+  char* w = static_cast<char*>(workspace) + kHeaderBytes + carry_bytes(d, cut);
   P.partial = reinterpret_cast<float*>(w);
   P.partial_bc = reinterpret_cast<float*>(w + round256(most_parts(d) * d.D * (d.N + 2) * 4));
   P.h0 = dhT;
@@ -1320,8 +1346,8 @@ cudaError_t launch_selective_scan_backward(const SelectiveDims& d, const Selecti
     using T = decltype(t);
     constexpr int N = decltype(n)::value;
     static std::atomic<bool> allowed[2][64];
-    cudaError_t e = cudaSuccess;
-    if (cut.split) {
+    cudaError_t e = check_offsets(P, stream);
+    if (e == cudaSuccess && cut.split) {
       e = launch_with(summary_kernel<T, N, true>, allowed[0], P.indexes * P.tiles, Steps<Wide<N>>::kThreads, sizeof(SummarySmem<T, N>), stream, P);
       if (e == cudaSuccess) e = launch_fold<true>(d, P, stream);
     }
@@ -1339,8 +1365,8 @@ cudaError_t launch_selective_scan_backward(const SelectiveDims& d, const Selecti
   }
   if (e != cudaSuccess || (!out.dA && !out.dskip && !out.dbias)) return e;
   const unsigned blocks = (unsigned)(((long long)d.D * (d.N + 2) + 31) / 32);
-  return launch_behind(scan_sums_kernel, blocks, 1024, 0, stream, P.packed, (const float*)P.partial,
-                       (int)parts, (long long)d.D, d.N, out.dA, out.dskip, out.dbias);
+  return launch_behind(scan_sums_kernel, blocks, 1024, 0, stream, P, (int)parts, d.N, out.dA, out.dskip,
+                       out.dbias);
 }
 
 cudaError_t launch_selective_scan_step(const SelectiveDims& d, const SelectiveInputs& in,

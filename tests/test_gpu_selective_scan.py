@@ -217,6 +217,31 @@ def test_bad_offsets_write_nothing(off):
     check(x, offsets(0, 10, 10, 100), 3, sdm.SDM_F32)
 
 
+@pytest.mark.parametrize("at,to", [(17, -1), (17, 101), (40, 101), (30, 5), (39, 100)])
+def test_bad_offsets_of_many_sequences(at, to):
+    good = sorted([0, 100] + [(7 * i) % 100 for i in range(1, 40)])
+    off = list(good)
+    off[at] = to
+    x = draw(100, 64, 40, 16, 1, sdm.SDM_BF16)
+    sh = sdm.make_selective(40, 100, 64, 16)
+    ins = [x[k] for k in ("x", "dt", "A", "B", "C")]
+    states = sdm.sdm_selective_scan_forward(sh, *ins, offsets=offsets(*good), save_states=True)["states"]
+    three = lambda *s, dtype=torch.bfloat16: torch.full(s, 3.0, device=DEV, dtype=dtype)
+    f32 = dict(dtype=torch.float32)
+    y, hT = three(100, 64), three(40, 64, 16, **f32)
+    sdm.sdm_selective_scan_forward(sh, *ins, offsets=offsets(*off), y=y, hT=hT)
+    bad = off != sorted(off) or off[0] < 0 or off[-1] > 100
+    assert bad == (at != 39)
+    assert sdm.sdm_get_device_status() == (5 if bad else 0)
+    outs = dict(dx=three(100, 64), ddt=three(100, 64), dz=three(100, 64), dB=three(100, 1, 16), dC=three(100, 1, 16), dA=three(64, 16, **f32),
+                dskip=three(64, **f32), dbias=three(64, **f32), dh0=three(40, 64, 16, **f32))
+    if bad:
+        sdm.sdm_selective_scan_backward(sh, *ins, states, x["dy"], z=x["z"], offsets=offsets(*off), **outs)
+        assert sdm.sdm_get_device_status() == 5
+        assert all((t == 3).all() for t in (y, hT, *outs.values()))
+    check(x, offsets(*good), 40, sdm.SDM_BF16)
+
+
 def test_no_sequences_gives_zero_sums():
     x = draw(8, 64, 1, 16, 1, sdm.SDM_F32)
     sh = sdm.make_selective(0, 8, 64, 16, dtype=sdm.SDM_F32)

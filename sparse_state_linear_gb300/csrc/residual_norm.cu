@@ -11,7 +11,8 @@
 //   dgamma = sum over rows of dout s inv (dout c inv),  dbeta = sum of dout.
 //
 // Measured at 32768 x 1024 bf16, RMS-Norm: forward 39.9 us (the copy rate), backward
-// 46.7 us (0.86); 8-bit output at 16384 x 3840, groups of 128, 75.1 us (0.88).
+// 46.7 us (0.86); 8-bit output at 16384 x 3840, groups of 128, 75.1 us (0.88).  Layer
+// norm: 39 and 48 us, 77 us.
 // All of it is bound by the bytes of the rows, each read and written once: a
 // row is held in the registers of a team of warps (eight channels a thread and
 // step, 16 bytes of a bf16 tensor) between the reduction and the output.  The

@@ -16,6 +16,12 @@
 // behind it from zeros: one kernel finds S and the sum of every chunk, one folds
 // them along each sequence, and the third walks every chunk from the state in
 // front of it (backward: behind it, from the last row to the first).
+//
+// Bound by instruction issue: 2^x (4 cycles a warp of its unit), packed fp32 pairs (2)
+// and the softplus, gates and sums over lanes around them.  Measured, bf16, N = 16:
+// 131072 x 1024 in one sequence 1006 us (summary 395, forward 600; its bytes alone would
+// take 159), 32768 x 1024 in eight sequences with its backward pass 986 us (summaries 115
+// and 124, forward 177, backward 542; 110), 64 single tokens of 1920 channels 5.1 us.
 #include <atomic>
 #include <type_traits>
 
@@ -37,7 +43,9 @@ constexpr int kStateRows = 16;             // rows between saved states
 // Blocks of the forward pass and of the summaries: two warps, eight rows at a time.  A
 // thread holds 16 neighbouring states (all 8 where N = 8) of CH channels, as pairs of
 // states, so that what a row of B and C brings from shared memory serves CH channels
-// and y is summed within a thread (over 2 or 4 lanes where N is 32 or 64).
+// and y is summed within a thread (over 2 or 4 lanes where N is 32 or 64).  (131072 x
+// 1024 x 16: with four states of four channels 1204 us, with 16 of one 1062, so 1022; the
+// forward kernel with 4, 8 and 16 rows at a time 628, 592 and 653.)
 template <int N>
 struct Wide {
   static constexpr int kWarps = 2, kRows = 8, kCols = 1024 / N;   // channels of a warp

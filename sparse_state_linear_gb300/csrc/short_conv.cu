@@ -9,7 +9,11 @@
 //
 // Bound by the bytes of x and y (x, dy and dx): a warp walks a run of rows of 128
 // channels, four a lane, with the last rows in registers, so that every row is
-// loaded once but for taps - 1 rows in front of (behind) a run.
+// loaded once but for taps - 1 rows in front of (behind) a run.  Where sequences begin
+// does not matter to the cutting, so that short ones cost no more than their rows.
+// Measured at 32768 x 2048 bf16: forward 48 us (0.83 of the copy rate), backward 95 us
+// (0.62: issue and latency at 12 warps a multiprocessor); at 10007 x 1000 float32 15 and
+// 29 us; 64 single tokens of 1920 channels 3.6 us, 4000 24 us.
 #include <type_traits>
 
 #include "common.cuh"

@@ -204,32 +204,41 @@ __global__ void __launch_bounds__(kBlock<TW>) forward_kernel(const ForwardArgs P
       }
     }
   }
-  int flip = 0;
-  const long long step = (long long)gridDim.x * kTeams<TW>;
-  Eight<T> ahead_s[NV], ahead_res[NV];
-  auto ask = [&](long long row) {
-    const size_t base = (size_t)row * D;
+  Eight<T> ahead_s[kAhead ? NV : 1], ahead_res[kAhead ? NV : 1];
+  auto ask = [&](long long r) {
+    const size_t base = (size_t)r * D;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TW * 32 + lane) * kVec;
-      if (c < D && row < P.rows) {
-        ahead_s[j].load(static_cast<const T*>(P.x) + base + c);
-        if (P.residual) ahead_res[j].load(static_cast<const T*>(P.residual) + base + c);
+      const int c = (j * TW * 32 + lane) * kVec, k = kAhead ? j : 0;
+      if (c < D && r < P.rows) {
+        ahead_s[k].load(static_cast<const T*>(P.x) + base + c);
+        if (P.residual) ahead_res[k].load(static_cast<const T*>(P.residual) + base + c);
       }
     }
   };
-  long long row = (long long)blockIdx.x * kTeams<TW> + team;
-  if (kAhead) ask(row);
-  for (; row < P.rows; row += step, flip ^= 1) {
+  if constexpr (kAhead) ask((long long)blockIdx.x * kTeams<TW> + team);
+  int flip = 0;
+  for (long long row = (long long)blockIdx.x * kTeams<TW> + team; row < P.rows;
+       row += (long long)gridDim.x * kTeams<TW>, flip ^= 1) {
     const size_t base = (size_t)row * D;
-    if (!kAhead) ask(row);
     Eight<T> s[NV], res[NV];
+    if constexpr (kAhead) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      s[j] = ahead_s[j];
-      res[j] = ahead_res[j];
+      for (int j = 0; j < NV; ++j) {
+        s[j] = ahead_s[j];
+        res[j] = ahead_res[j];
+      }
+      ask(row + (long long)gridDim.x * kTeams<TW>);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TW * 32 + lane) * kVec;
+        if (c < D) {
+          s[j].load(static_cast<const T*>(P.x) + base + c);
+          if (P.residual) res[j].load(static_cast<const T*>(P.residual) + base + c);
+        }
+      }
     }
-    if (kAhead) ask(row + step);
     float2 ss2 = both(0.f), sum2 = both(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {

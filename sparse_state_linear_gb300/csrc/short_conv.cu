@@ -31,7 +31,8 @@ namespace {
 // under way together.  Measured at 32768 x 2048 bf16, us: forward with 3, 4, 5, 6 blocks
 // 51, 48, 49, 61; backward with 3 blocks 95, with 2 and 8 rows 97, with 4 the registers do
 // not suffice (207).  At 10007 x 1000 float32 backward with 2 blocks 29, 3 37.
-constexpr int kPerSm = 4, kBackPerSm = 3, kBackPerSmF32 = 2;
+constexpr int kPerSm = 4, kBackPerSm = 3, kBackPerSmF32 = 3;
+constexpr int kRingBf16 = 4, kRingF32 = 3;
 constexpr int kThreads = 128, kWarps = kThreads / 32, kWarpCols = 128;
 
 struct ConvArgs {
@@ -83,6 +84,19 @@ __device__ __forceinline__ void put_raw(T* p, Raw<T> v) {
   *reinterpret_cast<Raw<T>*>(p) = v;
 }
 
+// The same on its way to shared memory.
+__device__ __forceinline__ void copy_raw(Raw<__nv_bfloat16>* to, const __nv_bfloat16* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_raw(Raw<float>* to, const float* from) { cp_async16(to, from); }
+
+// Rounded to T: apart from the store, so that a condition covers that alone.
+template <typename T>
+__device__ __forceinline__ Raw<T> raw_of(const Pair (&f)[2]) {
+  Raw<T> r;
+  store_row(reinterpret_cast<T*>(&r), float2_of(f[0]), float2_of(f[1]));
+  return r;
+}
 template <typename T>
 __device__ __forceinline__ void put(T* p, const Pair (&f)[2]) {
   store_row(p, float2_of(f[0]), float2_of(f[1]));
@@ -174,7 +188,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) forward_kernel(const ConvArg
   taps.load(P.w, P.bias, c);
 
   Pair window[K - 1][2];                   // the rows before the next, oldest first
-  auto row = [&](int t, const Raw<T>& raw) {
+  T* to;                                   // the next row of y
+  auto row = [&](const Raw<T>& raw) {
     Pair now[2], out[2];
     raw.get(now);
 #pragma unroll
@@ -182,17 +197,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm) forward_kernel(const ConvArg
       out[p] = taps.pre(window, now[p], p);
       if (kSilu) out[p] = mul2(out[p], taps.sigmoid(out[p]));
     }
-    if (in) put(y + (size_t)t * D, out);
+    const Raw<T> o = raw_of<T>(out);
+    if (in) put_raw(to, o);
+    to += D;
     shift(window, now);
   };
   // Batches of rows, the next one's loads on their way during one's arithmetic.
   auto rows = [&](int a, int e) {
     constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;
     Raw<T> next[kBatch];
+    const T* from = x + (size_t)a * P.ld;  // (a product of 64 bits per row otherwise)
+    to = y + (size_t)a * D;
     auto ask = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (t + i < e) next[i] = raw_at(x + (size_t)(t + i) * P.ld);
+      for (int i = 0; i < kBatch; ++i) {
+        if (t + i < e) next[i] = raw_at(from);
+        from += P.ld;
+      }
     };
     ask(a);
     for (int t = a; t < e; t += kBatch) {
@@ -202,11 +223,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) forward_kernel(const ConvArg
       ask(t + kBatch);
       if (t + kBatch <= e) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) row(t + i, now[i]);
+        for (int i = 0; i < kBatch; ++i) row(now[i]);
       } else {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-          if (t + i < e) row(t + i, now[i]);
+          if (t + i < e) row(now[i]);
       }
     }
   };
@@ -262,7 +283,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackP
     if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     return;
   }
-  __shared__ Pair sums[kWarps - 1][K + 1][2][32];
+  // Rows of x and dy on their way, every thread's own channels: a batch is worked on, the
+  // others are under way.  At the end the sums of the warps.
+  constexpr int kBatch = 4, kRing = sizeof(T) == 2 ? kRingBf16 : kRingF32;
+  __shared__ union Smem {
+    Raw<T> ring[kRing][kBatch][2][kThreads];
+    Pair sums[kWarps - 1][K + 1][2][32];
+    __device__ Smem() {}
+  } sh;
+  static_assert(sizeof(sh) <= 48 * 1024, "");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = P.D;
   const int part = blockIdx.x / P.col_tiles, parts = gridDim.x / P.col_tiles;
   const int col = (blockIdx.x % P.col_tiles * 32 + lane) * 4;
@@ -294,16 +323,22 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackP
       w.get(window[j]);
       dpre[j][0] = dpre[j][1] = 0;
     }
-    constexpr int kBatch = 4;
     const int stop = e + K - 1;            // dx of row t - (K - 1) leaves at t
-    Raw<T> next_x[kBatch], next_dy[kBatch];
-    auto ask = [&](int t) {
+    const T* from_x = x + (size_t)a * P.ld;   // (products of 64 bits per row otherwise)
+    const T* from_dy = dy + (size_t)a * D;
+    T* to = dx + (a - (K - 1)) * P.ld_grad;
+    const int known = min(stop, end);
+    auto ask = [&](int t, int slot) {      // (a group of copies a batch, if an empty one)
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (t + i < stop && t + i < end) {
-          next_x[i] = raw_at(x + (size_t)(t + i) * P.ld);
-          next_dy[i] = raw_at(dy + (size_t)(t + i) * D);
+      for (int i = 0; i < kBatch; ++i) {
+        if (t + i < known) {
+          copy_raw(&sh.ring[slot][i][0][threadIdx.x], from_x);
+          copy_raw(&sh.ring[slot][i][1][threadIdx.x], from_dy);
         }
+        from_x += P.ld;
+        from_dy += D;
+      }
+      cp_async_commit();
     };
     // One row: kInside where it and the row that leaves are rows a .. e - 1.
     auto row = [&](int t, const Raw<T>& raw_x, const Raw<T>& raw_dy, auto inside) {
@@ -338,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackP
       shift(dpre, g);
       const int out = t - (K - 1);
       if (kInside) {
-        if (in) put(dx + (size_t)out * P.ld_grad, leaves);
+        const Raw<T> o = raw_of<T>(leaves);
+        if (in) put_raw(to, o);
       } else if (in && (out >= a || (a == begin && P.dx0))) {
         if (P.dxT && out >= end - (K - 1)) {
           Pair f[2];
@@ -346,27 +382,27 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackP
           leaves[0] = add2(leaves[0], f[0]);
           leaves[1] = add2(leaves[1], f[1]);
         }
-        put(out >= a ? dx + (size_t)out * P.ld_grad
-                     : dx0 + ((size_t)s * (K - 1) + (K - 1) + out - begin) * D, leaves);
+        put(out >= a ? to : dx0 + ((size_t)s * (K - 1) + (K - 1) + out - begin) * D, leaves);
       }
+      to += P.ld_grad;
     };
-    ask(a);
-    for (int t = a; t < stop; t += kBatch) {
-      Raw<T> now[kBatch], grad[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        now[i] = next_x[i];
-        grad[i] = next_dy[i];
-      }
-      ask(t + kBatch);
+    for (int i = 0; i < kRing - 1; ++i) ask(a + i * kBatch, i);
+    int slot = 0, free = kRing - 1;        // the batch's place, and the one of the batch before
+    for (int t = a; t < stop; t += kBatch) {
+      cp_async_wait<kRing - 2>();
+      ask(t + (kRing - 1) * kBatch, free);
+      const auto& now = sh.ring[slot];
       if (t > a && t + kBatch <= e) {      // (kBatch >= K - 1: what leaves is at least row a)
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) row(t + i, now[i], grad[i], std::true_type{});
+        for (int i = 0; i < kBatch; ++i) row(t + i, now[i][0][threadIdx.x], now[i][1][threadIdx.x], std::true_type{});
       } else {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-          if (t + i < stop) row(t + i, now[i], grad[i], std::false_type{});
+          if (t + i < stop) row(t + i, now[i][0][threadIdx.x], now[i][1][threadIdx.x], std::false_type{});
       }
+      free = slot;
+      slot = slot + 1 == kRing ? 0 : slot + 1;
     }
   };
 
@@ -385,12 +421,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackP
     }
   }
   if (!P.partial) return;
+  cp_async_wait_all();
+  __syncthreads();                         // the warps are done with the rows
   if (warp > 0) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
 #pragma unroll
-      for (int j = 0; j < K; ++j) sums[warp - 1][j][p][lane] = dw[j][p];
-      sums[warp - 1][K][p][lane] = dbias[p];
+      for (int j = 0; j < K; ++j) sh.sums[warp - 1][j][p][lane] = dw[j][p];
+      sh.sums[warp - 1][K][p][lane] = dbias[p];
     }
   }
   __syncthreads();
@@ -403,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackP
     for (int p = 0; p < 2; ++p) {
       v[p] = j < K ? dw[j < K ? j : 0][p] : dbias[p];
 #pragma unroll
-      for (int q = 0; q < kWarps - 1; ++q) v[p] = add2(v[p], sums[q][j][p][lane]);
+      for (int q = 0; q < kWarps - 1; ++q) v[p] = add2(v[p], sh.sums[q][j][p][lane]);
     }
     put(to + (size_t)j * D, v);
   }

@@ -10,10 +10,13 @@
 // Bound by the bytes of x and y (x, dy and dx): a warp walks a run of rows of 128
 // channels, four a lane, with the last rows in registers, so that every row is
 // loaded once but for taps - 1 rows in front of (behind) a run.  Where sequences begin
-// does not matter to the cutting, so that short ones cost no more than their rows.
-// Measured at 32768 x 2048 bf16: forward 48 us (0.83 of the copy rate), backward 95 us
-// (0.62: issue and latency at 12 warps a multiprocessor); at 10007 x 1000 float32 15 and
-// 29 us; 64 single tokens of 1920 channels 3.6 us, 4000 24 us.
+// does not matter to the cutting, so that short ones cost no more than their rows.  Rows
+// come through shared memory a few batches ahead: in registers there was room for one
+// batch (32768 x 2048 bf16: backward 95 us, now 80; 6000 rows in 3000 sequences, 1920
+// channels: forward 39, now 34).
+// Measured at 32768 x 2048 bf16: forward 47 us (0.84 of the copy rate), backward 80 us
+// (0.75: issue, and half of the cycles of the fp32 units); at 10007 x 1000 float32 11 and
+// 24 us; 64 single tokens of 1920 channels 3.6 us, 4000 24 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -27,12 +30,17 @@
 namespace sdm {
 namespace {
 
-// Blocks a multiprocessor of the forward and the backward pass, and rows whose loads are
-// under way together.  Measured at 32768 x 2048 bf16, us: forward with 3, 4, 5, 6 blocks
-// 51, 48, 49, 61; backward with 3 blocks 95, with 2 and 8 rows 97, with 4 the registers do
-// not suffice (207).  At 10007 x 1000 float32 backward with 2 blocks 29, 3 37.
-constexpr int kPerSm = 4, kBackPerSm = 3, kBackPerSmF32 = 3;
-constexpr int kRingBf16 = 4, kRingF32 = 3;
+// Blocks a multiprocessor of the forward and the backward pass.  Measured at 32768 x 2048
+// bf16, us: forward with 4, 5, 6, 8 blocks 47, 48, 48, 50 (65535 sequences of four rows,
+// 1024 channels, which wait for their first rows: 623, 564, 532, 514); backward with 2, 3, 4
+// 77, 80, 82 (6000 rows in 3000 sequences, 1920 channels: 92, 75, 70).
+constexpr int kPerSm = 4, kBackPerSm = 3;
+// Batches of rows in shared memory, one of them being worked on: what 48 KB hold of float32
+// (backward).  Backward at 32768 x 2048 bf16 with 2, 3, 4, 6 batches of four rows 86, 80, 80,
+// 81 us; batches of three and six rows 82 and 80.
+constexpr int kBatch = 4, kRingBf16 = 4, kRingF32 = 3;
+template <typename T>
+constexpr int kRing = sizeof(T) == 2 ? kRingBf16 : kRingF32;
 constexpr int kThreads = 128, kWarps = kThreads / 32, kWarpCols = 128;
 
 struct ConvArgs {
@@ -173,6 +181,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) forward_kernel(const ConvArg
     if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
     return;
   }
+  // Rows of x on their way, every thread's own channels.
+  __shared__ Raw<T> ring[kRing<T>][kBatch][kThreads];
   const int lane = threadIdx.x & 31, run = blockIdx.x / P.col_tiles * kWarps + (threadIdx.x >> 5);
   if (run >= P.runs) return;
   const int D = P.D, col = (blockIdx.x % P.col_tiles * 32 + lane) * 4;
@@ -202,33 +212,35 @@ __global__ void __launch_bounds__(kThreads, kPerSm) forward_kernel(const ConvArg
     to += D;
     shift(window, now);
   };
-  // Batches of rows, the next one's loads on their way during one's arithmetic.
+  // Batches of rows, the next ones' copies on their way during one's arithmetic.
   auto rows = [&](int a, int e) {
-    constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;
-    Raw<T> next[kBatch];
     const T* from = x + (size_t)a * P.ld;  // (a product of 64 bits per row otherwise)
     to = y + (size_t)a * D;
-    auto ask = [&](int t) {
+    auto ask = [&](int t, int slot) {      // (a group of copies a batch, if an empty one)
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        if (t + i < e) next[i] = raw_at(from);
+        if (t + i < e) copy_raw(&ring[slot][i][threadIdx.x], from);
         from += P.ld;
       }
+      cp_async_commit();
     };
-    ask(a);
-    for (int t = a; t < e; t += kBatch) {
-      Raw<T> now[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) now[i] = next[i];
-      ask(t + kBatch);
+    for (int i = 0; i < kRing<T> - 1; ++i) ask(a + i * kBatch, i);
+    int slot = 0, free = kRing<T> - 1;        // the batch's place, and the one of the batch before
+    for (int t = a; t < e; t += kBatch) {
+      cp_async_wait<kRing<T> - 2>();
+      ask(t + (kRing<T> - 1) * kBatch, free);
+      const auto& now = ring[slot];
       if (t + kBatch <= e) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) row(now[i]);
+        for (int i = 0; i < kBatch; ++i) row(now[i][threadIdx.x]);
       } else {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-          if (t + i < e) row(now[i]);
+          if (t + i < e) row(now[i][threadIdx.x]);
       }
+      free = slot;
+      slot = slot + 1 == kRing<T> ? 0 : slot + 1;
     }
   };
 
@@ -277,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) forward_kernel(const ConvArg
 // rows t are walked to taps - 1 rows behind its last one: dx of a row is whole
 // once dpre of the taps - 1 rows behind it is known.
 template <typename T, int K, bool kSilu>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackPerSmF32) backward_kernel(const ConvArgs P) {
+__global__ void __launch_bounds__(kThreads, kBackPerSm) backward_kernel(const ConvArgs P) {
   wait_for_stream();
   if (!offsets_ok(P.packed)) {
     if (threadIdx.x == 0) record_status(P.status, SDM_ERR_DEVICE_BOUNDS);
@@ -285,9 +297,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackP
   }
   // Rows of x and dy on their way, every thread's own channels: a batch is worked on, the
   // others are under way.  At the end the sums of the warps.
-  constexpr int kBatch = 4, kRing = sizeof(T) == 2 ? kRingBf16 : kRingF32;
   __shared__ union Smem {
-    Raw<T> ring[kRing][kBatch][2][kThreads];
+    Raw<T> ring[kRing<T>][kBatch][2][kThreads];
     Pair sums[kWarps - 1][K + 1][2][32];
     __device__ Smem() {}
   } sh;
@@ -387,11 +398,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackP
       to += P.ld_grad;
     };
 #pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) ask(a + i * kBatch, i);
-    int slot = 0, free = kRing - 1;        // the batch's place, and the one of the batch before
+    for (int i = 0; i < kRing<T> - 1; ++i) ask(a + i * kBatch, i);
+    int slot = 0, free = kRing<T> - 1;        // the batch's place, and the one of the batch before
     for (int t = a; t < stop; t += kBatch) {
-      cp_async_wait<kRing - 2>();
-      ask(t + (kRing - 1) * kBatch, free);
+      cp_async_wait<kRing<T> - 2>();
+      ask(t + (kRing<T> - 1) * kBatch, free);
       const auto& now = sh.ring[slot];
       if (t > a && t + kBatch <= e) {      // (kBatch >= K - 1: what leaves is at least row a)
 #pragma unroll
@@ -402,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBackPerSm : kBackP
           if (t + i < stop) row(t + i, now[i][0][threadIdx.x], now[i][1][threadIdx.x], std::false_type{});
       }
       free = slot;
-      slot = slot + 1 == kRing ? 0 : slot + 1;
+      slot = slot + 1 == kRing<T> ? 0 : slot + 1;
     }
   };
 
@@ -598,7 +609,7 @@ cudaError_t launch_short_conv_backward(const ConvDims& d, const ConvInputs& in, 
     if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)d.D * 4, stream);
     return e;
   }
-  ConvArgs P = args_of(d, in, d.dtype == SDM_BF16 ? kBackPerSm : kBackPerSmF32, status);
+  ConvArgs P = args_of(d, in, kBackPerSm, status);
   P.dy = dy;
   P.dxT = dxT;
   P.dx = dx;

@@ -956,24 +956,32 @@ def sdm_selective_scan_states_size(sh: Selective) -> int:
 
 def _selective_inputs(sh, dt, dev, x, dt_, A, B, C, skip, bias, z):
     """Addresses of the inputs that every selective scan call has, in order."""
-    rows, D, bc = sh.rows, sh.D, sh.groups * sh.N
-    ld, ld_bc = sh.ld or D, sh.ld_bc or bc
+    rows, D, G, N = sh.rows, sh.D, sh.groups, sh.N
+    ld, ld_bc = sh.ld or D, sh.ld_bc or G * N
     return (_rows_at(x, "x", dt, rows, D, ld, dev), _rows_at(dt_, "dt", dt, rows, D, ld, dev),
-            _at(A, "A", _F32, D * sh.N, dev), _bc_at(B, "B", dt, rows, bc, ld_bc, dev),
-            _bc_at(C, "C", dt, rows, bc, ld_bc, dev),
+            _at(A, "A", _F32, D * N, dev), _bc_at(B, "B", dt, rows, G, N, ld_bc, dev),
+            _bc_at(C, "C", dt, rows, G, N, ld_bc, dev),
             None if skip is None else _at(skip, "skip", _F32, D, dev),
             None if bias is None else _at(bias, "bias", _F32, D, dev),
             None if z is None else _rows_at(z, "z", dt, rows, D, sh.ld_z or D, dev))
 
 
-def _bc_at(t, name, dtype, rows, width, ld, dev):
-    """Address of B or C, [rows, groups, N] or [rows, groups * N]."""
-    if ld != width and t is not None and t.dim() == 3:
-        if t.shape[1] * t.shape[2] != width or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError(f"{name} has shape {tuple(t.shape)} and strides {t.stride()}, "
-                             f"expected rows of {width} neighbouring elements")
-        t = t.flatten(1)
-    return _rows_at(t, name, dtype, rows, width, ld, dev)
+def _bc_at(t, name, dtype, rows, groups, N, ld, dev):
+    """Address of B or C, [rows, groups, N] or [rows, groups * N] (leading
+    dimensions as for _rows_at; one dimension is taken as it lies in memory)."""
+    width, s = groups * N, () if t is None else t.shape
+    if len(s) > 1 and s[-1] != width and (s[-1] != N or s[-2] != groups):
+        raise ValueError(f"{name} has shape {tuple(s)}, expected ({rows}, {groups}, {N})")
+    if ld == width or len(s) != 3:
+        return _rows_at(t, name, dtype, rows, width, ld, dev)
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype, rows * width, dev)
+    if s[0] < rows or s[1] != groups:
+        raise ValueError(f"{name} has shape {tuple(s)}, expected ({rows}, {groups}, {N})")
+    st = t.stride()
+    if rows > 0 and (st[2] != 1 or (groups > 1 and st[1] != N) or (rows > 1 and st[0] != ld)):
+        raise ValueError(f"{name} has strides {st}, expected ({ld}, {N}, 1)")
+    return t.data_ptr()
 
 
 def sdm_selective_scan_forward(sh: Selective, x, dt, A, B, C, skip=None, bias=None, z=None,
@@ -1048,8 +1056,9 @@ def sdm_selective_scan_backward(sh: Selective, x, dt, A, B, C, states, dy, skip=
         _at(dy, "dy", ty, rows * D, dev),
         None if dhT is None else _at(dhT, "dhT", _F32, n * D * sh.N, dev),
         _rows_at(dx, "dx", ty, rows, D, ldg, dev), _rows_at(ddt, "ddt", ty, rows, D, ldg, dev),
-        _at(dA, "dA", _F32, D * sh.N, dev), _bc_at(dB, "dB", ty, rows, bc, ldbg, dev),
-        _bc_at(dC, "dC", ty, rows, bc, ldbg, dev),
+        _at(dA, "dA", _F32, D * sh.N, dev),
+        _bc_at(dB, "dB", ty, rows, sh.groups, sh.N, ldbg, dev),
+        _bc_at(dC, "dC", ty, rows, sh.groups, sh.N, ldbg, dev),
         None if dskip is None else _at(dskip, "dskip", _F32, D, dev),
         None if dbias is None else _at(dbias, "dbias", _F32, D, dev),
         None if z is None else _rows_at(dz, "dz", ty, rows, D, ldzg, dev),

@@ -814,20 +814,21 @@ def sdm_add_layernorm_workspace_size(sh: Norm) -> int:
 
 
 def sdm_add_layernorm_backward(sh: Norm, s, dout, gamma=None, ds=None, eps: float = 1e-5, dx=None,
-                               dgamma=None, dbeta=None, workspace=None, stream=None):
+                               dgamma=None, dbeta=None, workspace=None, stream=None, beta=None):
     """Gradients of sdm_add_layernorm from dout [rows, D] and ds [rows, D] (the
     gradient that reaches s from elsewhere, or None).  Returns dict(dx, dgamma,
-    dbeta); dx is the gradient of x and of residual, dgamma and dbeta are made
-    only where gamma is given."""
+    dbeta); dx is the gradient of x and of residual, dgamma is made only where
+    gamma is given, dbeta where gamma or beta is (beta's numbers are not read)."""
     L = lib()
     dev, raw, ts = _where(s, stream)
     dt, rows, D = _torch_dtype(sh.dtype, "sdm_add_layernorm_backward"), sh.rows, sh.D
     n = rows * D
     if dx is None:
         dx = _make((rows, D), dt, s, ts)
-    if gamma is not None:
-        dgamma = _make((D,), _F32, s, ts) if dgamma is None else dgamma
-        dbeta = _make((D,), _F32, s, ts) if dbeta is None else dbeta
+    if gamma is not None and dgamma is None:
+        dgamma = _make((D,), _F32, s, ts)
+    if (gamma is not None or beta is not None) and dbeta is None:
+        dbeta = _make((D,), _F32, s, ts)
     ws, wsp, nws = None, None, 0
     if dgamma is not None or dbeta is not None:
         ws, wsp, nws = _scratch(workspace, L.sdm_add_layernorm_workspace_size(ctypes.byref(sh)), s,

@@ -17,11 +17,14 @@
 // them along each sequence, and the third walks every chunk from the state in
 // front of it (backward: behind it, from the last row to the first).
 //
-// Bound by instruction issue: 2^x (4 cycles a warp of its unit), packed fp32 pairs (2)
-// and the softplus, gates and sums over lanes around them.  Measured, bf16, N = 16:
-// 131072 x 1024 in one sequence 1006 us (summary 395, forward 600; its bytes alone would
-// take 159), 32768 x 1024 in eight sequences with its backward pass 986 us (summaries 115
-// and 124, forward 177, backward 542; 110), 64 single tokens of 1920 channels 5.1 us.
+// Bound by latency at few warps: the warps of a block load, form delta and u, meet, run the
+// rows and write out one after the other, and two to four warps a scheduler do not fill
+// these stretches.  No unit is saturated (issue slots 55 to 61%, fp32 46 to 52%, 2^x 25 to
+// 57%); by its 2^x (4 cycles a warp) and packed fp32 pairs (2) the work would take about half
+// the time.  Measured, bf16, N = 16: 131072 x 1024 in one sequence 996 us (summary 395,
+// forward 600; operations 560, bytes 159), 32768 x 1024 in eight sequences with its backward
+// pass 985 us (summaries 117 and 126, forward 174, backward 541; operations 420, bytes 110),
+// 64 single tokens of 1920 channels 5.2 us.
 #include <atomic>
 #include <type_traits>
 
@@ -64,6 +67,9 @@ struct Square {
 // Blocks a multiprocessor that the registers leave room for.  Measured, us: scan of 131072
 // x 1024 x 16 bf16 with 5, 6, 7, 8 forward blocks 1044, 1035, 1042, 1088; the backward
 // pass of 32768 x 1024 with 2 blocks 570, and with 3 of half the rows at a time 577.
+// (At 8 summary blocks the backward pass's summary of bf16, N = 16, spills 36 bytes.)  With
+// N = 8 a block has 256 channels and shared memory allows fewer: summaries 7 blocks (float32
+// 5), forward 5 (3), backward 1.
 constexpr int kSummaryBlocks = 8, kForwardBlocks = 6, kBackBlocks = 2;
 constexpr int kBlockStates = 2048;         // a block's states: its channels are 2048 / N
 // How a warp goes through rows of its channels: four channels a lane and step.

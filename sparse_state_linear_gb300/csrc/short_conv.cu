@@ -12,11 +12,11 @@
 // loaded once but for taps - 1 rows in front of (behind) a run.  Where sequences begin
 // does not matter to the cutting, so that short ones cost no more than their rows.  Rows
 // come through shared memory a few batches ahead: in registers there was room for one
-// batch (32768 x 2048 bf16: backward 95 us, now 80; 6000 rows in 3000 sequences, 1920
-// channels: forward 39, now 34).
-// Measured at 32768 x 2048 bf16: forward 47 us (0.84 of the copy rate), backward 80 us
-// (0.75: issue, and half of the cycles of the fp32 units); at 10007 x 1000 float32 11 and
-// 24 us; 64 single tokens of 1920 channels 3.6 us, 4000 24 us.
+// batch (32768 x 2048 bf16: backward 95 us, now 79; 3000 sequences of two rows, 1920
+// channels: forward 39, now 33).
+// Measured at 32768 x 2048 bf16: forward 47 us (0.84 of the copy rate), backward 79 us
+// (0.75: latency at three warps a scheduler, issue slots 54% and fp32 units 51% busy); at
+// 10007 x 1000 float32 11 and 24 us; 64 single tokens of 1920 channels 3.5 us, 4000 24 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -31,9 +31,9 @@ namespace sdm {
 namespace {
 
 // Blocks a multiprocessor of the forward and the backward pass.  Measured at 32768 x 2048
-// bf16, us: forward with 4, 5, 6, 8 blocks 47, 48, 48, 50 (65535 sequences of four rows,
-// 1024 channels, which wait for their first rows: 623, 564, 532, 514); backward with 2, 3, 4
-// 77, 80, 82 (6000 rows in 3000 sequences, 1920 channels: 92, 75, 70).
+// bf16, us: forward with 4, 5, 6, 8 blocks 47, 49, 48, 48 (65535 sequences of four rows,
+// 1024 channels, with starts, which wait for their first rows: 574, 492, 442, 411); backward
+// with 2, 3, 4 76, 79, 82 (3000 sequences of two rows, 1920 channels: 91, 72, 67).
 constexpr int kPerSm = 4, kBackPerSm = 3;
 // Batches of rows in shared memory, one of them being worked on: what 48 KB hold of float32
 // (backward).  Backward at 32768 x 2048 bf16 with 2, 3, 4, 6 batches of four rows 86, 80, 80,

@@ -100,7 +100,9 @@ struct SlotTable {
 // 64 where looking through all earlier slots is much of the work.  Measured, bf16, 1920
 // channels, us with one and with 16 (64) tokens a block: convolution, 512 rows 12.3 and
 // 6.8, 4000 67 and 24, 16384 304 and 107 (128 with 16); scan of 16 states, 256 rows 12.1
-// and 14.2, 1024 50 and 50, 4360 209 and 192, 16400 865 and 711.
+// and 14.2, 1024 50 and 50, 4360 209 and 192, 16400 865 and 711.  For the scan the switch
+// (16384 blocks) is where both take the same; for the convolution (2048 blocks, 512 rows of
+// 1920 channels) 16 tokens are well ahead there, and from where on they are was not measured.
 template <class F>
 cudaError_t with_group(int rows, long long blocks, int most, F f) {
   if (blocks < most && rows < 4096) return f(std::integral_constant<int, 1>{});

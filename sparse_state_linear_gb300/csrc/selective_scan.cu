@@ -873,7 +873,9 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, kBackBlocks) backw
         float du[4], dl[4], y[4], bc[8];
       };
       // Row t: h is the state behind it, and the state in front of it comes to `before`.
-      auto back = [&](int t, Pair (&before)[8], const Pair (&h)[8], Sums& out) {
+      // (A row that does not exist changes r by nothing, but a state or gradient that is not
+      // finite times its delta of 0 must not go into dA.)
+      auto back = [&](int t, Pair (&before)[8], const Pair (&h)[8], Sums& out, bool exists = true) {
         Pair sp[2], u[2], d[2], B[4], C[4], du[2], dl[2], y[2], dB[4], dC[4];
         load_pairs(&mem.sp[t][cl * 4], sp[0], sp[1]);
         load_pairs(&mem.u[t][cl * 4], u[0], u[1]);
@@ -891,7 +893,7 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, kBackBlocks) backw
             const Pair g = fma2(d[cp], C[k], r[i]);
             r[i] = mul2(g, ex2_pair(mul2(nA[i], sp[cp])));
             const Pair p = mul2(r[i], before[i]);
-            dA[i] = fma2(p, sp[cp], dA[i]);
+            if (exists) dA[i] = fma2(p, sp[cp], dA[i]);
             du[cp] = k ? fma2(g, B[k], du[cp]) : mul2(g, B[k]);
             dl[cp] = k ? fma2(p, nA[i], dl[cp]) : mul2(p, nA[i]);
             y[cp] = k ? fma2(C[k], h[i], y[cp]) : mul2(C[k], h[i]);
@@ -935,10 +937,11 @@ __global__ void __launch_bounds__(Steps<Square<N>>::kThreads, kBackBlocks) backw
           }
         }
       };
+      const int top = (n - 1) | 1;         // rows in pairs: the last one, or the one behind it
       Sums even, odd;
-      back(R - 1, other, h, odd);
+      back(top, other, h, odd, top < n);
 #pragma unroll 1
-      for (int t = R - 2; t > 0; t -= 2) {
+      for (int t = top - 1; t > 0; t -= 2) {
         __syncwarp();                      // row t + 1 has been read
         back(t, h, other, even);
         finish(t + 1, odd);
